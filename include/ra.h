@@ -71,10 +71,12 @@ typedef enum ra_status {
   RA_ERR_MISALIGNED = 3,  /* pointer alignment below what the path needs    */
   RA_ERR_ARCH = 4,        /* no CUDA device, or not compute capability 10.3  */
   RA_ERR_CUDA = 5,        /* a CUDA runtime/driver call failed               */
-  RA_ERR_TIMEOUT = 6      /* a kernel's bounded wait ran out (watchdog)      */
+  RA_ERR_TIMEOUT = 6,     /* a kernel's bounded wait ran out (watchdog)      */
+  RA_ERR_PAGE = 7         /* a cache call met a position or page outside the cache */
 } ra_status;
 
-typedef enum ra_dtype { RA_F32 = 0, RA_BF16 = 1 } ra_dtype;
+/* RA_E4M3 (8 bits) is a cache's element type only (ra_cache). */
+typedef enum ra_dtype { RA_F32 = 0, RA_BF16 = 1, RA_E4M3 = 2 } ra_dtype;
 
 /*
  * How the N tokens of a (b, h) slice are dealt to the P ring blocks ("Ring
@@ -370,6 +372,204 @@ RA_API ra_status ra_backward_block(const void* q, const void* k, const void* v, 
                                    int32_t d, int32_t causal, ra_dtype dtype,
                                    ra_stream_t stream);
 
+/* Largest head width of the norm, rotation and cache calls. */
+#define RA_MAX_HEAD_DIM 256
+
+/*
+ * Position rotation: pair i (of rot / 2) of a head turns by the angle
+ * positions[axis[i]][token] * inv_freq[i].  A HOST plan without pointers,
+ * filled by ra_rope_init and passed to the kernels by value; it may be
+ * copied, and is not needed after a call returns.
+ *   rot          rotated elements of a head, a multiple of 8, 0 .. d; the
+ *                elements from rot on pass through.
+ *   axes         position axes (1 for text; time, height, width: 3), 1 .. 8.
+ *   interleaved  0: pair i = elements (i, i + rot / 2); 1: (2i, 2i + 1).
+ *   turns        round(frac(inv_freq / 2 pi) 2^64): the angle in turns is the
+ *                fraction of position * turns / 2^64, an integer product that
+ *                wraps, so far positions lose no precision.
+ */
+typedef struct ra_rope {
+  int32_t rot;
+  int32_t axes;
+  int32_t interleaved;
+  uint8_t axis[RA_MAX_HEAD_DIM / 2];
+  uint64_t turns[RA_MAX_HEAD_DIM / 2];
+} ra_rope;
+
+/*
+ * ra_rope_init -- fill a plan (host arithmetic only).
+ *   inv_freq  HOST [rot / 2] radians per position, |inv_freq| < 2^31, finite.
+ *   axis      HOST [rot / 2], 0 .. axes - 1 each, or NULL (all axis 0).
+ * Errors: RA_ERR_INVALID_ARG (null, out of range), RA_ERR_UNSUPPORTED (rot
+ * not a multiple of 8 or > RA_MAX_HEAD_DIM, axes > 8).
+ */
+RA_API ra_status ra_rope_init(ra_rope* rope, const double* inv_freq, const int32_t* axis,
+                              int32_t rot, int32_t axes, int32_t interleaved);
+
+/*
+ * ra_qk_norm_rope -- what stands before the attention, in one pass over q
+ * and k: every head's row x is normalised, n = x * w / sqrt(mean(x^2) + eps),
+ * and its first rot elements are rotated by the row's position.  fp32
+ * arithmetic, rounded once.
+ *   q, k        [B, Hq, N, d] and [B, Hk, N, d] of `dtype`, read through
+ *               strides (elements) of batch, head and token; d contiguous.
+ *               NULL strides: dense.  The heads of a projection [B, N, H, d]
+ *               are strides {N*H*d, d, H*d}.
+ *   q_weight,   [d] of `dtype`, or NULL (no scaling).
+ *   k_weight
+ *   rope        a plan, or NULL (no rotation).
+ *   positions   int64 [axes, B, N], any value; may be NULL without a rope.
+ *   q_out,      [B, H, N, d] of `dtype`, dense: the layout ra_forward and
+ *   k_out       ra_cache_attention take.  They may not overlap q or k.
+ *   eps         >= 0; < 0: no norm (the weights must then be NULL).
+ * d is a multiple of 8 up to RA_MAX_HEAD_DIM; tensors are 8-byte (bf16) or
+ * 16-byte (f32) aligned and strides multiples of 4.  Hq or Hk may be 0.
+ * Errors: RA_ERR_INVALID_ARG (null pointer, negative size, bad dtype or
+ * plan, eps NaN), RA_ERR_UNSUPPORTED (d, rot > d, over 2^31 - 1 tokens),
+ * RA_ERR_MISALIGNED, RA_ERR_ARCH, RA_ERR_CUDA.
+ */
+RA_API ra_status ra_qk_norm_rope(const void* q, const int64_t* q_strides, const void* k,
+                                 const int64_t* k_strides, const void* q_weight,
+                                 const void* k_weight, const ra_rope* rope,
+                                 const int64_t* positions, void* q_out, void* k_out, int32_t B,
+                                 int32_t Hq, int32_t Hk, int64_t N, int32_t d, float eps,
+                                 ra_dtype dtype, ra_stream_t stream);
+
+/*
+ * ra_qk_norm_rope_backward -- gradients of ra_qk_norm_rope.  With dy the
+ * gradient of an output row, dz = dy rotated back and r = 1 / sqrt(mean(x^2)
+ * + eps):  dx = r (dz w) - x r^3 mean(dz w x),  dw = sum over rows of dz x r.
+ *   dq_out, dk_out   dense gradients of the outputs.
+ *   dq, dk           written through dq_strides, dk_strides (NULL: dense);
+ *                    their rows may not overlap.
+ *   dq_weight,       fp32 [d], written; NULL exactly where the weight is.
+ *   dk_weight
+ *   workspace        ra_qk_norm_rope_backward_workspace_bytes(d) bytes,
+ *                    16-byte aligned, overwritten; may be NULL without
+ *                    weights.  Sums run in a fixed order: the same inputs
+ *                    give the same bits.
+ * Other arguments, rules and errors as ra_qk_norm_rope.
+ */
+RA_API ra_status ra_qk_norm_rope_backward(
+    const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+    const void* q_weight, const void* k_weight, const ra_rope* rope, const int64_t* positions,
+    const void* dq_out, const void* dk_out, void* dq, const int64_t* dq_strides, void* dk,
+    const int64_t* dk_strides, float* dq_weight, float* dk_weight, void* workspace,
+    int64_t workspace_bytes, int32_t B, int32_t Hq, int32_t Hk, int64_t N, int32_t d, float eps,
+    ra_dtype dtype, ra_stream_t stream);
+
+/* Scratch bytes of ra_qk_norm_rope_backward (-1 for an unsupported d). */
+RA_API int64_t ra_qk_norm_rope_backward_workspace_bytes(int32_t d);
+
+/*
+ * A K/V cache in pages (device pointers, caller-owned).  Sequence b keeps
+ * its tokens in order in the pages table[b][0], table[b][1], ...: position p
+ * is row p % page of page table[b][p / page].
+ *   k, v          [pages, heads, page, d] of `dtype`
+ *   k_exp, v_exp  [pages, heads, page], RA_E4M3 only (NULL otherwise): the
+ *                 row stands for code * 2^(exp - 127).
+ *   dtype         RA_F32 or RA_BF16 (the inputs' own type), or RA_E4M3 with
+ *                 inputs of either type.
+ *   page          a power of two, 8 .. 1024.   d: a multiple of 8, <= 256.
+ * k, v are 16-byte aligned.
+ *
+ * The cache calls share these arguments:
+ *   table  int32 [B, width] page numbers; entries behind a sequence's last
+ *          page are not looked at.
+ *   lens   int32 [B] tokens in the cache before the call; < 0: the sequence
+ *          takes no part (padding of a batch).
+ *   count  int32 [B] new tokens, 0 .. T, or NULL (T each).
+ * They are read on the device, so a captured call follows their contents.  A
+ * position behind the table, a page number outside the cache or a count
+ * above T does not reach memory: a write skips the token, a read gives
+ * zeros, attention leaves the key out, and ra_last_device_status returns
+ * RA_ERR_PAGE once.
+ */
+typedef struct ra_cache {
+  void* k;
+  void* v;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  int64_t pages;
+  int32_t heads;
+  int32_t page;
+  int32_t d;
+  ra_dtype dtype;
+} ra_cache;
+
+/*
+ * ra_cache_write -- append the new tokens of every sequence: token t < count
+ * goes to position lens + t.  RA_E4M3 rows are quantised as they are
+ * written: e = the smallest exponent with max|x| <= 448 * 2^e over the
+ * row's finite elements (at least -126), code = e4m3(x * 2^-e), nearest
+ * even.  The scale is a power of two, so both products are exact and a row
+ * that is read and written again keeps its values.  Infinities saturate to
+ * 448 * 2^e; NaN stays NaN.
+ *   k, v  [B, heads, T, d] of `dtype`, strides as in ra_qk_norm_rope.
+ * Tokens of one call must go to different places: sequences that share a
+ * page may share only pages that the call does not write.  lens is not
+ * advanced.
+ * Errors: RA_ERR_INVALID_ARG (null pointer, negative size, bad enum),
+ * RA_ERR_UNSUPPORTED (page, d, type pair), RA_ERR_MISALIGNED, RA_ERR_ARCH,
+ * RA_ERR_CUDA.
+ */
+RA_API ra_status ra_cache_write(const ra_cache* cache, const void* k, const int64_t* k_strides,
+                                const void* v, const int64_t* v_strides, const int32_t* table,
+                                int32_t width, const int32_t* lens, const int32_t* count,
+                                int32_t B, int32_t T, ra_dtype dtype, ra_stream_t stream);
+
+/*
+ * ra_cache_read -- positions first .. first + n - 1 of every sequence, in
+ * `dtype` (the cache's type, or RA_F32 / RA_BF16 for an RA_E4M3 cache): the
+ * visiting blocks of ra_fold, or the K/V of a prompt that is continued.
+ *   k, v  [B, heads, n, d], dense, written; rows at or behind lens are 0.
+ * Values are exact (RA_E4M3 into RA_BF16 too, but where a value is below
+ * bf16's normal range).
+ * Errors as ra_cache_write.
+ */
+RA_API ra_status ra_cache_read(const ra_cache* cache, const int32_t* table, int32_t width,
+                               const int32_t* lens, int64_t first, int64_t n, void* k, void* v,
+                               int32_t B, ra_dtype dtype, ra_stream_t stream);
+
+/*
+ * ra_cache_attention -- attention of the newest tokens (one, or a tree of
+ * drafted ones) over the cache, in which ra_cache_write has put them.  Query
+ * t < count of a sequence sees every context key (positions 0 .. lens - 1)
+ * and of the drafted keys (position lens + j, j < count) those with
+ * mask[t][j], in the online-softmax form of ra_forward ("Ring Attention:
+ * the math", section "The online-softmax identity that makes streaming
+ * legal"); tau = 1 / sqrt(d).
+ *   q     [B, Hq, T, d] of `dtype`, dense; Hq a multiple of cache->heads:
+ *         query head h reads key head h / (Hq / heads).
+ *   mask  uint8 [T, T] per sequence, mask_stride bytes apart (0: one for
+ *         all); non-zero: seen.  NULL: j <= t.
+ *   out   [B, Hq, T, d] of `dtype`;  lse [B, Hq, T] fp32.  Rows that see no
+ *         key, rows t >= count and sequences with lens < 0 get out = 0 and
+ *         lse = -inf.
+ *   workspace  ra_cache_attention_workspace_bytes bytes, 256-byte aligned;
+ *              overwritten (no initial value needed).  Calls that may
+ *              overlap on the GPU, captured ones too, need their own.
+ * An element that is not finite, in a key or value row that a query does
+ * not see, does not reach that query's result.
+ * Types: RA_BF16 inputs over an RA_BF16 or RA_E4M3 cache run on the tensor
+ * cores (d in {64, 128}); RA_F32 inputs over an RA_F32 or RA_E4M3 cache on
+ * the FFMA path (any d the cache may have).
+ * Errors: as ra_cache_write; RA_ERR_INVALID_ARG also for heads not dividing
+ * Hq, a mask_stride that is neither 0 nor >= T * T, and a workspace that is
+ * NULL or too small.
+ */
+RA_API ra_status ra_cache_attention(const void* q, const ra_cache* cache, const int32_t* table,
+                                    int32_t width, const int32_t* lens, const int32_t* count,
+                                    const uint8_t* mask, int64_t mask_stride, void* out,
+                                    float* lse, void* workspace, int64_t workspace_bytes,
+                                    int32_t B, int32_t Hq, int32_t T, ra_dtype dtype,
+                                    ra_stream_t stream);
+
+/* Scratch bytes ra_cache_attention needs for `heads` key heads (-1 for
+   invalid sizes); does not depend on the lengths. */
+RA_API int64_t ra_cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t heads,
+                                                  int32_t T, int32_t d);
+
 /*
  * ra_state_init -- set a state to empty: m = -inf, l = 0, o = 0 ("Ring
  * Attention: the math", section "Accumulation math, step by step": "state = (m
@@ -443,7 +643,9 @@ RA_API void ra_watchdog_config(int64_t wait_cycles, int64_t stall_cta);
  * ra_last_device_status -- synchronise `stream`, then read and clear the
  * device-side watchdog word of the current device.  Returns RA_ERR_TIMEOUT if
  * any kernel since the last call gave up a bounded wait (its results are then
- * invalid), RA_ERR_CUDA if the synchronisation failed, else RA_OK.
+ * invalid), RA_ERR_PAGE if a cache call met a position or page outside the
+ * cache (the first of the two wins), RA_ERR_CUDA if the synchronisation
+ * failed, else RA_OK.
  */
 RA_API ra_status ra_last_device_status(ra_stream_t stream);
 

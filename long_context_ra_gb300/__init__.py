@@ -24,7 +24,11 @@ __all__ = ["RaError", "RaState", "ra_forward", "ra_forward_causal", "ra_forward_
            "ra_backward", "ra_backward_causal", "ra_backward_rowterms", "ra_backward_block",
            "ra_state_init",
            "ra_fold", "ra_merge",
-           "ra_last_device_status", "ra_watchdog_config", "new_state", "library_path"]
+           "ra_last_device_status", "ra_watchdog_config", "new_state", "library_path",
+           "RaCache", "RaRope", "new_cache", "new_rope", "ra_qk_norm_rope",
+           "ra_qk_norm_rope_backward", "ra_qk_norm_rope_backward_workspace_bytes",
+           "ra_cache_write", "ra_cache_read", "ra_cache_attention",
+           "ra_cache_attention_workspace_bytes"]
 
 
 class RaError(RuntimeError):
@@ -352,3 +356,9 @@ def ra_watchdog_config(wait_cycles: int = 0, stall_cta: int = -1) -> None:
     fold, dK/dV and dQ launches loads nothing, so its waits run out; -1:
     off)."""
     _native.lib().ra_watchdog_config(int(wait_cycles), int(stall_cta))
+
+
+from .serving import (RaCache, RaRope, new_cache, new_rope, ra_cache_attention,  # noqa: E402
+                      ra_cache_attention_workspace_bytes, ra_cache_read, ra_cache_write,
+                      ra_qk_norm_rope, ra_qk_norm_rope_backward,
+                      ra_qk_norm_rope_backward_workspace_bytes)

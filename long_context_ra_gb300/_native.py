@@ -12,10 +12,11 @@ from pathlib import Path
 LIB_PATH = Path(__file__).resolve().parent / "_lib" / "libra_gb300.so"
 
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_MISALIGNED, RA_ERR_ARCH, RA_ERR_CUDA, \
-    RA_ERR_TIMEOUT = range(7)
-RA_F32, RA_BF16 = 0, 1
+    RA_ERR_TIMEOUT, RA_ERR_PAGE = range(8)
+RA_F32, RA_BF16, RA_E4M3 = 0, 1, 2
 RA_LAYOUTS = {"contiguous": 0, "zigzag": 1, "striped": 2}
 RA_MAX_PARTIALS = 64
+RA_MAX_HEAD_DIM = 256
 RA_SPLIT_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -26,10 +27,27 @@ class RaStateC(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("d", ctypes.c_int32)]
 
 
+class RaRopeC(ctypes.Structure):
+    """``ra_rope``: the rotation plan (host values, no pointers)."""
+
+    _fields_ = [("rot", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * (RA_MAX_HEAD_DIM // 2)),
+                ("turns", ctypes.c_uint64 * (RA_MAX_HEAD_DIM // 2))]
+
+
+class RaCacheC(ctypes.Structure):
+    """``ra_cache``: device pointers of the pages and their shape."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 # Exported symbol -> (restype, argtypes).
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 _SP = ctypes.POINTER(RaStateC)
 PROTOTYPES = {
     "ra_forward": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _P]),
@@ -54,6 +72,17 @@ PROTOTYPES = {
     "ra_backward_rowterms": (_I32, [_P, _P, _P, _I64, _I32, _I32, _P, _P]),
     "ra_backward_block": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32,
                                  _P]),
+    "ra_rope_init": (_I32, [_P, _P, _P, _I32, _I32, _I32]),
+    "ra_qk_norm_rope": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I64,
+                               _I32, _F32, _I32, _P]),
+    "ra_qk_norm_rope_backward": (_I32, [_P] * 17 + [_I64, _I32, _I32, _I32, _I64, _I32, _F32,
+                                                    _I32, _P]),
+    "ra_qk_norm_rope_backward_workspace_bytes": (_I64, [_I32]),
+    "ra_cache_write": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _P]),
+    "ra_cache_read": (_I32, [_P, _P, _I32, _P, _I64, _I64, _P, _P, _I32, _I32, _P]),
+    "ra_cache_attention": (_I32, [_P, _P, _P, _I32, _P, _P, _P, _I64, _P, _P, _P, _I64, _I32,
+                                  _I32, _I32, _I32, _P]),
+    "ra_cache_attention_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32]),
     "ra_state_init": (_I32, [_SP, _P]),
     "ra_fold": (_I32, [_SP, _P, _P, _P, _I64, _I64, _I32, _P]),
     "ra_merge": (_I32, [_SP, _I32, _P, _P, _I32, _P]),

@@ -193,6 +193,17 @@ ra_status current_ordinal(int* dev) {
   return RA_OK;
 }
 
+ra_status device_ready(int** status) {
+  DeviceInfo di;
+  const ra_status st = current_device(&di);
+  if (st == RA_OK) *status = di.status;
+  return st;
+}
+
+int64_t wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
+int64_t stall_cta() { return g_stall_cta.load(std::memory_order_relaxed); }
+
 int device_sm_count() {
   DeviceInfo di;
   if (current_device(&di) != RA_OK) return 1;
@@ -675,7 +686,7 @@ RA_API ra_status ra_last_device_status(ra_stream_t stream) {
     return RA_ERR_CUDA;
   if (cudaMemcpy(di.status, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
     return RA_ERR_CUDA;
-  return word == 0 ? RA_OK : RA_ERR_TIMEOUT;
+  return word == 0 ? RA_OK : word == kStatusPage ? RA_ERR_PAGE : RA_ERR_TIMEOUT;
 }
 
 RA_API void ra_watchdog_config(int64_t wait_cycles, int64_t stall_cta) {
@@ -693,10 +704,11 @@ RA_API const char* ra_status_string(ra_status s) {
     case RA_ERR_ARCH: return "RA_ERR_ARCH: no compute capability 10.3 device";
     case RA_ERR_CUDA: return "RA_ERR_CUDA: CUDA call failed";
     case RA_ERR_TIMEOUT: return "RA_ERR_TIMEOUT: a kernel wait ran out (watchdog)";
+    case RA_ERR_PAGE: return "RA_ERR_PAGE: a position or page outside the cache";
   }
   return "unknown ra_status";
 }
 
-RA_API int32_t ra_version(void) { return 200; }  // 0.2.0
+RA_API int32_t ra_version(void) { return 300; }  // 0.3.0
 
 }  // extern "C"

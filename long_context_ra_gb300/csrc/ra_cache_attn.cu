@@ -1,0 +1,304 @@
+// Attention of new tokens over the paged cache: the FFMA kernel (fp32
+// inputs), the join of parts, and the choice of kernel.
+//
+// The FFMA kernel.  A unit is 16 query rows of one key head; 4 warps, each
+// with 4 rows.  A tile of 32 keys is brought to shared memory as fp32 (8-bit
+// rows multiplied by their scale); lane = key for the scores, lane = columns
+// for P V, so the online softmax of a row stays inside its warp:
+//   m' = max(m, max s),  l' = l e^(m-m') + sum p,  o' = o e^(m-m') + p V
+// A key that a row does not see has p = 0 and is left out of the sum rather
+// than multiplied, so what it holds does not matter.
+
+#include "ra_cache_attn.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kTile = 32;
+constexpr int kThreads = 128;
+constexpr int kColumns = RA_MAX_HEAD_DIM / 32;  // per lane
+
+template <typename E>
+__device__ __forceinline__ float to_float(E x) {
+  return static_cast<float>(x);
+}
+__device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+template <typename E, typename H>
+__global__ void __launch_bounds__(kThreads)
+    cache_attn_ffma_kernel(const __grid_constant__ CacheAttnArgs a,
+                           const __grid_constant__ AttnPlan p) {
+  constexpr bool k8 = sizeof(H) == 1;
+  extern __shared__ float4 smem4[];
+  __shared__ DivisionShared sh;
+  __shared__ int64_t key_row[kTile];
+  __shared__ float probs[kRows][kTile];
+  const PagedArgs& c = a.c;
+  const int d = c.d, ld = d + 4;
+  float* qs = reinterpret_cast<float*>(smem4);  // [kRows][d]
+  float* ks = qs + kRows * d;                   // [kTile][ld]
+  float* vs = ks + kTile * ld;                  // [kTile][d]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t rows = head_rows(a);
+
+  const int64_t run = division_start(c, p.div, blockIdx.x, sh);
+  UnitWalk u;
+  for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
+    const int head = u.unit / p.row_tiles;
+    const int64_t r0 = static_cast<int64_t>(u.unit % p.row_tiles) * kRows;
+    // q, out, lse row of row 0 of the unit
+    const int64_t q0 = (static_cast<int64_t>(u.b) * c.heads + head) * rows + r0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * d; i += kThreads) {
+      const int r = i / d;
+      qs[i] = r0 + r < rows ? to_float(static_cast<const E*>(a.q)[q0 * d + i]) * a.scale_log2 : 0.f;
+    }
+    float m[4], l[4], o[4][kColumns];
+    int t[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+      const int64_t row = r0 + 4 * warp + r;
+      t[r] = row < rows ? static_cast<int>(row % c.T) : c.T;
+#pragma unroll
+      for (int x = 0; x < kColumns; ++x) o[r][x] = 0.f;
+    }
+    for (int64_t tile = u.first; tile < u.last; ++tile) {
+      const int64_t pos0 = tile * kTile;
+      __syncthreads();
+      if (threadIdx.x < kTile) {
+        const int64_t pos = pos0 + threadIdx.x;
+        int64_t row = -1;
+        if (pos < u.seq.keys()) row = cache_row(c, u.b, pos);
+        key_row[threadIdx.x] = row < 0 ? -1 : row + (static_cast<int64_t>(head) << c.page_shift);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < kTile * d / 8; i += kThreads) {
+        const int key = i / (d / 8), e = (i % (d / 8)) * 8;
+        const int64_t row = key_row[key];
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (row >= 0) {
+          load8(static_cast<const H*>(c.k) + row * d + e, x);
+          load8(static_cast<const H*>(c.v) + row * d + e, y);
+          if (k8) {
+            const float sk = exp_scale(c.ke[row]), sv = exp_scale(c.ve[row]);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              x[z] *= sk;
+              y[z] *= sv;
+            }
+          }
+        }
+        store8(ks + key * ld + e, x);
+        store8(vs + key * d + e, y);
+      }
+      __syncthreads();
+      // scores of key `lane` for the warp's rows
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int e = 0; e < d; e += 4) {
+        const float4 kk = *reinterpret_cast<const float4*>(ks + lane * ld + e);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 qq = *reinterpret_cast<const float4*>(qs + (4 * warp + r) * d + e);
+          s[r] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[r]))));
+        }
+      }
+      const bool here = key_row[lane] >= 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool seen = here && sees(a, u.seq, u.b, t[r], pos0 + lane);
+        if (!seen) s[r] = -INFINITY;
+        float mx = s[r];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        mx = fmaxf(mx, m[r]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float alpha = exp2f(m[r] - ref);  // 0 for an empty state
+        const float pr = seen ? exp2f(s[r] - ref) : 0.f;
+        float sum = pr;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l[r] = l[r] * alpha + sum;
+        m[r] = mx;
+        probs[4 * warp + r][lane] = pr;
+#pragma unroll
+        for (int x = 0; x < kColumns; ++x) o[r][x] *= alpha;
+      }
+      __syncwarp();
+      for (int key = 0; key < kTile; ++key) {
+        float pr[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pr[r] = probs[4 * warp + r][key];
+#pragma unroll
+        for (int x = 0; x < kColumns; ++x) {
+          const int col = lane + 32 * x;
+          if (col < d) {
+            const float vv = vs[key * d + col];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (pr[r] != 0.f) o[r][x] = fmaf(pr[r], vv, o[r][x]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t row = r0 + 4 * warp + r;
+      if (row >= rows) continue;
+      if (u.whole()) {
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        E* dst = static_cast<E*>(a.out) + (q0 + 4 * warp + r) * d;
+#pragma unroll
+        for (int x = 0; x < kColumns; ++x)
+          if (lane + 32 * x < d) store_out(dst + lane + 32 * x, o[r][x] * inv);
+        if (lane == 0)
+          a.lse[q0 + 4 * warp + r] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2F;
+      } else {
+        const int slot = u.slot(blockIdx.x);
+        float* dst = slot_o(a, p, slot) + (4 * warp + r) * d;
+#pragma unroll
+        for (int x = 0; x < kColumns; ++x)
+          if (lane + 32 * x < d) dst[lane + 32 * x] = o[r][x];
+        if (lane == 0) {
+          float* ml = slot_ml(a, p, slot) + (4 * warp + r) * 2;
+          ml[0] = m[r];
+          ml[1] = l[r];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- join
+// One warp per query row whose unit was shared: the row's parts lie in the
+// slots of consecutive CTAs and are added in that order.  blockIdx.y is the
+// sequence; the units' places follow from the lengths, as in the walk.
+constexpr int kJoinWarps = 8;
+
+template <typename E>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a,
+                           const __grid_constant__ AttnPlan p) {
+  __shared__ DivisionShared sh;
+  __shared__ int64_t before;
+  const PagedArgs& c = a.c;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t rows = head_rows(a);
+  const int64_t seq_rows = rows * c.heads;
+  for (int b = blockIdx.y; b < c.B; b += gridDim.y) {
+    __syncthreads();
+    int64_t mine = 0, all = 0;
+    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+      const int64_t t = seq_tiles(c, p.div, i);
+      all += t;
+      if (i < b) mine += t;
+    }
+    const int64_t x = block_scan(mine, sh);
+    if (threadIdx.x == blockDim.x - 1) before = x;
+    __syncthreads();
+    block_scan(all, sh);
+    __syncthreads();
+    if (c.count && blockIdx.x == 0 && threadIdx.x == 0 && c.lens[b] >= 0 && c.count[b] > c.T)
+      flag_page(c.status);
+    const int64_t per = run_length(p.div, sh.total * p.div.units);
+    const int64_t tiles = seq_tiles(c, p.div, b);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+    if (row < seq_rows) {
+      const int64_t in_head = row % rows;
+      const int unit = static_cast<int>(row / rows) * p.row_tiles +
+                       static_cast<int>(in_head / p.rows);
+      const int local = static_cast<int>(in_head % p.rows);
+      const int64_t u0 = before * p.div.units + unit * tiles, u1 = u0 + tiles;
+      const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u1 - 1) / per);
+      if (c1 > c0) {
+        float ms = -INFINITY;
+        for (int i = c0 + lane; i <= c1; i += 32)
+          ms = fmaxf(ms, slot_ml(a, p, 2 * i + (i == c0 ? 1 : 0))[2 * local]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
+        const float ref = ms == -INFINITY ? 0.f : ms;
+        float l = 0.f, o[kColumns];
+#pragma unroll
+        for (int z = 0; z < kColumns; ++z) o[z] = 0.f;
+        for (int i = c0; i <= c1; ++i) {
+          const int slot = 2 * i + (i == c0 ? 1 : 0);
+          const float* ml = slot_ml(a, p, slot) + 2 * local;
+          if (ml[1] == 0.f) continue;  // an empty part
+          const float w = exp2f(ml[0] - ref);
+          l = fmaf(w, ml[1], l);
+          const float* src = slot_o(a, p, slot) + static_cast<int64_t>(local) * c.d;
+#pragma unroll
+          for (int z = 0; z < kColumns; ++z)
+            if (lane + 32 * z < c.d) o[z] = fmaf(w, src[lane + 32 * z], o[z]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = static_cast<int64_t>(b) * seq_rows + row;
+        E* dst = static_cast<E*>(a.out) + at * c.d;
+#pragma unroll
+        for (int z = 0; z < kColumns; ++z)
+          if (lane + 32 * z < c.d) store_out(dst + lane + 32 * z, o[z] * inv);
+        if (lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (ms + log2f(l)) * kLn2F;
+      }
+    }
+  }
+}
+
+constexpr int kFfmaCtas = 608;
+
+AttnPlan ffma_plan(const CacheAttnArgs& a) {
+  AttnPlan p;
+  p.rows = kRows;
+  p.row_tiles = static_cast<int>((head_rows(a) + kRows - 1) / kRows);
+  p.div.units = a.c.heads * p.row_tiles;
+  p.div.tile = kTile;
+  p.div.ctas = kFfmaCtas;
+  p.div.min_run = 4;
+  return p;
+}
+
+template <typename E, typename H>
+cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
+  const AttnPlan p = ffma_plan(a);
+  const int smem = (kRows * a.c.d + kTile * (2 * a.c.d + 4)) * 4;
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_ffma_kernel<E, H>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cache_attn_ffma_kernel<E, H><<<p.div.ctas, kThreads, smem, s>>>(a, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_cache_attn_join(a, p, sizeof(E) == 2, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
+                                   cudaStream_t s) {
+  const int64_t seq_rows = head_rows(a) * a.c.heads;
+  const dim3 grid(static_cast<unsigned>((seq_rows + kJoinWarps - 1) / kJoinWarps),
+                  static_cast<unsigned>(a.c.B < 65535 ? a.c.B : 65535));
+  if (bf16)
+    cache_attn_join_kernel<__nv_bfloat16><<<grid, kJoinWarps * 32, 0, s>>>(a, p);
+  else
+    cache_attn_join_kernel<float><<<grid, kJoinWarps * 32, 0, s>>>(a, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dtype held,
+                                   cudaStream_t s) {
+  if (dense == RA_F32)
+    return held == RA_E4M3 ? launch_ffma<float, __nv_fp8_e4m3>(a, s) : launch_ffma<float, float>(a, s);
+  return held == RA_E4M3 ? launch_ffma<__nv_bfloat16, __nv_fp8_e4m3>(a, s)
+                         : launch_ffma<__nv_bfloat16, __nv_bfloat16>(a, s);
+}
+
+int64_t cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,
+                                        int32_t d) {
+  (void)B, (void)Hq, (void)heads, (void)T;
+  return static_cast<int64_t>(2) * kFfmaCtas * kRows * (d + 2) * 4;
+}
+
+}  // namespace ra

@@ -1,0 +1,50 @@
+// Shared by the attention kernels over the paged cache: the query rows of a
+// unit, the visibility of keys, and the plan that divides the work.
+#pragma once
+
+#include "ra_paged.cuh"
+
+namespace ra {
+
+constexpr float kLog2eF = 1.4426950408889634f;
+constexpr float kLn2F = 0.6931471805599453f;
+
+// One launch's plan: how many query rows a unit holds and how its key tiles
+// are divided.  Partial states are [slots][rows][2] (m in log2 units, l)
+// followed by [slots][rows][d] (o).
+struct AttnPlan {
+  Division div;
+  int rows;       // query rows per unit
+  int row_tiles;  // units per (sequence, key head)
+};
+
+// Query rows of one key head: g heads x T tokens, token fastest, which is
+// the order they have in q, out and lse.
+__host__ __device__ __forceinline__ int64_t head_rows(const CacheAttnArgs& a) {
+  return static_cast<int64_t>(a.Hq / a.c.heads) * a.c.T;
+}
+
+__device__ __forceinline__ float* slot_ml(const CacheAttnArgs& a, const AttnPlan& p, int slot) {
+  return a.ws + static_cast<int64_t>(slot) * p.rows * 2;
+}
+__device__ __forceinline__ float* slot_o(const CacheAttnArgs& a, const AttnPlan& p, int slot) {
+  return a.ws + static_cast<int64_t>(2 * p.div.ctas) * p.rows * 2 +
+         static_cast<int64_t>(slot) * p.rows * a.c.d;
+}
+
+// Whether query t sees the key at position pos of its sequence.
+__device__ __forceinline__ bool sees(const CacheAttnArgs& a, const SeqInfo& s, int b, int t,
+                                     int64_t pos) {
+  if (t >= s.cnt) return false;
+  if (pos < s.len) return true;
+  const int64_t j = pos - s.len;
+  if (j >= s.cnt) return false;
+  if (!a.mask) return j <= t;
+  return a.mask[b * a.mask_stride + static_cast<int64_t>(t) * a.c.T + j] != 0;
+}
+
+// Joins the parts of the units that several CTAs shared.
+cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
+                                   cudaStream_t s);
+
+}  // namespace ra

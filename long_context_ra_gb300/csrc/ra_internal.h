@@ -125,8 +125,17 @@ cudaError_t launch_state_init(float* m, float* l, float* o, int64_t rows, int32_
 // 16-byte entry per ring step of a work unit in shared memory.
 constexpr int kMaxCausalSteps = 1024;
 
-// Watchdog codes written to FoldArgs::status.
+// Codes written to the device status word (FoldArgs::status).
 constexpr int kStatusTimeout = 1;
+constexpr int kStatusPage = 2;  // a position or page outside the cache
+
+// The current device's status word: RA_OK on a usable device, else the
+// status a call has to return.
+ra_status device_ready(int** status);
+
+// Settings of ra_watchdog_config for the next launch.
+int64_t wait_limit();
+int64_t stall_cta();
 
 // Number of SMs of the current device (cached).
 int device_sm_count();

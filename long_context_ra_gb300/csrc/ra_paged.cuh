@@ -1,0 +1,236 @@
+// Device helpers of the paged cache: a position's row, the 8-bit format, and
+// the division of a ragged batch's key tiles among the CTAs.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+#include "ra_internal.h"
+#include "ra_serve.h"
+
+namespace ra {
+
+__device__ __forceinline__ void flag_page(int* status) { atomicCAS(status, 0, kStatusPage); }
+
+// Row of head 0 of position `pos` of sequence b in the cache (add
+// h << page_shift for head h), or -1, with the status word set, for a
+// position or page outside the cache.
+__device__ __forceinline__ int64_t cache_row(const PagedArgs& c, int b, int64_t pos) {
+  const int64_t col = pos >> c.page_shift;
+  if (col < c.width) {
+    const int64_t page = c.table[static_cast<int64_t>(b) * c.width + col];
+    if (page >= 0 && page < c.pages)
+      return ((page * c.heads) << c.page_shift) + (pos & ((int64_t{1} << c.page_shift) - 1));
+  }
+  flag_page(c.status);
+  return -1;
+}
+
+// Context and new tokens of sequence b; a sequence with lens < 0 has none.
+struct SeqInfo {
+  int64_t len;
+  int cnt;
+  __device__ int64_t keys() const { return len + cnt; }
+};
+
+__device__ __forceinline__ SeqInfo sequence(const PagedArgs& c, int b) {
+  SeqInfo s;
+  const int32_t len = c.lens[b];
+  const int32_t cnt = c.count ? c.count[b] : c.T;
+  s.len = len < 0 ? 0 : len;
+  s.cnt = len < 0 ? 0 : max(0, min(cnt, c.T));
+  return s;
+}
+
+// 2^(e - 127) of an exponent byte.
+__device__ __forceinline__ float exp_scale(uint32_t e) {
+  return __uint_as_float(e ? e << 23 : 0x00400000u);
+}
+
+// Exponent byte of a row with largest magnitude amax: the smallest e >= -126
+// with amax <= 448 * 2^e (448 = 1.75 * 2^8, the largest e4m3 value).
+__device__ __forceinline__ uint32_t row_exponent(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(max(e, 1));
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(const float* x) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Two e4m3 bytes as two f16 (exact: every e4m3 value is an f16).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = e4m3x2_to_f16x2(w >> (16 * i));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// 8 consecutive elements as floats, and back.
+__device__ __forceinline__ void load8(const float* p, float* x) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_fp8_e4m3* p, float* x) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  unpack_e4m3x4(a.x, x);
+  unpack_e4m3x4(a.y, x + 4);
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------ work division
+//
+// A unit is one tile of query rows of one key head of one sequence; it walks
+// the sequence's key tiles.  The tiles of all units, in the order (sequence,
+// unit, tile), are cut into equal runs, one per CTA, so that a batch of
+// unlike lengths keeps every CTA busy for the same time.  A CTA meets at
+// most one unit that began before its run (its state goes to slot 2c) and
+// one that goes on behind it (slot 2c + 1); the units between are whole.
+struct Division {
+  int units;     // per sequence: key heads x row tiles
+  int tile;      // keys per tile
+  int ctas;
+  int min_run;   // tiles a CTA takes at least
+};
+
+__device__ __forceinline__ int64_t seq_tiles(const PagedArgs& c, const Division& v, int b) {
+  const int64_t n = sequence(c, b).keys();
+  return n <= v.tile ? 1 : (n + v.tile - 1) / v.tile;  // an empty sequence has one empty tile
+}
+
+__device__ __forceinline__ int64_t run_length(const Division& v, int64_t total) {
+  const int64_t per = (total + v.ctas - 1) / v.ctas;
+  return per < v.min_run ? v.min_run : per;
+}
+
+// Shared scratch of the block-wide sums below.
+struct DivisionShared {
+  int64_t warp[32];
+  int64_t total;  // tiles of all sequences (one unit each)
+  int64_t off;    // of the CTA's first tile within its sequence's tiles
+  int b;          // sequence of the CTA's first tile
+};
+
+// Inclusive scan of one value per thread; sh.total = the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t x, DivisionShared& sh) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = (blockDim.x + 31) / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh.warp[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+  for (int i = 0; i < warps; ++i) {
+    if (i < warp) before += sh.warp[i];
+    all += sh.warp[i];
+  }
+  if (threadIdx.x == 0) sh.total = all;
+  return x + before;
+}
+
+// The first (sequence, offset) of CTA `cta`'s run, and its end: fills sh and
+// returns the tiles of the run (0: nothing to do).  All threads take part.
+__device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Division& v, int cta,
+                                                  DivisionShared& sh) {
+  const int per_thread = (c.B + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(c.B, static_cast<int>(threadIdx.x) * per_thread);
+  const int b1 = min(c.B, b0 + per_thread);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_tiles(c, v, b);
+  int64_t at = block_scan(mine, sh) - mine;
+  __syncthreads();
+  const int64_t all = sh.total * v.units;
+  const int64_t run = run_length(v, all);
+  const int64_t begin = cta * run;
+  if (begin < all && begin >= at * v.units && begin < (at + mine) * v.units) {
+    for (int b = b0; b < b1; ++b) {
+      const int64_t t = seq_tiles(c, v, b);
+      if (begin < (at + t) * v.units) {
+        sh.b = b;
+        sh.off = begin - at * v.units;
+        break;
+      }
+      at += t;
+    }
+  }
+  __syncthreads();
+  if (begin >= all) return 0;
+  return min(run, all - begin);
+}
+
+// Walks a CTA's run unit by unit.
+struct UnitWalk {
+  int64_t left, off;  // tiles left in the run; offset within sequence b's tiles
+  int b;
+  // the present unit
+  SeqInfo seq;
+  int64_t tiles, first, last;  // of the unit; this CTA's part [first, last)
+  int unit;
+
+  __device__ void start(const PagedArgs& c, const Division& v, const DivisionShared& sh,
+                        int64_t n) {
+    left = n;
+    b = sh.b;
+    off = sh.off;
+    if (left > 0) load(c, v);
+  }
+  __device__ bool done() const { return left <= 0; }
+  __device__ void load(const PagedArgs& c, const Division& v) {
+    seq = sequence(c, b);
+    tiles = seq_tiles(c, v, b);
+    unit = static_cast<int>(off / tiles);
+    first = off - unit * tiles;
+    last = min(tiles, first + left);
+  }
+  __device__ void next(const PagedArgs& c, const Division& v) {
+    left -= last - first;
+    off += last - first;
+    if (off == tiles * v.units) {
+      ++b;
+      off = 0;
+    }
+    if (left > 0) load(c, v);
+  }
+  __device__ bool whole() const { return first == 0 && last == tiles; }
+  // Slot of a part that is not the whole unit.
+  __device__ int slot(int cta) const { return 2 * cta + (first == 0 ? 1 : 0); }
+};
+
+}  // namespace ra
