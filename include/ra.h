@@ -471,7 +471,7 @@ RA_API int64_t ra_qk_norm_rope_backward_workspace_bytes(int32_t d);
  *   dtype         RA_F32 or RA_BF16 (the inputs' own type), or RA_E4M3 with
  *                 inputs of either type.
  *   page          a power of two, 8 .. 1024.   d: a multiple of 8, <= 256.
- * k, v are 16-byte aligned.
+ * k, v are 16-byte aligned, k_exp and v_exp 8-byte.
  *
  * The cache calls share these arguments:
  *   table  int32 [B, width] page numbers; entries behind a sequence's last

@@ -18,6 +18,7 @@ constexpr int kRows = 16;
 constexpr int kTile = 32;
 constexpr int kThreads = 128;
 constexpr int kColumns = RA_MAX_HEAD_DIM / 32;  // per lane
+constexpr int kMaxSmem = (kRows * RA_MAX_HEAD_DIM + kTile * (2 * RA_MAX_HEAD_DIM + 4)) * 4;
 
 template <typename E>
 __device__ __forceinline__ float to_float(E x) {
@@ -247,8 +248,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
-constexpr int kFfmaCtas = 608;
-
 AttnPlan ffma_plan(const CacheAttnArgs& a) {
   AttnPlan p;
   p.rows = kRows;
@@ -264,9 +263,16 @@ template <typename E, typename H>
 cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
   const AttnPlan p = ffma_plan(a);
   const int smem = (kRows * a.c.d + kTile * (2 * a.c.d + 4)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_ffma_kernel<E, H>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(cache_attn_ffma_kernel<E, H>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
   cache_attn_ffma_kernel<E, H><<<p.div.ctas, kThreads, smem, s>>>(a, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -291,8 +297,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dt
                                    cudaStream_t s) {
   if (dense == RA_F32)
     return held == RA_E4M3 ? launch_ffma<float, __nv_fp8_e4m3>(a, s) : launch_ffma<float, float>(a, s);
-  return held == RA_E4M3 ? launch_ffma<__nv_bfloat16, __nv_fp8_e4m3>(a, s)
-                         : launch_ffma<__nv_bfloat16, __nv_bfloat16>(a, s);
+  return launch_cache_decode(a, held == RA_E4M3, s);
 }
 
 int64_t cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,

@@ -43,6 +43,13 @@ __device__ __forceinline__ bool sees(const CacheAttnArgs& a, const SeqInfo& s, i
   return a.mask[b * a.mask_stride + static_cast<int64_t>(t) * a.c.T + j] != 0;
 }
 
+// CTAs of the kernels, which fix the size of the workspace.
+constexpr int kFfmaCtas = 608;
+constexpr int kDecodeCtas = 304;  // two per SM
+constexpr int kDecodeRows = 16;
+
+cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s);
+
 // Joins the parts of the units that several CTAs shared.
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
                                    cudaStream_t s);

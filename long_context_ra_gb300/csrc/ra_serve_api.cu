@@ -104,7 +104,8 @@ ra_status check_cache(const ra_cache* cache, const int32_t* table, int32_t width
   if (cache->dtype == RA_E4M3 && cache->pages > 0 && (!cache->k_exp || !cache->v_exp))
     return RA_ERR_INVALID_ARG;
   if (B > 0 && (!lens || (width > 0 && !table))) return RA_ERR_INVALID_ARG;
-  if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(table, 4) || !aligned(lens, 4))
+  if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->k_exp, 8) ||
+      !aligned(cache->v_exp, 8) || !aligned(table, 4) || !aligned(lens, 4))
     return RA_ERR_MISALIGNED;
   *p = PagedArgs{};
   p->k = cache->k;
