@@ -297,13 +297,20 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dt
                                    cudaStream_t s) {
   if (dense == RA_F32)
     return held == RA_E4M3 ? launch_ffma<float, __nv_fp8_e4m3>(a, s) : launch_ffma<float, float>(a, s);
+  if (head_rows(a) > kDecodeRows) return launch_cache_tree(a, held == RA_E4M3, s);
   return launch_cache_decode(a, held == RA_E4M3, s);
 }
 
 int64_t cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,
                                         int32_t d) {
-  (void)B, (void)Hq, (void)heads, (void)T;
-  return static_cast<int64_t>(2) * kFfmaCtas * kRows * (d + 2) * 4;
+  // The largest of the kernels that may serve these sizes (the types are not
+  // known here): parts of 2 slots per CTA.
+  (void)B;
+  const int64_t rows = static_cast<int64_t>(Hq / heads) * T;
+  int64_t most = kFfmaCtas * kRows;
+  if (rows > kDecodeRows) most = kTreeCtas * (rows > 128 ? 256 : 128);
+  if (most < kFfmaCtas * kRows) most = kFfmaCtas * kRows;
+  return 2 * most * (d + 2) * 4;
 }
 
 }  // namespace ra

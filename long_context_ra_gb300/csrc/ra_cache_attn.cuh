@@ -47,8 +47,10 @@ __device__ __forceinline__ bool sees(const CacheAttnArgs& a, const SeqInfo& s, i
 constexpr int kFfmaCtas = 608;
 constexpr int kDecodeCtas = 304;  // two per SM
 constexpr int kDecodeRows = 16;
+constexpr int kTreeCtas = 152;  // one per SM
 
 cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s);
+cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s);
 
 // Joins the parts of the units that several CTAs shared.
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
