@@ -11,6 +11,7 @@
 
 #include "ra.h"
 #include "ra_internal.h"
+#include "ra_serve.h"
 #include "ra_trace.h"
 
 namespace ra {
@@ -191,6 +192,23 @@ ra_status current_ordinal(int* dev) {
   if (e != cudaSuccess) return RA_ERR_CUDA;
   if (*dev < 0 || *dev >= kMaxDevices) return RA_ERR_UNSUPPORTED;
   return RA_OK;
+}
+
+bool encode_pages(CUtensorMap* map, const void* ptr, const PagedArgs& c, int box_rows, bool bytes) {
+  if (get_encoder() != RA_OK) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.d) * (bytes ? 1 : 2);
+  const cuuint64_t page = cuuint64_t{1} << c.page_shift;
+  const cuuint64_t all = static_cast<cuuint64_t>(c.pages > 0 ? c.pages : 1) * c.heads;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), page, c.pages > 0 ? all : 1};
+  const cuuint64_t strides[2] = {row, row * page};
+  const cuuint32_t box[3] = {bytes ? static_cast<cuuint32_t>(c.d) : 64u,
+                             static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 ra_status device_ready(int** status) {

@@ -27,6 +27,13 @@ __device__ __forceinline__ float to_float(E x) {
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                            *reinterpret_cast<const uint32_t*>(&hi));
+}
+
 template <typename E, typename H>
 __global__ void __launch_bounds__(kThreads)
     cache_attn_ffma_kernel(const __grid_constant__ CacheAttnArgs a,
@@ -175,19 +182,25 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------- join
-// One warp per query row whose unit was shared: the row's parts lie in the
-// slots of consecutive CTAs and are added in that order.  blockIdx.y is the
-// sequence; the units' places follow from the lengths, as in the walk.
+// A query row whose unit was shared is joined by `kSplit` warps: its parts lie
+// in the slots of consecutive CTAs, a warp takes every kSplit-th, four at a
+// time (the loads of four parts are in flight together), and the warps' sums
+// are added in order.  blockIdx.y is the sequence; the units' places follow
+// from the lengths, as in the walk.  Every slot of a shared unit has been
+// written, an empty part with l = 0 and o = 0.
 constexpr int kJoinWarps = 8;
 
-template <typename E>
+template <typename E, int kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a,
                            const __grid_constant__ AttnPlan p) {
   __shared__ DivisionShared sh;
   __shared__ int64_t before;
+  __shared__ float4 sums[kJoinWarps][2][32];
+  __shared__ float sum_l[kJoinWarps];
   const PagedArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int sub = warp % kSplit;
   const int64_t rows = head_rows(a);
   const int64_t seq_rows = rows * c.heads;
   for (int b = blockIdx.y; b < c.B; b += gridDim.y) {
@@ -207,43 +220,86 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       flag_page(c.status);
     const int64_t per = run_length(p.div, sh.total * p.div.units);
     const int64_t tiles = seq_tiles(c, p.div, b);
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinWarps / kSplit) + warp / kSplit;
+    int c0 = 0, c1 = 0, local = 0;
     if (row < seq_rows) {
       const int64_t in_head = row % rows;
       const int unit = static_cast<int>(row / rows) * p.row_tiles +
                        static_cast<int>(in_head / p.rows);
-      const int local = static_cast<int>(in_head % p.rows);
-      const int64_t u0 = before * p.div.units + unit * tiles, u1 = u0 + tiles;
-      const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u1 - 1) / per);
-      if (c1 > c0) {
-        float ms = -INFINITY;
-        for (int i = c0 + lane; i <= c1; i += 32)
-          ms = fmaxf(ms, slot_ml(a, p, 2 * i + (i == c0 ? 1 : 0))[2 * local]);
+      local = static_cast<int>(in_head % p.rows);
+      const int64_t u0 = before * p.div.units + unit * tiles;
+      c0 = static_cast<int>(u0 / per);
+      c1 = static_cast<int>((u0 + tiles - 1) / per);
+    }
+    const bool shared = c1 > c0;
+    float ms = -INFINITY, l = 0.f;
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (shared) {
+      for (int i = c0 + lane; i <= c1; i += 32)
+        ms = fmaxf(ms, slot_ml(a, p, 2 * i + (i == c0 ? 1 : 0))[2 * local]);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
-        const float ref = ms == -INFINITY ? 0.f : ms;
-        float l = 0.f, o[kColumns];
+      for (int off = 16; off > 0; off >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
+      const float ref = ms == -INFINITY ? 0.f : ms;
+      for (int i = c0 + sub; i <= c1; i += 4 * kSplit) {
+        float2 ml[4];
+        float4 y[4][2];
 #pragma unroll
-        for (int z = 0; z < kColumns; ++z) o[z] = 0.f;
-        for (int i = c0; i <= c1; ++i) {
-          const int slot = 2 * i + (i == c0 ? 1 : 0);
-          const float* ml = slot_ml(a, p, slot) + 2 * local;
-          if (ml[1] == 0.f) continue;  // an empty part
-          const float w = exp2f(ml[0] - ref);
-          l = fmaf(w, ml[1], l);
-          const float* src = slot_o(a, p, slot) + static_cast<int64_t>(local) * c.d;
+        for (int z = 0; z < 4; ++z) {
+          const int at = i + z * kSplit;
+          const bool real = at <= c1;
+          const int slot = real ? 2 * at + (at == c0 ? 1 : 0) : 0;
+          ml[z] = real ? *reinterpret_cast<const float2*>(slot_ml(a, p, slot) + 2 * local)
+                       : make_float2(-INFINITY, 0.f);
+          const float4* src =
+              reinterpret_cast<const float4*>(slot_o(a, p, slot) + static_cast<int64_t>(local) * c.d);
 #pragma unroll
-          for (int z = 0; z < kColumns; ++z)
-            if (lane + 32 * z < c.d) o[z] = fmaf(w, src[lane + 32 * z], o[z]);
+          for (int h = 0; h < 2; ++h)
+            y[z][h] = real && 4 * (lane + 32 * h) < c.d ? src[lane + 32 * h]
+                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t at = static_cast<int64_t>(b) * seq_rows + row;
-        E* dst = static_cast<E*>(a.out) + at * c.d;
 #pragma unroll
-        for (int z = 0; z < kColumns; ++z)
-          if (lane + 32 * z < c.d) store_out(dst + lane + 32 * z, o[z] * inv);
-        if (lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (ms + log2f(l)) * kLn2F;
+        for (int z = 0; z < 4; ++z) {
+          const float w = ml[z].y == 0.f ? 0.f : exp2f(ml[z].x - ref);
+          l = fmaf(w, ml[z].y, l);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            o[h].x = fmaf(w, y[z][h].x, o[h].x);
+            o[h].y = fmaf(w, y[z][h].y, o[h].y);
+            o[h].z = fmaf(w, y[z][h].z, o[h].z);
+            o[h].w = fmaf(w, y[z][h].w, o[h].w);
+          }
+        }
       }
+    }
+    if (kSplit > 1) {
+      sums[warp][0][lane] = o[0];
+      sums[warp][1][lane] = o[1];
+      if (lane == 0) sum_l[warp] = l;
+      __syncthreads();
+      if (sub == 0) {
+        for (int z = 1; z < kSplit; ++z) {
+          l += sum_l[warp + z];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 y = sums[warp + z][h][lane];
+            o[h].x += y.x;
+            o[h].y += y.y;
+            o[h].z += y.z;
+            o[h].w += y.w;
+          }
+        }
+      }
+    }
+    if (shared && sub == 0) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t at = static_cast<int64_t>(b) * seq_rows + row;
+      E* dst = static_cast<E*>(a.out) + at * c.d;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = 4 * (lane + 32 * h);
+        if (col < c.d) store4(dst + col, make_float4(o[h].x * inv, o[h].y * inv, o[h].z * inv, o[h].w * inv));
+      }
+      if (lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (ms + log2f(l)) * kLn2F;
     }
   }
 }
@@ -257,6 +313,16 @@ AttnPlan ffma_plan(const CacheAttnArgs& a) {
   p.div.ctas = kFfmaCtas;
   p.div.min_run = 4;
   return p;
+}
+
+template <typename E, int kSplit>
+cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+  const int64_t seq_rows = head_rows(a) * a.c.heads;
+  constexpr int kRowsPerBlock = kJoinWarps / kSplit;
+  const dim3 grid(static_cast<unsigned>((seq_rows + kRowsPerBlock - 1) / kRowsPerBlock),
+                  static_cast<unsigned>(a.c.B < 65535 ? a.c.B : 65535));
+  cache_attn_join_kernel<E, kSplit><<<grid, kJoinWarps * 32, 0, s>>>(a, p);
+  return cudaGetLastError();
 }
 
 template <typename E, typename H>
@@ -283,14 +349,11 @@ cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
                                    cudaStream_t s) {
-  const int64_t seq_rows = head_rows(a) * a.c.heads;
-  const dim3 grid(static_cast<unsigned>((seq_rows + kJoinWarps - 1) / kJoinWarps),
-                  static_cast<unsigned>(a.c.B < 65535 ? a.c.B : 65535));
-  if (bf16)
-    cache_attn_join_kernel<__nv_bfloat16><<<grid, kJoinWarps * 32, 0, s>>>(a, p);
-  else
-    cache_attn_join_kernel<float><<<grid, kJoinWarps * 32, 0, s>>>(a, p);
-  return cudaGetLastError();
+  // A unit is shared by about ctas / units CTAs; with many parts per row, and
+  // so few rows, the warps of a block share a row.
+  const int64_t units = static_cast<int64_t>(a.c.B) * p.div.units;
+  if (p.div.ctas > 8 * units) return bf16 ? join_t<__nv_bfloat16, 8>(a, p, s) : join_t<float, 8>(a, p, s);
+  return bf16 ? join_t<__nv_bfloat16, 1>(a, p, s) : join_t<float, 1>(a, p, s);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dtype held,

@@ -10,25 +10,33 @@
 //   O += P V         tcgen05.mma
 //
 // Two streams keep the tensor cores and the exponentials busy together.
-// With two query tiles (kTwo) a stream is a query tile and both share the key
-// tile; with one, a stream is every other key tile, with a state of its own,
-// and the two states are joined at the end of the unit.
+// With two query tiles (kTwo) a stream is a query tile and both share a key
+// tile of 128; with one, a stream is every other key tile of 64 (four tiles
+// are held while two streams are at work, and the smaller ones leave room for
+// those on their way), with a state of its own, and the two states are joined
+// at the end of the unit.
 //
-// Warp roles (512 threads, 128 registers each at launch):
-//   warps 0-3, 4-7   softmax of stream 0, 1              (160 registers)
-//   warp  8          TMEM allocator, MMA issuer; 9-11 idle (64)
-//   warps 12-15      producers                            (128)
-// 2 x 128 x 160 + 128 x 64 + 128 x 128 = 65536.
+// Warp roles (512 threads of 128 registers):
+//   warps 0-3, 4-7   softmax of stream 0, 1
+//   warp  8          TMEM allocator, MMA issuer
+//   warp  9          loader: TMA boxes of the key and value tiles
+//   warps 10-15      8-bit cache: conversion, a pair of warps per tile, three
+//                    tiles under way; queries
+//   (bf16 cache)     warps 13-15: queries; warp 12: tiles that end a sequence
 //
-// A page may be as short as 8 rows, end inside a tile, or be missing, so the
-// producers place the rows themselves: 8 threads own 8 neighbouring rows (one
-// page) and write 16-byte pieces where the 128-byte swizzle puts them, zeros
-// for rows that do not exist.  bf16 rows go straight to the operand stages
-// with cp.async.  8-bit rows go through a raw ring (each thread converts the
-// pieces that it loaded itself, so nothing is waited for between threads) and
-// become bf16 with the row's scale inside: code * 2^e has 4 significant bits,
-// so it is exact in bf16 for values above 2^-126, and neither the scores nor
-// the probabilities need to know the scale.
+// A tile is a row of pages: the loader's lanes look up a page each, one tile
+// ahead, and bring it as one TMA box of a [pages x heads, page, d] view; a
+// page that does not exist is a box behind the view, which TMA fills with
+// zeros.  bf16 tiles land as operands.  Only value tiles that hold drafts or
+// the end of the sequence pass through warp 12, which clears the rows behind
+// the end.  8-bit tiles land in a raw ring and become bf16 in warps 12-15,
+// with the row's scale inside: code * 2^e has 4 significant bits, so it is
+// exact in bf16 for values above 2^-126, and neither the scores nor the
+// probabilities need to know the scale.
+//
+// Every role is a short loop in 32-bit arithmetic with the unit's constants
+// taken out: a tile of 128 keys is 1.1 us of tensor time, and a role of one
+// warp that spends 200 instructions on an item is slower than that.
 //
 // Unseen drafts: their scores are -inf, so p = 0; value rows of tiles with
 // drafts are looked through for elements that are not finite.  Those become 0
@@ -48,57 +56,65 @@ using namespace ptx;
 using namespace sm103;
 
 constexpr int kThreads = 512;
-constexpr uint32_t kRegsSoftmax = 160, kRegsMma = 64, kRegsLoad = 128;
-static_assert(kRegsLoad == 128 && 256 * kRegsSoftmax + 128 * kRegsMma + 128 * kRegsLoad == kThreads * 128,
-              "register split must equal the launch's register total");
 constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp = 12;
+constexpr int kLoadWarp = 9;
+constexpr int kHandWarp = 10;  // 8-bit cache
+constexpr int kFixWarp = 12;   // bf16 cache
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr float kFastSumBound = 256.0f;  // 2^kRescaleLog2: see the forward kernel
 
 template <bool k8, int D, bool kTwo>
 struct Layout {
-  static constexpr int kBox = 128 * 128;  // 128 rows x 128 bytes (64 bf16)
-  static constexpr int kTile = 128 * D * 2;
-  static constexpr int kRawTile = k8 ? 128 * D : 0;
-  static constexpr int kStages = D == 128 ? (k8 ? 3 : 5) : (k8 ? 5 : 8);
-  static constexpr int kRawStages = 4;
-  static constexpr int kLag = k8 ? kRawStages - 1 : 2;  // items in flight
+  static constexpr int kKeys = kTwo ? 128 : 64;  // per tile
+  static constexpr int kQBox = 128 * 128;        // 128 rows x 128 bytes (64 bf16)
+  static constexpr int kBox = kKeys * 128;
+  static constexpr int kQTile = 128 * D * 2;
+  static constexpr int kTile = kKeys * D * 2;
+  static constexpr int kRawTile = kKeys * D;
+  static constexpr int kStages = kTwo ? (D == 128 ? (k8 ? 3 : 5) : (k8 ? 5 : 8))
+                                      : (D == 128 ? (k8 ? 6 : 10) : (k8 ? 8 : 16));
+  static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 8 : 12);
+  static constexpr int kLoadStages = k8 ? kRawStages : kStages;  // of the ring the loader fills
   // the second query tile, or the exchange of the two streams' states:
   // [128][33] floats and [128][2]
-  static constexpr int kSecond = kTwo ? kTile : 18 * 1024;
+  static constexpr int kSecond = kTwo ? kQTile : 18 * 1024;
   static constexpr int kQ0 = 0;
-  static constexpr int kQ1 = kTile;
-  static constexpr int kKV = kTile + kSecond;
+  static constexpr int kQ1 = kQTile;
+  static constexpr int kKV = kQTile + kSecond;
   static constexpr int kRaw = kKV + kStages * kTile;
-  static constexpr int kRawExp = kRaw + (k8 ? kRawStages * kRawTile : 0);
-  static constexpr int kBar = kRawExp + (k8 ? kRawStages * 128 : 0);
-  static constexpr int kNumBars = 2 + 2 * kStages + 9;
+  static constexpr int kRawExp = kRaw + kRawStages * kRawTile;
+  static constexpr int kBar = kRawExp + kRawStages * kKeys;
+  static constexpr int kNumBars = 2 + 2 * kStages + 9 + kLoadStages + kRawStages;
   static constexpr int kMisc = (kBar + kNumBars * 8 + 15) / 16 * 16;  // TMEM base, abort flag
-  static constexpr int kPoison = kMisc + 16;                          // [8]
-  static constexpr int kLeftOut = kPoison + 32;                       // [8][16] bytes
+  // Rings of the last 32 units and key tiles: the loader is at most
+  // kLoadStages + kStages <= 24 items (12 key tiles, 12 units) ahead.
+  static constexpr int kPoison = kMisc + 16;        // [32]
+  static constexpr int kLeftOut = kPoison + 128;    // [32]
   static constexpr int kDivision = kLeftOut + 128;
   // walks of the 8 softmax warps: in shared memory, not in registers
   static constexpr int kWalks = (kDivision + static_cast<int>(sizeof(DivisionShared)) + 15) / 16 * 16;
   static constexpr int kBytes = kWalks + 8 * static_cast<int>(sizeof(UnitWalk));
   static constexpr int kSmem = kBytes + 1024;  // slack for 1024-byte alignment
   static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kRawStages + kStages <= 24, "rings");
 };
 
-template <int kStages>
+template <typename L>
 struct Bars {
+  static constexpr int kS = L::kStages;
   uint32_t base;
   __device__ uint32_t q_full() const { return base; }
   __device__ uint32_t q_empty() const { return base + 8; }
   __device__ uint32_t kv_full(int s) const { return base + 8 * (2 + s); }
-  __device__ uint32_t kv_empty(int s) const { return base + 8 * (2 + kStages + s); }
-  __device__ uint32_t s_full(int t) const { return base + 8 * (2 + 2 * kStages + t); }
-  __device__ uint32_t p_full(int t) const { return base + 8 * (4 + 2 * kStages + t); }
-  __device__ uint32_t o_full(int t) const { return base + 8 * (6 + 2 * kStages + t); }
-  __device__ uint32_t x_full() const { return base + 8 * (8 + 2 * kStages); }
-  __device__ uint32_t x_empty() const { return base + 8 * (9 + 2 * kStages); }
-  __device__ uint32_t drain() const { return base + 8 * (10 + 2 * kStages); }
+  __device__ uint32_t kv_empty(int s) const { return base + 8 * (2 + kS + s); }
+  __device__ uint32_t s_full(int t) const { return base + 8 * (2 + 2 * kS + t); }
+  __device__ uint32_t p_full(int t) const { return base + 8 * (4 + 2 * kS + t); }
+  __device__ uint32_t o_full(int t) const { return base + 8 * (6 + 2 * kS + t); }
+  __device__ uint32_t x_full() const { return base + 8 * (8 + 2 * kS); }
+  __device__ uint32_t x_empty() const { return base + 8 * (9 + 2 * kS); }
+  __device__ uint32_t drain() const { return base + 8 * (10 + 2 * kS); }
+  __device__ uint32_t raw_full(int s) const { return base + 8 * (11 + 2 * kS + s); }
+  __device__ uint32_t raw_empty(int s) const { return base + 8 * (11 + 2 * kS + L::kLoadStages + s); }
 };
 
 // Position in a ring of stages.
@@ -114,41 +130,41 @@ struct Ring {
   }
 };
 
-// Item x of a unit of n key tiles, in the order in which the MMA thread
-// takes them: which tile, K or V.  Two query tiles: K0 V0 K1 V1 ...; one:
-// K0 K1 V0 K2 V1 ... (two key tiles under way).
+// The MMA thread takes a unit's tiles in the order K0 V0 K1 V1 ... (two query
+// tiles) or K0 K1 V0 K2 V1 ... (one: two key tiles under way).  Place of V
+// tile `tile` of n in that order:
 template <bool kTwo>
-__device__ __forceinline__ void item(int64_t x, int64_t n, int64_t& tile, bool& v) {
-  if (kTwo) {
-    tile = x >> 1;
-    v = x & 1;
-  } else if (x == 0) {
-    tile = 0;
-    v = false;
-  } else if (x == 2 * n - 1) {
-    tile = n - 1;
-    v = true;
-  } else {
-    v = !(x & 1);
-    tile = v ? x / 2 - 1 : (x + 1) / 2;
+__device__ __forceinline__ int value_item(int tile, int n) {
+  return kTwo ? 2 * tile + 1 : tile + 1 == n ? 2 * n - 1 : 2 * tile + 2;
+}
+// f(tile, v) for the items of a unit of n tiles, in order, until f is false.
+template <bool kTwo, typename F>
+__device__ __forceinline__ bool each_item(int n, F f) {
+  if (!kTwo && !f(0, false)) return false;
+  for (int j = 0; j < n; ++j) {
+    const int k = kTwo ? j : j + 1;
+    if (k < n && !f(k, false)) return false;
+    if (!f(j, true)) return false;
   }
+  return true;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
+// Row (of a group's kRows) of a thread's x-th 16-byte piece of an 8-bit tile;
+// 8 threads share a group.  Lanes 4-7 take the rows in another order, so that
+// the 16-byte writes of a group's widened pieces meet no bank twice.
+template <int D, int kRows>
+__device__ __forceinline__ int piece_row(int x, int pc) {
+  return D == 128 ? x ^ (pc / 4) : (pc / 4) * (kRows / 2) + (x ^ (pc / 4));
+}
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 8 : 0)
                : "memory");
 }
-template <int bytes>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? bytes : 0), "n"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+// One arrival on `bar` when this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 x;
@@ -168,86 +184,129 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
          ((x & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
 
-// Two e4m3 values in the high bytes of the halves of x (low bytes zero) times
-// the powers of two in `up` and `up2`: sign and 7 bits moved to where bf16
-// has them mean value * 2^-120, so up = 2^(120 + e).  A NaN code would come
-// out as 480 and is put back.
-__device__ __forceinline__ uint32_t widen(uint32_t x, uint32_t up, uint32_t up2, bool twice) {
-  uint32_t m = mul_bf16x2((x >> 4) & 0x07f007f0u, up);
-  if (twice) m = mul_bf16x2(m, up2);
-  m |= ((x & 0x7f00u) == 0x7f00u ? 0x7fffu : 0u) |
-       ((x & 0x7f000000u) == 0x7f000000u ? 0x7fff0000u : 0u);
-  return m | (x & 0x80008000u);
-}
-
-template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
-  constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, false);
+// 16 e4m3 codes times 2^(e - 127) as bf16, in the order 0 2 1 3 of every four
+// (the bytes stay in their halves; queries and results follow that order).
+// Sign and 7 bits moved to where bf16 has them mean value * 2^-120, so the
+// factor is 2^(e - 7).  That factor passes bf16's range above e = 134, and a
+// NaN code would come out as 480: both are rare and go through widen_rare.
+__device__ __noinline__ uint4 widen_rare(uint2 w, uint32_t e) {
+  const uint32_t f1 = min(e + 120u, 254u);
+  const uint32_t up = (f1 << 7) * 0x10001u, up2 = ((e + 247u - f1) << 7) * 0x10001u;
+  uint32_t o[4];
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint64_t off = desc_step((kk / 4) * (kBM * 128) + (kk % 4) * 32);
-    mma_bf16_ss(d_tmem, dq + off, dk + off, idesc, kk > 0 ? 1u : 0u);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = (i & 1) ? (i < 2 ? w.x : w.y) : (i < 2 ? w.x : w.y) << 8;  // in the high bytes
+    uint32_t m = mul_bf16x2(mul_bf16x2((x >> 4) & 0x07f007f0u, up), up2);
+    m |= ((x & 0x7f00u) == 0x7f00u ? 0x7fffu : 0u) |
+         ((x & 0x7f000000u) == 0x7f000000u ? 0x7fff0000u : 0u);
+    o[i] = m | (x & 0x80008000u);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void widen16(const uint4& w4, uint32_t e, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+  uint32_t nan = 0;
+#pragma unroll
+  for (int z = 0; z < 4; ++z) nan |= (w[z] & 0x7f7f7f7fu) + 0x01010101u;
+  if ((nan & 0x80808080u) == 0u && e <= 134u) {
+    const uint32_t up = e * 0x00800080u + 120u * 0x00800080u;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      o[2 * z] = mul_bf16x2((w[z] << 4) & 0x07f007f0u, up) | ((w[z] << 8) & 0x80008000u);
+      o[2 * z + 1] = mul_bf16x2((w[z] >> 4) & 0x07f007f0u, up) | (w[z] & 0x80008000u);
+    }
+  } else {
+    const uint4 lo = widen_rare(make_uint2(w[0], w[1]), e), hi = widen_rare(make_uint2(w[2], w[3]), e);
+    o[0] = lo.x, o[1] = lo.y, o[2] = lo.z, o[3] = lo.w;
+    o[4] = hi.x, o[5] = hi.y, o[6] = hi.z, o[7] = hi.w;
   }
 }
 
-template <int D>
+template <int D, int kKeys>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kBM, kKeys, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    mma_bf16_ss(d_tmem, dq + desc_step((kk / 4) * (kBM * 128) + (kk % 4) * 32),
+                dk + desc_step((kk / 4) * (kKeys * 128) + (kk % 4) * 32), idesc, kk > 0 ? 1u : 0u);
+}
+
+template <int D, int kKeys>
 __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t dv,
                                          uint32_t accumulate) {
   constexpr uint32_t idesc = idesc_bf16_f32(kBM, D, true);
   mma_bf16_ts(d_tmem, p_tmem, dv, idesc, accumulate);
 #pragma unroll
-  for (int kk = 1; kk < kBN / 16; ++kk)
+  for (int kk = 1; kk < kKeys / 16; ++kk)
     mma_bf16_ts(d_tmem, p_tmem + kk * 8, dv + desc_step(kk * 16 * 128), idesc, 1u);
 }
 
-// 32 scores of the row, those not in `seen` at -inf.
-__device__ __forceinline__ void apply_mask(uint32_t (&s)[32], uint32_t seen) {
+// p = 2^(s * scale + neg) of 32 scores as bf16 pairs at tP; adds p to acc.
+__device__ __forceinline__ void exp_part(const uint32_t (&s)[32], uint64_t scale2, uint64_t neg2,
+                                         uint64_t (&acc)[2], uint32_t tP) {
+  uint32_t pk[16];
 #pragma unroll
-  for (int x = 0; x < 32; ++x)
-    if (!((seen >> x) & 1u)) s[x] = __float_as_uint(-INFINITY);
+  for (int j = 0; j < 16; ++j) {
+    const uint64_t x =
+        fma_f32x2(pack_f32x2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), scale2, neg2);
+    float x0, x1;
+    unpack_f32x2(x, x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
+    acc[j & 1] = add_f32x2(acc[j & 1], pack_f32x2(p0, p1));
+    pk[j] = pack_bf16x2(p0, p1);
+  }
+  tmem_st16(tP, pk);
 }
 
-// f(q, scores of columns 32 q .. 32 q + 31) for the row's 128 scores; the
-// next quarter is on its way from TMEM while one is worked on.
-template <typename F>
-__device__ __forceinline__ void each_quarter(uint32_t tS, bool masked, const uint32_t (&seen)[4], F f) {
-  uint32_t s[2][32];
-  tmem_ld32(tS, s[0]);
-  tmem_ld_wait();
-  reg_fence(s[0], 32);
+// Which of the keys pos .. pos + 31 query t sees; `left` has a bit for every
+// 8 of them that are not in the cache.
+__device__ __forceinline__ uint32_t first_bits(int64_t n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+__device__ __noinline__ uint32_t seen_word(const CacheAttnArgs& a, const SeqInfo& s, int b, int t,
+                                              int64_t pos, uint32_t left) {
+  if (t >= s.cnt) return 0u;
+  const int64_t j0 = pos - s.len;  // draft of bit 0
+  uint32_t seen = first_bits(-j0);
+  if (!a.mask) {
+    seen = first_bits(t - j0 + 1);
+  } else if (j0 > -32 && j0 < s.cnt) {
+    const uint8_t* m = a.mask + b * a.mask_stride + static_cast<int64_t>(t) * a.c.T + j0;
+    const int from = static_cast<int>(max(-j0, int64_t{0}));
+    const int to = static_cast<int>(min(s.cnt - j0, int64_t{32}));
+#pragma unroll 4
+    for (int x = from; x < to; ++x) seen |= (m[x] != 0 ? 1u : 0u) << x;
+  }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
-    if (masked) apply_mask(s[q & 1], seen[q]);
-    f(q, s[q & 1]);
-    if (q < 3) {
-      tmem_ld_wait();
-      reg_fence(s[(q + 1) & 1], 32);
+  for (int x = 0; x < 4; ++x)
+    if ((left >> x) & 1u) seen &= ~(0xffu << (8 * x));
+  return seen;
+}
+
+// Which of columns x .. x + 31 of the drafts that query t sees in the walk's
+// part hold a value that is not finite (a bit each).
+template <bool k8, int D>
+__device__ __noinline__ uint32_t poisoned_columns(const CacheAttnArgs& a, const UnitWalk& u, int head,
+                                                  int t, int x, int tile) {
+  const PagedArgs& c = a.c;
+  uint32_t bad = 0;
+  const int64_t end = min(u.last * tile, u.seq.keys());
+  for (int64_t pos = max(u.first * tile, u.seq.len); pos < end; ++pos) {
+    if (!sees(a, u.seq, u.b, t, pos)) continue;
+    int64_t row = cache_row(c, u.b, pos);
+    if (row < 0) continue;
+    row += static_cast<int64_t>(head) << c.page_shift;
+#pragma unroll 1
+    for (int e = 0; e < 32; ++e) {
+      uint32_t y;
+      if (k8)
+        y = widen_rare(make_uint2(static_cast<const uint8_t*>(c.v)[row * D + x + e], 0u), c.ve[row]).x;
+      else
+        y = static_cast<const uint16_t*>(c.v)[row * D + x + e];
+      if ((y & 0x7f80u) == 0x7f80u) bad |= 1u << e;
     }
   }
-}
-
-// p = 2^(s * scale + neg) as bf16 pairs; returns the row's sum.  The scores
-// stay in TMEM until the caller stores p over them.
-__device__ __forceinline__ float exp_row(uint32_t tS, bool masked, const uint32_t (&seen)[4],
-                                         uint64_t scale2, uint64_t neg2, uint32_t (&pk)[64]) {
-  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-  each_quarter(tS, masked, seen, [&](int q, uint32_t (&s)[32]) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint64_t x = fma_f32x2(
-          pack_f32x2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), scale2, neg2);
-      float x0, x1;
-      unpack_f32x2(x, x0, x1);
-      const float p0 = ex2(x0), p1 = ex2(x1);
-      acc[j & 3] = add_f32x2(acc[j & 3], pack_f32x2(p0, p1));
-      pk[16 * q + j] = pack_bf16x2(p0, p1);
-    }
-  });
-  float r[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) unpack_f32x2(acc[i], r[2 * i], r[2 * i + 1]);
-  return ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
+  return bad;
 }
 
 // What a role needs of the present unit.
@@ -264,14 +323,15 @@ struct Unit {
 
 template <bool k8, int D, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
-    cache_tree_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ AttnPlan p) {
+    cache_tree_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ AttnPlan p,
+                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using L = Layout<k8, D, kTwo>;
-  constexpr int kS = L::kStages;
+  constexpr int kS = L::kStages, kKeys = L::kKeys, kN = kKeys / 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const Bars<kS> bars{base + L::kBar};
+  const Bars<L> bars{base + L::kBar};
   volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(gbase + L::kMisc);
   const Abort ab{tmem_holder + 1, a.c.status, a.wait_limit > 0 ? a.wait_limit : kWaitLimit};
   volatile uint32_t* poison = reinterpret_cast<volatile uint32_t*>(gbase + L::kPoison);
@@ -282,12 +342,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- set-up
   if (threadIdx.x == 0) {
-    mbar_init(bars.q_full(), 128);
+    mbar_init(bars.q_full(), k8 ? 192 : 96);
     mbar_init(bars.q_empty(), 1);
     for (int s = 0; s < kS; ++s) {
-      mbar_init(bars.kv_full(s), 128);
+      mbar_init(bars.kv_full(s), k8 ? 64 : 1);
       mbar_init(bars.kv_empty(s), 1);
     }
+    for (int s = 0; s < L::kLoadStages; ++s) mbar_init(bars.raw_full(s), k8 ? 33 : 1);
+    for (int s = 0; s < L::kRawStages; ++s) mbar_init(bars.raw_empty(s), 64);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bars.s_full(t), 1);
       mbar_init(bars.p_full(t), 128);
@@ -297,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bars.x_empty(), 128);
     mbar_init(bars.drain(), 1);
     *ab.flag = 0u;
-    for (int i = 0; i < 8; ++i) poison[i] = 0u;
+    for (int i = 0; i < 32; ++i) poison[i] = 0u;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -310,200 +372,268 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp >= kLoadWarp) {
-    // ================= producers =================
-    // keeps the registers it was launched with
-    const int tid = threadIdx.x - kLoadWarp * 32;
-    const int grp = tid / 8, pc = tid % 8;  // rows 8 grp .. 8 grp + 7
-    UnitWalk iw, pw;                         // items issued; items handed over
-    iw.start(c, p.div, sh, run);
-    pw = iw;
-    int64_t ix = 0, px = 0;
-    int iunit = 0, punit = 0;
-    int ktiles = 0;  // K tiles issued, for the left-out ring
-    Ring ir, pr;     // operand stages
-    int iraw = 0, praw = 0;
-    bool ok = static_cast<int64_t>(blockIdx.x) != a.stall_cta;
-    const uint8_t* cache_k = static_cast<const uint8_t*>(c.k);
-    const uint8_t* cache_v = static_cast<const uint8_t*>(c.v);
-    for (int64_t i = 0; ok && !pw.done(); ++i) {
-      __syncwarp();  // every lane has read the exponents whose place is refilled now
-      // ---- issue one item
-      if (!iw.done()) {
-        const int64_t n = iw.last - iw.first;
-        int64_t tile;
-        bool v;
-        item<kTwo>(ix, n, tile, v);
-        const int64_t pos = (iw.first + tile) * kBN + 8 * grp;
-        const int64_t keys = iw.seq.keys();
-        int page = -1;
-        if (pos < keys) {
-          const int64_t col = pos >> c.page_shift;
-          if (col < c.width) page = __ldg(c.table + static_cast<int64_t>(iw.b) * c.width + col);
-          if (page < 0 || page >= c.pages) {
-            page = -1;
-            if (pc == 0) flag_page(c.status);
-          }
-        }
-        const int head = iw.unit / p.row_tiles;
-        const int64_t row = ((static_cast<int64_t>(page) * c.heads + head) << c.page_shift) +
-                            (pos & ((int64_t{1} << c.page_shift) - 1));
-        if (!v) {  // which 8-key groups are not in the cache
-          if (pc == 0) gbase[L::kLeftOut + (ktiles & 7) * 16 + grp] = pos < keys && page < 0;
-          ++ktiles;
-        }
-        const uint8_t* src = v ? cache_v : cache_k;
-        const int nrows = page < 0 ? 0 : static_cast<int>(min(keys - pos, int64_t{8}));
-        if (k8) {
-          constexpr int kPieces = D / 16;  // of a row
-          const uint32_t dst = base + L::kRaw + iraw * L::kRawTile + tid * 16;
-          const int r0 = kPieces == 8 ? 0 : (pc / 4) * 4;
-          const int cc = kPieces == 8 ? pc : pc % 4;
+  if (warp >= (k8 ? kHandWarp : kFixWarp)) {
+    // ================= queries, conversion =================
+    const int tid = threadIdx.x - (k8 ? kHandWarp : kFixWarp) * 32;
+    // The unit's queries, by `count` threads of which this is `id`.
+    auto load_queries = [&](const UnitWalk& w, uint32_t ord, int id, int count) {
+      const Unit un(a, p, w, rows);
+      if (!wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) return false;
+      const int64_t left = rows - un.r0;
+      const int pieces = (kTwo && left > 128 ? 256 : 128) * (D / 8);
+      const uint8_t* src = static_cast<const uint8_t*>(a.q) + un.q0 * (2 * D);
+      for (int i0 = id; i0 < pieces; i0 += 4 * count) {
+        uint4 q[4];
 #pragma unroll
-          for (int x = 0; x < kPieces; ++x) {
-            const bool real = r0 + x < nrows;
-            cp_async16(dst + x * 2048, real ? src + (row + r0 + x) * D + cc * 16 : a.q, real);
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + x * count;
+          q[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (i < pieces && i / (D / 8) < left)
+            q[x] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(i) * 16);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + x * count;
+          if (i >= pieces) break;
+          const int r = i / (D / 8), pc = i % (D / 8);
+          if (k8)  // in the order of widen16
+            q[x] = make_uint4(__byte_perm(q[x].x, q[x].y, 0x5410), __byte_perm(q[x].x, q[x].y, 0x7632),
+                              __byte_perm(q[x].z, q[x].w, 0x5410), __byte_perm(q[x].z, q[x].w, 0x7632));
+          st_shared_v4(base + (r < 128 ? L::kQ0 : L::kQ1) + (pc / 8) * L::kQBox + (r % 128) * 128 +
+                           (((pc % 8) ^ (r % 8)) << 4),
+                       q[x].x, q[x].y, q[x].z, q[x].w);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bars.q_full());
+      return true;
+    };
+    UnitWalk w;
+    w.start(c, p.div, sh, run);
+    if (k8) {
+      Ring in, out;  // raw stages; operand stages
+      constexpr int kPairs = 3;
+      constexpr int kGroup = kKeys / 8;  // rows per 8 of a pair's 64 threads
+      constexpr int kPieces = D * kKeys / 16 / 64;
+      const int pair = tid / 64, grp = tid % 64 / 8, pc = tid % 8;
+      int turn = 0;  // of the pair that takes the next tile
+      const uint32_t src0 = base + L::kRaw + (D == 128 ? pc : pc % 4) * 16;
+      const uint32_t dst0 = base + L::kKV + (D == 128 ? pc / 4 : 0) * L::kBox;
+      const int ch = 2 * (pc % 4);
+      for (uint32_t ord = 0; !w.done(); ++ord, w.next(c, p.div)) {
+        if (!load_queries(w, ord, tid, 192)) break;
+        const int n = static_cast<int>(w.last - w.first);
+        // keys and context keys of this part
+        const int64_t before = w.first * kKeys;
+        const int keys = static_cast<int>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
+        const int context = static_cast<int>(min(w.seq.len - before, static_cast<int64_t>(n) * kKeys));
+        const bool ok = each_item<kTwo>(n, [&](int tile, bool v) {
+          const bool other = turn != pair;
+          turn = turn + 1 == kPairs ? 0 : turn + 1;
+          if (other) {
+            in.step<L::kLoadStages>();
+            out.step<kS>();
+            return true;
           }
-          if (pc == 0)
-            cp_async_small<8>(base + L::kRawExp + iraw * 128 + grp * 8,
-                              nrows > 0 ? static_cast<const void*>((v ? c.ve : c.ke) + row) : a.q,
-                              nrows > 0);
-          iraw = iraw + 1 == L::kRawStages ? 0 : iraw + 1;
-        } else {
-          if (!wait_warp(bars.kv_empty(ir.stage), ir.phase ^ 1u, ab)) {
+          if (!wait_warp(bars.raw_full(in.stage), in.phase, ab)) return false;
+          if (!wait_warp(bars.kv_empty(out.stage), out.phase ^ 1u, ab)) return false;
+          const uint32_t src = src0 + in.stage * L::kRawTile;
+          const uint8_t* ex = gbase + L::kRawExp + in.stage * kKeys;
+          const uint32_t dst = dst0 + out.stage * L::kTile;
+          const bool border = v && (tile + 1) * kKeys > context;
+          bool bad = false;
+          constexpr int kBatch = kPieces < 4 ? kPieces : 4;  // loads in flight
+#pragma unroll 1
+          for (int z0 = 0; z0 < kPieces; z0 += kBatch) {
+            uint4 w4[kBatch];
+            uint32_t e[kBatch];
+#pragma unroll
+            for (int z = 0; z < kBatch; ++z) {
+              const int r = grp * kGroup + piece_row<D, kGroup>(z0 + z, pc);
+              w4[z] = lds128(src + r * D);
+              e[z] = ex[r];
+            }
+#pragma unroll
+            for (int z = 0; z < kBatch; ++z) {
+              const int r = grp * kGroup + piece_row<D, kGroup>(z0 + z, pc);
+              uint32_t o[8];
+              widen16(w4[z], e[z], o);
+              if (border) {
+                const bool real = tile * kKeys + r < keys;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                  const uint32_t nf = real ? not_finite(o[y]) : 0u;
+                  bad = bad || nf;
+                  o[y] = real ? o[y] & ~nf : 0u;
+                }
+              }
+              st_shared_v4(dst + r * 128 + ((ch ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+              st_shared_v4(dst + r * 128 + (((ch + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+            }
+          }
+          mbar_arrive(bars.raw_empty(in.stage));
+          if (bad) poison[ord & 31] = ord + 1u;
+          fence_proxy_async_smem();
+          mbar_arrive(bars.kv_full(out.stage));
+          in.step<L::kLoadStages>();
+          out.step<kS>();
+          return true;
+        });
+        if (!ok) break;
+      }
+    } else if (warp > kFixWarp) {
+      for (uint32_t ord = 0; !w.done(); ++ord, w.next(c, p.div))
+        if (!load_queries(w, ord, tid - 32, 96)) break;
+    } else {
+      // value tiles with drafts or the end
+      uint32_t first_item = 0, used = 0;  // items before the unit; phases of raw_full, a bit each
+      bool ok = true;
+      for (uint32_t ord = 0; ok && !w.done(); ++ord, w.next(c, p.div)) {
+        const int n = static_cast<int>(w.last - w.first);
+        const int64_t before = w.first * kKeys;
+        const int keys = static_cast<int>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
+        const int from =
+            static_cast<int>(min(max(w.seq.len / kKeys - w.first, int64_t{0}), static_cast<int64_t>(n)));
+        for (int tile = from; tile < n; ++tile) {
+          const int stage = static_cast<int>((first_item + value_item<kTwo>(tile, n)) % kS);
+          if (!wait_warp(bars.raw_full(stage), (used >> stage) & 1u, ab)) {
             ok = false;
             break;
           }
-          const uint32_t dst = base + L::kKV + ir.stage * L::kTile + grp * 1024;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-              const bool real = x < nrows;
-              cp_async16(dst + b * L::kBox + x * 128 + ((pc ^ x) << 4),
-                         real ? src + (row + x) * (2 * D) + b * 128 + pc * 16 : a.q, real);
-            }
-          }
-          ir.step<kS>();
-        }
-        if (++ix == 2 * n) {
-          ix = 0;
-          ++iunit;
-          iw.next(c, p.div);
-        }
-      }
-      cp_commit();
-      if (i < L::kLag) continue;
-
-      // ---- hand over the item issued kLag before
-      const int64_t n = pw.last - pw.first;
-      int64_t tile;
-      bool v;
-      item<kTwo>(px, n, tile, v);
-      if (px == 0) {
-        // the unit's queries, ahead of its first key tile
-        const Unit un(a, p, pw, rows);
-        if (!wait_warp(bars.q_empty(), (punit & 1) ^ 1u, ab)) {
-          ok = false;
-          break;
-        }
-        const int qt = kTwo && un.r0 + 128 < rows ? 2 : 1;
-        for (int t = 0; t < qt; ++t) {
-          const uint32_t dst = base + (t ? L::kQ1 : L::kQ0) + grp * 1024;
-          const uint8_t* src = static_cast<const uint8_t*>(a.q) + (un.q0 + t * 128 + 8 * grp) * (2 * D);
-          const int64_t left = rows - un.r0 - t * 128 - 8 * grp;
-#pragma unroll
-          for (int b = 0; b < D / 64; ++b) {
-            uint4 q[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              q[x] = x < left ? *reinterpret_cast<const uint4*>(src + x * 2 * D + b * 128 + pc * 16)
-                              : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              st_shared_v4(dst + b * L::kBox + x * 128 + ((pc ^ x) << 4), q[x].x, q[x].y, q[x].z, q[x].w);
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bars.q_full());
-      }
-      const bool border = (pw.first + tile + 1) * kBN > pw.seq.len;
-      cp_wait<L::kLag>();
-      bool bad = false;
-      if (k8) {
-        __syncwarp();  // the exponents were loaded by one thread of each group
-        if (!wait_warp(bars.kv_empty(pr.stage), pr.phase ^ 1u, ab)) {
-          ok = false;
-          break;
-        }
-        constexpr int kPieces = D / 16;
-        const uint32_t src = base + L::kRaw + praw * L::kRawTile + tid * 16;
-        const uint8_t* ex = gbase + L::kRawExp + praw * 128 + grp * 8;
-        const uint32_t dst = base + L::kKV + pr.stage * L::kTile + grp * 1024;
-        const int r0 = kPieces == 8 ? 0 : (pc / 4) * 4;
-        const int cc = kPieces == 8 ? pc : pc % 4;
-        const int box = cc / 4;
-        // the two 16-byte halves are written in another order by half of the
-        // lanes, so that a row's eight writes meet no bank twice
-        const int odd = kPieces == 8 ? box : (pc / 4);
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x) {
-          const uint4 w4 = lds128(src + x * 2048);
-          const int e = ex[r0 + x];
-          const int f1 = min(e + 120, 254);
-          const uint32_t up = static_cast<uint32_t>(f1 << 7) * 0x10001u;
-          const uint32_t up2 = static_cast<uint32_t>((e + 120 - f1 + 127) << 7) * 0x10001u;
-          const bool twice = e > 134;
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          uint32_t o[8];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            o[2 * z] = widen(__byte_perm(w[z], 0u, 0x1404), up, up2, twice);
-            o[2 * z + 1] = widen(__byte_perm(w[z], 0u, 0x3424), up, up2, twice);
-          }
-          if (v && border) {
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              const uint32_t nf = not_finite(o[z]);
-              bad = bad || nf;
-              o[z] &= ~nf;
-            }
-          }
-          const int r = r0 + x, ch = 2 * (cc % 4);
-          const uint32_t at = dst + box * L::kBox + r * 128;
-          const uint32_t first = at + (((ch + odd) ^ r) << 4), second = at + (((ch + 1 - odd) ^ r) << 4);
-          st_shared_v4(first, odd ? o[4] : o[0], odd ? o[5] : o[1], odd ? o[6] : o[2], odd ? o[7] : o[3]);
-          st_shared_v4(second, odd ? o[0] : o[4], odd ? o[1] : o[5], odd ? o[2] : o[6], odd ? o[3] : o[7]);
-        }
-        praw = praw + 1 == L::kRawStages ? 0 : praw + 1;
-      } else if (v && border) {
-        const uint32_t dst = base + L::kKV + pr.stage * L::kTile + grp * 1024;
+          used ^= 1u << stage;
+          bool bad = false;
+          const uint32_t at = base + L::kKV + stage * L::kTile;
 #pragma unroll 1
-        for (int x = 0; x < 8 * (D / 64); ++x) {
-          const uint32_t at = dst + (x / 8) * L::kBox + (x % 8) * 128 + ((pc ^ (x % 8)) << 4);
-          const uint4 w = lds128(at);
-          const uint32_t n0 = not_finite(w.x), n1 = not_finite(w.y), n2 = not_finite(w.z),
-                         n3 = not_finite(w.w);
-          if (n0 | n1 | n2 | n3) {
-            bad = true;
-            st_shared_v4(at, w.x & ~n0, w.y & ~n1, w.z & ~n2, w.w & ~n3);
+          for (int i = lane; i < kKeys * D / 8; i += 32) {  // 16-byte pieces, box by box
+            const uint4 y = lds128(at + i * 16);
+            const uint32_t n0 = not_finite(y.x), n1 = not_finite(y.y), n2 = not_finite(y.z),
+                           n3 = not_finite(y.w);
+            if (tile * kKeys + (i / 8) % kKeys >= keys) {
+              st_shared_v4(at + i * 16, 0u, 0u, 0u, 0u);
+            } else if (n0 | n1 | n2 | n3) {
+              bad = true;
+              st_shared_v4(at + i * 16, y.x & ~n0, y.y & ~n1, y.z & ~n2, y.w & ~n3);
+            }
           }
+          if (bad) poison[ord & 31] = ord + 1u;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.kv_full(stage));
         }
-      }
-      if (bad) poison[punit & 7] = static_cast<uint32_t>(punit) + 1u;
-      fence_proxy_async_smem();
-      mbar_arrive(bars.kv_full(pr.stage));
-      pr.step<kS>();
-      if (++px == 2 * n) {
-        px = 0;
-        ++punit;
-        pw.next(c, p.div);
+        first_item += 2u * static_cast<uint32_t>(n);
       }
     }
-    cp_wait<0>();
+  } else if (warp == kLoadWarp) {
+    // ================= loader =================
+    const int page_rows = min(1 << c.page_shift, kKeys);  // of a box
+    const int boxes = kKeys / page_rows;
+    constexpr int kHalves = k8 ? 1 : D / 64;
+    const bool mine = lane < boxes * kHalves;
+    const int box = lane % boxes, half = lane / boxes;
+    const uint32_t dst_off =
+        half * L::kBox + box * page_rows * (k8 ? D : 128) + (k8 ? L::kRaw : L::kKV) + base;
+    constexpr uint32_t kLoadTile = k8 ? L::kRawTile : L::kTile;
+    const int from = min(lane * 8 / page_rows, boxes - 1);  // the box of rows 8 lane ..
+    const uint32_t in_page = (1u << c.page_shift) - 1u;
+    const int32_t behind = static_cast<int32_t>((c.pages > 0 ? c.pages * c.heads : 1));
+    const uint64_t map_k = reinterpret_cast<uint64_t>(&tk), map_v = reinterpret_cast<uint64_t>(&tv);
+    UnitWalk w;
+    w.start(c, p.div, sh, run);
+    Ring r;
+    uint32_t ktiles = 0;
+    // a bit per stage: loaded, to arrive at raw_full, and the phase of that
+    uint32_t issued = 0, hand = 0, last = 0, raw_phase = 0;
+    bool ok = static_cast<int64_t>(blockIdx.x) != a.stall_cta;
+    for (; ok && !w.done(); w.next(c, p.div)) {
+      const int n = static_cast<int>(w.last - w.first);
+      const int head = w.unit / p.row_tiles;
+      const uint32_t pos0 = static_cast<uint32_t>(w.first) * kKeys;  // positions stay below 2^32
+      const uint32_t keys = static_cast<uint32_t>(w.seq.keys());
+      // the first tile with drafts or the end
+      const int border =
+          static_cast<int>(min(max(w.seq.len / kKeys - w.first, int64_t{0}), static_cast<int64_t>(n)));
+      const int32_t* row_of_table = c.table + static_cast<int64_t>(w.b) * c.width;
+      // this lane's page of a tile: its number, -1 for one that is missing,
+      // -2 for none
+      auto look_up = [&](int tile) {
+        const uint32_t pos = pos0 + static_cast<uint32_t>(tile) * kKeys + box * page_rows;
+        if (!mine || tile >= n || pos >= keys) return -2;
+        const uint32_t col = pos >> c.page_shift;
+        return col < static_cast<uint32_t>(c.width) ? max(__ldg(row_of_table + col), -1) : -1;
+      };
+      int page = -2, ahead = look_up(0);  // of the last key tile loaded; of the next
+      int32_t z = 0, zv = 0;              // its TMA coordinate; that of the value tile to come
+      int64_t erow = 0, erow_v = 0;       // exponent rows (8 per lane), -1: none
+      ok = each_item<kTwo>(n, [&](int tile, bool v) {
+        if (!v) {
+          page = ahead;
+          ahead = look_up(tile + 1);
+          const bool there = page >= 0 && page < c.pages;
+          const uint32_t lost = __ballot_sync(0xffffffffu, page != -2 && !there);
+          uint32_t left = 0;  // bit i: rows 8 i .. 8 i + 7 are wanted but not in the cache
+          if (lost) {
+            if (page != -2 && !there) flag_page(c.status);
+            left = __ballot_sync(0xffffffffu, lane < kKeys / 8 && ((lost >> from) & 1u));
+          }
+          if (lane == 0)
+            *reinterpret_cast<volatile uint32_t*>(gbase + L::kLeftOut + (ktiles & 31u) * 4) = left;
+          ++ktiles;
+          zv = z;
+          z = there ? page * c.heads + head : behind;
+          if (k8) {
+            erow_v = erow;
+            const int32_t ze = __shfl_sync(0xffffffffu, z, from);
+            const uint32_t pos = pos0 + static_cast<uint32_t>(tile) * kKeys + lane * 8;
+            erow = lane < kKeys / 8 && ze != behind
+                       ? (static_cast<int64_t>(ze) << c.page_shift) + (pos & in_page)
+                       : -1;
+          }
+        }
+        // in the order with two key tiles under way the value tile is the one
+        // before, unless it is the last
+        const bool older = !kTwo && v && tile + 1 < n;
+        const int32_t zz = older ? zv : z;
+        if (!wait_warp(k8 ? bars.raw_empty(r.stage) : bars.kv_empty(r.stage), r.phase ^ 1u, ab))
+          return false;
+        // where the arrival is seen: by the MMA thread, or by who converts or clears
+        const bool by_hand = k8 || (v && tile >= border);
+        const uint32_t bar = by_hand ? bars.raw_full(r.stage) : bars.kv_full(r.stage);
+        if (lane == 0) mbar_arrive_expect_tx(bar, kLoadTile);
+        __syncwarp();
+        if (mine)
+          tma_load_3d(dst_off + r.stage * kLoadTile, reinterpret_cast<const CUtensorMap*>(v ? map_v : map_k),
+                      half * 64, static_cast<int32_t>((pos0 + static_cast<uint32_t>(tile) * kKeys) & in_page),
+                      zz, bar);
+        if (k8) {
+          const int64_t er = older ? erow_v : erow;
+          if (lane < kKeys / 8)
+            cp_async8(base + L::kRawExp + r.stage * kKeys + lane * 8,
+                      er >= 0 ? static_cast<const void*>((v ? c.ve : c.ke) + er) : a.q, er >= 0);
+          cp_arrive(bar);
+        }
+        const uint32_t bit = 1u << r.stage;
+        issued |= bit;
+        if (by_hand) {
+          hand |= bit;
+          last = (last & ~bit) | (raw_phase & bit);
+          raw_phase ^= bit;
+        } else {
+          hand &= ~bit;
+          last = (last & ~bit) | (r.phase << r.stage);
+        }
+        r.step<L::kLoadStages>();
+        return true;
+      });
+    }
+    // What is on its way lands before the CTA goes, also after a timeout.
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (*ab.flag) {
+      for (int s = 0; s < L::kLoadStages; ++s)
+        if ((issued >> s) & 1u)
+          wait_drain((hand >> s) & 1u ? bars.raw_full(s) : bars.kv_full(s), (last >> s) & 1u);
+    }
   } else if (warp >= kMmaWarp) {
-    // ================= MMA issuer =================
-    setmaxnreg_dec<kRegsMma>();
+    // ================= MMA issuer (and two idle warps) =================
     if (warp == kMmaWarp && lane == 0) {
       const uint64_t dQ0 = desc_sw128(base + L::kQ0, 16, 1024);
       const uint64_t dQ1 = desc_sw128(base + L::kQ1, 16, 1024);
@@ -536,10 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Unit un(a, p, u, rows);
           const bool two = un.r0 + 128 < rows;
           uint64_t dk = dK + desc_step(sk * L::kTile);
-          issue_qk<D>(tS0, dQ0, dk);
+          issue_qk<D, kKeys>(tS0, dQ0, dk);
           mma_commit(bars.s_full(0));
           if (two) {
-            issue_qk<D>(tS1, dQ1, dk);
+            issue_qk<D, kKeys>(tS1, dQ1, dk);
             mma_commit(bars.s_full(1));
           }
           mma_commit(bars.kv_empty(sk));
@@ -551,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint64_t dv = dV + desc_step(sv * L::kTile);
-            issue_pv<D>(tO0, tS0, dv, it > 0);
+            issue_pv<D, kKeys>(tO0, tS0, dv, it > 0);
             const bool more = it + 1 < n;
             if (more) {
               sk = take();
@@ -560,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               dk = dK + desc_step(sk * L::kTile);
-              issue_qk<D>(tS0, dQ0, dk);
+              issue_qk<D, kKeys>(tS0, dQ0, dk);
               mma_commit(bars.s_full(0));
             }
             if (two) {
@@ -569,12 +699,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               tc_fence_after();
-              issue_pv<D>(tO1, tS1, dv, it > 0);
+              issue_pv<D, kKeys>(tO1, tS1, dv, it > 0);
             }
             mma_commit(bars.kv_empty(sv));
             if (more) {
               if (two) {
-                issue_qk<D>(tS1, dQ1, dk);
+                issue_qk<D, kKeys>(tS1, dQ1, dk);
                 mma_commit(bars.s_full(1));
               }
               mma_commit(bars.kv_empty(sk));
@@ -586,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (two) mma_commit(bars.o_full(1));
           }
         } else {
-          issue_qk<D>(tS0, dQ0, dK + desc_step(sk * L::kTile));
+          issue_qk<D, kKeys>(tS0, dQ0, dK + desc_step(sk * L::kTile));
           mma_commit(bars.s_full(0));
           mma_commit(bars.kv_empty(sk));
           if (n > 1) {
@@ -595,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            issue_qk<D>(tS1, dQ0, dK + desc_step(sk * L::kTile));
+            issue_qk<D, kKeys>(tS1, dQ0, dK + desc_step(sk * L::kTile));
             mma_commit(bars.s_full(1));
             mma_commit(bars.kv_empty(sk));
           }
@@ -608,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t tS = t ? tS1 : tS0;
-            issue_pv<D>(t ? tO1 : tO0, tS, dV + desc_step(sv * L::kTile), it > 1);
+            issue_pv<D, kKeys>(t ? tO1 : tO0, tS, dV + desc_step(sv * L::kTile), it > 1);
             mma_commit(bars.kv_empty(sv));
             if (it + 2 < n) {
               sk = take();
@@ -616,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
               }
-              issue_qk<D>(tS, dQ0, dK + desc_step(sk * L::kTile));
+              issue_qk<D, kKeys>(tS, dQ0, dK + desc_step(sk * L::kTile));
               mma_commit(bars.s_full(t));
               mma_commit(bars.kv_empty(sk));
             }
@@ -635,7 +765,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ================= softmax =================
-    setmaxnreg_inc<kRegsSoftmax>();
     const int t = warp / 4, wq = warp % 4;
     const int row = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -653,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = static_cast<int>(u.last - u.first);
       // the first tile of this part that holds drafts or the end
       const int border = static_cast<int>(
-          min(max(u.seq.len / kBN - u.first, int64_t{0}), static_cast<int64_t>(n)));
+          min(max(u.seq.len / kKeys - u.first, int64_t{0}), static_cast<int64_t>(n)));
       int tok;
       bool active, exists;
       {
@@ -675,77 +804,93 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (warp_live) {
-            const uint4 left = lds128(base + L::kLeftOut + ((kt + it) & 7u) * 16u);
-            const bool masked = it >= border || (left.x | left.y | left.z | left.w);
-            uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-            if (masked) {
-              const int64_t pos = (u.first + it) * kBN;
-              const uint32_t lw[4] = {left.x, left.y, left.z, left.w};
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                seen[w] = 0;
+            const uint32_t left = *reinterpret_cast<volatile uint32_t*>(
+                gbase + L::kLeftOut + ((kt + it) & 31u) * 4);
+            const bool masked = it >= border || left != 0u;
+            if (masked) {  // scores that are not seen become -inf in TMEM
 #pragma unroll 1
-                for (int x = 0; x < 32; ++x) {
-                  const bool out = (lw[w] >> (8 * (x / 8))) & 0xffu;
-                  if (!out && sees(a, u.seq, u.b, tok, pos + 32 * w + x)) seen[w] |= 1u << x;
+              for (int w = 0; w < kN; ++w) {
+                const uint32_t seen =
+                    seen_word(a, u.seq, u.b, tok, (u.first + it) * kKeys + 32 * w, left >> (4 * w));
+                uint32_t s[32];
+                __syncwarp();
+                tmem_ld32(tS + 32 * w, s);
+                tmem_ld_wait();
+                reg_fence(s, 32);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  if (!((seen >> x) & 1u)) s[x] = __float_as_uint(-INFINITY);
+                tmem_st32(tS + 32 * w, s);
+              }
+              tmem_st_wait();
+            }
+            // Two passes over the row's scores: the maximum, then the
+            // probabilities, whose bf16 pairs take the place of scores that
+            // have been read.  Rolled loops: see the head of the file.
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int w = 0; w < kN; w += 2) {
+              uint32_t s[64];
+              tmem_ld32(tS + 32 * w, s);
+              tmem_ld32(tS + 32 * w + 32, s + 32);
+              tmem_ld_wait();
+              reg_fence(s, 64);
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 8]));
+#pragma unroll
+              for (int j = 16; j < 64; j += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  v[e] = fmax3(v[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + 8 + e]));
+              mx = fmax3(mx, fmax3(v[0], v[1], v[2]), fmax3(fmax3(v[3], v[4], v[5]), v[6], v[7]));
+            }
+            const float m_new = mx * a.scale_log2;
+            const bool need = m_new > m_ref + kRescaleLog2;
+            if (__any_sync(0xffffffffu, need)) {
+              const float alpha = need ? ex2(m_ref - m_new) : 1.f;
+              if (o_valid) {
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                  uint32_t r[32];
+                  tmem_ld32(tO + x, r);
+                  tmem_ld_wait();
+                  reg_fence(r, 32);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                  tmem_st32(tO + x, r);
                 }
+                tmem_st_wait();
+              }
+              if (need) {
+                l *= alpha;
+                m_ref = m_new;
               }
             }
-            // As in the forward: exponentials against the present reference
-            // first; a row sum of at most 2^kRescaleLog2 rules out that the
-            // reference has to move.
-            uint32_t pk[64];
-            bool redo = true;
-            if (__all_sync(0xffffffffu, m_ref != -INFINITY)) {
-              const float lt = exp_row(tS, masked, seen, scale2, pack_f32x2(-m_ref, -m_ref), pk);
-              if (!__any_sync(0xffffffffu, lt > kFastSumBound)) {
-                l += lt;
-                redo = false;
-              }
+            // a row that has seen no key yet keeps m_ref = -inf: p = 0, not NaN
+            const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+            const uint64_t neg2 = pack_f32x2(neg, neg);
+            uint64_t acc[2] = {0ull, 0ull};
+            // 32 scores are on their way from TMEM while 32 are worked on
+            uint32_t s0[32], s1[32];
+            tmem_ld32(tS, s0);
+            tmem_ld_wait();
+            reg_fence(s0, 32);
+#pragma unroll 1
+            for (int w = 0; w < kN; w += 2) {
+              tmem_ld32(tS + 32 * w + 32, s1);
+              exp_part(s0, scale2, neg2, acc, tS + 16 * w);
+              tmem_ld_wait();
+              reg_fence(s1, 32);
+              if (w + 2 < kN) tmem_ld32(tS + 32 * w + 64, s0);
+              exp_part(s1, scale2, neg2, acc, tS + 16 * w + 16);
+              tmem_ld_wait();
+              reg_fence(s0, 32);
             }
-            if (redo) {
-              float mx = -INFINITY;
-              each_quarter(tS, masked, seen, [&](int, uint32_t (&s)[32]) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(s[e]);
-#pragma unroll
-                for (int j = 4; j < 28; j += 8)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    v[e] = fmax3(v[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + 4 + e]));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fmaxf(v[e], __uint_as_float(s[28 + e]));
-                mx = fmax3(mx, fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-              });
-              const float m_new = mx * a.scale_log2;
-              const bool need = m_new > m_ref + kRescaleLog2;
-              if (__any_sync(0xffffffffu, need)) {
-                const float alpha = need ? ex2(m_ref - m_new) : 1.f;
-                if (o_valid) {
-#pragma unroll
-                  for (int x = 0; x < D; x += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(tO + x, r);
-                    tmem_ld_wait();
-                    reg_fence(r, 32);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                    tmem_st32(tO + x, r);
-                  }
-                  tmem_st_wait();
-                }
-                if (need) {
-                  l *= alpha;
-                  m_ref = m_new;
-                }
-              }
-              // a row that has seen no key yet keeps m_ref = -inf: p = 0, not NaN
-              const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-              l += exp_row(tS, masked, seen, scale2, pack_f32x2(neg, neg), pk);
-            }
-            tmem_st32(tS, pk);
-            tmem_st32(tS + 32, pk + 32);
+            float a0, a1, a2, a3;
+            unpack_f32x2(acc[0], a0, a1);
+            unpack_f32x2(acc[1], a2, a3);
+            l += (a0 + a1) + (a2 + a3);
             tmem_st_wait();
           }
           tc_fence_before();
@@ -764,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_ref = -INFINITY;
         l = 0.f;
       }
-      const bool poisoned = poison[unit & 7] == unit + 1u;
+      const bool poisoned = poison[unit & 31] == unit + 1u;
 
       // ---- one query tile: stream 1 hands its state to stream 0
       const bool exchange = !kTwo && n > 1;
@@ -783,6 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = u.slot(blockIdx.x);
         const int local = (kTwo ? t * 128 : 0) + row;
         float inv = 1.f;
+#pragma unroll 1
         for (int x = 0; x < D; x += 32) {
           uint32_t r[32];
           if (active) {
@@ -830,36 +976,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0u;
           }
-          if (poisoned && live) {
-            // elements of the drafts that were left out because they are not finite
-            int64_t pos = max(u.first * kBN, u.seq.len);
-            const int64_t end = min(u.last * kBN, u.seq.keys());
-            for (; pos < end; ++pos) {
-              if (!sees(a, u.seq, u.b, tok, pos)) continue;
-              const int64_t at = cache_row(c, u.b, pos);
-              if (at < 0) continue;
-              const int64_t vr = at + (static_cast<int64_t>(un.head) << c.page_shift);
-#pragma unroll 1
-              for (int e = 0; e < 32; ++e) {
-                float y;
-                if (k8) {
-                  const uint8_t code = static_cast<const uint8_t*>(c.v)[vr * D + x + e];
-                  const uint32_t z = widen(static_cast<uint32_t>(code) << 8,
-                                           static_cast<uint32_t>(min(c.ve[vr] + 120, 254)) << 7,
-                                           static_cast<uint32_t>(c.ve[vr] + 247 - min(c.ve[vr] + 120, 254)) << 7,
-                                           c.ve[vr] > 134);
-                  y = __uint_as_float(z << 16);
-                } else {
-                  y = __uint_as_float(static_cast<uint32_t>(
-                          static_cast<const uint16_t*>(c.v)[vr * D + x + e]) << 16);
-                }
-                if (!isfinite(y)) {
+          if (k8) {  // back to the order of the head's elements
 #pragma unroll
-                  for (int z = 0; z < 32; ++z)
-                    if (z == e) r[z] = 0x7fffffffu;
-                }
-              }
+            for (int e = 0; e < 32; e += 4) {
+              const uint32_t y = r[e + 1];
+              r[e + 1] = r[e + 2];
+              r[e + 2] = y;
             }
+          }
+          if (poisoned && live) {
+            // elements of drafts that were left out because they are not finite
+            const uint32_t bad = poisoned_columns<k8, D>(a, u, un.head, tok, x, kKeys);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((bad >> e) & 1u) r[e] = 0x7fffffffu;
           }
           if (exists) {
             if (whole) {
@@ -909,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool k8, int D, bool kTwo>
-cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
   using L = Layout<k8, D, kTwo>;
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -921,7 +1051,14 @@ cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) 
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  cache_tree_kernel<k8, D, kTwo><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p);
+  CUtensorMap tk, tv;
+  const int rows = (1 << a.c.page_shift) < L::kKeys ? 1 << a.c.page_shift : L::kKeys;
+  if (!encode_pages(&tk, a.c.pages > 0 ? a.c.k : a.q, a.c, rows, k8) ||
+      !encode_pages(&tv, a.c.pages > 0 ? a.c.v : a.q, a.c, rows, k8))
+    return cudaErrorUnknown;
+  AttnPlan p = plan;
+  p.div.tile = L::kKeys;
+  cache_tree_kernel<k8, D, kTwo><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv);
   e = cudaGetLastError();
   return e == cudaSuccess ? launch_cache_attn_join(a, p, true, s) : e;
 }
@@ -939,7 +1076,6 @@ cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s) {
   p.rows = rows > 128 ? 256 : 128;
   p.row_tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
   p.div.units = a.c.heads * p.row_tiles;
-  p.div.tile = kBN;
   p.div.ctas = kTreeCtas;
   p.div.min_run = 1;
   if (a.c.d == 128) return k8 ? by_rows<true, 128>(a, p, s) : by_rows<false, 128>(a, p, s);

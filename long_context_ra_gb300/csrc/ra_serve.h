@@ -2,6 +2,7 @@
 // rotation of queries and keys, and the paged K/V cache.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -58,6 +59,11 @@ struct PagedArgs {
   int32_t B, T;
   int* status;
 };
+
+// TMA view of one side of a cache, [pages x heads, page, d], with boxes of
+// box_rows rows: 64 bf16 columns with the 128-byte swizzle of the MMA
+// operands, or whole rows of bytes.
+bool encode_pages(CUtensorMap* map, const void* ptr, const PagedArgs& c, int box_rows, bool bytes);
 
 struct CacheCopyArgs {
   PagedArgs c;

@@ -99,7 +99,9 @@ ra_status check_cache(const ra_cache* cache, const int32_t* table, int32_t width
     return RA_ERR_UNSUPPORTED;
   if (cache->page < 8 || cache->page > 1024 || (cache->page & (cache->page - 1)) != 0)
     return RA_ERR_UNSUPPORTED;
-  if (cache->pages > INT32_MAX || B * T > kMaxTokens) return RA_ERR_UNSUPPORTED;
+  // page numbers and TMA coordinates are int32
+  if (cache->pages > INT32_MAX || cache->pages * cache->heads > INT32_MAX || B * T > kMaxTokens)
+    return RA_ERR_UNSUPPORTED;
   if (cache->pages > 0 && (!cache->k || !cache->v)) return RA_ERR_INVALID_ARG;
   if (cache->dtype == RA_E4M3 && cache->pages > 0 && (!cache->k_exp || !cache->v_exp))
     return RA_ERR_INVALID_ARG;
