@@ -113,6 +113,74 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// kV consecutive elements of a row as they lie in memory: loaded with wide
+// loads that bypass L1, unpacked to floats when they are used, so that many
+// can be on their way.
+template <typename E, int kV>
+struct Packed {
+  static constexpr int kBytes = kV * static_cast<int>(sizeof(E));
+  static constexpr int kWords = kBytes / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const void* p) {
+    if (kBytes == 8) {
+      asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
+                   : "=r"(w[0]), "=r"(w[1])
+                   : "l"(p));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                     : "l"(static_cast<const uint8_t*>(p) + 4 * i));
+    }
+  }
+  __device__ __forceinline__ void store(void* p) const {
+    if (kBytes == 8) {
+      *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p) + 4 * i) =
+            make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[kV]) const {
+    if (sizeof(E) == 4) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) x[i] = __uint_as_float(w[i % kWords]);
+    } else if (sizeof(E) == 2) {
+#pragma unroll
+      for (int i = 0; i < kV; i += 2) {
+        x[i] = __uint_as_float(w[(i / 2) % kWords] << 16);
+        x[i + 1] = __uint_as_float(w[(i / 2) % kWords] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; i += 4) unpack_e4m3x4(w[(i / 4) % kWords], x + i);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&x)[kV]) {
+    if (sizeof(E) == 4) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) w[i % kWords] = __float_as_uint(x[i]);
+    } else if (sizeof(E) == 2) {
+#pragma unroll
+      for (int i = 0; i < kV; i += 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[i], x[i + 1]);
+        w[(i / 2) % kWords] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; i += 4) w[(i / 4) % kWords] = pack_e4m3x4(x + i);
+    }
+  }
+};
+
 // ------------------------------------------------------------ work division
 //
 // A unit is one tile of query rows of one key head of one sequence; it walks
