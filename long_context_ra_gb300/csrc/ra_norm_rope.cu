@@ -12,7 +12,9 @@
 // belongs to d / 2kP lanes, padded to a power of two for the row's sums.  A
 // group of lanes stays with one token and walks over its heads: the angles
 // of a lane are computed once per token, and the next heads are loaded,
-// packed, before the present ones are worked on.
+// packed, before the present ones are worked on.  The arithmetic runs on
+// pairs of floats (fma.rn.f32x2): with single ones the backward was bound by
+// its instructions.
 //
 // The angle is exact for any position: pos * turns wraps modulo 2^64 and its
 // upper half is the signed fraction of a turn.
@@ -20,9 +22,12 @@
 #include <cuda_bf16.h>
 
 #include "ra_paged.cuh"
+#include "sm103_ptx.cuh"
 
 namespace ra {
 namespace {
+
+using namespace ptx;
 
 constexpr int kThreads = 256;
 
@@ -34,8 +39,63 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// A lane's part of a row as floats: the first and the second elements of its
+// kP rotation pairs, two pairs to a register pair.
+template <int kP>
+struct Row {
+  uint64_t p[kP / 2], q[kP / 2];
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int i = 0; i < kP / 2; ++i) p[i] = q[i] = pack_f32x2(x, x);
+  }
+  // Sum of products with another row's part.
+  __device__ __forceinline__ float dot(const Row& o) const {
+    uint64_t u = mul_f32x2(p[0], o.p[0]), v = mul_f32x2(q[0], o.q[0]);
+#pragma unroll
+    for (int i = 1; i < kP / 2; ++i) {
+      u = fma_f32x2(p[i], o.p[i], u);
+      v = fma_f32x2(q[i], o.q[i], v);
+    }
+    float a, b;
+    unpack_f32x2(add_f32x2(u, v), a, b);
+    return a + b;
+  }
+  __device__ __forceinline__ void scale(float x) {
+    const uint64_t y = pack_f32x2(x, x);
+#pragma unroll
+    for (int i = 0; i < kP / 2; ++i) {
+      p[i] = mul_f32x2(p[i], y);
+      q[i] = mul_f32x2(q[i], y);
+    }
+  }
+  __device__ __forceinline__ void times(const Row& o) {
+#pragma unroll
+    for (int i = 0; i < kP / 2; ++i) {
+      p[i] = mul_f32x2(p[i], o.p[i]);
+      q[i] = mul_f32x2(q[i], o.q[i]);
+    }
+  }
+  // this += a * b
+  __device__ __forceinline__ void add_product(const Row& a, const Row& b) {
+#pragma unroll
+    for (int i = 0; i < kP / 2; ++i) {
+      p[i] = fma_f32x2(a.p[i], b.p[i], p[i]);
+      q[i] = fma_f32x2(a.q[i], b.q[i], q[i]);
+    }
+  }
+  // this += a * x
+  __device__ __forceinline__ void add_scaled(const Row& a, float x) {
+    const uint64_t y = pack_f32x2(x, x);
+#pragma unroll
+    for (int i = 0; i < kP / 2; ++i) {
+      p[i] = fma_f32x2(a.p[i], y, p[i]);
+      q[i] = fma_f32x2(a.q[i], y, q[i]);
+    }
+  }
+};
+
 // A lane's two pieces of a row, as they lie in memory.
-template <typename E, int kP>
+template <typename E, int kP, bool kInterleaved>
 struct Pieces {
   Packed<E, kP> lo, hi;
   __device__ __forceinline__ void zero() {
@@ -46,38 +106,58 @@ struct Pieces {
     lo.load(p + o1);
     hi.load(p + o2);
   }
-  __device__ __forceinline__ void get(float (&x)[2 * kP]) const {
-    float y[kP];
-    lo.get(y);
-#pragma unroll
-    for (int i = 0; i < kP; ++i) x[i] = y[i];
+  __device__ __forceinline__ void get(Row<kP>& r) const {
+    float x[kP], y[kP];
+    lo.get(x);
     hi.get(y);
 #pragma unroll
-    for (int i = 0; i < kP; ++i) x[kP + i] = y[i];
+    for (int i = 0; i < kP / 2; ++i) {
+      if (kInterleaved) {  // elements p0 q0 p1 q1 ... through both pieces
+        const float* z = 4 * i < kP ? x + 4 * i : y + 4 * i - kP;
+        r.p[i] = pack_f32x2(z[0], z[2]);
+        r.q[i] = pack_f32x2(z[1], z[3]);
+      } else {
+        r.p[i] = pack_f32x2(x[2 * i], x[2 * i + 1]);
+        r.q[i] = pack_f32x2(y[2 * i], y[2 * i + 1]);
+      }
+    }
   }
 };
 
-template <typename E, int kP>
-__device__ __forceinline__ void store_pieces(E* p, int o1, int o2, const float (&x)[2 * kP]) {
-  float y[kP];
+// The floats of a part in the order of its two pieces.
+template <int kP, bool kInterleaved>
+__device__ __forceinline__ void in_order(const Row<kP>& r, float (&x)[kP], float (&y)[kP]) {
+#pragma unroll
+  for (int i = 0; i < kP / 2; ++i) {
+    if (kInterleaved) {
+      float* z = 4 * i < kP ? x + 4 * i : y + 4 * i - kP;
+      unpack_f32x2(r.p[i], z[0], z[2]);
+      unpack_f32x2(r.q[i], z[1], z[3]);
+    } else {
+      unpack_f32x2(r.p[i], x[2 * i], x[2 * i + 1]);
+      unpack_f32x2(r.q[i], y[2 * i], y[2 * i + 1]);
+    }
+  }
+}
+
+template <typename E, int kP, bool kInterleaved>
+__device__ __forceinline__ void store_pieces(E* p, int o1, int o2, const Row<kP>& r) {
+  float x[kP], y[kP];
+  in_order<kP, kInterleaved>(r, x, y);
   Packed<E, kP> w;
-#pragma unroll
-  for (int i = 0; i < kP; ++i) y[i] = x[i];
-  w.set(y);
+  w.set(x);
   w.store(p + o1);
-#pragma unroll
-  for (int i = 0; i < kP; ++i) y[i] = x[kP + i];
   w.set(y);
   w.store(p + o2);
 }
 
 // One lane's place in a row: the offsets of its two pieces and the
-// rotations of its pairs for one token (cosine 1, sine 0 past rot).
+// rotations of its pairs for one token.
 template <int kP>
 struct LanePlace {
   int o1, o2;
   bool live, rotated;
-  float c[kP], s[kP];
+  uint64_t c[kP / 2], s[kP / 2];
 
   __device__ void place(int l, int d, int rot, bool interleaved) {
     live = 2 * kP * l < d;
@@ -90,42 +170,41 @@ struct LanePlace {
       o2 = o1 + kP;
     }
   }
-  __device__ void angles(const NormArgs& a, int l, int64_t token) {
-#pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      c[i] = 1.f;
-      s[i] = 0.f;
-    }
+  // sign -1: rotates back.
+  __device__ void angles(const NormArgs& a, int l, int64_t token, float sign) {
     if (!rotated) return;
+    float cs[kP], sn[kP];
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
       const int64_t pos = a.positions[a.rope.axis[kP * l + i] * a.tokens + token];
       const uint64_t turn = static_cast<uint64_t>(pos) * a.rope.turns[kP * l + i];
       const int32_t frac = static_cast<int32_t>(turn >> 32);  // turns * 2^32, signed
-      sincospif(static_cast<float>(frac) * 0x1p-31f, &s[i], &c[i]);
+      sincospif(static_cast<float>(frac) * 0x1p-31f, &sn[i], &cs[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kP / 2; ++i) {
+      c[i] = pack_f32x2(cs[2 * i], cs[2 * i + 1]);
+      s[i] = pack_f32x2(sign * sn[2 * i], sign * sn[2 * i + 1]);
     }
   }
-  // x[0 .. kP) at o1, x[kP .. 2 kP) at o2; sign -1 rotates back.
-  __device__ void rotate(float (&x)[2 * kP], bool interleaved, float sign) const {
+  __device__ __forceinline__ void rotate(Row<kP>& r) const {
+    const uint64_t minus = pack_f32x2(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      const float si = sign * s[i];
-      float& p = interleaved ? x[2 * i] : x[i];
-      float& q = interleaved ? x[2 * i + 1] : x[i + kP];
-      const float u = p * c[i] - q * si;
-      q = q * c[i] + p * si;
-      p = u;
+    for (int i = 0; i < kP / 2; ++i) {
+      const uint64_t qs = mul_f32x2(r.q[i], s[i]);
+      const uint64_t qc = mul_f32x2(r.q[i], c[i]);
+      const uint64_t p = r.p[i];
+      r.p[i] = fma_f32x2(p, c[i], mul_f32x2(qs, minus));
+      r.q[i] = fma_f32x2(p, s[i], qc);
     }
   }
 };
 
-template <typename E, int kP>
-__device__ __forceinline__ void load_weight(const NormSide& s, const LanePlace<kP>& lp,
-                                            float (&w)[2 * kP]) {
-#pragma unroll
-  for (int i = 0; i < 2 * kP; ++i) w[i] = 1.f;
+template <typename E, int kP, bool kInterleaved>
+__device__ __forceinline__ void load_weight(const NormSide& s, const LanePlace<kP>& lp, Row<kP>& w) {
+  w.fill(1.f);
   if (s.weight && lp.live) {
-    Pieces<E, kP> x;
+    Pieces<E, kP, kInterleaved> x;
     x.load(static_cast<const E*>(s.weight), lp.o1, lp.o2);
     x.get(w);
   }
@@ -135,7 +214,7 @@ __device__ __forceinline__ void load_weight(const NormSide& s, const LanePlace<k
 template <typename E, int kP, int kLanes, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormArgs a,
                                                              int run) {
-  constexpr int kAhead = sizeof(E) * kP >= 32 ? 2 : 4;
+  constexpr int kAhead = (sizeof(E) * kP >= 32 ? 2 : 4);
   const int l = threadIdx.x % kLanes;
   const int64_t token =
       static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
@@ -144,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   LanePlace<kP> lp;
   lp.place(l, a.d, a.has_rope ? a.rope.rot : 0, kInterleaved);
   const bool live = lp.live && here;
+  const float inv_d = 1.f / a.d;
   const int hq = a.side[0].heads;
   const int h_begin = blockIdx.y * run, h_end = min(hq + a.side[1].heads, h_begin + run);
   const E* src[2];
@@ -153,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     src[t] = static_cast<const E*>(a.side[t].x) + b * a.side[t].xs.b + n * a.side[t].xs.n;
     dst[t] = static_cast<E*>(a.side[t].y) + b * a.side[t].ys.b + n * a.side[t].ys.n;
   }
-  Pieces<E, kP> next[kAhead];
+  Pieces<E, kP, kInterleaved> next[kAhead];
   auto fetch = [&](int h0) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -165,11 +245,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     }
   };
   fetch(h_begin);
-  lp.angles(a, l, here ? token : 0);
-  float w[2 * kP];
+  lp.angles(a, l, here ? token : 0, 1.f);
+  Row<kP> w;
   int loaded = -1;
   for (int h0 = h_begin; h0 < h_end; h0 += kAhead) {
-    Pieces<E, kP> now[kAhead];
+    Pieces<E, kP, kInterleaved> now[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) now[j] = next[j];
     if (h0 + kAhead < h_end) fetch(h0 + kAhead);
@@ -178,47 +258,42 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       const int h = h0 + j;
       if (h >= h_end) break;
       const int side = h >= hq;
-      float x[2 * kP];
+      Row<kP> x;
       now[j].get(x);
       if (a.eps >= 0.f) {
         if (side != loaded) {
-          load_weight<E, kP>(a.side[side], lp, w);
+          load_weight<E, kP, kInterleaved>(a.side[side], lp, w);
           loaded = side;
         }
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * kP; ++i) ss = fmaf(x[i], x[i], ss);
-        const float r = rsqrtf(row_sum<kLanes>(ss) / a.d + a.eps);
-#pragma unroll
-        for (int i = 0; i < 2 * kP; ++i) x[i] = x[i] * r * w[i];
+        x.scale(rsqrtf(row_sum<kLanes>(x.dot(x)) * inv_d + a.eps));
+        x.times(w);
       }
-      if (lp.rotated) lp.rotate(x, kInterleaved, 1.f);
+      if (lp.rotated) lp.rotate(x);
       if (live)
-        store_pieces<E, kP>(side ? dst[1] + (h - hq) * a.side[1].ys.h : dst[0] + h * a.side[0].ys.h,
-                            lp.o1, lp.o2, x);
+        store_pieces<E, kP, kInterleaved>(
+            side ? dst[1] + (h - hq) * a.side[1].ys.h : dst[0] + h * a.side[0].ys.h, lp.o1, lp.o2, x);
     }
   }
 }
 
-// A fixed grid walks over (token tile, run of heads) items and keeps dw of
-// one side in registers (a run lies within one side); block sums go to
-// a.partial, one row per block and side.
+// A fixed grid, two blocks per SM, walks over (token tile, run of heads)
+// items of one side and then of the other with dw in registers; block sums go
+// to a.partial, one row per block and side.
 template <typename E, int kP, int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     norm_rope_backward_kernel(const __grid_constant__ NormArgs a, int run, int64_t tiles) {
   constexpr int kGroups = kThreads / kLanes;
-  constexpr int kAhead = sizeof(E) * kP >= 32 ? 1 : 2;
   __shared__ float sums[kGroups][kLanes * 2 * kP + 4];
   const int l = threadIdx.x % kLanes;
   const int group = threadIdx.x / kLanes;
+  const float inv_d = 1.f / a.d;
   LanePlace<kP> lp;
   lp.place(l, a.d, a.has_rope ? a.rope.rot : 0, kInterleaved);
   for (int t = 0; t < 2; ++t) {
     const NormSide& s = a.side[t];
-    float dw[2 * kP], w[2 * kP];
-    load_weight<E, kP>(s, lp, w);
-#pragma unroll
-    for (int i = 0; i < 2 * kP; ++i) dw[i] = 0.f;
+    Row<kP> dw, w;
+    load_weight<E, kP, kInterleaved>(s, lp, w);
+    dw.fill(0.f);
     const int runs = (s.heads + run - 1) / run;
     for (int64_t item = blockIdx.x; item < tiles * runs; item += gridDim.x) {
       const int64_t token = (item / runs) * kGroups + group;
@@ -230,63 +305,45 @@ __global__ void __launch_bounds__(kThreads)
       const E* src = static_cast<const E*>(s.x) + b * s.xs.b + n * s.xs.n;
       const E* dy = static_cast<const E*>(s.dy) + (b * s.heads * a.N + n) * a.d;
       E* dst = static_cast<E*>(s.y) + b * s.ys.b + n * s.ys.n;
-      Pieces<E, kP> next_x[kAhead], next_g[kAhead];
-      auto fetch = [&](int h0) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int h = h0 + j;
-          next_x[j].zero();
-          next_g[j].zero();
-          if (h < h_end && live) {
-            next_g[j].load(dy + static_cast<int64_t>(h) * a.N * a.d, lp.o1, lp.o2);
-            if (a.eps >= 0.f) next_x[j].load(src + h * s.xs.h, lp.o1, lp.o2);
-          }
+      Pieces<E, kP, kInterleaved> next_x, next_g;
+      auto fetch = [&](int h) {
+        next_x.zero();
+        next_g.zero();
+        if (live) {
+          next_g.load(dy + static_cast<int64_t>(h) * a.N * a.d, lp.o1, lp.o2);
+          if (a.eps >= 0.f) next_x.load(src + h * s.xs.h, lp.o1, lp.o2);
         }
       };
       fetch(h_begin);
-      lp.angles(a, l, here ? token : 0);
-      for (int h0 = h_begin; h0 < h_end; h0 += kAhead) {
-        Pieces<E, kP> now_x[kAhead], now_g[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          now_x[j] = next_x[j];
-          now_g[j] = next_g[j];
+      lp.angles(a, l, here ? token : 0, -1.f);
+      for (int h = h_begin; h < h_end; ++h) {
+        Row<kP> g, x;
+        next_g.get(g);
+        next_x.get(x);
+        if (h + 1 < h_end) fetch(h + 1);
+        if (lp.rotated) lp.rotate(g);
+        if (a.eps >= 0.f) {
+          const float r = rsqrtf(row_sum<kLanes>(x.dot(x)) * inv_d + a.eps);
+          x.scale(r);  // the normalised row
+          dw.add_product(g, x);
+          g.times(w);
+          const float mean = row_sum<kLanes>(g.dot(x)) * inv_d;
+          g.add_scaled(x, -mean);
+          g.scale(r);
         }
-        if (h0 + kAhead < h_end) fetch(h0 + kAhead);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int h = h0 + j;
-          if (h >= h_end) break;
-          float g[2 * kP];
-          now_g[j].get(g);
-          if (lp.rotated) lp.rotate(g, kInterleaved, -1.f);
-          if (a.eps >= 0.f) {
-            float x[2 * kP];
-            now_x[j].get(x);
-            float ss = 0.f, dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < 2 * kP; ++i) ss = fmaf(x[i], x[i], ss);
-            const float r = rsqrtf(row_sum<kLanes>(ss) / a.d + a.eps);
-#pragma unroll
-            for (int i = 0; i < 2 * kP; ++i) {
-              x[i] *= r;  // the normalised row
-              dw[i] = fmaf(g[i], x[i], dw[i]);
-              g[i] *= w[i];
-              dot = fmaf(g[i], x[i], dot);
-            }
-            const float mean = row_sum<kLanes>(dot) / a.d;
-#pragma unroll
-            for (int i = 0; i < 2 * kP; ++i) g[i] = r * (g[i] - x[i] * mean);
-          }
-          if (live) store_pieces<E, kP>(dst + h * s.ys.h, lp.o1, lp.o2, g);
-        }
+        if (live) store_pieces<E, kP, kInterleaved>(dst + h * s.ys.h, lp.o1, lp.o2, g);
       }
     }
     if (!a.partial) continue;
     __syncthreads();
     if (lp.live) {
+      float x[kP], y[kP];
+      in_order<kP, kInterleaved>(dw, x, y);
 #pragma unroll
-      for (int i = 0; i < 2 * kP; ++i) sums[group][i < kP ? lp.o1 + i : lp.o2 + i - kP] = dw[i];
+      for (int i = 0; i < kP; ++i) {
+        sums[group][lp.o1 + i] = x[i];
+        sums[group][lp.o2 + i] = y[i];
+      }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.d; e += kThreads) {

@@ -38,7 +38,7 @@ struct NormArgs {
 };
 
 // Blocks of the backward, and so the rows of its partial sums.
-constexpr int kNormBackwardBlocks = 456;  // three per SM
+constexpr int kNormBackwardBlocks = 304;  // two per SM
 
 cudaError_t launch_norm_rope(const NormArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_norm_rope_backward(const NormArgs& a, bool bf16, cudaStream_t s);
