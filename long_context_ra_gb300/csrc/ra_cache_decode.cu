@@ -4,11 +4,13 @@
 //
 // Bound by the bytes of the cache: with 16 rows a byte of K or V feeds 16 to
 // 32 multiply-adds.  So the kernel is built around the loads.  A CTA is 4
-// warps, each on keys of its own (16 of every tile of 64) with a state of its
+// warps, each on keys of its own (32 of every tile of 128) with a state of its
 // own, joined at the end of a unit: nothing but the loads is waited for in
-// between.  Each warp brings its 16-key chunks with cp.async through a ring
-// of kStages chunks in shared memory; the page numbers of the next 32 chunks
-// are held by the 32 lanes, one coalesced load ahead.
+// between.  Each warp brings its chunks of 32 keys, K and V in turn, with
+// cp.async through a ring of kStages places in shared memory; the page numbers
+// of the next chunks are held by the 32 lanes, one coalesced load ahead.  32
+// keys make four score products and two value products independent of one
+// another, which two warps per scheduler need to hide the latency of each.
 //
 // The products are m16n8k16 mma with the 16 query rows as M, which leaves
 // the order of the contracted index free: a lane takes 16 contiguous bytes of
@@ -39,7 +41,7 @@ using namespace ptx;
 
 constexpr int kRows = 16;
 constexpr int kWarps = 4;
-constexpr int kChunk = 16;
+constexpr int kChunk = 32;
 constexpr int kTile = kWarps * kChunk;
 constexpr int kThreads = kWarps * 32;
 constexpr float kSlack = 8.f;      // log2: how far a score may pass the reference
@@ -50,14 +52,14 @@ struct Shape {
   static constexpr int kRowBytes = k8 ? D : 2 * D;
   static constexpr int kPieces = kRowBytes / 16;
   static constexpr int kSide = kChunk * kRowBytes;          // K or V of a chunk
-  static constexpr int kStage = 2 * kSide + (k8 ? 32 : 0);  // + exponent bytes of K, V
-  static constexpr int kStages = kStage > 4096 + 32 ? 3 : 6;  // two CTAs fit an SM
+  static constexpr int kStage = kSide + (k8 ? kChunk : 0);  // + its exponent bytes
+  static constexpr int kStages = kSide > 4096 ? 3 : 6;      // two CTAs fit an SM
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kLd = D + 4;                          // row pitch of the joined states
   static constexpr int kJoin = kWarps * kRows * (kLd + 2) * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
   static constexpr int kTilesN = D / 8;
-  // Byte offset of 16-byte piece c of row r: K is read as (two neighbouring
+  // Byte offset of 16-byte piece c of row r.  K is read as (two neighbouring
   // rows, four pieces), V as (four rows 2 apart, two pieces) per phase.
   __device__ static int at_k(int r, int c) {
     if (kPieces == 4) return (r >> 1) * 128 + ((((r & 1) << 2) + c) ^ (((r >> 1) & 3) << 1)) * 16;
@@ -156,8 +158,11 @@ __device__ __forceinline__ void each_value_tile(const uint32_t (&w)[4][kWords], 
         const uint32_t sel = z ? 0x7362u : 0x5140u;  // bytes (key 0, key 1) of two elements
         const uint32_t x = __byte_perm(w[0][q], w[1][q], sel);
         const uint32_t y = __byte_perm(w[2][q], w[3][q], sel);
-        f(4 * q + 2 * z, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-        f(4 * q + 2 * z + 1, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+        uint32_t x0, x1, y0, y1;
+        e4m3x4_to_f16x4(x, x0, x1);
+        e4m3x4_to_f16x4(y, y0, y1);
+        f(4 * q + 2 * z, x0, y0);
+        f(4 * q + 2 * z + 1, x1, y1);
       }
     } else {
 #pragma unroll
@@ -192,62 +197,90 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n = static_cast<int>(u.last - u.first);  // chunks of this warp
     const int64_t key0 = u.first * kTile + warp * kChunk;
 
-    // ---- page numbers: lane i holds those of chunk base + i (its two halves)
-    int pg0 = -1, pg1 = -1, nx0 = -1, nx1 = -1;
-    auto pages = [&](int base, int& lo, int& hi) {
-      lo = hi = -1;
-      const int64_t pos = key0 + static_cast<int64_t>(base + lane) * kTile;
-      if (base + lane >= n) return;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t at = pos + 8 * h;
-        if (at >= keys) break;
-        const int64_t col = at >> c.page_shift;
-        int page = col < c.width ? c.table[static_cast<int64_t>(u.b) * c.width + col] : -1;
-        if (page < 0 || page >= c.pages) {
-          page = -1;
-          flag_page(c.status);
-        }
-        (h ? hi : lo) = page;
-      }
+    // ---- page numbers.  A chunk lies in `per` pages (granules of min(page,
+    // 32) rows); lane i holds granule base * per + i.
+    const int gshift = min(c.page_shift, 5), per = kChunk >> gshift;
+    int pg = -1, nx = -1;
+    auto pages = [&](int base) {
+      const int chunk = base + lane / per;
+      const int64_t at = key0 + static_cast<int64_t>(chunk) * kTile + ((lane % per) << gshift);
+      if (chunk >= n || at >= keys) return -1;
+      const int64_t col = at >> c.page_shift;
+      const int page = col < c.width ? c.table[static_cast<int64_t>(u.b) * c.width + col] : -1;
+      if (page >= 0 && page < c.pages) return page;
+      flag_page(c.status);
+      return -1;
     };
-    uint32_t left_out = 0;  // bits 2 stage, 2 stage + 1: a half whose page is not in the cache
-    auto issue = [&](int i) {
+    const int batch = 32 / per;  // chunks whose pages the lanes hold
+    uint32_t left_out = 0;       // of the chunk loaded last: a bit per 8 rows not in the cache
+    uint32_t left_ring = 0;      // the same of the chunks under way, 4 bits each, newest lowest
+    const int64_t in_page = (int64_t{1} << c.page_shift) - 1;
+    auto issue = [&](int m) {  // item m: K (even) or V (odd) of chunk m / 2
+      const int i = m >> 1;
+      const bool v = m & 1;
+      if (!v && i > 0 && i % batch == 0) {
+        pg = nx;
+        nx = pages(i + batch);
+      }
       const int64_t pos = key0 + static_cast<int64_t>(i) * kTile;
-      const int lo = __shfl_sync(0xffffffffu, pg0, i % 32), hi = __shfl_sync(0xffffffffu, pg1, i % 32);
-      const uint32_t dst = ring + (i % S::kStages) * S::kStage;
-      left_out = (left_out & ~(3u << (2 * (i % S::kStages)))) |
-                 (((lo < 0 ? 1u : 0u) | (hi < 0 ? 2u : 0u)) << (2 * (i % S::kStages)));
-      const int64_t mask = (int64_t{1} << c.page_shift) - 1;
-      // cache rows of the chunk's two 8-key halves
-      const int64_t row_lo = ((static_cast<int64_t>(lo) * c.heads + head) << c.page_shift) + (pos & mask);
-      const int64_t row_hi =
-          ((static_cast<int64_t>(hi) * c.heads + head) << c.page_shift) + ((pos + 8) & mask);
+      const uint32_t dst = ring + (m % S::kStages) * S::kStage;
+      const uint8_t* src = static_cast<const uint8_t*>(v ? c.v : c.k);
+      const uint8_t* exps = v ? c.ve : c.ke;
+      const int first = (i % batch) * per;
+      const int page0 = __shfl_sync(0xffffffffu, pg, first);
+      if (per == 1 && page0 >= 0 && pos + kChunk <= keys) {
+        // the chunk is 32 rows of one page
+        const int64_t row = ((static_cast<int64_t>(page0) * c.heads + head) << c.page_shift) + (pos & in_page);
+        const uint8_t* p0 = src + row * S::kRowBytes + lane * 16;
 #pragma unroll
-      for (int x = 0; x < kChunk * S::kPieces / 32; ++x) {
-        const int piece = x * 32 + lane, r = piece / S::kPieces, pc = piece % S::kPieces;
-        const bool real = pos + r < keys && (r < 8 ? lo : hi) >= 0;
-        const int64_t off = ((r < 8 ? row_lo : row_hi) + (r & 7)) * S::kRowBytes + pc * 16;
-        cp_async16(dst + S::at_k(r, pc), real ? static_cast<const uint8_t*>(c.k) + off : a.q, real);
-        cp_async16(dst + S::kSide + S::at_v(r, pc),
-                   real ? static_cast<const uint8_t*>(c.v) + off : a.q, real);
+        for (int x = 0; x < S::kSide / 512; ++x) {
+          const int piece = x * 32 + lane, r = piece / S::kPieces, pc = piece % S::kPieces;
+          cp_async16(dst + (v ? S::at_v(r, pc) : S::at_k(r, pc)), p0 + x * 512, true);
+        }
+        if (k8 && lane < 4) cp_async8(dst + S::kSide + lane * 8, exps + row + lane * 8, true);
+        if (!v) left_out = 0;
+      } else {
+        uint32_t out = 0;
+#pragma unroll 1
+        for (int x = 0; x < S::kSide / 512; ++x) {
+          const int piece = x * 32 + lane, r = piece / S::kPieces, pc = piece % S::kPieces;
+          const int page = __shfl_sync(0xffffffffu, pg, first + (r >> gshift));
+          const bool real = pos + r < keys && page >= 0;
+          const int64_t row =
+              ((static_cast<int64_t>(page) * c.heads + head) << c.page_shift) + ((pos + r) & in_page);
+          cp_async16(dst + (v ? S::at_v(r, pc) : S::at_k(r, pc)),
+                     real ? src + row * S::kRowBytes + pc * 16 : a.q, real);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {  // rows 8 x .. 8 x + 7
+          const int page = __shfl_sync(0xffffffffu, pg, first + ((8 * x) >> gshift));
+          const bool real = pos + 8 * x < keys && page >= 0;
+          if (page < 0) out |= 1u << x;
+          const int64_t row =
+              ((static_cast<int64_t>(page) * c.heads + head) << c.page_shift) + ((pos + 8 * x) & in_page);
+          if (k8 && lane == x)
+            cp_async8(dst + S::kSide + x * 8, real ? static_cast<const void*>(exps + row) : a.q, real);
+        }
+        if (!v) left_out = out;
       }
-      if (k8 && lane < 4) {
-        const bool upper = lane & 1;
-        const bool real = pos + 8 * upper < keys && (upper ? hi : lo) >= 0;
-        const int64_t row = upper ? row_hi : row_lo;
-        const uint8_t* src = lane < 2 ? c.ke : c.ve;
-        cp_async8(dst + 2 * S::kSide + lane * 8, real ? static_cast<const void*>(src + row) : a.q, real);
-      }
+      if (!v) left_ring = (left_ring << 4) | left_out;
     };
 
-    pages(0, pg0, pg1);
-    pages(32, nx0, nx1);
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-      if (i < n) issue(i);
+    pg = pages(0);
+    nx = pages(batch);
+#pragma unroll 1
+    for (int m = 0; m < S::kStages - 1; ++m) {
+      if (m < 2 * n) issue(m);
       cp_commit();
     }
+    // waits for item m and brings the item kStages - 1 behind it
+    auto arrive = [&](int m) {
+      cp_wait<S::kStages - 2>();
+      __syncwarp();
+      if (m + S::kStages - 1 < 2 * n) issue(m + S::kStages - 1);
+      cp_commit();
+      return ring + (m % S::kStages) * S::kStage;
+    };
 
     // ---- queries as A fragments, in the order in which K rows are read
     uint32_t qf[D / 16][4];
@@ -302,64 +335,67 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int z = 0; z < 4; ++z) o[nn][z] = 0.f;
 
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      cp_wait<S::kStages - 2>();
-      __syncwarp();
-      {
-        const int j = i + S::kStages - 1;
-        if (j % 32 == 0) {
-          pg0 = nx0;
-          pg1 = nx1;
-          pages(j + 32, nx0, nx1);
-        }
-        if (j < n) issue(j);
-        cp_commit();
-      }
-      const uint32_t kb = ring + (i % S::kStages) * S::kStage, vb = kb + S::kSide;
+      const uint32_t kb = arrive(2 * i);
       const int64_t pos = key0 + static_cast<int64_t>(i) * kTile;
+      // chunks loaded but not worked on yet, this one the oldest: its bits
+      const int newest = min((2 * i + S::kStages - 1) >> 1, n - 1);
+      const uint32_t out = (left_ring >> (4 * (newest - i))) & 15u;
 
-      // ---- scores of 16 keys (two n-tiles)
-      float s[2][4];
+      // ---- scores of 32 keys (four n-tiles)
+      float s[4][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int z = 0; z < 4; ++z) s[j][z] = 0.f;
 #pragma unroll
-        for (int x = 0; x < S::kPieces / 4; ++x) {
-          const uint4 w4 = lds128(kb + S::at_k(8 * j + g, t + 4 * x));
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          if (k8) {
+      for (int x = 0; x < S::kPieces / 4; ++x) {
+        uint4 w4[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              mma16816<k8>(s[j], qf[4 * x + z], e4m3x2_to_f16x2(w[z]), e4m3x2_to_f16x2(w[z] >> 16));
-          } else {
-            mma16816<k8>(s[j], qf[2 * x], w[0], w[1]);
-            mma16816<k8>(s[j], qf[2 * x + 1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j) w4[j] = lds128(kb + S::at_k(8 * j + g, t + 4 * x));
+#pragma unroll
+        for (int z = 0; z < (k8 ? 4 : 2); ++z) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w[4] = {w4[j].x, w4[j].y, w4[j].z, w4[j].w};
+            if (k8) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16x4(w[z], b0, b1);
+              mma16816<k8>(s[j], qf[4 * x + z], b0, b1);
+            } else {
+              mma16816<k8>(s[j], qf[2 * x + z], w[2 * z], w[2 * z + 1]);
+            }
           }
         }
       }
-      float ev[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // log2 of the V scales of this lane's columns
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 4; ++j) {
         float ks[2] = {1.f, 1.f};
         if (k8) {
-          const uint32_t ek = lds16(kb + 2 * S::kSide + 8 * j + 2 * t);
-          const uint32_t e2 = lds16(kb + 2 * S::kSide + 16 + 8 * j + 2 * t);
+          const uint32_t ek = lds16(kb + S::kSide + 8 * j + 2 * t);
           ks[0] = exp_scale(ek & 255u);
           ks[1] = exp_scale(ek >> 8);
-          ev[j][0] = static_cast<float>(static_cast<int>(e2 & 255u) - 127);
-          ev[j][1] = static_cast<float>(static_cast<int>(e2 >> 8) - 127);
         }
 #pragma unroll
         for (int z = 0; z < 4; ++z) s[j][z] *= k8 ? scale[z / 2] * ks[z % 2] : scale[z / 2];
       }
+      const uint32_t vb = arrive(2 * i + 1);
+      float ev[4][2];  // log2 of the V scales of this lane's columns
+      if (k8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t e2 = lds16(vb + S::kSide + 8 * j + 2 * t);
+          ev[j][0] = static_cast<float>(static_cast<int>(e2 & 255u) - 127);
+          ev[j][1] = static_cast<float>(static_cast<int>(e2 >> 8) - 127);
+        }
+      }
       // every row sees every key, but for drafts, the end, and pages left out
-      const uint32_t out = (left_out >> (2 * (i % S::kStages))) & 3u;
       const bool all_seen = pos + kChunk <= u.seq.len && out == 0;
-      uint32_t seen = 0xffu;  // bit 4 j + z: of score s[j][z]
+      uint32_t seen = 0xffffu;  // bit 4 j + z: of score s[j][z]
       if (!all_seen) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
+        for (int x = 0; x < 16; ++x) {
           const int j = x / 4, z = x % 4;
           if (((out >> j) & 1u) || !sees(a, u.seq, u.b, tq[z / 2], pos + 8 * j + 2 * t + z % 2)) {
             seen &= ~(1u << x);
@@ -370,27 +406,23 @@ __global__ void __launch_bounds__(kThreads, 2)
 
       // ---- reference, probabilities, sums
       bool pass = false;
+      float xm[2], ym[2];  // this lane's largest s, and s + ev
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        xm[h] = -INFINITY;
+        ym[h] = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            pass = pass || s[j][2 * h + z] > m[h] + kSlack;
-            if (k8) pass = pass || s[j][2 * h + z] + ev[j][z] > mo[h] + kSlack;
-          }
+        for (int j = 0; j < 4; ++j) {
+          xm[h] = fmax3(xm[h], s[j][2 * h], s[j][2 * h + 1]);
+          if (k8) ym[h] = fmax3(ym[h], s[j][2 * h] + ev[j][0], s[j][2 * h + 1] + ev[j][1]);
+        }
+        pass = pass || xm[h] > m[h] + kSlack;
+        if (k8) pass = pass || ym[h] > mo[h] + kSlack;
       }
       if (__any_sync(0xffffffffu, pass)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float x = m[h], y = mo[h];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              x = fmaxf(x, s[j][2 * h + z]);
-              if (k8) y = fmaxf(y, s[j][2 * h + z] + ev[j][z]);
-            }
+          float x = fmaxf(m[h], xm[h]), y = fmaxf(mo[h], ym[h]);
 #pragma unroll
           for (int w = 1; w < 4; w <<= 1) {
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
@@ -408,73 +440,79 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      uint32_t pf[4];
+      uint32_t pf[2][4];  // A fragments of the two halves of the chunk
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float ref = m[h] == -INFINITY ? 0.f : m[h];
         const float refo = mo[h] == -INFINITY ? 0.f : mo[h] - kF16Offset;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float p0 = ex2(s[j][2 * h] - ref), p1 = ex2(s[j][2 * h + 1] - ref);
           l[h] += p0 + p1;
-          pf[2 * j + h] = k8 ? pack_p<k8>(ex2(s[j][2 * h] + ev[j][0] - refo),
-                                          ex2(s[j][2 * h + 1] + ev[j][1] - refo))
-                             : pack_p<k8>(p0, p1);
+          pf[j / 2][2 * (j % 2) + h] = k8 ? pack_p<k8>(ex2(s[j][2 * h] + ev[j][0] - refo),
+                                                       ex2(s[j][2 * h + 1] + ev[j][1] - refo))
+                                          : pack_p<k8>(p0, p1);
         }
       }
 
       // ---- values: this lane's columns of keys 2t, 2t + 1, 8 + 2t, 9 + 2t
-      constexpr int kWords = (S::kRowBytes / 8) / 4;  // of one key row per lane
-      uint32_t w[4][kWords];
+      // of each half; kWords 32-bit words of a key row at a time
+      constexpr int kWords = D == 64 && k8 ? 2 : 4;
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        const int r = 8 * (z / 2) + 2 * t + (z & 1);
-        if (kWords == 2) {
-          const uint2 x = lds64(vb + S::at_v(r, g / 2) + 8 * (g & 1));
-          w[z][0] = x.x;
-          w[z][1] = x.y;
-        } else {
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int x = 0; x < kWords / 4; ++x) {
-            const uint4 y = lds128(vb + S::at_v(r, g + 8 * x));
-            w[z][4 * x] = y.x;
-            w[z][4 * x + 1] = y.y;
-            w[z][4 * x + 2] = y.z;
-            w[z][4 * x + 3] = y.w;
+        for (int part = 0; part < S::kRowBytes / 32 / kWords; ++part) {
+          uint32_t w[4][kWords];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int r = 16 * half + 8 * (z / 2) + 2 * t + (z & 1);
+            if (kWords == 2) {
+              const uint2 x = lds64(vb + S::at_v(r, g / 2) + 8 * (g & 1));
+              w[z][0] = x.x;
+              w[z][1] = x.y;
+            } else {
+              const uint4 y = lds128(vb + S::at_v(r, g + 8 * part));
+              w[z][0] = y.x;
+              w[z][1] = y.y;
+              w[z][kWords - 2] = y.z;
+              w[z][kWords - 1] = y.w;
+            }
+          }
+          bool poison = false;
+          if (!all_seen) {
+            each_value_tile<k8, kWords>(w, [&](int, uint32_t b0, uint32_t b1) {
+              poison = poison || not_finite<k8>(b0) || not_finite<k8>(b1);
+            });
+            poison = __any_sync(0xffffffffu, poison);
+          }
+          if (!poison) {
+            each_value_tile<k8, kWords>(w, [&](int nn, uint32_t b0, uint32_t b1) {
+              mma16816<k8>(o[8 * part + nn], pf[half], b0, b1);
+            });
+          } else {
+            // Values that are not finite reach the rows that see their key and
+            // no others: they are left out of the product, and a second product
+            // counts, per row and column, those the row sees.
+            constexpr uint32_t one = k8 ? 0x3c003c00u : 0x3f803f80u;
+            uint32_t sf[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t two = seen >> (4 * (2 * half + j) + 2 * h);
+                sf[2 * j + h] = one & ((two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u));
+              }
+            each_value_tile<k8, kWords>(w, [&](int nn, uint32_t b0, uint32_t b1) {
+              const uint32_t n0 = not_finite<k8>(b0), n1 = not_finite<k8>(b1);
+              float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<k8>(cnt, sf, one & n0, one & n1);
+              mma16816<k8>(o[8 * part + nn], pf[half], b0 & ~n0, b1 & ~n1);
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                if (cnt[z] > 0.f) o[8 * part + nn][z] = NAN;
+            });
           }
         }
-      }
-      bool poison = false;
-      if (!all_seen) {
-        each_value_tile<k8, kWords>(w, [&](int, uint32_t b0, uint32_t b1) {
-          poison = poison || not_finite<k8>(b0) || not_finite<k8>(b1);
-        });
-        poison = __any_sync(0xffffffffu, poison);
-      }
-      if (!poison) {
-        each_value_tile<k8, kWords>(
-            w, [&](int nn, uint32_t b0, uint32_t b1) { mma16816<k8>(o[nn], pf, b0, b1); });
-      } else {
-        // Values that are not finite reach the rows that see their key and no
-        // others: they are left out of the product, and a second product
-        // counts, per row and column, those the row sees.
-        constexpr uint32_t one = k8 ? 0x3c003c00u : 0x3f803f80u;
-        uint32_t sf[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            sf[2 * j + h] = one & (((seen >> (4 * j + 2 * h)) & 1u ? 0xffffu : 0u) |
-                                   ((seen >> (4 * j + 2 * h)) & 2u ? 0xffff0000u : 0u));
-        each_value_tile<k8, kWords>(w, [&](int nn, uint32_t b0, uint32_t b1) {
-          const uint32_t n0 = not_finite<k8>(b0), n1 = not_finite<k8>(b1);
-          float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816<k8>(cnt, sf, one & n0, one & n1);
-          mma16816<k8>(o[nn], pf, b0 & ~n0, b1 & ~n1);
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            if (cnt[z] > 0.f) o[nn][z] = NAN;
-        });
       }
     }
 

@@ -63,18 +63,23 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(const float* x) {
   return lo | (hi << 16);
 }
 
-// Two e4m3 bytes as two f16 (exact: every e4m3 value is an f16).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// The four e4m3 bytes of w as two pairs of f16 (exact: every e4m3 value is an
+// f16).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float* x) {
+  uint32_t h[2];
+  e4m3x4_to_f16x4(w, h[0], h[1]);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t h = e4m3x2_to_f16x2(w >> (16 * i));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     x[2 * i] = f.x;
     x[2 * i + 1] = f.y;
   }
