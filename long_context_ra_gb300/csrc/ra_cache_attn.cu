@@ -7,7 +7,10 @@
 // for P V, so the online softmax of a row stays inside its warp:
 //   m' = max(m, max s),  l' = l e^(m-m') + sum p,  o' = o e^(m-m') + p V
 // A key that a row does not see has p = 0 and is left out of the sum rather
-// than multiplied, so what it holds does not matter.
+// than multiplied, so what it holds does not matter.  Four CTAs share an SM and
+// hide one another's loads; a CTA takes single tiles while there are few, since
+// a tile's chain of look-up, load, scores and sum is what a short call waits
+// for.
 
 #include "ra_cache_attn.cuh"
 
@@ -25,7 +28,6 @@ __device__ __forceinline__ float to_float(E x) {
   return static_cast<float>(x);
 }
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
@@ -35,14 +37,14 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
 }
 
 template <typename E, typename H>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     cache_attn_ffma_kernel(const __grid_constant__ CacheAttnArgs a,
                            const __grid_constant__ AttnPlan p) {
   constexpr bool k8 = sizeof(H) == 1;
   extern __shared__ float4 smem4[];
   __shared__ DivisionShared sh;
   __shared__ int64_t key_row[kTile];
-  __shared__ float probs[kRows][kTile];
+  __shared__ float4 probs[4][kTile];  // of a warp's 4 rows, per key
   const PagedArgs& c = a.c;
   const int d = c.d, ld = d + 4;
   float* qs = reinterpret_cast<float*>(smem4);  // [kRows][d]
@@ -51,6 +53,7 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t rows = head_rows(a);
 
+  allow_join();
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   UnitWalk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
@@ -84,25 +87,48 @@ __global__ void __launch_bounds__(kThreads)
         key_row[threadIdx.x] = row < 0 ? -1 : row + (static_cast<int64_t>(head) << c.page_shift);
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < kTile * d / 8; i += kThreads) {
-        const int key = i / (d / 8), e = (i % (d / 8)) * 8;
-        const int64_t row = key_row[key];
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (row >= 0) {
-          load8(static_cast<const H*>(c.k) + row * d + e, x);
-          load8(static_cast<const H*>(c.v) + row * d + e, y);
-          if (k8) {
-            const float sk = exp_scale(c.ke[row]), sv = exp_scale(c.ve[row]);
+      for (int i0 = threadIdx.x; i0 < kTile * d / 8; i0 += 4 * kThreads) {
+        // four pieces of 8 elements of K and of V are on their way together
+        Packed<H, 8> x[4], y[4];
+        uint32_t ek[4], ev[4];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              x[z] *= sk;
-              y[z] *= sv;
+        for (int z = 0; z < 4; ++z) {
+          const int i = i0 + z * kThreads;
+          const int key = i / (d / 8), e = (i % (d / 8)) * 8;
+          const int64_t row = i < kTile * d / 8 ? key_row[key] : -1;
+          x[z].zero();
+          y[z].zero();
+          ek[z] = ev[z] = 127;
+          if (row >= 0) {
+            x[z].load(static_cast<const H*>(c.k) + row * d + e);
+            y[z].load(static_cast<const H*>(c.v) + row * d + e);
+            if (k8) {
+              ek[z] = c.ke[row];
+              ev[z] = c.ve[row];
             }
           }
         }
-        store8(ks + key * ld + e, x);
-        store8(vs + key * d + e, y);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int i = i0 + z * kThreads;
+          if (i >= kTile * d / 8) break;
+          const int key = i / (d / 8), e = (i % (d / 8)) * 8;
+          float f[8];
+          x[z].get(f);
+          if (k8) {
+            const float sk = exp_scale(ek[z]);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) f[w] *= sk;
+          }
+          store8(ks + key * ld + e, f);
+          y[z].get(f);
+          if (k8) {
+            const float sv = exp_scale(ev[z]);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) f[w] *= sv;
+          }
+          store8(vs + key * d + e, f);
+        }
       }
       __syncthreads();
       // scores of key `lane` for the warp's rows
@@ -116,6 +142,7 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
       const bool here = key_row[lane] >= 0;
+      float pr4[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const bool seen = here && sees(a, u.seq, u.b, t[r], pos0 + lane);
@@ -132,23 +159,25 @@ __global__ void __launch_bounds__(kThreads)
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         l[r] = l[r] * alpha + sum;
         m[r] = mx;
-        probs[4 * warp + r][lane] = pr;
+        pr4[r] = pr;
 #pragma unroll
         for (int x = 0; x < kColumns; ++x) o[r][x] *= alpha;
       }
+      probs[warp][lane] = make_float4(pr4[0], pr4[1], pr4[2], pr4[3]);
       __syncwarp();
-      for (int key = 0; key < kTile; ++key) {
-        float pr[4];
+      if (r0 + 4 * warp < rows) {
+#pragma unroll 4
+        for (int key = 0; key < kTile; ++key) {
+          const float4 pr = probs[warp][key];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) pr[r] = probs[4 * warp + r][key];
-#pragma unroll
-        for (int x = 0; x < kColumns; ++x) {
-          const int col = lane + 32 * x;
-          if (col < d) {
-            const float vv = vs[key * d + col];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (pr[r] != 0.f) o[r][x] = fmaf(pr[r], vv, o[r][x]);
+          for (int x = 0; x < kColumns; ++x) {
+            if (32 * x >= d) break;
+            const int col = lane + 32 * x;
+            const float vv = vs[key * d + (col < d ? col : 0)];
+            o[0][x] = fmaf(pr.x, pr.x != 0.f ? vv : 0.f, o[0][x]);
+            o[1][x] = fmaf(pr.y, pr.y != 0.f ? vv : 0.f, o[1][x]);
+            o[2][x] = fmaf(pr.z, pr.z != 0.f ? vv : 0.f, o[2][x]);
+            o[3][x] = fmaf(pr.w, pr.w != 0.f ? vv : 0.f, o[3][x]);
           }
         }
       }
@@ -232,6 +261,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       c1 = static_cast<int>((u0 + tiles - 1) / per);
     }
     const bool shared = c1 > c0;
+    wait_for_parts();
     float ms = -INFINITY, l = 0.f;
     float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     if (shared) {
@@ -311,7 +341,7 @@ AttnPlan ffma_plan(const CacheAttnArgs& a) {
   p.div.units = a.c.heads * p.row_tiles;
   p.div.tile = kTile;
   p.div.ctas = kFfmaCtas;
-  p.div.min_run = 4;
+  p.div.min_run = 1;
   return p;
 }
 
@@ -321,8 +351,16 @@ cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   constexpr int kRowsPerBlock = kJoinWarps / kSplit;
   const dim3 grid(static_cast<unsigned>((seq_rows + kRowsPerBlock - 1) / kRowsPerBlock),
                   static_cast<unsigned>(a.c.B < 65535 ? a.c.B : 65535));
-  cache_attn_join_kernel<E, kSplit><<<grid, kJoinWarps * 32, 0, s>>>(a, p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<E, kSplit>, a, p);
 }
 
 template <typename E, typename H>

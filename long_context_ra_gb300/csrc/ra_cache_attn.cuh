@@ -32,6 +32,12 @@ __device__ __forceinline__ float* slot_o(const CacheAttnArgs& a, const AttnPlan&
          static_cast<int64_t>(slot) * p.rows * a.c.d;
 }
 
+// The join is launched while the kernel that writes the parts still runs
+// (programmatic dependent launch): the kernel allows it at its start, the join
+// works out where its rows lie and then waits for the kernel's end.
+__device__ __forceinline__ void allow_join() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Whether query t sees the key at position pos of its sequence.
 __device__ __forceinline__ bool sees(const CacheAttnArgs& a, const SeqInfo& s, int b, int t,
                                      int64_t pos) {

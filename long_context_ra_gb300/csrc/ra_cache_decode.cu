@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStage);
   const int64_t rows = head_rows(a);
 
+  allow_join();
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   UnitWalk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {

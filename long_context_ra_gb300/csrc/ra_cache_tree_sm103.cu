@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t rows = head_rows(a);
 
   // ---- set-up
+  allow_join();
   if (threadIdx.x == 0) {
     mbar_init(bars.q_full(), k8 ? 192 : 96);
     mbar_init(bars.q_empty(), 1);

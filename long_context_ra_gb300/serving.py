@@ -19,34 +19,57 @@ from ._native import RA_BF16, RA_E4M3, RA_F32, RaCacheC, RaRopeC
 _CACHE_TYPES = {torch.float32: RA_F32, torch.bfloat16: RA_BF16, torch.float8_e4m3fn: RA_E4M3}
 
 
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else \
+    torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(t: torch.Tensor) -> int:
+    """The current device, which has to be the tensor's."""
+    index = t.get_device()
+    if index < 0 or index != _device():
+        raise ValueError("tensors must be on the current CUDA device")
+    return index
+
+
+def _on_stream(stream, index: int) -> int:
+    """The handle of the given stream, or of the device's current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(index)
+    return _stream(stream)
+
+
 def _dev(t: torch.Tensor, index: int, dtype=None, shape=None, what: str = "tensor") -> int:
     """The address of a contiguous tensor on the current device."""
-    if not t.is_cuda or t.device.index != index:
+    if t.get_device() != index:
         raise ValueError(f"{what} must be on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, index: int, dtype, shape, what: str):
     """Address and batch, head, token strides of a [B, H, N, d] tensor (None:
     dense)."""
-    if not t.is_cuda or t.device.index != index:
+    if t.get_device() != index:
         raise ValueError(f"{what} must be on the current CUDA device")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return t.data_ptr(), None
     st = t.stride()
     if st[3] != 1:
         raise ValueError(f"the last dimension of {what} must be contiguous")
-    return t.data_ptr(), (ctypes.c_int64 * 3)(st[0], st[1], st[2])
+    return t.data_ptr(), _Strides(*st[:3])
+
+
+_Strides = ctypes.c_int64 * 3
 
 
 class _on:
@@ -70,6 +93,9 @@ class RaRope:
     """A rotation plan (see `new_rope`)."""
 
     c: RaRopeC = field(repr=False)
+
+    def __post_init__(self):
+        self.ref = ctypes.byref(self.c)
 
     @property
     def rot(self) -> int:
@@ -104,16 +130,14 @@ def new_rope(inv_freq, axis=None, interleaved: bool = False, axes: int | None = 
 
 
 def _plan(rope, positions, B, N, index):
-    if rope is None:
+    if rope is None or rope.c.rot == 0:
         return None, None
-    if rope.rot == 0:
-        return ctypes.byref(rope.c), None
     if positions is None:
         raise ValueError("a rotation needs positions")
-    shape = tuple(positions.shape)
-    if shape != (rope.axes, B, N) and not (rope.axes == 1 and shape == (B, N)):
-        raise ValueError(f"positions must have shape {(rope.axes, B, N)}, got {shape}")
-    return ctypes.byref(rope.c), _dev(positions, index, torch.int64, what="positions")
+    shape = positions.shape
+    if shape != (rope.c.axes, B, N) and not (rope.c.axes == 1 and shape == (B, N)):
+        raise ValueError(f"positions must have shape {(rope.axes, B, N)}, got {tuple(shape)}")
+    return rope.ref, _dev(positions, index, torch.int64, what="positions")
 
 
 def _weight(w, d, dtype, index, what):
@@ -128,7 +152,7 @@ def ra_qk_norm_rope(q, k, rope: RaRope | None = None, positions=None, q_weight=N
     eps=None: rotation only.  Returns dense (q_out, k_out)."""
     B, Hq, N, d = q.shape
     Hk = k.shape[1]
-    dt, index = q.dtype, torch.cuda.current_device()
+    dt, index = q.dtype, _here(q)
     code = _dtype_code(q)
     qp, qs = _rows(q, index, dt, (B, Hq, N, d), "q")
     kp, ks = _rows(k, index, dt, (B, Hk, N, d), "k")
@@ -144,7 +168,7 @@ def ra_qk_norm_rope(q, k, rope: RaRope | None = None, positions=None, q_weight=N
         _weight(k_weight, d, dt, index, "k_weight"), plan, pos,
         _dev(q_out, index, dt, (B, Hq, N, d), "q_out"),
         _dev(k_out, index, dt, (B, Hk, N, d), "k_out"), B, Hq, Hk, N, d,
-        -1.0 if eps is None else eps, code, _stream(stream))
+        -1.0 if eps is None else eps, code, _on_stream(stream, index))
     _check(res, "ra_qk_norm_rope")
     return q_out, k_out
 
@@ -162,7 +186,7 @@ def ra_qk_norm_rope_backward(q, k, dq_out, dk_out, rope: RaRope | None = None, p
     are fp32 (None without a weight)."""
     B, Hq, N, d = q.shape
     Hk = k.shape[1]
-    dt, index = q.dtype, torch.cuda.current_device()
+    dt, index = q.dtype, _here(q)
     code = _dtype_code(q)
     qp, qs = _rows(q, index, dt, (B, Hq, N, d), "q")
     kp, ks = _rows(k, index, dt, (B, Hk, N, d), "k")
@@ -190,7 +214,7 @@ def ra_qk_norm_rope_backward(q, k, dq_out, dk_out, rope: RaRope | None = None, p
         None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
         None if workspace is None else _dev(workspace, index, torch.uint8, what="workspace"),
         0 if workspace is None else workspace.numel(), B, Hq, Hk, N, d,
-        -1.0 if eps is None else eps, code, _stream(stream))
+        -1.0 if eps is None else eps, code, _on_stream(stream, index))
     _check(res, "ra_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
 
@@ -253,12 +277,12 @@ def ra_cache_write(cache: RaCache, k, v, table, lens, count=None, stream=None) -
     strides), token t < count[b] goes to position lens[b] + t of sequence b.
     An 8-bit cache is quantised as it is written.  lens is not advanced."""
     B, heads, T, d = k.shape
-    index = torch.cuda.current_device()
+    index = _here(k)
     tab, width, ln, cnt = _sequences(cache, table, lens, count, B, index)
     kp, ks = _rows(k, index, k.dtype, (B, cache.heads, T, cache.d), "k")
     vp, vs = _rows(v, index, k.dtype, (B, cache.heads, T, cache.d), "v")
     res = _native.lib().ra_cache_write(cache.ref, kp, ks, vp, vs, tab, width, ln, cnt, B, T,
-                                       _dtype_code(k), _stream(stream))
+                                       _dtype_code(k), _on_stream(stream, index))
     _check(res, "ra_cache_write")
     return cache
 
@@ -269,7 +293,7 @@ def ra_cache_read(cache: RaCache, table, lens, first: int, n: int, dtype=None, k
     [B, heads, n, d]; rows at or behind lens[b] are 0.  dtype: the result's
     (default: that of a given k or v, the cache's, or bfloat16 for 8 bits)."""
     B = table.shape[0]
-    index = torch.cuda.current_device()
+    index = _here(table)
     tab, width, ln, _ = _sequences(cache, table, lens, None, B, index)
     if dtype is None:
         given = k if k is not None else v
@@ -287,7 +311,7 @@ def ra_cache_read(cache: RaCache, table, lens, first: int, n: int, dtype=None, k
     res = _native.lib().ra_cache_read(cache.ref, tab, width, ln, first, n,
                                       _dev(k, index, dtype, shape, "k"),
                                       _dev(v, index, dtype, shape, "v"), B, _dtype_code(k),
-                                      _stream(stream))
+                                      _on_stream(stream, index))
     _check(res, "ra_cache_read")
     return k, v
 
@@ -305,7 +329,7 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
     cache's heads.  `workspace` (uint8, ra_cache_attention_workspace_bytes) is
     allocated when not given.  Returns (out [B, Hq, T, d], lse [B, Hq, T])."""
     B, Hq, T, d = q.shape
-    index = torch.cuda.current_device()
+    index = _here(q)
     tab, width, ln, cnt = _sequences(cache, table, lens, count, B, index)
     if d != cache.d:
         raise ValueError(f"q has head width {d}, the cache {cache.d}")
@@ -331,6 +355,6 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
         _dev(out, index, q.dtype, (B, Hq, T, d), "out"),
         _dev(lse, index, torch.float32, (B, Hq, T), "lse"),
         _dev(workspace, index, torch.uint8, what="workspace"), workspace.numel(), B, Hq, T,
-        _dtype_code(q), _stream(stream))
+        _dtype_code(q), _on_stream(stream, index))
     _check(res, "ra_cache_attention")
     return out, lse
