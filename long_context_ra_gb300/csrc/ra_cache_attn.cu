@@ -233,21 +233,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int64_t rows = head_rows(a);
   const int64_t seq_rows = rows * c.heads;
   for (int b = blockIdx.y; b < c.B; b += gridDim.y) {
-    __syncthreads();
-    int64_t mine = 0, all = 0;
-    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
-      const int64_t t = seq_tiles(c, p.div, i);
-      all += t;
-      if (i < b) mine += t;
+    // tiles (of one unit) of the sequences before b, and of all
+    int64_t ahead, total;
+    if (c.B <= 32) {
+      const int64_t upto = warp_scan(lane < c.B ? seq_tiles(c, p.div, lane) : 0);
+      ahead = b > 0 ? __shfl_sync(0xffffffffu, upto, b - 1) : 0;
+      total = __shfl_sync(0xffffffffu, upto, 31);
+    } else {
+      __syncthreads();
+      int64_t mine = 0, all = 0;
+      for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+        const int64_t t = seq_tiles(c, p.div, i);
+        all += t;
+        if (i < b) mine += t;
+      }
+      const int64_t x = block_scan(mine, sh);
+      if (threadIdx.x == blockDim.x - 1) before = x;
+      __syncthreads();
+      block_scan(all, sh);
+      __syncthreads();
+      ahead = before;
+      total = sh.total;
     }
-    const int64_t x = block_scan(mine, sh);
-    if (threadIdx.x == blockDim.x - 1) before = x;
-    __syncthreads();
-    block_scan(all, sh);
-    __syncthreads();
     if (c.count && blockIdx.x == 0 && threadIdx.x == 0 && c.lens[b] >= 0 && c.count[b] > c.T)
       flag_page(c.status);
-    const int64_t per = run_length(p.div, sh.total * p.div.units);
+    const int64_t per = run_length(p.div, total * p.div.units);
     const int64_t tiles = seq_tiles(c, p.div, b);
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinWarps / kSplit) + warp / kSplit;
     int c0 = 0, c1 = 0, local = 0;
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       const int unit = static_cast<int>(row / rows) * p.row_tiles +
                        static_cast<int>(in_head / p.rows);
       local = static_cast<int>(in_head % p.rows);
-      const int64_t u0 = before * p.div.units + unit * tiles;
+      const int64_t u0 = ahead * p.div.units + unit * tiles;
       c0 = static_cast<int>(u0 / per);
       c1 = static_cast<int>((u0 + tiles - 1) / per);
     }
@@ -387,10 +397,11 @@ cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
                                    cudaStream_t s) {
-  // A unit is shared by about ctas / units CTAs; with many parts per row, and
-  // so few rows, the warps of a block share a row.
+  // A unit is shared by about ctas / units CTAs.  A warp takes the parts of a
+  // row four at a time; with more than two such rounds several share the row.
   const int64_t units = static_cast<int64_t>(a.c.B) * p.div.units;
-  if (p.div.ctas > 8 * units) return bf16 ? join_t<__nv_bfloat16, 8>(a, p, s) : join_t<float, 8>(a, p, s);
+  if (p.div.ctas > 48 * units) return bf16 ? join_t<__nv_bfloat16, 8>(a, p, s) : join_t<float, 8>(a, p, s);
+  if (p.div.ctas > 8 * units) return bf16 ? join_t<__nv_bfloat16, 2>(a, p, s) : join_t<float, 2>(a, p, s);
   return bf16 ? join_t<__nv_bfloat16, 1>(a, p, s) : join_t<float, 1>(a, p, s);
 }
 

@@ -16,13 +16,14 @@
 // those on their way), with a state of its own, and the two states are joined
 // at the end of the unit.
 //
-// Warp roles (512 threads of 128 registers):
-//   warps 0-3, 4-7   softmax of stream 0, 1
-//   warp  8          TMEM allocator, MMA issuer
+// Warp roles (640 threads, 96 registers each at launch):
+//   warps 0-3, 4-7   softmax of stream 0, 1                           (112)
+//   warp  8          TMEM allocator, MMA issuer                       (112)
 //   warp  9          loader: TMA boxes of the key and value tiles
-//   warps 10-15      8-bit cache: conversion, a pair of warps per tile, three
-//                    tiles under way; queries
-//   (bf16 cache)     warps 13-15: queries; warp 12: tiles that end a sequence
+//   warps 12-19      8-bit cache: conversion, two tiles of 128 keys or four
+//                    of 64 under way; queries                          (72)
+//   (bf16 cache)     warp 12: tiles that end a sequence; 13-19: queries
+// 3 x 128 x 112 + 2 x 128 x 72 = 61440 = 640 x 96.
 //
 // A tile is a row of pages: the loader's lanes look up a page each, one tile
 // ahead, and bring it as one TMA box of a [pages x heads, page, d] view; a
@@ -55,11 +56,15 @@ namespace {
 using namespace ptx;
 using namespace sm103;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr uint32_t kRegs = 96;        // per thread at launch
+constexpr uint32_t kRegsMain = 112;   // softmax, MMA issuer, loader
+constexpr uint32_t kRegsHand = 72;    // queries, conversion
+static_assert(3 * 128 * kRegsMain + 2 * 128 * kRegsHand == kThreads * kRegs,
+              "register split must equal the launch's register total");
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
-constexpr int kHandWarp = 10;  // 8-bit cache
-constexpr int kFixWarp = 12;   // bf16 cache
+constexpr int kHandWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -74,6 +79,7 @@ struct Layout {
   static constexpr int kStages = kTwo ? (D == 128 ? (k8 ? 3 : 5) : (k8 ? 5 : 8))
                                       : (D == 128 ? (k8 ? 6 : 10) : (k8 ? 8 : 16));
   static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 8 : 12);
+  static constexpr int kTeam = kTwo ? 128 : 64;  // threads that convert a tile
   static constexpr int kLoadStages = k8 ? kRawStages : kStages;  // of the ring the loader fills
   // the second query tile, or the exchange of the two streams' states:
   // [128][33] floats and [128][2]
@@ -343,14 +349,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- set-up
   allow_join();
   if (threadIdx.x == 0) {
-    mbar_init(bars.q_full(), k8 ? 192 : 96);
+    mbar_init(bars.q_full(), k8 ? 256 : 224);
     mbar_init(bars.q_empty(), 1);
     for (int s = 0; s < kS; ++s) {
-      mbar_init(bars.kv_full(s), k8 ? 64 : 1);
+      mbar_init(bars.kv_full(s), k8 ? L::kTeam : 1);
       mbar_init(bars.kv_empty(s), 1);
     }
     for (int s = 0; s < L::kLoadStages; ++s) mbar_init(bars.raw_full(s), k8 ? 33 : 1);
-    for (int s = 0; s < L::kRawStages; ++s) mbar_init(bars.raw_empty(s), 64);
+    for (int s = 0; s < L::kRawStages; ++s) mbar_init(bars.raw_empty(s), L::kTeam);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bars.s_full(t), 1);
       mbar_init(bars.p_full(t), 128);
@@ -373,9 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp >= (k8 ? kHandWarp : kFixWarp)) {
+  if (warp >= kHandWarp) {
     // ================= queries, conversion =================
-    const int tid = threadIdx.x - (k8 ? kHandWarp : kFixWarp) * 32;
+    setmaxnreg_dec<kRegsHand>();
+    const int tid = threadIdx.x - kHandWarp * 32;
     // The unit's queries, by `count` threads of which this is `id`.
     auto load_queries = [&](const UnitWalk& w, uint32_t ord, int id, int count) {
       const Unit un(a, p, w, rows);
@@ -413,24 +420,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.start(c, p.div, sh, run);
     if (k8) {
       Ring in, out;  // raw stages; operand stages
-      constexpr int kPairs = 3;
-      constexpr int kGroup = kKeys / 8;  // rows per 8 of a pair's 64 threads
-      constexpr int kPieces = D * kKeys / 16 / 64;
-      const int pair = tid / 64, grp = tid % 64 / 8, pc = tid % 8;
-      int turn = 0;  // of the pair that takes the next tile
+      constexpr int kTeams = 256 / L::kTeam;
+      constexpr int kGroup = kKeys / (L::kTeam / 8);  // rows per 8 threads
+      constexpr int kPieces = D * kKeys / 16 / L::kTeam;
+      const int team = tid / L::kTeam, grp = tid % L::kTeam / 8, pc = tid % 8;
+      int turn = 0;  // of the team that takes the next tile
       const uint32_t src0 = base + L::kRaw + (D == 128 ? pc : pc % 4) * 16;
       const uint32_t dst0 = base + L::kKV + (D == 128 ? pc / 4 : 0) * L::kBox;
       const int ch = 2 * (pc % 4);
       for (uint32_t ord = 0; !w.done(); ++ord, w.next(c, p.div)) {
-        if (!load_queries(w, ord, tid, 192)) break;
+        if (!load_queries(w, ord, tid, 256)) break;
         const int n = static_cast<int>(w.last - w.first);
         // keys and context keys of this part
         const int64_t before = w.first * kKeys;
         const int keys = static_cast<int>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
         const int context = static_cast<int>(min(w.seq.len - before, static_cast<int64_t>(n) * kKeys));
         const bool ok = each_item<kTwo>(n, [&](int tile, bool v) {
-          const bool other = turn != pair;
-          turn = turn + 1 == kPairs ? 0 : turn + 1;
+          const bool other = turn != team;
+          turn = turn + 1 == kTeams ? 0 : turn + 1;
           if (other) {
             in.step<L::kLoadStages>();
             out.step<kS>();
@@ -482,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
         if (!ok) break;
       }
-    } else if (warp > kFixWarp) {
+    } else if (warp > kHandWarp) {
       for (uint32_t ord = 0; !w.done(); ++ord, w.next(c, p.div))
-        if (!load_queries(w, ord, tid - 32, 96)) break;
+        if (!load_queries(w, ord, tid - 32, 224)) break;
     } else {
       // value tiles with drafts or the end
       uint32_t first_item = 0, used = 0;  // items before the unit; phases of raw_full, a bit each
@@ -526,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kLoadWarp) {
     // ================= loader =================
+    setmaxnreg_inc<kRegsMain>();
     const int page_rows = min(1 << c.page_shift, kKeys);  // of a box
     const int boxes = kKeys / page_rows;
     constexpr int kHalves = k8 ? 1 : D / 64;
@@ -635,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kMmaWarp) {
     // ================= MMA issuer (and two idle warps) =================
+    setmaxnreg_inc<kRegsMain>();
     if (warp == kMmaWarp && lane == 0) {
       const uint64_t dQ0 = desc_sw128(base + L::kQ0, 16, 1024);
       const uint64_t dQ1 = desc_sw128(base + L::kQ1, 16, 1024);
@@ -766,6 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ================= softmax =================
+    setmaxnreg_inc<kRegsMain>();
     const int t = warp / 4, wq = warp % 4;
     const int row = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;

@@ -238,10 +238,37 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, DivisionShared& sh) {
   return x + before;
 }
 
+// Inclusive scan over the lanes of a warp.
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 // The first (sequence, offset) of CTA `cta`'s run, and its end: fills sh and
 // returns the tiles of the run (0: nothing to do).  All threads take part.
+// Up to 32 sequences are a lane each: every warp finds the place by itself.
 __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Division& v, int cta,
                                                   DivisionShared& sh) {
+  if (c.B <= 32) {
+    const int lane = threadIdx.x % 32;
+    const int64_t tiles = lane < c.B ? seq_tiles(c, v, lane) * v.units : 0;
+    const int64_t upto = warp_scan(tiles);
+    const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+    const int64_t run = run_length(v, all);
+    const int64_t begin = cta * run;
+    if (begin >= upto - tiles && begin < upto) {
+      // one lane of every warp: all write the same
+      sh.b = lane;
+      sh.off = begin - (upto - tiles);
+    }
+    __syncthreads();
+    return begin >= all ? 0 : min(run, all - begin);
+  }
   const int per_thread = (c.B + blockDim.x - 1) / blockDim.x;
   const int b0 = min(c.B, static_cast<int>(threadIdx.x) * per_thread);
   const int b1 = min(c.B, b0 + per_thread);
