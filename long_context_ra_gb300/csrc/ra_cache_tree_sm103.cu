@@ -17,11 +17,10 @@
 // at the end of the unit.
 //
 // Warp roles (640 threads, 96 registers each at launch):
-//   warps 0-3, 4-7   softmax of stream 0, 1                           (112)
-//   warp  8          TMEM allocator, MMA issuer                       (112)
-//   warp  9          loader: TMA boxes of the key and value tiles
-//   warps 12-19      8-bit cache: conversion, two tiles of 128 keys or four
-//                    of 64 under way; queries                          (72)
+//   warps 0-3, 4-7   softmax of stream 0, 1                            (112)
+//   warp  9          loader: TMA boxes of the key and value tiles      (112)
+//   warp  11         TMEM allocator, MMA issuer
+//   warps 12-19      8-bit cache: conversion, two tiles under way; queries (72)
 //   (bf16 cache)     warp 12: tiles that end a sequence; 13-19: queries
 // 3 x 128 x 112 + 2 x 128 x 72 = 61440 = 640 x 96.
 //
@@ -62,7 +61,7 @@ constexpr uint32_t kRegsMain = 112;   // softmax, MMA issuer, loader
 constexpr uint32_t kRegsHand = 72;    // queries, conversion
 static_assert(3 * 128 * kRegsMain + 2 * 128 * kRegsHand == kThreads * kRegs,
               "register split must equal the launch's register total");
-constexpr int kMmaWarp = 8;
+constexpr int kMmaWarp = 11;
 constexpr int kLoadWarp = 9;
 constexpr int kHandWarp = 12;
 constexpr uint32_t kTmemCols = 512;
@@ -79,7 +78,7 @@ struct Layout {
   static constexpr int kStages = kTwo ? (D == 128 ? (k8 ? 3 : 5) : (k8 ? 5 : 8))
                                       : (D == 128 ? (k8 ? 6 : 10) : (k8 ? 8 : 16));
   static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 8 : 12);
-  static constexpr int kTeam = kTwo ? 128 : 64;  // threads that convert a tile
+  static constexpr int kTeam = 128;  // threads that convert a tile
   static constexpr int kLoadStages = k8 ? kRawStages : kStages;  // of the ring the loader fills
   // the second query tile, or the exchange of the two streams' states:
   // [128][33] floats and [128][2]
@@ -144,6 +143,8 @@ __device__ __forceinline__ int value_item(int tile, int n) {
   return kTwo ? 2 * tile + 1 : tile + 1 == n ? 2 * n - 1 : 2 * tile + 2;
 }
 // f(tile, v) for the items of a unit of n tiles, in order, until f is false.
+// v is a constant at each place f stands: without the tests that only value
+// tiles need, key tiles are converted a tenth faster.
 template <bool kTwo, typename F>
 __device__ __forceinline__ bool each_item(int n, F f) {
   if (!kTwo && !f(0, false)) return false;
@@ -450,7 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = dst0 + out.stage * L::kTile;
           const bool border = v && (tile + 1) * kKeys > context;
           bool bad = false;
-          constexpr int kBatch = kPieces < 4 ? kPieces : 4;  // loads in flight
+          // loads in flight; four spill, and are slower
+          constexpr int kBatch = kPieces < 2 ? kPieces : 2;
 #pragma unroll 1
           for (int z0 = 0; z0 < kPieces; z0 += kBatch) {
             uint4 w4[kBatch];
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((issued >> s) & 1u)
           wait_drain((hand >> s) & 1u ? bars.raw_full(s) : bars.kv_full(s), (last >> s) & 1u);
     }
-  } else if (warp >= kMmaWarp) {
+  } else if (warp >= 8) {
     // ================= MMA issuer (and two idle warps) =================
     setmaxnreg_inc<kRegsMain>();
     if (warp == kMmaWarp && lane == 0) {
