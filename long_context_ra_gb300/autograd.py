@@ -6,12 +6,15 @@ Functions: the forward is the library's forward and the backward its
 backward ("Ring attention, explained", step 6: the backward runs on the same
 ring).  They hold no arithmetic of their own; out is differentiable, lse is
 returned as a non-differentiable tensor (the backward takes the gradient of
-out only)."""
+out only).  `qk_norm_rope` is what stands before either: the norm of every
+head of q and k and the rotation by their positions."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import ra_backward, ra_forward, ra_forward_causal
+from . import (ra_backward, ra_forward, ra_forward_causal, ra_qk_norm_rope,
+               ra_qk_norm_rope_backward)
 
 
 class _Attention(torch.autograd.Function):
@@ -76,3 +79,33 @@ def ring_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, group=None
     up).  `ops` / `bops` replace the forward / backward operations (default:
     the library's kernels).  Returns (out, lse) of the block."""
     return _RingAttention.apply(q, k, v, group, causal, layout, ops, bops)
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, rope, positions, eps):
+        q_out, k_out = ra_qk_norm_rope(q, k, rope, positions, q_weight, k_weight, eps)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions)
+        ctx.rope, ctx.eps = rope, eps
+        return q_out, k_out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, positions = ctx.saved_tensors
+        dq, dk, dwq, dwk = ra_qk_norm_rope_backward(q, k, dq_out.contiguous(), dk_out.contiguous(),
+                                                    ctx.rope, positions, q_weight, k_weight,
+                                                    ctx.eps)
+        return (dq, dk, None if dwq is None else dwq.to(q_weight.dtype),
+                None if dwk is None else dwk.to(k_weight.dtype), None, None, None)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope=None, positions=None,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                 eps: float | None = 1e-6):
+    """Differentiable ra_qk_norm_rope: q [B, Hq, N, d] and k [B, Hk, N, d]
+    (views of a projection are read through their strides) normalised per
+    head and rotated by positions, dense and ready for `attention`.  On a rank
+    of `ring_attention`, `positions` are those of the block's tokens.
+    Gradients flow to q, k and the weights."""
+    return _QkNormRope.apply(q, k, q_weight, k_weight, rope, positions, eps)
