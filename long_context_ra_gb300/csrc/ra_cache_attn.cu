@@ -1,33 +1,38 @@
 // Attention of new tokens over the paged cache: the FFMA kernel (fp32
 // inputs), the join of parts, and the choice of kernel.
 //
-// The FFMA kernel.  A unit is 16 query rows of one key head; 4 warps, each
-// with 4 rows.  A tile of 32 keys is brought to shared memory as fp32 (8-bit
-// rows multiplied by their scale); lane = key for the scores, lane = columns
-// for P V, so the online softmax of a row stays inside its warp:
+// The FFMA kernel.  A tile of keys is brought to shared memory as fp32 (8-bit
+// rows multiplied by their scale).  A warp has kRW query rows and 32 kKL keys
+// of the tile: lane = key for the scores, lane = columns for P V, so the
+// online softmax of a row stays inside its warp:
 //   m' = max(m, max s),  l' = l e^(m-m') + sum p,  o' = o e^(m-m') + p V
-// A key that a row does not see has p = 0 and is left out of the sum rather
-// than multiplied, so what it holds does not matter.  Four CTAs share an SM and
-// hide one another's loads; a CTA takes single tiles while there are few, since
-// a tile's chain of look-up, load, scores and sum is what a short call waits
-// for.
+// As in the other kernels m moves only when a score passes it by 2^8, which a
+// vote tells, and l is summed over the lanes at the end.  kRG warps take the
+// rows, kKG the keys of a tile (their states are joined at the end of a unit),
+// so that four rows keep four warps busy as well as 16 do.
+//
+// Few rows wait for the chain of look-up, load, scores and sum of each tile;
+// three or more CTAs share an SM and hide one another's, the page look-up runs
+// a tile ahead, and a CTA takes single tiles while there are few.  Many rows
+// are bound by instructions: both products run on pairs (fma.rn.f32x2), of
+// neighbouring elements for the scores and of neighbouring columns for P V,
+// whose probabilities are kept twice side by side; 8 rows x 2 keys a lane are
+// 32 paired FFMA for 10 reads of 16 bytes.
+//
+// In tiles with drafts or the end a key that a row does not see has p = 0 and
+// is left out of the sum rather than multiplied, so what it holds does not
+// matter.
 
 #include "ra_cache_attn.cuh"
+#include "sm103_ptx.cuh"
 
 namespace ra {
 namespace {
 
-constexpr int kRows = 16;
-constexpr int kTile = 32;
-constexpr int kThreads = 128;
-constexpr int kColumns = RA_MAX_HEAD_DIM / 32;  // per lane
-constexpr int kMaxSmem = (kRows * RA_MAX_HEAD_DIM + kTile * (2 * RA_MAX_HEAD_DIM + 4)) * 4;
+using namespace ptx;
 
-template <typename E>
-__device__ __forceinline__ float to_float(E x) {
-  return static_cast<float>(x);
-}
-__device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
+constexpr int kFfmaSmem = 192 * 1024;  // dynamic, beside 33 KB of static
+constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
@@ -36,21 +41,38 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
                                             *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <typename E, typename H>
-__global__ void __launch_bounds__(kThreads, 4)
+// NC: pairs of columns of a head per lane, 2 (d <= 128) or 4.
+template <int RW, int KL, int RG, int KG, int NC>
+struct Ffma {
+  static constexpr int kRW = RW, kKL = KL, kRG = RG, kKG = KG, kPairs = NC;
+  static constexpr int kCtas = 32 * RG * KG > 128 ? (NC == 2 ? 2 : 1) : 4;  // per SM, by registers
+  static constexpr int kWarps = RG * KG;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRows = RG * RW;
+  static constexpr int kWarpKeys = 32 * KL;
+  static constexpr int kTile = KG * kWarpKeys;
+  // queries, K (pitch d + 4), V; the joined states take the place of K and V
+  static int smem(int d) { return (kRows * d + kTile * (2 * d + 4)) * 4; }
+};
+
+template <typename H, typename F>
+__global__ void __launch_bounds__(F::kThreads, F::kCtas)
     cache_attn_ffma_kernel(const __grid_constant__ CacheAttnArgs a,
                            const __grid_constant__ AttnPlan p) {
   constexpr bool k8 = sizeof(H) == 1;
+  constexpr int kRW = F::kRW, kKL = F::kKL, kTile = F::kTile, kPairs = F::kPairs;
   extern __shared__ float4 smem4[];
   __shared__ DivisionShared sh;
-  __shared__ int64_t key_row[kTile];
-  __shared__ float4 probs[4][kTile];  // of a warp's 4 rows, per key
+  __shared__ int64_t key_row[2][kTile];
+  __shared__ float4 probs[F::kWarps][F::kWarpKeys][kRW / 2];  // (p, p, p', p') of two rows
+  __shared__ float states[F::kWarps][kRW][2];
   const PagedArgs& c = a.c;
   const int d = c.d, ld = d + 4;
   float* qs = reinterpret_cast<float*>(smem4);  // [kRows][d]
-  float* ks = qs + kRows * d;                   // [kTile][ld]
+  float* ks = qs + F::kRows * d;                // [kTile][ld]
   float* vs = ks + kTile * ld;                  // [kTile][d]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rg = warp % F::kRG, kg = warp / F::kRG;
   const int64_t rows = head_rows(a);
 
   allow_join();
@@ -58,48 +80,56 @@ __global__ void __launch_bounds__(kThreads, 4)
   UnitWalk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
     const int head = u.unit / p.row_tiles;
-    const int64_t r0 = static_cast<int64_t>(u.unit % p.row_tiles) * kRows;
+    const int64_t r0 = static_cast<int64_t>(u.unit % p.row_tiles) * F::kRows;
     // q, out, lse row of row 0 of the unit
     const int64_t q0 = (static_cast<int64_t>(u.b) * c.heads + head) * rows + r0;
+    const int64_t keys = u.seq.keys(), context = u.seq.len;
+    auto look_up = [&](int64_t tile) {
+      if (threadIdx.x < kTile && tile < u.last) {
+        const int64_t pos = tile * kTile + threadIdx.x;
+        const int64_t row = pos < keys ? cache_row(c, u.b, pos) : -1;
+        key_row[tile & 1][threadIdx.x] =
+            row < 0 ? -1 : row + (static_cast<int64_t>(head) << c.page_shift);
+      }
+    };
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * d; i += kThreads) {
-      const int r = i / d;
-      qs[i] = r0 + r < rows ? to_float(static_cast<const E*>(a.q)[q0 * d + i]) * a.scale_log2 : 0.f;
+    look_up(u.first);
+    const float* q = static_cast<const float*>(a.q) + q0 * d;
+    for (int i = threadIdx.x * 4; i < F::kRows * d; i += F::kThreads * 4) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r0 + i / d < rows) x = *reinterpret_cast<const float4*>(q + i);
+      const float t = a.scale_log2;
+      *reinterpret_cast<float4*>(qs + i) = make_float4(x.x * t, x.y * t, x.z * t, x.w * t);
     }
-    float m[4], l[4], o[4][kColumns];
-    int t[4];
+    float m[kRW], l[kRW];
+    uint64_t o[kRW][kPairs];  // columns 2 lane, 2 lane + 1 of every 64
+    int t[kRW];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < kRW; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
-      const int64_t row = r0 + 4 * warp + r;
+      const int64_t row = r0 + rg * kRW + r;
       t[r] = row < rows ? static_cast<int>(row % c.T) : c.T;
 #pragma unroll
-      for (int x = 0; x < kColumns; ++x) o[r][x] = 0.f;
+      for (int x = 0; x < kPairs; ++x) o[r][x] = 0ull;
     }
     for (int64_t tile = u.first; tile < u.last; ++tile) {
-      const int64_t pos0 = tile * kTile;
+      const int64_t* at = key_row[tile & 1];
       __syncthreads();
-      if (threadIdx.x < kTile) {
-        const int64_t pos = pos0 + threadIdx.x;
-        int64_t row = -1;
-        if (pos < u.seq.keys()) row = cache_row(c, u.b, pos);
-        key_row[threadIdx.x] = row < 0 ? -1 : row + (static_cast<int64_t>(head) << c.page_shift);
-      }
-      __syncthreads();
-      for (int i0 = threadIdx.x; i0 < kTile * d / 8; i0 += 4 * kThreads) {
+      look_up(tile + 1);
+      for (int i0 = threadIdx.x; i0 < kTile * d / 8; i0 += 4 * F::kThreads) {
         // four pieces of 8 elements of K and of V are on their way together
         Packed<H, 8> x[4], y[4];
         uint32_t ek[4], ev[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          const int i = i0 + z * kThreads;
-          const int key = i / (d / 8), e = (i % (d / 8)) * 8;
-          const int64_t row = i < kTile * d / 8 ? key_row[key] : -1;
+          const int i = i0 + z * F::kThreads;
+          const int64_t row = i < kTile * d / 8 ? at[i / (d / 8)] : -1;
           x[z].zero();
           y[z].zero();
           ek[z] = ev[z] = 127;
           if (row >= 0) {
+            const int e = (i % (d / 8)) * 8;
             x[z].load(static_cast<const H*>(c.k) + row * d + e);
             y[z].load(static_cast<const H*>(c.v) + row * d + e);
             if (k8) {
@@ -110,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         }
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          const int i = i0 + z * kThreads;
+          const int i = i0 + z * F::kThreads;
           if (i >= kTile * d / 8) break;
           const int key = i / (d / 8), e = (i % (d / 8)) * 8;
           float f[8];
@@ -131,77 +161,200 @@ __global__ void __launch_bounds__(kThreads, 4)
         }
       }
       __syncthreads();
-      // scores of key `lane` for the warp's rows
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int e = 0; e < d; e += 4) {
-        const float4 kk = *reinterpret_cast<const float4*>(ks + lane * ld + e);
+      if (r0 + rg * kRW >= rows) continue;  // no row of this warp's
+      // ---- scores of keys lane, lane + 32 of the warp's part of the tile
+      const float* kw = ks + (kg * F::kWarpKeys + lane) * ld;
+      const float* qw = qs + rg * kRW * d;
+      uint64_t s2[kRW][kKL];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float4 qq = *reinterpret_cast<const float4*>(qs + (4 * warp + r) * d + e);
-          s[r] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[r]))));
+      for (int r = 0; r < kRW; ++r)
+#pragma unroll
+        for (int z = 0; z < kKL; ++z) s2[r][z] = 0ull;
+#pragma unroll 2
+      for (int e = 0; e < d; e += 4) {
+        ulonglong2 kk[kKL];
+#pragma unroll
+        for (int z = 0; z < kKL; ++z) kk[z] = *reinterpret_cast<const ulonglong2*>(kw + 32 * z * ld + e);
+#pragma unroll
+        for (int r = 0; r < kRW; ++r) {
+          const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(qw + r * d + e);
+#pragma unroll
+          for (int z = 0; z < kKL; ++z)
+            s2[r][z] = fma_f32x2(qq.x, kk[z].x, fma_f32x2(qq.y, kk[z].y, s2[r][z]));
         }
       }
-      const bool here = key_row[lane] >= 0;
-      float pr4[4];
+      float s[kRW][kKL];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool seen = here && sees(a, u.seq, u.b, t[r], pos0 + lane);
-        if (!seen) s[r] = -INFINITY;
-        float mx = s[r];
+      for (int r = 0; r < kRW; ++r)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        mx = fmaxf(mx, m[r]);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        const float alpha = exp2f(m[r] - ref);  // 0 for an empty state
-        const float pr = seen ? exp2f(s[r] - ref) : 0.f;
-        float sum = pr;
+        for (int z = 0; z < kKL; ++z) {
+          float lo, hi;
+          unpack_f32x2(s2[r][z], lo, hi);
+          s[r][z] = lo + hi;
+        }
+      const int64_t pos0 = tile * kTile + kg * F::kWarpKeys;
+      bool whole_tile = pos0 + F::kWarpKeys <= context;  // every row sees every key
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        l[r] = l[r] * alpha + sum;
-        m[r] = mx;
-        pr4[r] = pr;
+      for (int z = 0; z < kKL; ++z) whole_tile = whole_tile && at[kg * F::kWarpKeys + lane + 32 * z] >= 0;
+      whole_tile = __all_sync(0xffffffffu, whole_tile);
+      if (!whole_tile) {
 #pragma unroll
-        for (int x = 0; x < kColumns; ++x) o[r][x] *= alpha;
+        for (int z = 0; z < kKL; ++z) {
+          const int64_t pos = pos0 + lane + 32 * z;
+          const bool here = at[kg * F::kWarpKeys + lane + 32 * z] >= 0;
+#pragma unroll
+          for (int r = 0; r < kRW; ++r)
+            if (!here || !sees(a, u.seq, u.b, t[r], pos)) s[r][z] = -INFINITY;
+        }
       }
-      probs[warp][lane] = make_float4(pr4[0], pr4[1], pr4[2], pr4[3]);
-      __syncwarp();
-      if (r0 + 4 * warp < rows) {
-#pragma unroll 4
-        for (int key = 0; key < kTile; ++key) {
-          const float4 pr = probs[warp][key];
+      // ---- reference, probabilities
+      bool pass = false;
 #pragma unroll
-          for (int x = 0; x < kColumns; ++x) {
-            if (32 * x >= d) break;
-            const int col = lane + 32 * x;
-            const float vv = vs[key * d + (col < d ? col : 0)];
-            o[0][x] = fmaf(pr.x, pr.x != 0.f ? vv : 0.f, o[0][x]);
-            o[1][x] = fmaf(pr.y, pr.y != 0.f ? vv : 0.f, o[1][x]);
-            o[2][x] = fmaf(pr.z, pr.z != 0.f ? vv : 0.f, o[2][x]);
-            o[3][x] = fmaf(pr.w, pr.w != 0.f ? vv : 0.f, o[3][x]);
+      for (int r = 0; r < kRW; ++r)
+#pragma unroll
+        for (int z = 0; z < kKL; ++z) pass = pass || s[r][z] > m[r] + kSlack;
+      if (__any_sync(0xffffffffu, pass)) {
+#pragma unroll
+        for (int r = 0; r < kRW; ++r) {
+          float x = m[r];
+#pragma unroll
+          for (int z = 0; z < kKL; ++z) x = fmaxf(x, s[r][z]);
+#pragma unroll
+          for (int w = 16; w > 0; w >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+          const float alpha = m[r] == x ? 1.f : exp2f(m[r] - x);
+          m[r] = x;
+          l[r] *= alpha;
+#pragma unroll
+          for (int z = 0; z < kPairs; ++z) o[r][z] = mul_f32x2(o[r][z], pack_f32x2(alpha, alpha));
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < kKL; ++z) {
+#pragma unroll
+        for (int r = 0; r < kRW; r += 2) {
+          const float p0 = exp2f(s[r][z] - (m[r] == -INFINITY ? 0.f : m[r]));
+          const float p1 = exp2f(s[r + 1][z] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]));
+          l[r] += p0;
+          l[r + 1] += p1;
+          probs[warp][lane + 32 * z][r / 2] = make_float4(p0, p0, p1, p1);
+        }
+      }
+      __syncwarp();
+      // ---- values
+      const float* vw = vs + kg * F::kWarpKeys * d;
+      int col[kPairs];
+#pragma unroll
+      for (int x = 0; x < kPairs; ++x) col[x] = 2 * lane + 64 * x < d ? 2 * lane + 64 * x : 0;
+#pragma unroll 2
+      for (int key = 0; key < F::kWarpKeys; ++key, vw += d) {
+        ulonglong2 pr[kRW / 2];
+#pragma unroll
+        for (int r = 0; r < kRW / 2; ++r) pr[r] = *reinterpret_cast<const ulonglong2*>(&probs[warp][key][r]);
+        uint64_t vv[kPairs];
+#pragma unroll
+        for (int x = 0; x < kPairs; ++x)
+          if (64 * x < d) vv[x] = *reinterpret_cast<const uint64_t*>(vw + col[x]);
+        if (whole_tile) {
+#pragma unroll
+          for (int x = 0; x < kPairs; ++x)
+            if (64 * x < d) {
+#pragma unroll
+              for (int r = 0; r < kRW; r += 2) {
+                o[r][x] = fma_f32x2(pr[r / 2].x, vv[x], o[r][x]);
+                o[r + 1][x] = fma_f32x2(pr[r / 2].y, vv[x], o[r + 1][x]);
+              }
+            }
+        } else {
+#pragma unroll
+          for (int r = 0; r < kRW; r += 2) {
+            // the same for every lane: a row's probability of this key
+            const bool s0 = pr[r / 2].x != 0ull, s1 = pr[r / 2].y != 0ull;
+#pragma unroll
+            for (int x = 0; x < kPairs; ++x)
+              if (64 * x < d) {
+                if (s0) o[r][x] = fma_f32x2(pr[r / 2].x, vv[x], o[r][x]);
+                if (s1) o[r + 1][x] = fma_f32x2(pr[r / 2].y, vv[x], o[r + 1][x]);
+              }
           }
         }
       }
+      __syncwarp();
     }
+    // ---- join the key groups' states, then out, or this CTA's part
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t row = r0 + 4 * warp + r;
-      if (row >= rows) continue;
-      if (u.whole()) {
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-        E* dst = static_cast<E*>(a.out) + (q0 + 4 * warp + r) * d;
+    for (int r = 0; r < kRW; ++r)
 #pragma unroll
-        for (int x = 0; x < kColumns; ++x)
-          if (lane + 32 * x < d) store_out(dst + lane + 32 * x, o[r][x] * inv);
-        if (lane == 0)
-          a.lse[q0 + 4 * warp + r] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2F;
-      } else {
-        const int slot = u.slot(blockIdx.x);
-        float* dst = slot_o(a, p, slot) + (4 * warp + r) * d;
+      for (int w = 16; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+    float* parts = ks;  // [kKG - 1][kRows][d]
+    if (F::kKG > 1) {
+      __syncthreads();
 #pragma unroll
-        for (int x = 0; x < kColumns; ++x)
-          if (lane + 32 * x < d) dst[lane + 32 * x] = o[r][x];
+      for (int r = 0; r < kRW; ++r) {
         if (lane == 0) {
-          float* ml = slot_ml(a, p, slot) + (4 * warp + r) * 2;
+          states[warp][r][0] = m[r];
+          states[warp][r][1] = l[r];
+        }
+        if (kg > 0) {
+#pragma unroll
+          for (int x = 0; x < kPairs; ++x)
+            if (2 * lane + 64 * x < d)
+              *reinterpret_cast<uint64_t*>(
+                  parts + ((kg - 1) * F::kRows + rg * kRW + r) * d + 2 * lane + 64 * x) = o[r][x];
+        }
+      }
+      __syncthreads();
+    }
+    if (kg > 0) continue;
+#pragma unroll
+    for (int r = 0; r < kRW; ++r) {
+      const int local = rg * kRW + r;
+      if (r0 + local >= rows) continue;
+      if (F::kKG > 1) {
+        float ms = m[r];
+#pragma unroll
+        for (int g = 1; g < F::kKG; ++g) ms = fmaxf(ms, states[g * F::kRG + rg][r][0]);
+        const float ref = ms == -INFINITY ? 0.f : ms;
+        const float f0 = l[r] == 0.f ? 0.f : exp2f(m[r] - ref);
+        float ls = f0 * l[r];
+#pragma unroll
+        for (int x = 0; x < kPairs; ++x) o[r][x] = f0 == 0.f ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f0, f0));
+#pragma unroll
+        for (int g = 1; g < F::kKG; ++g) {
+          const float lg = states[g * F::kRG + rg][r][1];
+          const float f = lg == 0.f ? 0.f : exp2f(states[g * F::kRG + rg][r][0] - ref);
+          ls += f * lg;
+          if (f != 0.f) {
+#pragma unroll
+            for (int x = 0; x < kPairs; ++x)
+              if (2 * lane + 64 * x < d)
+                o[r][x] = fma_f32x2(pack_f32x2(f, f),
+                                    *reinterpret_cast<const uint64_t*>(
+                                        parts + ((g - 1) * F::kRows + local) * d + 2 * lane + 64 * x),
+                                    o[r][x]);
+          }
+        }
+        m[r] = ms;
+        l[r] = ls;
+      }
+      if (t[r] >= u.seq.cnt) {  // no query: an empty state
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+      }
+      const bool whole = u.whole();
+      const float f = l[r] == 0.f ? 0.f : whole ? 1.f / l[r] : 1.f;
+      const int slot = u.slot(blockIdx.x);
+      float* dst = whole ? static_cast<float*>(a.out) + (q0 + local) * d
+                         : slot_o(a, p, slot) + static_cast<int64_t>(local) * d;
+#pragma unroll
+      for (int x = 0; x < kPairs; ++x)
+        if (2 * lane + 64 * x < d)
+          *reinterpret_cast<uint64_t*>(dst + 2 * lane + 64 * x) =
+              f == 0.f ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f, f));
+      if (lane == 0) {
+        if (whole) {
+          a.lse[q0 + local] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2F;
+        } else {
+          float* ml = slot_ml(a, p, slot) + 2 * local;
           ml[0] = m[r];
           ml[1] = l[r];
         }
@@ -344,17 +497,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
-AttnPlan ffma_plan(const CacheAttnArgs& a) {
-  AttnPlan p;
-  p.rows = kRows;
-  p.row_tiles = static_cast<int>((head_rows(a) + kRows - 1) / kRows);
-  p.div.units = a.c.heads * p.row_tiles;
-  p.div.tile = kTile;
-  p.div.ctas = kFfmaCtas;
-  p.div.min_run = 1;
-  return p;
-}
-
 template <typename E, int kSplit>
 cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   const int64_t seq_rows = head_rows(a) * a.c.heads;
@@ -373,24 +515,45 @@ cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<E, kSplit>, a, p);
 }
 
-template <typename E, typename H>
-cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
-  const AttnPlan p = ffma_plan(a);
-  const int smem = (kRows * a.c.d + kTile * (2 * a.c.d + 4)) * 4;
+template <typename H, typename F>
+cudaError_t launch_ffma_t(const CacheAttnArgs& a, int ctas, cudaStream_t s) {
+  AttnPlan p;
+  p.rows = F::kRows;
+  p.row_tiles = static_cast<int>((head_rows(a) + F::kRows - 1) / F::kRows);
+  p.div.units = a.c.heads * p.row_tiles;
+  p.div.tile = F::kTile;
+  p.div.ctas = ctas;
+  p.div.min_run = 1;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(cache_attn_ffma_kernel<E, H>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    const int most = F::smem(RA_MAX_HEAD_DIM);
+    e = cudaFuncSetAttribute(cache_attn_ffma_kernel<H, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             most < kFfmaSmem ? most : kFfmaSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  cache_attn_ffma_kernel<E, H><<<p.div.ctas, kThreads, smem, s>>>(a, p);
+  cache_attn_ffma_kernel<H, F><<<p.div.ctas, F::kThreads, F::smem(a.c.d), s>>>(a, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_cache_attn_join(a, p, sizeof(E) == 2, s);
+  return e == cudaSuccess ? launch_cache_attn_join(a, p, false, s) : e;
+}
+
+template <typename H, int NC>
+cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
+  const int64_t rows = head_rows(a);
+  // The smallest group of rows that holds a head's, with as many warps on the
+  // keys as leave room for three CTAs on an SM.
+  using F4 = Ffma<4, 1, 1, 4, NC>;
+  using F8 = Ffma<4, 1, 2, 2, NC>;
+  using F16 = Ffma<4, 1, 4, 1, NC>;
+  using F64 = Ffma<8, 2, 8, 1, NC>;
+  constexpr int third = kFfmaSmem / 3;
+  if (rows <= 4 && F4::smem(a.c.d) <= third) return launch_ffma_t<H, F4>(a, kFfmaCtas, s);
+  if (rows <= 8 && F8::smem(a.c.d) <= third) return launch_ffma_t<H, F8>(a, kFfmaCtas, s);
+  if (rows <= 16 || F64::smem(a.c.d) > kFfmaSmem) return launch_ffma_t<H, F16>(a, kFfmaCtas, s);
+  return launch_ffma_t<H, F64>(a, kFfmaCtas / 2, s);
 }
 
 }  // namespace
@@ -408,7 +571,8 @@ cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bo
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dtype held,
                                    cudaStream_t s) {
   if (dense == RA_F32)
-    return held == RA_E4M3 ? launch_ffma<float, __nv_fp8_e4m3>(a, s) : launch_ffma<float, float>(a, s);
+    return a.c.d <= 128 ? (held == RA_E4M3 ? launch_ffma<__nv_fp8_e4m3, 2>(a, s) : launch_ffma<float, 2>(a, s))
+                        : (held == RA_E4M3 ? launch_ffma<__nv_fp8_e4m3, 4>(a, s) : launch_ffma<float, 4>(a, s));
   // The decode kernel reads a key head once per 16 query rows, the tree kernel
   // once per 256.  Up to 16 rows the former is ahead throughout.  With 17 to 32
   // rows it still is over 8-bit caches, which the tree kernel has to widen
@@ -425,9 +589,8 @@ int64_t cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, in
   // known here): parts of 2 slots per CTA.
   (void)B;
   const int64_t rows = static_cast<int64_t>(Hq / heads) * T;
-  int64_t most = kFfmaCtas * kRows;
-  if (rows > kDecodeRows) most = kTreeCtas * (rows > 128 ? 256 : 128);
-  if (most < kFfmaCtas * kRows) most = kFfmaCtas * kRows;
+  int64_t most = kFfmaCtas * 16;
+  if (rows > 16) most = kTreeCtas * (rows > 128 ? 256 : 128);
   return 2 * most * (d + 2) * 4;
 }
 
