@@ -364,78 +364,70 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 }
 
 // ------------------------------------------------------------------- join
-// A query row whose unit was shared is joined by `kSplit` warps: its parts lie
-// in the slots of consecutive CTAs, a warp takes every kSplit-th, four at a
-// time (the loads of four parts are in flight together), and the warps' sums
-// are added in order.  blockIdx.y is the sequence; the units' places follow
-// from the lengths, as in the walk.  Every slot of a shared unit has been
-// written, an empty part with l = 0 and o = 0.
+// Only units that the border between two CTAs' runs cuts have parts.
+// blockIdx.y is a unit, or, where there are fewer of those, such a border: the
+// first one inside a unit stands for it.  The blocks of others leave at once.
+// blockIdx.x is a group of the unit's rows.
+// A row is joined by kSplit warps: its parts lie in the slots of consecutive
+// CTAs, a warp takes every kSplit-th, four at a time (the loads of four parts
+// are in flight together), and the warps' sums are added in order.  Every slot
+// of a shared unit has been written, an empty part with l = 0 and o = 0.
 constexpr int kJoinWarps = 8;
+
+template <typename E, int kSplit>
+struct Join {
+  static constexpr int kStep = kJoinWarps / kSplit;  // rows at a time
+};
 
 template <typename E, int kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a,
-                           const __grid_constant__ AttnPlan p) {
+                           const __grid_constant__ AttnPlan p, int block_rows, bool by_unit) {
   __shared__ DivisionShared sh;
-  __shared__ int64_t before;
   __shared__ float4 sums[kJoinWarps][2][32];
   __shared__ float sum_l[kJoinWarps];
+  using J = Join<E, kSplit>;
   const PagedArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int sub = warp % kSplit;
-  const int64_t rows = head_rows(a);
-  const int64_t seq_rows = rows * c.heads;
-  for (int b = blockIdx.y; b < c.B; b += gridDim.y) {
-    // tiles (of one unit) of the sequences before b, and of all
+  int b, unit, c0, c1;
+  if (by_unit) {
+    b = blockIdx.y / p.div.units;
+    unit = blockIdx.y % p.div.units;
     int64_t ahead, total;
-    if (c.B <= 32) {
-      const int64_t upto = warp_scan(lane < c.B ? seq_tiles(c, p.div, lane) : 0);
-      ahead = b > 0 ? __shfl_sync(0xffffffffu, upto, b - 1) : 0;
-      total = __shfl_sync(0xffffffffu, upto, 31);
-    } else {
-      __syncthreads();
-      int64_t mine = 0, all = 0;
-      for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
-        const int64_t t = seq_tiles(c, p.div, i);
-        all += t;
-        if (i < b) mine += t;
-      }
-      const int64_t x = block_scan(mine, sh);
-      if (threadIdx.x == blockDim.x - 1) before = x;
-      __syncthreads();
-      block_scan(all, sh);
-      __syncthreads();
-      ahead = before;
-      total = sh.total;
-    }
-    if (c.count && blockIdx.x == 0 && threadIdx.x == 0 && c.lens[b] >= 0 && c.count[b] > c.T)
-      flag_page(c.status);
-    const int64_t per = run_length(p.div, total * p.div.units);
+    division_before(c, p.div, b, sh, ahead, total);
+    const int64_t tiles = seq_tiles(c, p.div, b), run = run_length(p.div, total * p.div.units);
+    const int64_t u0 = ahead * p.div.units + unit * tiles;
+    c0 = static_cast<int>(u0 / run);
+    c1 = static_cast<int>((u0 + tiles - 1) / run);
+    if (c0 == c1) return;
+  } else {
+    const int border = blockIdx.y + 1;
+    if (division_start(c, p.div, border, sh) == 0) return;
+    b = sh.b;
     const int64_t tiles = seq_tiles(c, p.div, b);
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinWarps / kSplit) + warp / kSplit;
-    int c0 = 0, c1 = 0, local = 0;
-    if (row < seq_rows) {
-      const int64_t in_head = row % rows;
-      const int unit = static_cast<int>(row / rows) * p.row_tiles +
-                       static_cast<int>(in_head / p.rows);
-      local = static_cast<int>(in_head % p.rows);
-      const int64_t u0 = ahead * p.div.units + unit * tiles;
-      c0 = static_cast<int>(u0 / per);
-      c1 = static_cast<int>((u0 + tiles - 1) / per);
-    }
-    const bool shared = c1 > c0;
-    wait_for_parts();
+    unit = static_cast<int>(sh.off / tiles);
+    const int64_t inside = sh.off - unit * tiles;  // tiles of the unit before the border
+    if (inside == 0 || inside > sh.run) return;    // a unit begins here, or was cut before
+    c0 = border - 1;
+    c1 = static_cast<int>((border * sh.run - inside + tiles - 1) / sh.run);
+  }
+  const int64_t rows = head_rows(a);
+  const int64_t r0 = static_cast<int64_t>(unit % p.row_tiles) * p.rows;
+  const int64_t q0 = (static_cast<int64_t>(b) * c.heads + unit / p.row_tiles) * rows + r0;
+  const int some = static_cast<int>(min(rows - r0, static_cast<int64_t>(p.rows)));
+  wait_for_parts();
+  const int begin = blockIdx.x * block_rows, end = min(some, begin + block_rows);
+  for (int first = begin; first < end; first += J::kStep) {
+    const int local = first + warp / kSplit;
+    const bool shared = local < end;
     float ms = -INFINITY, l = 0.f;
     float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     if (shared) {
-      for (int i = c0 + lane; i <= c1; i += 32)
-        ms = fmaxf(ms, slot_ml(a, p, 2 * i + (i == c0 ? 1 : 0))[2 * local]);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
-      const float ref = ms == -INFINITY ? 0.f : ms;
-      for (int i = c0 + sub; i <= c1; i += 4 * kSplit) {
-        float2 ml[4];
-        float4 y[4][2];
+      // the loads of four parts, which need no weight yet
+      float2 ml[4];
+      float4 y[4][2];
+      auto fetch = [&](int i) {
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const int at = i + z * kSplit;
@@ -450,6 +442,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             y[z][h] = real && 4 * (lane + 32 * h) < c.d ? src[lane + 32 * h]
                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+      };
+      fetch(c0 + sub);
+      for (int i = c0 + lane; i <= c1; i += 32)
+        ms = fmaxf(ms, slot_ml(a, p, 2 * i + (i == c0 ? 1 : 0))[2 * local]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
+      const float ref = ms == -INFINITY ? 0.f : ms;
+      for (int i = c0 + sub; i <= c1; i += 4 * kSplit) {
+        if (i > c0 + sub) fetch(i);
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const float w = ml[z].y == 0.f ? 0.f : exp2f(ml[z].x - ref);
@@ -465,6 +466,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       }
     }
     if (kSplit > 1) {
+      __syncthreads();
       sums[warp][0][lane] = o[0];
       sums[warp][1][lane] = o[1];
       if (lane == 0) sum_l[warp] = l;
@@ -485,34 +487,40 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     }
     if (shared && sub == 0) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t at = static_cast<int64_t>(b) * seq_rows + row;
-      E* dst = static_cast<E*>(a.out) + at * c.d;
+      E* dst = static_cast<E*>(a.out) + (q0 + local) * c.d;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int col = 4 * (lane + 32 * h);
         if (col < c.d) store4(dst + col, make_float4(o[h].x * inv, o[h].y * inv, o[h].z * inv, o[h].w * inv));
       }
-      if (lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (ms + log2f(l)) * kLn2F;
+      if (lane == 0) a.lse[q0 + local] = l == 0.f ? -INFINITY : (ms + log2f(l)) * kLn2F;
     }
   }
 }
 
 template <typename E, int kSplit>
 cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-  const int64_t seq_rows = head_rows(a) * a.c.heads;
-  constexpr int kRowsPerBlock = kJoinWarps / kSplit;
-  const dim3 grid(static_cast<unsigned>((seq_rows + kRowsPerBlock - 1) / kRowsPerBlock),
-                  static_cast<unsigned>(a.c.B < 65535 ? a.c.B : 65535));
+  using J = Join<E, kSplit>;
+  const int64_t rows = head_rows(a) < p.rows ? head_rows(a) : p.rows;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
+  // A block waits for its parts, so it takes rows one after another only where
+  // there would be more blocks than the SMs hold at once.
+  const int64_t steps = (rows + J::kStep - 1) / J::kStep;
+  const int64_t units = static_cast<int64_t>(a.c.B) * p.div.units, borders = p.div.ctas - 1;
+  const bool by_unit = units <= borders;
+  const int64_t held = static_cast<int64_t>(device_sm_count()) * 8;
+  const int64_t passes = (steps * (by_unit ? units : borders) + held - 1) / held;
+  const int block_rows = static_cast<int>(passes) * J::kStep;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + block_rows - 1) / block_rows),
+                     static_cast<unsigned>(by_unit ? units : borders));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<E, kSplit>, a, p);
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<E, kSplit>, a, p, block_rows, by_unit);
 }
 
 template <typename H, typename F>

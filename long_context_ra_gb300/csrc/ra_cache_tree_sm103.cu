@@ -76,20 +76,20 @@ struct Layout {
   static constexpr int kTile = kKeys * D * 2;
   static constexpr int kRawTile = kKeys * D;
   static constexpr int kStages = kTwo ? (D == 128 ? (k8 ? 3 : 5) : (k8 ? 5 : 8))
-                                      : (D == 128 ? (k8 ? 6 : 10) : (k8 ? 8 : 16));
-  static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 8 : 12);
+                                      : (D == 128 ? (k8 ? 6 : 9) : (k8 ? 8 : 16));
+  static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 12);
   static constexpr int kTeam = 128;  // threads that convert a tile
   static constexpr int kLoadStages = k8 ? kRawStages : kStages;  // of the ring the loader fills
-  // the second query tile, or the exchange of the two streams' states:
-  // [128][33] floats and [128][2]
-  static constexpr int kSecond = kTwo ? kQTile : 18 * 1024;
+  // the second query tile, or the exchange of the two streams' states: twice
+  // [128][33] floats, and [128][2]
+  static constexpr int kSecond = kTwo ? kQTile : 34 * 1024;
   static constexpr int kQ0 = 0;
   static constexpr int kQ1 = kQTile;
   static constexpr int kKV = kQTile + kSecond;
   static constexpr int kRaw = kKV + kStages * kTile;
   static constexpr int kRawExp = kRaw + kRawStages * kRawTile;
   static constexpr int kBar = kRawExp + kRawStages * kKeys;
-  static constexpr int kNumBars = 2 + 2 * kStages + 9 + kLoadStages + kRawStages;
+  static constexpr int kNumBars = 2 + 2 * kStages + 11 + kLoadStages + kRawStages;
   static constexpr int kMisc = (kBar + kNumBars * 8 + 15) / 16 * 16;  // TMEM base, abort flag
   // Rings of the last 32 units and key tiles: the loader is at most
   // kLoadStages + kStages <= 24 items (12 key tiles, 12 units) ahead.
@@ -115,11 +115,11 @@ struct Bars {
   __device__ uint32_t s_full(int t) const { return base + 8 * (2 + 2 * kS + t); }
   __device__ uint32_t p_full(int t) const { return base + 8 * (4 + 2 * kS + t); }
   __device__ uint32_t o_full(int t) const { return base + 8 * (6 + 2 * kS + t); }
-  __device__ uint32_t x_full() const { return base + 8 * (8 + 2 * kS); }
-  __device__ uint32_t x_empty() const { return base + 8 * (9 + 2 * kS); }
-  __device__ uint32_t drain() const { return base + 8 * (10 + 2 * kS); }
-  __device__ uint32_t raw_full(int s) const { return base + 8 * (11 + 2 * kS + s); }
-  __device__ uint32_t raw_empty(int s) const { return base + 8 * (11 + 2 * kS + L::kLoadStages + s); }
+  __device__ uint32_t x_full(int i) const { return base + 8 * (8 + 2 * kS + i); }
+  __device__ uint32_t x_empty(int i) const { return base + 8 * (10 + 2 * kS + i); }
+  __device__ uint32_t drain() const { return base + 8 * (12 + 2 * kS); }
+  __device__ uint32_t raw_full(int s) const { return base + 8 * (13 + 2 * kS + s); }
+  __device__ uint32_t raw_empty(int s) const { return base + 8 * (13 + 2 * kS + L::kLoadStages + s); }
 };
 
 // Position in a ring of stages.
@@ -281,8 +281,9 @@ __device__ __noinline__ uint32_t seen_word(const CacheAttnArgs& a, const SeqInfo
     const uint8_t* m = a.mask + b * a.mask_stride + static_cast<int64_t>(t) * a.c.T + j0;
     const int from = static_cast<int>(max(-j0, int64_t{0}));
     const int to = static_cast<int>(min(s.cnt - j0, int64_t{32}));
-#pragma unroll 4
-    for (int x = from; x < to; ++x) seen |= (m[x] != 0 ? 1u : 0u) << x;
+#pragma unroll
+    for (int x = 0; x < 32; ++x)  // all loads under way together
+      if (x >= from && x < to) seen |= (m[x] != 0 ? 1u : 0u) << x;
   }
 #pragma unroll
   for (int x = 0; x < 4; ++x)
@@ -363,8 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars.p_full(t), 128);
       mbar_init(bars.o_full(t), 1);
     }
-    mbar_init(bars.x_full(), 128);
-    mbar_init(bars.x_empty(), 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars.x_full(i), 128);
+      mbar_init(bars.x_empty(i), 128);
+    }
     mbar_init(bars.drain(), 1);
     *ab.flag = 0u;
     for (int i = 0; i < 32; ++i) poison[i] = 0u;
@@ -391,17 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t left = rows - un.r0;
       const int pieces = (kTwo && left > 128 ? 256 : 128) * (D / 8);
       const uint8_t* src = static_cast<const uint8_t*>(a.q) + un.q0 * (2 * D);
-      for (int i0 = id; i0 < pieces; i0 += 4 * count) {
-        uint4 q[4];
+      for (int i0 = id; i0 < pieces; i0 += 5 * count) {
+        uint4 q[5];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 5; ++x) {
           const int i = i0 + x * count;
           q[x] = make_uint4(0u, 0u, 0u, 0u);
           if (i < pieces && i / (D / 8) < left)
             q[x] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(i) * 16);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 5; ++x) {
           const int i = i0 + x * count;
           if (i >= pieces) break;
           const int r = i / (D / 8), pc = i % (D / 8);
@@ -784,8 +787,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(t * 128);
     const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(t * D);
     const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2);
-    float* xo = reinterpret_cast<float*>(gbase + L::kQ1);  // [128][33]
-    float* xml = xo + 128 * 33;                            // [128][2]
+    float* xo = reinterpret_cast<float*>(gbase + L::kQ1);  // [2][128][33]
+    float* xml = xo + 2 * 128 * 33;                        // [128][2]
     uint32_t ns = 0, no = 0, unit = 0, xc = 0, kt = 0;     // phases; K tiles before the unit
     bool ok = true;
     UnitWalk& u = reinterpret_cast<UnitWalk*>(gbase + L::kWalks)[warp];
@@ -928,7 +931,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool exchange = !kTwo && n > 1;
       float f0 = 1.f, f1 = 0.f;  // weights of the two streams' sums
       if (exchange && t == 1) {
-        if (!wait_warp(bars.x_empty(), (xc & 1u) ^ 1u, ab)) {
+        // chunk 0 of the unit before has been read, and with it m and l
+        if (!wait_warp(bars.x_empty(xc & 1u), ((xc >> 1) & 1u) ^ 1u, ab)) {
           ok = false;
           break;
         }
@@ -951,18 +955,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!kTwo && t == 1) {
             if (!exchange) break;
-            if (x > 0 && !wait_warp(bars.x_empty(), (xc & 1u) ^ 1u, ab)) {
+            if (x > 0 && !wait_warp(bars.x_empty(xc & 1u), ((xc >> 1) & 1u) ^ 1u, ab)) {
               ok = false;
               break;
             }
+            float* to = xo + ((xc & 1u) * 128 + row) * 33;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) xo[row * 33 + e] = __uint_as_float(r[e]);
-            mbar_arrive(bars.x_full());
+            for (int e = 0; e < 32; ++e) to[e] = __uint_as_float(r[e]);
+            mbar_arrive(bars.x_full(xc & 1u));
             ++xc;
             continue;
           }
           if (exchange) {
-            if (!wait_warp(bars.x_full(), xc & 1u, ab)) {
+            if (!wait_warp(bars.x_full(xc & 1u), (xc >> 1) & 1u, ab)) {
               ok = false;
               break;
             }
@@ -974,14 +979,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               l = f0 * l + f1 * l1;
               m_ref = ms;
             }
+            const float* from = xo + ((xc & 1u) * 128 + row) * 33;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const float y = xo[row * 33 + e];
+              const float y = from[e];
               float z = f0 == 0.f ? 0.f : f0 * __uint_as_float(r[e]);
               if (f1 != 0.f) z = fmaf(f1, y, z);
               r[e] = __float_as_uint(z);
             }
-            mbar_arrive(bars.x_empty());
+            mbar_arrive(bars.x_empty(xc & 1u));
             ++xc;
           }
           if (x == 0 && whole) inv = l == 0.f ? 0.f : 1.f / l;

@@ -217,6 +217,7 @@ struct DivisionShared {
   int64_t total;  // tiles of all sequences (one unit each)
   int64_t off;    // of the CTA's first tile within its sequence's tiles
   int b;          // sequence of the CTA's first tile
+  int64_t run;    // tiles of a CTA
 };
 
 // Inclusive scan of one value per thread; sh.total = the sum.
@@ -265,7 +266,10 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
       // one lane of every warp: all write the same
       sh.b = lane;
       sh.off = begin - (upto - tiles);
+      sh.run = run;
     }
+    if (cta == 0 && c.count && lane < c.B && c.lens[lane] >= 0 && c.count[lane] > c.T)
+      flag_page(c.status);
     __syncthreads();
     return begin >= all ? 0 : min(run, all - begin);
   }
@@ -273,7 +277,10 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
   const int b0 = min(c.B, static_cast<int>(threadIdx.x) * per_thread);
   const int b1 = min(c.B, b0 + per_thread);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_tiles(c, v, b);
+  for (int b = b0; b < b1; ++b) {
+    mine += seq_tiles(c, v, b);
+    if (cta == 0 && c.count && c.lens[b] >= 0 && c.count[b] > c.T) flag_page(c.status);
+  }
   int64_t at = block_scan(mine, sh) - mine;
   __syncthreads();
   const int64_t all = sh.total * v.units;
@@ -285,6 +292,7 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
       if (begin < (at + t) * v.units) {
         sh.b = b;
         sh.off = begin - at * v.units;
+        sh.run = run;
         break;
       }
       at += t;
@@ -293,6 +301,32 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
   __syncthreads();
   if (begin >= all) return 0;
   return min(run, all - begin);
+}
+
+// Tiles (of one unit) of the sequences before b, and of all.  All threads of
+// the block take part.
+__device__ __forceinline__ void division_before(const PagedArgs& c, const Division& v, int b,
+                                                DivisionShared& sh, int64_t& ahead, int64_t& total) {
+  if (c.B <= 32) {
+    const int lane = threadIdx.x % 32;
+    const int64_t upto = warp_scan(lane < c.B ? seq_tiles(c, v, lane) : 0);
+    ahead = b > 0 ? __shfl_sync(0xffffffffu, upto, b - 1) : 0;
+    total = __shfl_sync(0xffffffffu, upto, 31);
+    return;
+  }
+  int64_t mine = 0, all = 0;
+  for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+    const int64_t t = seq_tiles(c, v, i);
+    all += t;
+    if (i < b) mine += t;
+  }
+  block_scan(mine, sh);
+  __syncthreads();
+  ahead = sh.total;
+  __syncthreads();
+  block_scan(all, sh);
+  __syncthreads();
+  total = sh.total;
 }
 
 // Walks a CTA's run unit by unit.
