@@ -80,9 +80,9 @@ struct Layout {
   static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 12);
   static constexpr int kTeam = 128;  // threads that convert a tile
   static constexpr int kLoadStages = k8 ? kRawStages : kStages;  // of the ring the loader fills
-  // the second query tile, or the exchange of the two streams' states: twice
-  // [128][33] floats, and [128][2]
-  static constexpr int kSecond = kTwo ? kQTile : 34 * 1024;
+  // the second query tile, or the exchange of the two streams' states: per
+  // stream [128][33] floats, and [128][2]
+  static constexpr int kSecond = kTwo ? kQTile : 36 * 1024;
   static constexpr int kQ0 = 0;
   static constexpr int kQ1 = kQTile;
   static constexpr int kKV = kQTile + kSecond;
@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = static_cast<int>(w.last - w.first);
         const int64_t before = w.first * kKeys;
         const int keys = static_cast<int>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
+        const int context = static_cast<int>(min(w.seq.len - before, static_cast<int64_t>(n) * kKeys));
         const int from =
             static_cast<int>(min(max(w.seq.len / kKeys - w.first, int64_t{0}), static_cast<int64_t>(n)));
         for (int tile = from; tile < n; ++tile) {
@@ -515,17 +516,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           used ^= 1u << stage;
           bool bad = false;
-          const uint32_t at = base + L::kKV + stage * L::kTile;
+          // the rows behind the context, 16-byte pieces, four at a time
+          const uint32_t at = base + L::kKV + stage * L::kTile + (lane % 8) * 16;
+          const int skip = max(context - tile * kKeys, 0);
+          constexpr int kBoxes = D / 64;
 #pragma unroll 1
-          for (int i = lane; i < kKeys * D / 8; i += 32) {  // 16-byte pieces, box by box
-            const uint4 y = lds128(at + i * 16);
-            const uint32_t n0 = not_finite(y.x), n1 = not_finite(y.y), n2 = not_finite(y.z),
-                           n3 = not_finite(y.w);
-            if (tile * kKeys + (i / 8) % kKeys >= keys) {
-              st_shared_v4(at + i * 16, 0u, 0u, 0u, 0u);
-            } else if (n0 | n1 | n2 | n3) {
-              bad = true;
-              st_shared_v4(at + i * 16, y.x & ~n0, y.y & ~n1, y.z & ~n2, y.w & ~n3);
+          for (int i0 = skip + lane / 8; i0 < kKeys; i0 += 16 / kBoxes) {
+            uint4 y[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int r = i0 + 4 * (z / kBoxes);
+              y[z] = r < kKeys ? lds128(at + (z % kBoxes) * L::kBox + r * 128) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int r = i0 + 4 * (z / kBoxes);
+              const uint32_t n0 = not_finite(y[z].x), n1 = not_finite(y[z].y), n2 = not_finite(y[z].z),
+                             n3 = not_finite(y[z].w);
+              if (r >= kKeys) continue;
+              const uint32_t to = at + (z % kBoxes) * L::kBox + r * 128;
+              if (tile * kKeys + r >= keys) {
+                st_shared_v4(to, 0u, 0u, 0u, 0u);
+              } else if (n0 | n1 | n2 | n3) {
+                bad = true;
+                st_shared_v4(to, y[z].x & ~n0, y[z].y & ~n1, y[z].z & ~n2, y[z].w & ~n3);
+              }
             }
           }
           if (bad) poison[ord & 31] = ord + 1u;
@@ -788,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(t * D);
     const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2);
     float* xo = reinterpret_cast<float*>(gbase + L::kQ1);  // [2][128][33]
-    float* xml = xo + 2 * 128 * 33;                        // [128][2]
+    float* xml = xo + 2 * 128 * 33;                        // [2][128][2]
     uint32_t ns = 0, no = 0, unit = 0, xc = 0, kt = 0;     // phases; K tiles before the unit
     bool ok = true;
     UnitWalk& u = reinterpret_cast<UnitWalk*>(gbase + L::kWalks)[warp];
@@ -927,59 +942,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool poisoned = poison[unit & 31] == unit + 1u;
 
-      // ---- one query tile: stream 1 hands its state to stream 0
+      // ---- one query tile: the streams exchange halves of their states, so
+      // that each finishes half of the columns
       const bool exchange = !kTwo && n > 1;
-      float f0 = 1.f, f1 = 0.f;  // weights of the two streams' sums
-      if (exchange && t == 1) {
-        // chunk 0 of the unit before has been read, and with it m and l
-        if (!wait_warp(bars.x_empty(xc & 1u), ((xc >> 1) & 1u) ^ 1u, ab)) {
-          ok = false;
-          break;
-        }
-        xml[2 * row] = m_ref;
-        xml[2 * row + 1] = l;
-      }
-      if (kTwo ? active : true) {
+      float f0 = 1.f, f1 = 0.f;  // weights of this stream's and the other's sums
+      if (kTwo ? active : t == 0 || exchange) {
         const Unit un(a, p, u, rows);
         const bool whole = u.whole();
         const int slot = u.slot(blockIdx.x);
         const int local = (kTwo ? t * 128 : 0) + row;
+        const int first = exchange ? t * (D / 2) : 0;
+        const int count = exchange ? D / 64 : D / 32;
         float inv = 1.f;
 #pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
+        for (int i = 0; i < count; ++i) {
+          const int x = first + 32 * i;
           uint32_t r[32];
-          if (active) {
-            tmem_ld32(tO + x, r);
+          if (exchange) {
+            // the other's half of this stream, through this stream's buffer
+            if (!wait_warp(bars.x_empty(t), (xc & 1u) ^ 1u, ab)) {
+              ok = false;
+              break;
+            }
+            if (i == 0) {
+              xml[(t * 128 + row) * 2] = m_ref;
+              xml[(t * 128 + row) * 2 + 1] = l;
+            }
+            tmem_ld32(tO + (D / 2 - first) + 32 * i, r);
             tmem_ld_wait();
             reg_fence(r, 32);
-          }
-          if (!kTwo && t == 1) {
-            if (!exchange) break;
-            if (x > 0 && !wait_warp(bars.x_empty(xc & 1u), ((xc >> 1) & 1u) ^ 1u, ab)) {
-              ok = false;
-              break;
-            }
-            float* to = xo + ((xc & 1u) * 128 + row) * 33;
+            float* to = xo + (t * 128 + row) * 33;
 #pragma unroll
             for (int e = 0; e < 32; ++e) to[e] = __uint_as_float(r[e]);
-            mbar_arrive(bars.x_full(xc & 1u));
-            ++xc;
-            continue;
+            mbar_arrive(bars.x_full(t));
           }
+          tmem_ld32(tO + x, r);
+          tmem_ld_wait();
+          reg_fence(r, 32);
           if (exchange) {
-            if (!wait_warp(bars.x_full(xc & 1u), (xc >> 1) & 1u, ab)) {
+            if (!wait_warp(bars.x_full(1 - t), xc & 1u, ab)) {
               ok = false;
               break;
             }
-            if (x == 0) {
-              const float m1 = xml[2 * row], l1 = xml[2 * row + 1];
+            if (i == 0) {
+              const float m1 = xml[((1 - t) * 128 + row) * 2], l1 = xml[((1 - t) * 128 + row) * 2 + 1];
               const float ms = fmaxf(m_ref, m1);
               f0 = l == 0.f ? 0.f : ex2(m_ref - ms);
               f1 = l1 == 0.f ? 0.f : ex2(m1 - ms);
               l = f0 * l + f1 * l1;
               m_ref = ms;
             }
-            const float* from = xo + ((xc & 1u) * 128 + row) * 33;
+            const float* from = xo + ((1 - t) * 128 + row) * 33;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float y = from[e];
@@ -987,10 +1000,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (f1 != 0.f) z = fmaf(f1, y, z);
               r[e] = __float_as_uint(z);
             }
-            mbar_arrive(bars.x_empty(xc & 1u));
+            mbar_arrive(bars.x_empty(1 - t));
             ++xc;
           }
-          if (x == 0 && whole) inv = l == 0.f ? 0.f : 1.f / l;
+          if (i == 0 && whole) inv = l == 0.f ? 0.f : 1.f / l;
           if (l == 0.f) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0u;
