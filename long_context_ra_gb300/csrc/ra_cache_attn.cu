@@ -372,6 +372,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 // CTAs, a warp takes every kSplit-th, four at a time (the loads of four parts
 // are in flight together), and the warps' sums are added in order.  Every slot
 // of a shared unit has been written, an empty part with l = 0 and o = 0.
+// A lane holds kCols times 4 columns: 1 up to d = 128, which keeps the block at
+// 64 registers a thread, four blocks on an SM (8 sequences of 32 tokens: 97.7
+// -> 96.2 us; eight parts in flight take 98 registers: 100.3 us).
 constexpr int kJoinWarps = 8;
 
 template <typename E, int kSplit>
@@ -379,14 +382,15 @@ struct Join {
   static constexpr int kStep = kJoinWarps / kSplit;  // rows at a time
 };
 
-template <typename E, int kSplit>
+template <typename E, int kSplit, int kCols>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a,
                            const __grid_constant__ AttnPlan p, int block_rows, bool by_unit) {
   __shared__ DivisionShared sh;
-  __shared__ float4 sums[kJoinWarps][2][32];
+  __shared__ float4 sums[kJoinWarps][kCols][32];
   __shared__ float sum_l[kJoinWarps];
   using J = Join<E, kSplit>;
+  constexpr int kParts = 4;
   const PagedArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int sub = warp % kSplit;
@@ -416,47 +420,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int64_t r0 = static_cast<int64_t>(unit % p.row_tiles) * p.rows;
   const int64_t q0 = (static_cast<int64_t>(b) * c.heads + unit / p.row_tiles) * rows + r0;
   const int some = static_cast<int>(min(rows - r0, static_cast<int64_t>(p.rows)));
+  // rows of all slots: fewer than 2^17, of d floats each
+  const float2* all_ml = reinterpret_cast<const float2*>(slot_ml(a, p, 0));
+  const float4* all_o = reinterpret_cast<const float4*>(slot_o(a, p, 0));
+  const uint32_t quads = c.d / 4;
   wait_for_parts();
   const int begin = blockIdx.x * block_rows, end = min(some, begin + block_rows);
   for (int first = begin; first < end; first += J::kStep) {
     const int local = first + warp / kSplit;
     const bool shared = local < end;
     float ms = -INFINITY, l = 0.f;
-    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float4 o[kCols];
+#pragma unroll
+    for (int h = 0; h < kCols; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (shared) {
-      // the loads of four parts, which need no weight yet
-      float2 ml[4];
-      float4 y[4][2];
+      // the loads of a round's parts, which need no weight yet
+      float2 ml[kParts];
+      float4 y[kParts][kCols];
       auto fetch = [&](int i) {
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
+        for (int z = 0; z < kParts; ++z) {
           const int at = i + z * kSplit;
           const bool real = at <= c1;
-          const int slot = real ? 2 * at + (at == c0 ? 1 : 0) : 0;
-          ml[z] = real ? *reinterpret_cast<const float2*>(slot_ml(a, p, slot) + 2 * local)
-                       : make_float2(-INFINITY, 0.f);
-          const float4* src =
-              reinterpret_cast<const float4*>(slot_o(a, p, slot) + static_cast<int64_t>(local) * c.d);
+          const uint32_t row = (2u * at + (at == c0 ? 1u : 0u)) * p.rows + local;
+          ml[z] = real ? all_ml[row] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            y[z][h] = real && 4 * (lane + 32 * h) < c.d ? src[lane + 32 * h]
-                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int h = 0; h < kCols; ++h)
+            y[z][h] = real && lane + 32 * h < quads ? all_o[row * quads + lane + 32 * h]
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       };
       fetch(c0 + sub);
       for (int i = c0 + lane; i <= c1; i += 32)
-        ms = fmaxf(ms, slot_ml(a, p, 2 * i + (i == c0 ? 1 : 0))[2 * local]);
+        ms = fmaxf(ms, all_ml[(2u * i + (i == c0 ? 1u : 0u)) * p.rows + local].x);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
       const float ref = ms == -INFINITY ? 0.f : ms;
-      for (int i = c0 + sub; i <= c1; i += 4 * kSplit) {
+      for (int i = c0 + sub; i <= c1; i += kParts * kSplit) {
         if (i > c0 + sub) fetch(i);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
+        for (int z = 0; z < kParts; ++z) {
           const float w = ml[z].y == 0.f ? 0.f : exp2f(ml[z].x - ref);
           l = fmaf(w, ml[z].y, l);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kCols; ++h) {
             o[h].x = fmaf(w, y[z][h].x, o[h].x);
             o[h].y = fmaf(w, y[z][h].y, o[h].y);
             o[h].z = fmaf(w, y[z][h].z, o[h].z);
@@ -467,15 +474,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     }
     if (kSplit > 1) {
       __syncthreads();
-      sums[warp][0][lane] = o[0];
-      sums[warp][1][lane] = o[1];
+#pragma unroll
+      for (int h = 0; h < kCols; ++h) sums[warp][h][lane] = o[h];
       if (lane == 0) sum_l[warp] = l;
       __syncthreads();
       if (sub == 0) {
         for (int z = 1; z < kSplit; ++z) {
           l += sum_l[warp + z];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kCols; ++h) {
             const float4 y = sums[warp + z][h][lane];
             o[h].x += y.x;
             o[h].y += y.y;
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       E* dst = static_cast<E*>(a.out) + (q0 + local) * c.d;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kCols; ++h) {
         const int col = 4 * (lane + 32 * h);
         if (col < c.d) store4(dst + col, make_float4(o[h].x * inv, o[h].y * inv, o[h].z * inv, o[h].w * inv));
       }
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
-template <typename E, int kSplit>
+template <typename E, int kSplit, int kCols>
 cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   using J = Join<E, kSplit>;
   const int64_t rows = head_rows(a) < p.rows ? head_rows(a) : p.rows;
@@ -520,7 +527,14 @@ cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<E, kSplit>, a, p, block_rows, by_unit);
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<E, kSplit, kCols>, a, p, block_rows, by_unit);
+}
+
+template <int kSplit>
+cudaError_t join_s(const CacheAttnArgs& a, const AttnPlan& p, bool bf16, cudaStream_t s) {
+  if (a.c.d <= 128)
+    return bf16 ? join_t<__nv_bfloat16, kSplit, 1>(a, p, s) : join_t<float, kSplit, 1>(a, p, s);
+  return bf16 ? join_t<__nv_bfloat16, kSplit, 2>(a, p, s) : join_t<float, kSplit, 2>(a, p, s);
 }
 
 template <typename H, typename F>
@@ -568,12 +582,15 @@ cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
                                    cudaStream_t s) {
-  // A unit is shared by about ctas / units CTAs.  A warp takes the parts of a
-  // row four at a time; with more than two such rounds several share the row.
+  // A unit is shared by about ctas / units CTAs, and a row's parts are taken
+  // four at a time.  Several warps for a row shorten that chain, but then there
+  // are more blocks, and a block's own start costs as much as a round or two
+  // (8 units of 128 rows over 152 CTAs, the whole call: 1, 2, 4, 8 warps 77.8,
+  // 78.6, 81.9, 82.7 us; 1 unit over 304 CTAs, 1 row: 2 or 8 warps 27.6, 20.2 us).
   const int64_t units = static_cast<int64_t>(a.c.B) * p.div.units;
-  if (p.div.ctas > 48 * units) return bf16 ? join_t<__nv_bfloat16, 8>(a, p, s) : join_t<float, 8>(a, p, s);
-  if (p.div.ctas > 8 * units) return bf16 ? join_t<__nv_bfloat16, 2>(a, p, s) : join_t<float, 2>(a, p, s);
-  return bf16 ? join_t<__nv_bfloat16, 1>(a, p, s) : join_t<float, 1>(a, p, s);
+  if (p.div.ctas > 48 * units) return join_s<8>(a, p, bf16, s);
+  if (p.div.ctas > 16 * units) return join_s<2>(a, p, bf16, s);
+  return join_s<1>(a, p, bf16, s);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dtype held,

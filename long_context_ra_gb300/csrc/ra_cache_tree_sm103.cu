@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The unit's queries, by `count` threads of which this is `id`.
     auto load_queries = [&](const UnitWalk& w, uint32_t ord, int id, int count) {
       const Unit un(a, p, w, rows);
-      if (!wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) return false;
       const int64_t left = rows - un.r0;
       const int pieces = (kTwo && left > 128 ? 256 : 128) * (D / 8);
       const uint8_t* src = static_cast<const uint8_t*>(a.q) + un.q0 * (2 * D);
@@ -403,6 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i < pieces && i / (D / 8) < left)
             q[x] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(i) * 16);
         }
+        // the first loads are on their way before the unit before is done
+        if (i0 == id && !wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) return false;
 #pragma unroll
         for (int x = 0; x < 5; ++x) {
           const int i = i0 + x * count;
@@ -703,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(bars.s_full(1));
           }
           mma_commit(bars.kv_empty(sk));
+          if (n == 1) mma_commit(bars.q_empty());
           for (int it = 0; it < n; ++it) {
             const int sv = take();
             if (sv < 0 || !wait1(bars.p_full(0), np0++ & 1u, ab)) {
@@ -738,10 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(bars.s_full(1));
               }
               mma_commit(bars.kv_empty(sk));
+              if (it + 2 == n) mma_commit(bars.q_empty());  // the last scores
             }
           }
           if (ok) {
-            mma_commit(bars.q_empty());
             mma_commit(bars.o_full(0));
             if (two) mma_commit(bars.o_full(1));
           }
@@ -759,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(bars.s_full(1));
             mma_commit(bars.kv_empty(sk));
           }
+          if (n <= 2) mma_commit(bars.q_empty());
           for (int it = 0; it < n; ++it) {
             const int t = it & 1;
             const int sv = take();
@@ -779,10 +782,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               issue_qk<D, kKeys>(tS, dQ0, dK + desc_step(sk * L::kTile));
               mma_commit(bars.s_full(t));
               mma_commit(bars.kv_empty(sk));
+              if (it + 3 == n) mma_commit(bars.q_empty());  // the last scores
             }
           }
           if (ok) {
-            mma_commit(bars.q_empty());
             mma_commit(bars.o_full(0));
             if (n > 1) mma_commit(bars.o_full(1));
           }
