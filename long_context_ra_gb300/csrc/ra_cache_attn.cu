@@ -366,7 +366,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 // ------------------------------------------------------------------- join
 // Only units that the border between two CTAs' runs cuts have parts.
 // blockIdx.y is a unit, or, where there are fewer of those, such a border: the
-// first one inside a unit stands for it.  The blocks of others leave at once.
+// first one inside a unit stands for it.  The blocks of others have nothing to
+// join, but wait as well: what follows the join on the stream may only begin
+// when the kernel before it has ended.
 // blockIdx.x is a group of the unit's rows.
 // A row is joined by kSplit warps: its parts lie in the slots of consecutive
 // CTAs, a warp takes every kSplit-th, four at a time (the loads of four parts
@@ -404,15 +406,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const int64_t u0 = ahead * p.div.units + unit * tiles;
     c0 = static_cast<int>(u0 / run);
     c1 = static_cast<int>((u0 + tiles - 1) / run);
-    if (c0 == c1) return;
+    if (c0 == c1) return wait_for_parts();
   } else {
     const int border = blockIdx.y + 1;
-    if (division_start(c, p.div, border, sh) == 0) return;
+    if (division_start(c, p.div, border, sh) == 0) return wait_for_parts();
     b = sh.b;
     const int64_t tiles = seq_tiles(c, p.div, b);
     unit = static_cast<int>(sh.off / tiles);
     const int64_t inside = sh.off - unit * tiles;  // tiles of the unit before the border
-    if (inside == 0 || inside > sh.run) return;    // a unit begins here, or was cut before
+    // a unit begins here, or was cut before
+    if (inside == 0 || inside > sh.run) return wait_for_parts();
     c0 = border - 1;
     c1 = static_cast<int>((border * sh.run - inside + tiles - 1) / sh.run);
   }

@@ -276,6 +276,35 @@ def test_two_captured_graphs_run_side_by_side(T):
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("dtype,held,B,T", [(BF16, BF16, 38, 1), (BF16, E4M3, 38, 1), (BF16, BF16, 19, 20),
+                                            (BF16, E4M3, 19, 40), (torch.float32, torch.float32, 76, 1)])
+def test_the_next_kernel_sees_the_whole_result(dtype, held, B, T):
+    """Equal lengths and as many units as CTAs: no unit is shared, so nothing
+    is joined, and what follows on the stream still comes after every CTA."""
+    heads, page, n = 8, 64, 1500
+    per = -(-(n + T) // page)
+    cache = ra.new_cache(B * per, heads, page, 64, held)
+    table = torch.arange(B * per, dtype=torch.int32, device=DEV).reshape(B, per)
+    x = rnd(3, 2, B, heads, n + T, 64, dtype=dtype)
+    ra.ra_cache_write(cache, x[0], x[1], table, i32(*[0] * B))
+    q = rnd(4, B, heads * (4 if T > 1 else 1), T, 64, dtype=dtype)
+    lens = i32(*[n] * B)
+    out, lse = ra.ra_cache_attention(q, cache, table, lens)
+    torch.cuda.synchronize()
+    assert out.abs().amax(-1).min() > 0
+    out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    ws = torch.empty(ra.ra_cache_attention_workspace_bytes(B, q.shape[1], heads, T, 64), device=DEV,
+                     dtype=torch.uint8)
+    copies = []
+    for _ in range(20):
+        out2.zero_()
+        lse2.zero_()
+        ra.ra_cache_attention(q, cache, table, lens, out=out2, lse=lse2, workspace=ws)
+        copies.append((out2.clone(), lse2.clone()))
+    for o, s in copies:
+        assert torch.equal(o, out) and torch.equal(s, lse)
+
+
 def test_calls_on_a_given_stream():
     """stream=: work and the call's own allocations belong to that stream."""
     heads, Hq, d, page, L, T = 2, 8, 64, 32, 700, 20
