@@ -293,7 +293,8 @@ RA_API ra_status ra_cache_read(const ra_cache* cache, const int32_t* table, int3
   if ((st = device_ready(&a.c.status)) != RA_OK) return st;
   a.k = k;
   a.v = v;
-  a.first = first;
+  // lens is an int32: behind 2^31 every row is 0, and first + n must not wrap
+  a.first = first < kMaxTokens + 1 ? first : kMaxTokens + 1;
   a.n = n;
   return launched(launch_cache_read(a, dtype, cache->dtype, cu(stream)));
 }

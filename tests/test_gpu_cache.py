@@ -201,6 +201,21 @@ def test_positions_outside_the_cache_touch_nothing(what):
                 assert not rk[b, :, lens[b] + t].any()
 
 
+@pytest.mark.parametrize("first", [200, 2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1, 2 ** 63 - 40])
+def test_reading_behind_the_end_gives_zeros(first):
+    cache = filled_cache(4, 2, 64, 64, torch.bfloat16, 9)
+    table = torch.tensor([[2, 0, 3], [1, 0, 2]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([190, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    k, v = ra.ra_cache_read(cache, table, lens[:1].repeat(2), first, 70)
+    assert not k.any() and not v.any()
+    assert _native.lib().ra_last_device_status(None) == _native.RA_OK
+    # a length beyond the table: zeros too, and the status says so
+    k, v = ra.ra_cache_read(cache, table, lens, first, 70)
+    assert not k.any() and not v.any()
+    assert _native.lib().ra_last_device_status(None) == (
+        _native.RA_ERR_PAGE if first < 2 ** 31 - 1 else _native.RA_OK)
+
+
 def test_rows_of_other_sequences_and_pages_are_left():
     """Guard rows: only the new tokens' rows change."""
     table, pages = R.make_paged([40], 16, 11, spare=4)
