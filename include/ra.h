@@ -471,6 +471,7 @@ RA_API int64_t ra_qk_norm_rope_backward_workspace_bytes(int32_t d);
  *   dtype         RA_F32 or RA_BF16 (the inputs' own type), or RA_E4M3 with
  *                 inputs of either type.
  *   page          a power of two, 8 .. 1024.   d: a multiple of 8, <= 256.
+ *   pages * heads at most 2^31 - 1.
  * k, v are 16-byte aligned, k_exp and v_exp 8-byte.
  *
  * The cache calls share these arguments:
@@ -504,7 +505,8 @@ typedef struct ra_cache {
  * row's finite elements (at least -126), code = e4m3(x * 2^-e), nearest
  * even.  The scale is a power of two, so both products are exact and a row
  * that is read and written again keeps its values.  Infinities saturate to
- * 448 * 2^e; NaN stays NaN.
+ * 448 * 2^e; NaN stays NaN.  (Magnitudes from 1.9375 * 2^127 on round up to
+ * 2^128, which reads back as infinity.)
  *   k, v  [B, heads, T, d] of `dtype`, strides as in ra_qk_norm_rope.
  * Tokens of one call must go to different places: sequences that share a
  * page may share only pages that the call does not write.  lens is not
@@ -550,7 +552,8 @@ RA_API ra_status ra_cache_read(const ra_cache* cache, const int32_t* table, int3
  *              overwritten (no initial value needed).  Calls that may
  *              overlap on the GPU, captured ones too, need their own.
  * An element that is not finite, in a key or value row that a query does
- * not see, does not reach that query's result.
+ * not see, does not reach that query's result.  Of a value row that it sees,
+ * it makes that column of the result infinite or NaN.
  * Types: RA_BF16 inputs over an RA_BF16 or RA_E4M3 cache run on the tensor
  * cores (d in {64, 128}); RA_F32 inputs over an RA_F32 or RA_E4M3 cache on
  * the FFMA path (any d the cache may have).
@@ -620,8 +623,10 @@ RA_API ra_status ra_merge(const ra_state* partials, int32_t G, void* out, float*
 
 /*
  * ra_watchdog_config -- settings of the bounded waits in the tensor-core
- * kernels (bf16 forward, fold, partial, split and backward calls).  The
- * pages have no counterpart: it belongs to the library's failure detection.
+ * kernels (bf16 forward, fold, partial, split and backward calls, and the
+ * kernel of ra_cache_attention for more than 16 query rows per key head; 32
+ * over an RA_E4M3 cache).  The pages have no counterpart: it belongs to the
+ * library's failure detection.
  *   wait_cycles  SM clock cycles one wait of a kernel may take before the
  *                kernel gives up: it records RA_ERR_TIMEOUT (read by
  *                ra_last_device_status), lets the copies and products it
@@ -630,7 +635,8 @@ RA_API ra_status ra_merge(const ra_state* partials, int32_t G, void* out, float*
  *   stall_cta    a test aid: >= 0 makes the CTA with this index of every
  *                later tensor-core launch (the fold kernel of the forward,
  *                causal, partial, fold and split calls; the dK/dV and dQ
- *                kernels of the backward calls) load no input, so that its
+ *                kernels of the backward calls; the many-row kernel of
+ *                ra_cache_attention) load no input, so that its
  *                waits run out and the call reports RA_ERR_TIMEOUT; the rows
  *                of that CTA are then not written.  -1 (the default) turns
  *                it off.

@@ -30,6 +30,12 @@
 //
 // As in the forward, the reference of the exponentials moves only when a
 // score passes it by more than 2^8: a vote per chunk instead of a row maximum.
+//
+// Measured, 32 ragged sequences of up to 32768, 8 key heads of 128, 4 queries
+// each: 8-bit cache (1.25 GB) 226 us, 5.5 TB/s, 81 % of the copy rate.  With 64
+// keys a chunk it took 348 us, with 32 and V behind all of K 303; the packed
+// conversions made that 230.  One sequence of 1000 takes 12 us, most of it the
+// two launches and the chain of look-up, load and join.
 
 #include "ra_cache_attn.cuh"
 #include "sm103_ptx.cuh"

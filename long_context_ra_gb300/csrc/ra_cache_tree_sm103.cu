@@ -34,9 +34,22 @@
 // exact in bf16 for values above 2^-126, and neither the scores nor the
 // probabilities need to know the scale.
 //
-// Every role is a short loop in 32-bit arithmetic with the unit's constants
-// taken out: a tile of 128 keys is 1.1 us of tensor time, and a role of one
-// warp that spends 200 instructions on an item is slower than that.
+// Code size sets the pace before anything else: 20 warps in five roles share
+// one instruction cache.  With the score and exponential loops unrolled a tile
+// of 128 keys and 256 rows took 7.3 us; rolled, 3.  Every role is a short loop
+// in 32-bit arithmetic with the unit's constants taken out: a role of one warp
+// that spends some hundred instructions on an item is slower than the 1.1 us
+// of tensor time that the tile needs.
+//
+// Measured per tile of 128 keys on one SM (152 at work, d = 128): one query
+// tile, bf16 1.6 us (the tile's bytes alone take 1.5 at the copy rate), 8 bits
+// 1.9; two query tiles, bf16 2.0 us, 8 bits 2.35 (without conversion 2.0,
+// without softmax 1.9: both share the issue slots with the issuer's warp).
+// 512 rows over 2^20 keys of 8 heads out of 8 bits: 1.95 ms, 57 % of the tensor
+// rate.  A unit more on a CTA costs about 10 us beside its tiles: pipeline
+// start (the scores of the first tile wait for the queries, the results for
+// the last), 3 us of epilogue, 3 of queries.  So the next unit's queries load
+// as soon as the last scores of the present one are out.
 //
 // Unseen drafts: their scores are -inf, so p = 0; value rows of tiles with
 // drafts are looked through for elements that are not finite.  Those become 0
@@ -438,8 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = static_cast<int>(w.last - w.first);
         // keys and context keys of this part
         const int64_t before = w.first * kKeys;
-        const int keys = static_cast<int>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
-        const int context = static_cast<int>(min(w.seq.len - before, static_cast<int64_t>(n) * kKeys));
+        const uint32_t keys = static_cast<uint32_t>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
+        const uint32_t context = static_cast<uint32_t>(
+            min(max(w.seq.len - before, int64_t{0}), static_cast<int64_t>(n) * kKeys));
         const bool ok = each_item<kTwo>(n, [&](int tile, bool v) {
           const bool other = turn != team;
           turn = turn + 1 == kTeams ? 0 : turn + 1;
@@ -453,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t src = src0 + in.stage * L::kRawTile;
           const uint8_t* ex = gbase + L::kRawExp + in.stage * kKeys;
           const uint32_t dst = dst0 + out.stage * L::kTile;
-          const bool border = v && (tile + 1) * kKeys > context;
+          const uint32_t row0 = static_cast<uint32_t>(tile) * kKeys;
+          const bool border = v && row0 + kKeys > context;
           bool bad = false;
           // loads in flight; four spill, and are slower
           constexpr int kBatch = kPieces < 2 ? kPieces : 2;
@@ -473,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t o[8];
               widen16(w4[z], e[z], o);
               if (border) {
-                const bool real = tile * kKeys + r < keys;
+                const bool real = row0 + r < keys;
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
                   const uint32_t nf = real ? not_finite(o[y]) : 0u;
@@ -505,8 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t ord = 0; ok && !w.done(); ++ord, w.next(c, p.div)) {
         const int n = static_cast<int>(w.last - w.first);
         const int64_t before = w.first * kKeys;
-        const int keys = static_cast<int>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
-        const int context = static_cast<int>(min(w.seq.len - before, static_cast<int64_t>(n) * kKeys));
+        const uint32_t keys = static_cast<uint32_t>(min(w.seq.keys() - before, static_cast<int64_t>(n) * kKeys));
+        const uint32_t context = static_cast<uint32_t>(
+            min(max(w.seq.len - before, int64_t{0}), static_cast<int64_t>(n) * kKeys));
         const int from =
             static_cast<int>(min(max(w.seq.len / kKeys - w.first, int64_t{0}), static_cast<int64_t>(n)));
         for (int tile = from; tile < n; ++tile) {
@@ -519,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool bad = false;
           // the rows behind the context, 16-byte pieces, four at a time
           const uint32_t at = base + L::kKV + stage * L::kTile + (lane % 8) * 16;
-          const int skip = max(context - tile * kKeys, 0);
+          const uint32_t row0 = static_cast<uint32_t>(tile) * kKeys;
+          const int skip = context > row0 ? static_cast<int>(context - row0) : 0;
           constexpr int kBoxes = D / 64;
 #pragma unroll 1
           for (int i0 = skip + lane / 8; i0 < kKeys; i0 += 16 / kBoxes) {
@@ -536,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              n3 = not_finite(y[z].w);
               if (r >= kKeys) continue;
               const uint32_t to = at + (z % kBoxes) * L::kBox + r * 128;
-              if (tile * kKeys + r >= keys) {
+              if (row0 + r >= keys) {
                 st_shared_v4(to, 0u, 0u, 0u, 0u);
               } else if (n0 | n1 | n2 | n3) {
                 bad = true;
@@ -860,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Two passes over the row's scores: the maximum, then the
             // probabilities, whose bf16 pairs take the place of scores that
-            // have been read.  Rolled loops: see the head of the file.
+            // have been read.  Rolled loops, for the instruction cache.
             float mx = -INFINITY;
 #pragma unroll 1
             for (int w = 0; w < kN; w += 2) {
