@@ -11,10 +11,11 @@
 //
 // Two streams keep the tensor cores and the exponentials busy together.
 // With two query tiles (kTwo) a stream is a query tile and both share a key
-// tile of 128; with one, a stream is every other key tile of 64 (four tiles
-// are held while two streams are at work, and the smaller ones leave room for
-// those on their way), with a state of its own, and the two states are joined
-// at the end of the unit.
+// tile of 128; with one, a stream is every other key tile, with a state of its
+// own, and the two states are joined at the end of the unit.  Four tiles are
+// held while two streams are at work, so at d = 128 those are of 64 keys, which
+// leaves room for tiles on their way; at d = 64 128 keys fit (2 sequences of
+// 60000, 8 heads, 32 rows: 72 -> 56 us, out of 8 bits 103 -> 84).
 //
 // Warp roles (640 threads, 96 registers each at launch):
 //   warps 0-3, 4-7   softmax of stream 0, 1                            (112)
@@ -82,15 +83,15 @@ constexpr float kRescaleLog2 = 8.0f;
 
 template <bool k8, int D, bool kTwo>
 struct Layout {
-  static constexpr int kKeys = kTwo ? 128 : 64;  // per tile
+  static constexpr int kKeys = kTwo || D == 64 ? 128 : 64;  // per tile
   static constexpr int kQBox = 128 * 128;        // 128 rows x 128 bytes (64 bf16)
   static constexpr int kBox = kKeys * 128;
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kTile = kKeys * D * 2;
   static constexpr int kRawTile = kKeys * D;
   static constexpr int kStages = kTwo ? (D == 128 ? (k8 ? 3 : 5) : (k8 ? 5 : 8))
-                                      : (D == 128 ? (k8 ? 6 : 9) : (k8 ? 8 : 16));
-  static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 12);
+                                      : (D == 128 ? (k8 ? 6 : 9) : (k8 ? 6 : 9));
+  static constexpr int kRawStages = !k8 ? 0 : kTwo ? (D == 128 ? 4 : 8) : (D == 128 ? 6 : 8);
   static constexpr int kTeam = 128;  // threads that convert a tile
   static constexpr int kLoadStages = k8 ? kRawStages : kStages;  // of the ring the loader fills
   // the second query tile, or the exchange of the two streams' states: per
