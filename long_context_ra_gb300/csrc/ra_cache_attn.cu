@@ -386,6 +386,46 @@ struct Join {
   static constexpr int kStep = kJoinWarps / kSplit;  // rows at a time
 };
 
+// A unit that has parts: false where the block has none to join.
+struct Shared {
+  int64_t q0;   // row of the unit's first row in q, out, lse
+  int some;     // rows of the unit
+  int c0, c1;   // the CTAs that shared it
+};
+
+__device__ bool shared_unit(const CacheAttnArgs& a, const AttnPlan& p, bool by_unit, DivisionShared& sh,
+                            Shared& j) {
+  const PagedArgs& c = a.c;
+  int b, unit;
+  if (by_unit) {
+    b = blockIdx.y / p.div.units;
+    unit = blockIdx.y % p.div.units;
+    int64_t ahead, total;
+    division_before(c, p.div, b, sh, ahead, total);
+    const int64_t tiles = seq_tiles(c, p.div, b), run = run_length(p.div, total * p.div.units);
+    const int64_t u0 = ahead * p.div.units + unit * tiles;
+    j.c0 = static_cast<int>(u0 / run);
+    j.c1 = static_cast<int>((u0 + tiles - 1) / run);
+    if (j.c0 == j.c1) return false;
+  } else {
+    const int border = blockIdx.y + 1;
+    if (division_start(c, p.div, border, sh) == 0) return false;
+    b = sh.b;
+    const int64_t tiles = seq_tiles(c, p.div, b);
+    unit = static_cast<int>(sh.off / tiles);
+    const int64_t inside = sh.off - unit * tiles;  // tiles of the unit before the border
+    // a unit begins here, or was cut before
+    if (inside == 0 || inside > sh.run) return false;
+    j.c0 = border - 1;
+    j.c1 = static_cast<int>((border * sh.run - inside + tiles - 1) / sh.run);
+  }
+  const int64_t rows = head_rows(a);
+  const int64_t r0 = static_cast<int64_t>(unit % p.row_tiles) * p.rows;
+  j.q0 = (static_cast<int64_t>(b) * c.heads + unit / p.row_tiles) * rows + r0;
+  j.some = static_cast<int>(min(rows - r0, static_cast<int64_t>(p.rows)));
+  return true;
+}
+
 template <typename E, int kSplit, int kCols>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a,
@@ -398,33 +438,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const PagedArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int sub = warp % kSplit;
-  int b, unit, c0, c1;
-  if (by_unit) {
-    b = blockIdx.y / p.div.units;
-    unit = blockIdx.y % p.div.units;
-    int64_t ahead, total;
-    division_before(c, p.div, b, sh, ahead, total);
-    const int64_t tiles = seq_tiles(c, p.div, b), run = run_length(p.div, total * p.div.units);
-    const int64_t u0 = ahead * p.div.units + unit * tiles;
-    c0 = static_cast<int>(u0 / run);
-    c1 = static_cast<int>((u0 + tiles - 1) / run);
-    if (c0 == c1) return wait_for_parts();
-  } else {
-    const int border = blockIdx.y + 1;
-    if (division_start(c, p.div, border, sh) == 0) return wait_for_parts();
-    b = sh.b;
-    const int64_t tiles = seq_tiles(c, p.div, b);
-    unit = static_cast<int>(sh.off / tiles);
-    const int64_t inside = sh.off - unit * tiles;  // tiles of the unit before the border
-    // a unit begins here, or was cut before
-    if (inside == 0 || inside > sh.run) return wait_for_parts();
-    c0 = border - 1;
-    c1 = static_cast<int>((border * sh.run - inside + tiles - 1) / sh.run);
-  }
-  const int64_t rows = head_rows(a);
-  const int64_t r0 = static_cast<int64_t>(unit % p.row_tiles) * p.rows;
-  const int64_t q0 = (static_cast<int64_t>(b) * c.heads + unit / p.row_tiles) * rows + r0;
-  const int some = static_cast<int>(min(rows - r0, static_cast<int64_t>(p.rows)));
+  Shared j;
+  if (!shared_unit(a, p, by_unit, sh, j)) return wait_for_parts();
+  const int64_t q0 = j.q0;
+  const int some = j.some, c0 = j.c0, c1 = j.c1;
   // rows of all slots: fewer than 2^17, of d floats each
   const float2* all_ml = reinterpret_cast<const float2*>(slot_ml(a, p, 0));
   const float4* all_o = reinterpret_cast<const float4*>(slot_o(a, p, 0));
@@ -508,6 +525,121 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       if (lane == 0) a.lse[q0 + local] = l == 0.f ? -INFINITY : (ms + log2f(l)) * kLn2F;
     }
   }
+}
+
+// The same for parts of the many-row kernel: a warp takes 32 rows, one to a
+// lane, and 4 kQuads columns of them, so that its loads are whole lines.  It
+// keeps a running reference as the attention does, so that no pass over the
+// parts' maxima comes first.  The row-by-row order took 4.7 us more for 8 units
+// of 256 rows over 64 CTAs (28.8 -> 22.7 us, most of it in the writes: a store
+// of 32 rows meets 32 lines), and 6 of 98 for 8 trees of 32 drafts.
+template <int kSplit, int kQuads, int kParts>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    cache_tree_join_kernel(const __grid_constant__ CacheAttnArgs a,
+                           const __grid_constant__ AttnPlan p, bool by_unit) {
+  __shared__ DivisionShared sh;
+  __shared__ float4 sums[kSplit > 1 ? kJoinWarps : 1][kQuads][32];
+  __shared__ float2 sum_ml[kSplit > 1 ? kJoinWarps : 1][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kSplit;
+  Shared j;
+  if (!shared_unit(a, p, by_unit, sh, j)) return wait_for_parts();
+  const int item = blockIdx.x * (kJoinWarps / kSplit) + warp / kSplit;
+  const int quads = a.c.d / 4, quad = item % (quads / kQuads) * kQuads;
+  const int local = item / (quads / kQuads) * 32 + lane;
+  const bool here = local < j.some;
+  // rows of all slots: fewer than 2^17, of d floats each
+  const float2* all_ml = reinterpret_cast<const float2*>(slot_ml(a, p, 0)) + local;
+  const float4* all_o = reinterpret_cast<const float4*>(slot_o(a, p, 0)) + quad * p.rows + local;
+  const uint32_t rows = p.rows;
+  wait_for_parts();
+  float m = -INFINITY, l = 0.f;
+  float4 o[kQuads];
+#pragma unroll
+  for (int h = 0; h < kQuads; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // o += w y, l += w x, in a state that holds the reference m
+  auto add = [&](float w, float x, const float4 (&y)[kQuads]) {
+    l = fmaf(w, x, l);
+#pragma unroll
+    for (int h = 0; h < kQuads; ++h) {
+      o[h].x = fmaf(w, y[h].x, o[h].x);
+      o[h].y = fmaf(w, y[h].y, o[h].y);
+      o[h].z = fmaf(w, y[h].z, o[h].z);
+      o[h].w = fmaf(w, y[h].w, o[h].w);
+    }
+  };
+  auto scale = [&](float w) {
+    l *= w;
+#pragma unroll
+    for (int h = 0; h < kQuads; ++h)
+      o[h] = make_float4(o[h].x * w, o[h].y * w, o[h].z * w, o[h].w * w);
+  };
+  if (here) {
+    for (int i = j.c0 + sub; i <= j.c1; i += kParts * kSplit) {
+      float2 ml[kParts];
+      float4 y[kParts][kQuads];
+#pragma unroll
+      for (int z = 0; z < kParts; ++z) {
+        const int part = i + z * kSplit;
+        const bool real = part <= j.c1;
+        const uint32_t at = real ? (2u * part + (part == j.c0 ? 1u : 0u)) * rows : 0u;
+        ml[z] = real ? all_ml[at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int h = 0; h < kQuads; ++h)
+          y[z][h] = real ? all_o[at * quads + h * rows] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float top = m;
+#pragma unroll
+      for (int z = 0; z < kParts; ++z) top = fmaxf(top, ml[z].x);
+      if (i > j.c0 + sub && top > m) scale(exp2f(m - top));
+      m = top;
+#pragma unroll
+      for (int z = 0; z < kParts; ++z) add(ml[z].y == 0.f ? 0.f : exp2f(ml[z].x - m), ml[z].y, y[z]);
+    }
+  }
+  if (kSplit > 1) {
+#pragma unroll
+    for (int h = 0; h < kQuads; ++h) sums[warp][h][lane] = o[h];
+    sum_ml[warp][lane] = make_float2(m, l);
+    __syncthreads();
+    if (sub != 0) return;
+    float top = m;
+    for (int z = 1; z < kSplit; ++z) top = fmaxf(top, sum_ml[warp + z][lane].x);
+    if (top > m) scale(exp2f(m - top));
+    m = top;
+    for (int z = 1; z < kSplit; ++z) {
+      const float2 ml = sum_ml[warp + z][lane];
+      float4 y[kQuads];
+#pragma unroll
+      for (int h = 0; h < kQuads; ++h) y[h] = sums[warp + z][h][lane];
+      add(ml.y == 0.f ? 0.f : exp2f(ml.x - m), ml.y, y);
+    }
+  }
+  if (!here) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (j.q0 + local) * a.c.d + 4 * quad;
+#pragma unroll
+  for (int h = 0; h < kQuads; ++h)
+    store4(dst + 4 * h, make_float4(o[h].x * inv, o[h].y * inv, o[h].z * inv, o[h].w * inv));
+  if (quad == 0) a.lse[j.q0 + local] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
+}
+
+template <int kSplit, int kQuads, int kParts>
+cudaError_t tree_join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+  const int64_t rows = head_rows(a) < p.rows ? head_rows(a) : p.rows;
+  const int64_t units = static_cast<int64_t>(a.c.B) * p.div.units, borders = p.div.ctas - 1;
+  const bool by_unit = units <= borders;
+  const int64_t items = (rows + 31) / 32 * (a.c.d / (4 * kQuads));
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((items * kSplit + kJoinWarps - 1) / kJoinWarps),
+                     static_cast<unsigned>(by_unit ? units : borders));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_tree_join_kernel<kSplit, kQuads, kParts>, a, p, by_unit);
 }
 
 template <typename E, int kSplit, int kCols>
@@ -596,6 +728,16 @@ cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bo
   if (p.div.ctas > 48 * units) return join_s<8>(a, p, bf16, s);
   if (p.div.ctas > 16 * units) return join_s<2>(a, p, bf16, s);
   return join_s<1>(a, p, bf16, s);
+}
+
+cudaError_t launch_cache_tree_join(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+  // Many parts: warps share them.  Few: many units or borders, so fewer and
+  // larger blocks (12 sequences of 552 rows, 9 heads: 4 column quads a warp 78
+  // us, 1 quad 90; one unit of 120 rows over 152 CTAs: 8 warps a row 29 us).
+  const int64_t units = static_cast<int64_t>(a.c.B) * p.div.units;
+  if (p.div.ctas > 32 * units) return tree_join_t<8, 1, 4>(a, p, s);
+  if (p.div.ctas > 8 * units) return tree_join_t<2, 2, 4>(a, p, s);
+  return tree_join_t<1, 4, 2>(a, p, s);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dtype held,

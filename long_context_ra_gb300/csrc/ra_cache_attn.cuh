@@ -11,7 +11,8 @@ constexpr float kLn2F = 0.6931471805599453f;
 
 // One launch's plan: how many query rows a unit holds and how its key tiles
 // are divided.  Partial states are [slots][rows][2] (m in log2 units, l)
-// followed by [slots][rows][d] (o).
+// followed by [slots][rows][d] (o); the many-row kernel, whose threads hold a
+// row each, writes o as [slots][d / 4][rows][4].
 struct AttnPlan {
   Division div;
   int rows;       // query rows per unit
@@ -61,5 +62,6 @@ cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s);
 // Joins the parts of the units that several CTAs shared.
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
                                    cudaStream_t s);
+cudaError_t launch_cache_tree_join(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
 }  // namespace ra

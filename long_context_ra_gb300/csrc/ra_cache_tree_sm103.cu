@@ -331,6 +331,32 @@ __device__ __noinline__ uint32_t poisoned_columns(const CacheAttnArgs& a, const 
   return bad;
 }
 
+// Lane 4 i + j gives y[k] to lane 4 i + k and gets that lane's y[j]: rows of a
+// quad of lanes become columns, so that its lanes store neighbouring pieces.  A
+// store instruction then meets 8 lines, not 32: a unit's end is bound by those.
+__device__ __forceinline__ void transpose4(uint4 (&y)[4], int lane) {
+#pragma unroll
+  for (int z = 1; z < 4; z <<= 1) {
+    const bool up = lane & z;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & z) continue;
+      uint4& lo = y[k];
+      uint4& hi = y[k | z];
+      const uint4 give = up ? lo : hi;
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, z);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, z);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, z);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, z);
+      if (up)
+        lo = got;
+      else
+        hi = got;
+    }
+  }
+}
+
 // What a role needs of the present unit.
 struct Unit {
   int head;
@@ -1044,32 +1070,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if ((bad >> e) & 1u) r[e] = 0x7fffffffu;
           }
-          if (exists) {
-            if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (un.q0 + local) * D + x);
+          if (whole) {
+            uint4 y[4];  // 8 columns each
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint4 w;
-                w.x = pack_bf16x2(__uint_as_float(r[8 * e + 0]) * inv, __uint_as_float(r[8 * e + 1]) * inv);
-                w.y = pack_bf16x2(__uint_as_float(r[8 * e + 2]) * inv, __uint_as_float(r[8 * e + 3]) * inv);
-                w.z = pack_bf16x2(__uint_as_float(r[8 * e + 4]) * inv, __uint_as_float(r[8 * e + 5]) * inv);
-                w.w = pack_bf16x2(__uint_as_float(r[8 * e + 6]) * inv, __uint_as_float(r[8 * e + 7]) * inv);
-                dst[e] = w;
-              }
-              if (x == 0)
-                a.lse[un.q0 + local] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * kLn2F;
-            } else {
-              float4* dst = reinterpret_cast<float4*>(slot_o(a, p, slot) + static_cast<int64_t>(local) * D + x);
+            for (int e = 0; e < 4; ++e)
+              y[e] = make_uint4(
+                  pack_bf16x2(__uint_as_float(r[8 * e + 0]) * inv, __uint_as_float(r[8 * e + 1]) * inv),
+                  pack_bf16x2(__uint_as_float(r[8 * e + 2]) * inv, __uint_as_float(r[8 * e + 3]) * inv),
+                  pack_bf16x2(__uint_as_float(r[8 * e + 4]) * inv, __uint_as_float(r[8 * e + 5]) * inv),
+                  pack_bf16x2(__uint_as_float(r[8 * e + 6]) * inv, __uint_as_float(r[8 * e + 7]) * inv));
+            // lane 4 i + j: the columns 8 j .. of rows 4 i .. 4 i + 3
+            transpose4(y, lane);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                                  (un.q0 + local - lane % 4) * D + x + 8 * (lane % 4));
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                     __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-              if (x == 0) {
-                float* ml = slot_ml(a, p, slot) + 2 * local;
-                ml[0] = m_ref;
-                ml[1] = l;
-              }
-            }
+            for (int e = 0; e < 4; ++e)
+              if (un.r0 + local - lane % 4 + e < rows) dst[e * (D / 8)] = y[e];
+            if (x == 0 && exists)
+              a.lse[un.q0 + local] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * kLn2F;
+          } else if (exists) {
+            float4* dst = reinterpret_cast<float4*>(slot_o(a, p, slot)) + x / 4 * p.rows + local;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e * p.rows] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                            __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+            if (x == 0)
+              *reinterpret_cast<float2*>(slot_ml(a, p, slot) + 2 * local) = make_float2(m_ref, l);
           }
         }
         tc_fence_before();
@@ -1113,7 +1139,7 @@ cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& plan, cudaStream_t 
   p.div.tile = L::kKeys;
   cache_tree_kernel<k8, D, kTwo><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_cache_attn_join(a, p, true, s) : e;
+  return e == cudaSuccess ? launch_cache_tree_join(a, p, s) : e;
 }
 
 template <bool k8, int D>
