@@ -211,6 +211,10 @@ bool encode_pages(CUtensorMap* map, const void* ptr, const PagedArgs& c, int box
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_rows(CUtensorMap* map, const void* ptr, int64_t rows, int d) {
+  return get_encoder() == RA_OK && make_map(map, ptr, rows, d) == RA_OK;
+}
+
 ra_status device_ready(int** status) {
   DeviceInfo di;
   const ra_status st = current_device(&di);

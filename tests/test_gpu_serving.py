@@ -305,6 +305,32 @@ def test_the_next_kernel_sees_the_whole_result(dtype, held, B, T):
         assert torch.equal(o, out) and torch.equal(s, lse)
 
 
+@pytest.mark.parametrize("dtype,held", [(BF16, BF16), (BF16, E4M3), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("T", [1, 9, 40, 100])
+def test_queries_that_are_not_finite_stay_in_their_rows(dtype, held, T):
+    """Kernels work on rows of several tokens and heads together; a NaN or an
+    infinity in one query reaches no other row's bits."""
+    B, heads, g, d, page = 2, 2, 3, 64, 32
+    n = 200 + T
+    per = -(-n // page)
+    cache = ra.new_cache(B * per, heads, page, d, held)
+    table = torch.arange(B * per, dtype=torch.int32, device=DEV).reshape(B, per)
+    x = rnd(7, 2, B, heads, n, d, dtype=dtype)
+    ra.ra_cache_write(cache, x[0], x[1], table, i32(0, 0))
+    q = rnd(8, B, heads * g, T, d, dtype=dtype)
+    bad = q.clone()
+    bad[0, 2, T - 1, 5] = math.nan
+    bad[0, 3, 0, 7] = math.inf
+    bad[1, 5] = math.nan
+    want = ra.ra_cache_attention(q, cache, table, i32(200, 77))
+    got = ra.ra_cache_attention(bad, cache, table, i32(200, 77))
+    same = torch.ones(B, heads * g, T, dtype=torch.bool, device=DEV)
+    same[0, 2, T - 1] = same[0, 3, 0] = False
+    same[1, 5] = False
+    assert torch.equal(got[0][same], want[0][same]) and torch.equal(got[1][same], want[1][same])
+    assert got[0][~same].isnan().any(-1).all()
+
+
 def test_calls_on_a_given_stream():
     """stream=: work and the call's own allocations belong to that stream."""
     heads, Hq, d, page, L, T = 2, 8, 64, 32, 700, 20
