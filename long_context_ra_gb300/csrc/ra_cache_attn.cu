@@ -703,7 +703,14 @@ template <typename H, int NC>
 cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
   const int64_t rows = head_rows(a);
   // The smallest group of rows that holds a head's, with as many warps on the
-  // keys as leave room for three CTAs on an SM.
+  // keys as leave room for three CTAs on an SM.  Groups of 64 rows feed more
+  // products from a read, but groups of 16 keep four CTAs on an SM and none of
+  // their rows idle: the latter are ahead until a head has `few` rows (2 heads, 4
+  // or 32 sequences of 4000, us with groups of 16 and of 64: d = 64, 40 rows 37
+  // 43 / 135 124, 64 rows 41 48 / 181 143; d = 128, 64 rows 58 84 / 279 285, 96
+  // rows 76 107 / 408 502, 128 rows 92 119 / 548 530; d = 176, 40 rows 93 96 / 456
+  // 322; one tile of d = 240, 18 rows 22 49).
+  const int few = a.c.d > 128 ? 32 : a.c.d > 64 ? 96 : 48;
   using F4 = Ffma<4, 1, 1, 4, NC>;
   using F8 = Ffma<4, 1, 2, 2, NC>;
   using F16 = Ffma<4, 1, 4, 1, NC>;
@@ -711,7 +718,7 @@ cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
   constexpr int third = kFfmaSmem / 3;
   if (rows <= 4 && F4::smem(a.c.d) <= third) return launch_ffma_t<H, F4>(a, kFfmaCtas, s);
   if (rows <= 8 && F8::smem(a.c.d) <= third) return launch_ffma_t<H, F8>(a, kFfmaCtas, s);
-  if (rows <= 16 || F64::smem(a.c.d) > kFfmaSmem) return launch_ffma_t<H, F16>(a, kFfmaCtas, s);
+  if (rows <= few || F64::smem(a.c.d) > kFfmaSmem) return launch_ffma_t<H, F16>(a, kFfmaCtas, s);
   return launch_ffma_t<H, F64>(a, kFfmaCtas / 2, s);
 }
 
