@@ -21,9 +21,10 @@
 // heads of 80, 6 rows each 20 us a call (70 with one warp per row and a tile at
 // a time); 256 rows over 4096 keys of 128: 17 TFLOP/s.
 //
-// In tiles with drafts or the end a key that a row does not see has p = 0 and
-// is left out of the sum rather than multiplied, so what it holds does not
-// matter.
+// A key that a row does not see has p = 0.  In tiles with drafts or the end that
+// hold a value that is not finite it is left out of the sum rather than
+// multiplied, so what it holds does not matter.  (Leaving keys out costs a branch
+// per key and row: 651 rows of 34 sequences of 98 keys 886 us, not 674.)
 
 #include "ra_cache_attn.cuh"
 #include "sm103_ptx.cuh"
@@ -119,6 +120,8 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
       const int64_t* at = key_row[tile & 1];
       __syncthreads();
       look_up(tile + 1);
+      const bool border = tile * kTile + kTile > context;
+      bool bad = false;  // a value that is not finite in a tile that not every row sees
       for (int i0 = threadIdx.x; i0 < kTile * d / 8; i0 += 4 * F::kThreads) {
         // four pieces of 8 elements of K and of V are on their way together
         Packed<H, 8> x[4], y[4];
@@ -159,10 +162,14 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 #pragma unroll
             for (int w = 0; w < 8; ++w) f[w] *= sv;
           }
+          if (border) {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) bad = bad || !(fabsf(f[w]) < INFINITY);
+          }
           store8(vs + key * d + e, f);
         }
       }
-      __syncthreads();
+      const bool clean = !__syncthreads_or(bad);
       if (r0 + rg * kRW >= rows) continue;  // no row of this warp's
       // ---- scores of keys lane, lane + 32 of the warp's part of the tile
       const float* kw = ks + (kg * F::kWarpKeys + lane) * ld;
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 #pragma unroll
         for (int x = 0; x < kPairs; ++x)
           if (64 * x < d) vv[x] = *reinterpret_cast<const uint64_t*>(vw + col[x]);
-        if (whole_tile) {
+        if (whole_tile || clean) {
 #pragma unroll
           for (int x = 0; x < kPairs; ++x)
             if (64 * x < d) {
