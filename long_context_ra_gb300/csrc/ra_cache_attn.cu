@@ -18,7 +18,7 @@
 // neighbouring elements for the scores and of neighbouring columns for P V,
 // whose probabilities are kept twice side by side; 8 rows x 2 keys a lane are
 // 32 paired FFMA for 10 reads of 16 bytes.  Measured: 2 sequences of 4096, 3 key
-// heads of 80, 6 rows each 20 us a call (70 with one warp per row and a tile at
+// heads of 80, 6 rows each 19 us a call (70 with one warp per row and a tile at
 // a time); 256 rows over 4096 keys of 128: 17 TFLOP/s.
 //
 // A key that a row does not see has p = 0.  In tiles with drafts or the end that

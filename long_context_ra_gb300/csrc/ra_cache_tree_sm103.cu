@@ -45,9 +45,9 @@
 //
 // Measured per tile of 128 keys on one SM (152 at work, d = 128): one query
 // tile, bf16 1.6 us (the tile's bytes alone take 1.5 at the copy rate), 8 bits
-// 1.9; two query tiles, bf16 2.0 us, 8 bits 2.35 (without conversion 2.0,
-// without softmax 1.9: both share the issue slots with the issuer's warp).
-// 512 rows over 2^20 keys of 8 heads out of 8 bits: 1.95 ms, 57 % of the tensor
+// 1.7; two query tiles, bf16 2.0 us, 8 bits 2.35 (without conversion 1.8,
+// without softmax 1.85; 57 % of the issue slots are used).
+// 488 rows over 2^20 keys of 8 heads out of 8 bits: 1.97 ms, 56 % of the tensor
 // rate.  A unit costs some 8 us beside its tiles: pipeline start (clocks from
 // the launch: place in the division 2900, queries and first keys 6200, scores
 // 7900, probabilities 10400, first results 12300) and end (5000 for 256 rows'
