@@ -45,7 +45,7 @@
 //
 // Measured per tile of 128 keys on one SM (152 at work, d = 128): one query
 // tile, bf16 1.6 us (the tile's bytes alone take 1.5 at the copy rate), 8 bits
-// 1.7; two query tiles, bf16 2.0 us, 8 bits 2.35 (without conversion 1.8,
+// 1.9; two query tiles, bf16 2.0 us, 8 bits 2.35 (without conversion 1.8,
 // without softmax 1.85; 57 % of the issue slots are used).
 // 488 rows over 2^20 keys of 8 heads out of 8 bits: 1.97 ms, 56 % of the tensor
 // rate.  A unit costs some 8 us beside its tiles: pipeline start (clocks from
