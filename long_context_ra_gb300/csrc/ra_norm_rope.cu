@@ -414,7 +414,11 @@ __global__ void __launch_bounds__(256) norm_weight_kernel(const float* partial, 
 
 // Heads per run: all of a token's heads while that makes `blocks` blocks per
 // SM, else fewer: short blocks even the end of the launch, and a decode
-// step's few tokens spread out.
+// step's few tokens spread out.  16 for the forward; 1 for the backward, whose
+// items load nothing ahead of one another, so that longer runs pay more than
+// an even end (32 + 8 heads of 128, us at 1 and 16: 300 tokens 16.6 20.6, 1560
+// 28.8 32.9, 6000 53.4 51.4, 9000 63.6 72.7; 8 + 2 heads: 3000 tokens 20.7 24.6,
+// 16000 41.1 47.3).
 int heads_per_run(int64_t token_tiles, int heads, int blocks) {
   const int64_t want = static_cast<int64_t>(device_sm_count()) * blocks;
   int64_t runs = (want + token_tiles - 1) / token_tiles;
@@ -427,7 +431,7 @@ cudaError_t launch_t(const NormArgs& a, bool backward, cudaStream_t s) {
   const int heads = a.side[0].heads + a.side[1].heads;
   const int groups = (backward ? kThreads : kForwardThreads) / kLanes;
   const int64_t tiles = (a.tokens + groups - 1) / groups;
-  const int run = heads_per_run(tiles, heads, 16);
+  const int run = heads_per_run(tiles, heads, backward ? 1 : 16);
   const bool inter = a.has_rope && a.rope.interleaved;
   if (!backward) {
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + run - 1) / run));
