@@ -21,7 +21,7 @@
 //
 // Measured, 32768 tokens of 32 + 8 heads of 128, bf16: forward 110 us (671 MB,
 // 89 % of the copy rate; with 4-element pieces and one head ahead 219), backward
-// 193 us (1007 MB, 77 %; single-float arithmetic 269, one head ahead 207).  The
+// 195 us (1007 MB, 76 %; single-float arithmetic 269, one head ahead 207).  The
 // backward's rows need two sums that depend on one another, so it lives from
 // the heads that are on their way: two at 128 registers with the weight in
 // shared memory.  Three heads spill (217 us; 205 with the rotation in shared
@@ -326,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool here = token < a.tokens;
       const int64_t b = here ? token / a.N : 0, n = here ? token % a.N : 0;
       const bool live = lp.live && here;
+      // A group without a token adds zeros to dw; with eps = 0 they would be 0 * inf.
+      const float eps = here ? a.eps : 1.f;
       const E* src = static_cast<const E*>(s.x) + b * s.xs.b + n * s.xs.n;
       const E* dy = static_cast<const E*>(s.dy) + (b * s.heads * a.N + n) * a.d;
       E* dst = static_cast<E*>(s.y) + b * s.ys.b + n * s.ys.n;
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           fetch(h + kAhead, j);
           if (lp.rotated) lp.rotate(g);
           if (a.eps >= 0.f) {
-            const float r = rsqrtf(row_sum<kLanes>(x.dot(x)) * inv_d + a.eps);
+            const float r = rsqrtf(row_sum<kLanes>(x.dot(x)) * inv_d + eps);
             x.scale(r);  // the normalised row
             dw.add_product(g, x);
 #pragma unroll

@@ -190,3 +190,25 @@ def test_on_another_stream():
     got = ra.ra_qk_norm_rope(q, k, rope, pos, wq, wk, stream=s)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [
+    (1, 1, 2, 1, 64, 64, 1, False),
+    (1, 33, 4, 2, 128, 128, 1, False),
+    (2, 37, 3, 1, 128, 96, 3, True),
+    (1, 37, 2, 2, 24, 24, 1, False),   # 3 lanes of 4 hold a row
+    (3, 301, 5, 1, 80, 0, 1, False),
+])
+def test_backward_without_an_epsilon(shape, dtype):
+    """eps = 0, and token counts that leave groups of the last block without a
+    token: no row is zero, so every gradient is finite, within the same bounds."""
+    q, k, wq, wk, rope, pos, angle = case(shape, dtype, 12)
+    g = torch.Generator(device=DEV).manual_seed(13)
+    dys = [torch.randn(x.shape, device=DEV, generator=g).to(dtype) for x in (q, k)]
+    dq, dk, dwq, dwk = ra.ra_qk_norm_rope_backward(q, k, *dys, rope, pos, wq, wk, 0.0)
+    for x, w, dy, dx, dw in ((q, wq, dys[0], dq, dwq), (k, wk, dys[1], dk, dwk)):
+        want, want_w, size, terms = R.norm_rope_backward(x, w, 0.0, angle, shape[7], dy)
+        tol = R.EPS_HALF[dtype] * want.abs() + 64 * R.U * math.sqrt(2) * size
+        assert ((R.f64(dx) - want).abs() <= tol).all()
+        assert ((R.f64(dw) - want_w).abs() <= 280 * R.U * math.sqrt(2) * terms).all()
