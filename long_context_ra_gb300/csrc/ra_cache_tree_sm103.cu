@@ -55,10 +55,11 @@
 // as soon as the last scores of the present one are out (by 224 threads they
 // were there at 9700), and results leave in whole lines (12100 by rows).
 //
-// Unseen drafts: their scores are -inf, so p = 0; value rows of tiles with
-// drafts are looked through for elements that are not finite.  Those become 0
-// in the operand, and a unit that met one adds them at its end, row by row,
-// to the queries that see them.
+// Unseen drafts: their scores are -inf, so p = 0; value rows of drafts are
+// looked through for elements that are not finite.  Those become 0 in the
+// operand, and a unit that met one adds them at its end, row by row, to the
+// queries that see them.  Rows of the context, which every query sees, stay
+// as they are.
 //
 // Every wait is bounded, as in the forward kernel.
 
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int r = grp * kGroup + piece_row<D, kGroup>(z0 + z, pc);
               uint32_t o[8];
               widen16(w4[z], e[z], o);
-              if (border) {
+              if (border && row0 + r >= context) {
                 const bool real = row0 + r < keys;
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {

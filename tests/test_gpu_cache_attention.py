@@ -225,3 +225,50 @@ def test_results_repeat_and_do_not_depend_on_the_workspace():
             ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
             again = ra.ra_cache_attention(q, cache, table.to(DEV), ln, workspace=ws)
             assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def with_value(cache, table, places, head, column, value):
+    """A copy of the cache with `value` in one column of V at the given
+    (sequence, position) places of one key head."""
+    v = cache.v.clone()
+    page = v.shape[2]
+    for b, n in places:
+        p = int(table[b, n // page])
+        if v.dtype == E4M3:
+            assert math.isnan(value)
+            v.view(torch.uint8)[p, head, n % page, column] = 0x7f
+        else:
+            v[p, head, n % page, column] = value
+    return ra.RaCache(cache.k, v, cache.k_exp, cache.v_exp)
+
+
+def check_one_column(got, want, g, head, column, lens, count, T):
+    """Column `column` of the rows of key head `head` is not finite; all else
+    has the bits of `want`."""
+    live = torch.zeros(got[0].shape[:3], dtype=torch.bool, device=DEV)
+    for b, n in enumerate(lens):
+        if n >= 0:
+            live[b, :, :T if count is None else count[b]] = True
+    assert not got[0][:, head * g:(head + 1) * g, :, column][live[:, head * g:(head + 1) * g]].isfinite().any()
+    same = torch.ones(got[0].shape, dtype=torch.bool, device=DEV)
+    same[:, head * g:(head + 1) * g, :, column] = False
+    same |= ~live[..., None]
+    assert torch.equal(got[0][same], want[0][same]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype,held,d,value", [
+    (*t, x) for t in TYPES[3:] + TYPES[:1] for x in (math.nan, math.inf)
+    if t[1] != E4M3 or math.isnan(x)])   # an 8-bit code is finite or NaN
+@pytest.mark.parametrize("T", [1, 3, 40, 100])
+def test_context_values_that_are_not_finite(dtype, held, d, value, T):
+    """A NaN or an infinity in the last rows of the context, which share a tile
+    with the new tokens, reaches every query, in its column only."""
+    lens, Hq, heads, page = [70, 2000, 200, 2, -1], 4, 2, 16
+    count = [T, T, max(1, T // 2), T, T]
+    q, cache, table, ln, cnt = make(lens, count, T, Hq, heads, page, d, dtype, held, 15)
+    want = ra.ra_cache_attention(q, cache, table.to(DEV), ln, cnt)
+    for back, column, head in ((1, 5, 0), (2, d - 1, 1)):
+        bad = with_value(cache, table, [(b, n - back) for b, n in enumerate(lens) if n > 0], head, column, value)
+        got = ra.ra_cache_attention(q, bad, table.to(DEV), ln, cnt)
+        check_one_column(got, want, 2, head, column, lens, count, T)
+    assert ra.ra_last_device_status() == 0
