@@ -23,8 +23,9 @@
 //
 // A key that a row does not see has p = 0.  In tiles with drafts or the end that
 // hold a value that is not finite it is left out of the sum rather than
-// multiplied, so what it holds does not matter.  (Leaving keys out costs a branch
-// per key and row: 651 rows of 34 sequences of 98 keys 886 us, not 674.)
+// multiplied, so what it holds does not matter; -0 in place of p tells it from a
+// key that is seen and whose p is 0.  (Leaving keys out costs a branch per key and
+// row: 651 rows of 34 sequences of 98 keys 886 us, not 674.)
 
 #include "ra_cache_attn.cuh"
 #include "sm103_ptx.cuh"
@@ -248,6 +249,17 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
           probs[warp][lane + 32 * z][r / 2] = make_float4(p0, p0, p1, p1);
         }
       }
+      if (!whole_tile && !clean) {  // -0 for keys that are not seen: a seen one's p may be 0
+#pragma unroll
+        for (int z = 0; z < kKL; ++z) {
+          const int64_t pos = pos0 + lane + 32 * z;
+          const bool here = at[kg * F::kWarpKeys + lane + 32 * z] >= 0;
+          float2* pr = reinterpret_cast<float2*>(probs[warp][lane + 32 * z]);
+#pragma unroll
+          for (int r = 0; r < kRW; ++r)
+            if (!here || !sees(a, u.seq, u.b, t[r], pos)) pr[r] = make_float2(-0.f, -0.f);
+        }
+      }
       __syncwarp();
       // ---- values
       const float* vw = vs + kg * F::kWarpKeys * d;
@@ -276,8 +288,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         } else {
 #pragma unroll
           for (int r = 0; r < kRW; r += 2) {
-            // the same for every lane: a row's probability of this key
-            const bool s0 = pr[r / 2].x != 0ull, s1 = pr[r / 2].y != 0ull;
+            // the same for every lane: whether a row sees this key
+            constexpr uint64_t unseen = 0x8000000080000000ull;
+            const bool s0 = pr[r / 2].x != unseen, s1 = pr[r / 2].y != unseen;
 #pragma unroll
             for (int x = 0; x < kPairs; ++x)
               if (64 * x < d) {

@@ -272,3 +272,34 @@ def test_context_values_that_are_not_finite(dtype, held, d, value, T):
         got = ra.ra_cache_attention(q, bad, table.to(DEV), ln, cnt)
         check_one_column(got, want, 2, head, column, lens, count, T)
     assert ra.ra_last_device_status() == 0
+
+
+def check_weight_zero(places, T, dtype, held, d):
+    """For each (top, at) of `places` a sequence of 3000 in which key `top`
+    scores 200 or more above all others, whose weights so are 0 in fp32: a NaN
+    in the value row at `at`, which every query sees, makes its column NaN."""
+    Hq, heads, page, n = 4, 2, 32, 3000
+    lens = [n] * len(places)
+    B = len(lens)
+    table, pages = R.make_paged([n + T] * B, page, 16)
+    cache = ra.new_cache(pages, heads, page, d, held)
+    g = torch.Generator(device=DEV).manual_seed(17)
+    k = torch.zeros(B, heads, n + T, d, device=DEV, dtype=dtype)
+    v = torch.randn(B, heads, n + T, d, device=DEV, generator=g).to(dtype)
+    for b, (top, _) in enumerate(places):
+        k[b, :, top] = 8
+    zero = torch.zeros(B, dtype=torch.int32, device=DEV)
+    ra.ra_cache_write(cache, k, v, table.to(DEV), zero)
+    q = torch.full((B, Hq, T, d), 4.0, device=DEV, dtype=dtype)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = ra.ra_cache_attention(q, cache, table.to(DEV), ln)
+    bad = with_value(cache, table, [(b, at) for b, (_, at) in enumerate(places)], 1, 7, math.nan)
+    got = ra.ra_cache_attention(q, bad, table.to(DEV), ln)
+    check_one_column(got, want, 2, 1, 7, lens, None, T)
+
+
+@pytest.mark.parametrize("dtype,held,d", TYPES[:3])
+@pytest.mark.parametrize("T", [1, 3, 24, 100])
+def test_nan_at_weight_zero_in_the_last_tile(T, dtype, held, d):
+    """Both keys in the tile that holds the end of the context."""
+    check_weight_zero([(2999, 2998), (2998, 3000)], T, dtype, held, d)
