@@ -336,29 +336,29 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 #pragma unroll
         for (int g = 1; g < F::kKG; ++g) ms = fmaxf(ms, states[g * F::kRG + rg][r][0]);
         const float ref = ms == -INFINITY ? 0.f : ms;
+        // A weight of 0 multiplies too: o may be NaN, and is 0 without a seen key.
         const float f0 = l[r] == 0.f ? 0.f : exp2f(m[r] - ref);
         float ls = f0 * l[r];
 #pragma unroll
-        for (int x = 0; x < kPairs; ++x) o[r][x] = f0 == 0.f ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f0, f0));
+        for (int x = 0; x < kPairs; ++x) o[r][x] = mul_f32x2(o[r][x], pack_f32x2(f0, f0));
 #pragma unroll
         for (int g = 1; g < F::kKG; ++g) {
           const float lg = states[g * F::kRG + rg][r][1];
           const float f = lg == 0.f ? 0.f : exp2f(states[g * F::kRG + rg][r][0] - ref);
           ls += f * lg;
-          if (f != 0.f) {
 #pragma unroll
-            for (int x = 0; x < kPairs; ++x)
-              if (2 * lane + 64 * x < d)
-                o[r][x] = fma_f32x2(pack_f32x2(f, f),
-                                    *reinterpret_cast<const uint64_t*>(
-                                        parts + ((g - 1) * F::kRows + local) * d + 2 * lane + 64 * x),
-                                    o[r][x]);
-          }
+          for (int x = 0; x < kPairs; ++x)
+            if (2 * lane + 64 * x < d)
+              o[r][x] = fma_f32x2(pack_f32x2(f, f),
+                                  *reinterpret_cast<const uint64_t*>(
+                                      parts + ((g - 1) * F::kRows + local) * d + 2 * lane + 64 * x),
+                                  o[r][x]);
         }
         m[r] = ms;
         l[r] = ls;
       }
-      if (t[r] >= u.seq.cnt) {  // no query: an empty state
+      const bool dead = t[r] >= u.seq.cnt;  // no query: an empty state
+      if (dead) {
         m[r] = -INFINITY;
         l[r] = 0.f;
       }
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
       for (int x = 0; x < kPairs; ++x)
         if (2 * lane + 64 * x < d)
           *reinterpret_cast<uint64_t*>(dst + 2 * lane + 64 * x) =
-              f == 0.f ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f, f));
+              dead ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f, f));
       if (lane == 0) {
         if (whole) {
           a.lse[q0 + local] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2F;

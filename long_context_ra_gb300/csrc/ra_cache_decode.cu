@@ -547,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int nn = 0; nn < S::kTilesN; ++nn)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) js[row * S::kLd + S::column(nn, 2 * t + z)] = o[nn][2 * h + z] * f;
+        for (int z = 0; z < 2; ++z)
+          js[row * S::kLd + S::column(nn, 2 * t + z)] = dead ? 0.f : o[nn][2 * h + z] * f;
     }
     __syncthreads();
     {
@@ -582,12 +583,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float4 y = *reinterpret_cast<const float4*>(js + (w * kRows + r) * S::kLd + 32 * x + x0);
-            if (f[w] != 0.f) {
-              v[0] = fmaf(f[w], y.x, v[0]);
-              v[1] = fmaf(f[w], y.y, v[1]);
-              v[2] = fmaf(f[w], y.z, v[2]);
-              v[3] = fmaf(f[w], y.w, v[3]);
-            }
+            // a weight of 0 too: y may be NaN, and is 0 without a seen key
+            v[0] = fmaf(f[w], y.x, v[0]);
+            v[1] = fmaf(f[w], y.y, v[1]);
+            v[2] = fmaf(f[w], y.z, v[2]);
+            v[3] = fmaf(f[w], y.w, v[3]);
           }
           if (whole) {
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (q0 + r) * D + 32 * x + x0) =

@@ -1056,16 +1056,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* from = xo + ((1 - t) * 128 + row) * 33;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const float y = from[e];
-              float z = f0 == 0.f ? 0.f : f0 * __uint_as_float(r[e]);
-              if (f1 != 0.f) z = fmaf(f1, y, z);
-              r[e] = __float_as_uint(z);
+              r[e] = __float_as_uint(fmaf(f1, from[e], f0 * __uint_as_float(r[e])));
             }
             mbar_arrive(bars.x_empty(1 - t));
             ++xc;
           }
           if (i == 0 && whole) inv = l == 0.f ? 0.f : 1.f / l;
-          if (l == 0.f) {
+          // A row without a query may hold anything.  Of one that sees no key, or
+          // a stream that it sees none of, the sums are 0; a weight of 0
+          // multiplies all the same, since sums may be NaN.
+          if (!live) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0u;
           }

@@ -303,3 +303,12 @@ def check_weight_zero(places, T, dtype, held, d):
 def test_nan_at_weight_zero_in_the_last_tile(T, dtype, held, d):
     """Both keys in the tile that holds the end of the context."""
     check_weight_zero([(2999, 2998), (2998, 3000)], T, dtype, held, d)
+
+
+@pytest.mark.parametrize("dtype,held,d", TYPES[:2] + TYPES[3:])
+@pytest.mark.parametrize("T", [1, 3, 24, 100])
+def test_nan_at_weight_zero_in_another_part(T, dtype, held, d):
+    """The two keys in the same or in other tiles, which other warps, streams
+    or blocks may work on: their states are joined with weight 0."""
+    check_weight_zero([(0, 40), (40, 0), (5, 2990), (2990, 5), (100, 164), (64, 2999), (2999, 2998),
+                       (2998, 3000)], T, dtype, held, d)
