@@ -649,8 +649,8 @@ RA_API void ra_watchdog_config(int64_t wait_cycles, int64_t stall_cta);
  * ra_last_device_status -- synchronise `stream`, then read and clear the
  * device-side watchdog word of the current device.  Returns RA_ERR_TIMEOUT if
  * any kernel since the last call gave up a bounded wait (its results are then
- * invalid), RA_ERR_PAGE if a cache call met a position or page outside the
- * cache (the first of the two wins), RA_ERR_CUDA if the synchronisation
+ * invalid), else RA_ERR_PAGE if a cache call met a position or page outside
+ * the cache (its other results are valid), RA_ERR_CUDA if the synchronisation
  * failed, else RA_OK.
  */
 RA_API ra_status ra_last_device_status(ra_stream_t stream);

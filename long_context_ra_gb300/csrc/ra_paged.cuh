@@ -12,6 +12,7 @@
 
 namespace ra {
 
+// A timeout, whose results are invalid, is not replaced.
 __device__ __forceinline__ void flag_page(int* status) { atomicCAS(status, 0, kStatusPage); }
 
 // Row of head 0 of position `pos` of sequence b in the cache (add

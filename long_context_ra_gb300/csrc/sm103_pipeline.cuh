@@ -32,7 +32,7 @@ struct Abort {
   long long limit;  // SM cycles a wait may take before it gives up
   __device__ void raise() const {
     *flag = 1u;
-    atomicCAS(status, 0, kStatusTimeout);
+    atomicExch(status, kStatusTimeout);  // also over a page error, which leaves results valid
   }
 };
 

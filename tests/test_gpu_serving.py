@@ -400,6 +400,34 @@ def test_stalled_cta_of_the_tree_kernel_times_out(held, T):
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
 
 
+@pytest.mark.parametrize("T", [10, 40])
+def test_a_timeout_is_reported_over_a_missing_page(T):
+    """A page outside the cache leaves the other results valid, a timeout does
+    not: with both since the last look, the timeout is what is reported."""
+    heads, Hq, d, page, L = 1, 8, 128, 64, 1500
+    table, pages = R.make_paged([L + T], page, 15)
+    tab, lens = table.to(DEV), i32(L)
+    cache = ra.new_cache(pages, heads, page, d)
+    ra.ra_cache_write(cache, *rnd(1, 2, 1, heads, L + T, d, dtype=BF16), tab, i32(0))
+    q = rnd(2, 1, Hq, T, d, dtype=BF16)
+    bad = table.clone()
+    bad[0, 3] = pages
+    assert ra.ra_last_device_status() == 0
+    ra.ra_cache_read(cache, bad.to(DEV), lens, 0, L)
+    torch.cuda.synchronize()
+    try:
+        ra.ra_watchdog_config(20_000_000, 1)
+        ra.ra_cache_attention(q, cache, tab, lens)
+        torch.cuda.synchronize()
+        ra.ra_cache_read(cache, bad.to(DEV), lens, 0, L)   # nor does a page behind it hide it
+        assert ra.ra_last_device_status() == _native.RA_ERR_TIMEOUT
+    finally:
+        ra.ra_watchdog_config(0, -1)
+    assert ra.ra_last_device_status() == 0
+    ra.ra_cache_read(cache, bad.to(DEV), lens, 0, L)
+    assert ra.ra_last_device_status() == _native.RA_ERR_PAGE
+
+
 # -------------------------------------------------------------------- refusals
 def test_the_binding_refuses_what_does_not_fit():
     cache = ra.new_cache(4, 2, 16, 64)
