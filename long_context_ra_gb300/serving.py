@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass, field
+from typing import NamedTuple
 
 import torch
 
@@ -220,10 +221,22 @@ def ra_qk_norm_rope_backward(q, k, dq_out, dk_out, rope: RaRope | None = None, p
 
 
 # ------------------------------------------------------------------ the cache
+class _Found(NamedTuple):
+    """A cache's fields, checked."""
+
+    places: tuple
+    c: RaCacheC
+    ref: object  # to c
+    heads: int
+    d: int
+    index: int
+
+
 @dataclass
 class RaCache:
     """Pages of K and V, [pages, heads, page, d] (float32, bfloat16, or
-    float8_e4m3fn with exponent bytes k_exp, v_exp [pages, heads, page])."""
+    float8_e4m3fn with exponent bytes k_exp, v_exp [pages, heads, page]).  A
+    call takes the tensors that the fields hold then."""
 
     k: torch.Tensor
     v: torch.Tensor
@@ -231,6 +244,27 @@ class RaCache:
     v_exp: torch.Tensor | None = None
 
     def __post_init__(self):
+        self._check()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, "_found", None)  # checked anew by the next call
+        object.__setattr__(self, name, value)
+
+    @property
+    def heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def d(self) -> int:
+        return self.k.shape[3]
+
+    def _places(self):
+        """What a tensor changed in place shows: addresses and sizes."""
+        k, v, ke, ve = self.k, self.v, self.k_exp, self.v_exp
+        return (k.data_ptr(), v.data_ptr(), 0 if ke is None else ke.data_ptr(),
+                0 if ve is None else ve.data_ptr(), k.numel(), v.numel())
+
+    def _check(self):
         k, v = self.k, self.v
         if k.dtype not in _CACHE_TYPES:
             raise TypeError(f"unsupported cache dtype {k.dtype}")
@@ -246,9 +280,18 @@ class RaCache:
         elif self.k_exp is not None or self.v_exp is not None:
             raise ValueError("only an 8-bit cache has exponents")
         pages, heads, page, d = k.shape
-        self.heads, self.d, self.device_index = heads, d, index
-        self.c = RaCacheC(*ptrs, pages, heads, page, d, _CACHE_TYPES[k.dtype])
-        self.ref = ctypes.byref(self.c)
+        c = RaCacheC(*ptrs, pages, heads, page, d, _CACHE_TYPES[k.dtype])
+        object.__setattr__(self, "_found", _Found(self._places(), c, ctypes.byref(c), heads, d, index))
+
+    def found(self, index) -> _Found:
+        """The fields as the C calls take them, on device `index`."""
+        f = self._found
+        if f is None or f.places != self._places():
+            self._check()
+            f = self._found
+        if f.index != index:
+            raise ValueError("the cache must be on the current CUDA device")
+        return f
 
 
 def new_cache(pages: int, heads: int, page: int, d: int, dtype=torch.bfloat16,
@@ -262,9 +305,7 @@ def new_cache(pages: int, heads: int, page: int, d: int, dtype=torch.bfloat16,
                            for _ in range(2)))
 
 
-def _sequences(cache: RaCache, table, lens, count, B: int, index: int):
-    if cache.device_index != index:
-        raise ValueError("the cache must be on the current CUDA device")
+def _sequences(table, lens, count, B: int, index: int):
     if table.dim() != 2 or table.shape[0] != B:
         raise ValueError("table must be [B, width]")
     return (_dev(table, index, torch.int32, what="table"), table.shape[1],
@@ -278,10 +319,11 @@ def ra_cache_write(cache: RaCache, k, v, table, lens, count=None, stream=None) -
     An 8-bit cache is quantised as it is written.  lens is not advanced."""
     B, heads, T, d = k.shape
     index = _here(k)
-    tab, width, ln, cnt = _sequences(cache, table, lens, count, B, index)
-    kp, ks = _rows(k, index, k.dtype, (B, cache.heads, T, cache.d), "k")
-    vp, vs = _rows(v, index, k.dtype, (B, cache.heads, T, cache.d), "v")
-    res = _native.lib().ra_cache_write(cache.ref, kp, ks, vp, vs, tab, width, ln, cnt, B, T,
+    c = cache.found(index)
+    tab, width, ln, cnt = _sequences(table, lens, count, B, index)
+    kp, ks = _rows(k, index, k.dtype, (B, c.heads, T, c.d), "k")
+    vp, vs = _rows(v, index, k.dtype, (B, c.heads, T, c.d), "v")
+    res = _native.lib().ra_cache_write(c.ref, kp, ks, vp, vs, tab, width, ln, cnt, B, T,
                                        _dtype_code(k), _on_stream(stream, index))
     _check(res, "ra_cache_write")
     return cache
@@ -294,21 +336,22 @@ def ra_cache_read(cache: RaCache, table, lens, first: int, n: int, dtype=None, k
     (default: that of a given k or v, the cache's, or bfloat16 for 8 bits)."""
     B = table.shape[0]
     index = _here(table)
-    tab, width, ln, _ = _sequences(cache, table, lens, None, B, index)
+    c = cache.found(index)
+    tab, width, ln, _ = _sequences(table, lens, None, B, index)
     if dtype is None:
         given = k if k is not None else v
         if given is not None:
             dtype = given.dtype
         else:
-            dtype = torch.bfloat16 if cache.c.dtype == RA_E4M3 else cache.k.dtype
-    shape = (B, cache.heads, n, cache.d)
+            dtype = torch.bfloat16 if c.c.dtype == RA_E4M3 else cache.k.dtype
+    shape = (B, c.heads, n, c.d)
     if k is None or v is None:
         with _on(stream):
             if k is None:
                 k = torch.empty(shape, device=cache.k.device, dtype=dtype)
             if v is None:
                 v = torch.empty(shape, device=cache.k.device, dtype=dtype)
-    res = _native.lib().ra_cache_read(cache.ref, tab, width, ln, first, n,
+    res = _native.lib().ra_cache_read(c.ref, tab, width, ln, first, n,
                                       _dev(k, index, dtype, shape, "k"),
                                       _dev(v, index, dtype, shape, "v"), B, _dtype_code(k),
                                       _on_stream(stream, index))
@@ -330,9 +373,10 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
     allocated when not given.  Returns (out [B, Hq, T, d], lse [B, Hq, T])."""
     B, Hq, T, d = q.shape
     index = _here(q)
-    tab, width, ln, cnt = _sequences(cache, table, lens, count, B, index)
-    if d != cache.d:
-        raise ValueError(f"q has head width {d}, the cache {cache.d}")
+    c = cache.found(index)
+    tab, width, ln, cnt = _sequences(table, lens, count, B, index)
+    if d != c.d:
+        raise ValueError(f"q has head width {d}, the cache {c.d}")
     mp, ms = None, 0
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8):
@@ -348,10 +392,10 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
             if lse is None:
                 lse = torch.empty((B, Hq, T), device=q.device, dtype=torch.float32)
             if workspace is None:
-                n = ra_cache_attention_workspace_bytes(B, Hq, cache.heads, T, d)
+                n = ra_cache_attention_workspace_bytes(B, Hq, c.heads, T, d)
                 workspace = torch.empty(max(n, 0), device=q.device, dtype=torch.uint8)
     res = _native.lib().ra_cache_attention(
-        _dev(q, index, shape=(B, Hq, T, d), what="q"), cache.ref, tab, width, ln, cnt, mp, ms,
+        _dev(q, index, shape=(B, Hq, T, d), what="q"), c.ref, tab, width, ln, cnt, mp, ms,
         _dev(out, index, q.dtype, (B, Hq, T, d), "out"),
         _dev(lse, index, torch.float32, (B, Hq, T), "lse"),
         _dev(workspace, index, torch.uint8, what="workspace"), workspace.numel(), B, Hq, T,

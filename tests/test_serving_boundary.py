@@ -242,3 +242,56 @@ def test_binding_refuses_host_tensors_and_wrong_caches(monkeypatch):
         ra.RaCache(x.half(), x.half())
     with pytest.raises(ValueError):
         ra.RaCache(x, x[:, :1])
+
+
+def test_a_cache_follows_its_fields(monkeypatch):
+    """A call takes the tensors that the cache has then: a field assigned anew
+    or a storage that moved reaches it, and what does not fit is refused."""
+    seen = []
+
+    class Lib:
+        def ra_cache_read(self, ref, *rest):
+            c = ctypes.cast(ref, ctypes.POINTER(_native.RaCacheC)).contents
+            seen.append((c.k, c.v, c.k_exp, c.v_exp, c.pages, c.dtype))
+            return 0
+
+    from long_context_ra_gb300 import serving
+    monkeypatch.setattr(serving, "_here", lambda t: None)
+    monkeypatch.setattr(serving, "_dev", lambda t, *a, **kw: t.data_ptr())
+    monkeypatch.setattr(serving, "_on_stream", lambda *a: 0)
+    monkeypatch.setattr(_native, "lib", Lib)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+
+    def call(c, code=_native.RA_BF16):
+        ra.ra_cache_read(c, table, lens, 0, 4, dtype=torch.bfloat16)
+        want = tuple(None if t is None else t.data_ptr() for t in (c.k, c.v, c.k_exp, c.v_exp))
+        assert seen[-1] == want + (c.k.shape[0], code)
+
+    pool = lambda pages: torch.zeros(pages, 2, 16, 64, dtype=torch.bfloat16)
+    c = ra.RaCache(pool(4), pool(4))
+    call(c)
+    c.k = pool(4)
+    call(c)
+    c.v = pool(4)
+    call(c)
+    before = c.k.data_ptr()
+    held = c.k.untyped_storage()
+    held.resize_(1 << 26)                       # in place: the storage moves
+    assert c.k.data_ptr() != before
+    call(c)
+    c.k, c.v = pool(9), pool(9)                 # grown: both sides, then the call
+    call(c)
+    c.k = pool(5)
+    with pytest.raises(ValueError):
+        call(c)
+    c.v = pool(5)
+    call(c)
+    c.k_exp = torch.zeros(5, 2, 16, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        call(c)
+    c.k, c.v = (x.to(torch.float8_e4m3fn) for x in (c.k, c.v))
+    with pytest.raises(ValueError):
+        call(c)
+    c.v_exp = torch.zeros(5, 2, 16, dtype=torch.uint8)
+    call(c, _native.RA_E4M3)
+    assert (c.heads, c.d) == (2, 64)
