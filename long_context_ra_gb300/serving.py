@@ -89,14 +89,15 @@ class _on:
 
 
 # ---------------------------------------------------------- norm and rotation
-@dataclass
+@dataclass(frozen=True)
 class RaRope:
-    """A rotation plan (see `new_rope`)."""
+    """A rotation plan (see `new_rope`); a backward pass takes it as the forward
+    had it, so its field is not assigned anew."""
 
     c: RaRopeC = field(repr=False)
 
     def __post_init__(self):
-        self.ref = ctypes.byref(self.c)
+        object.__setattr__(self, "ref", ctypes.byref(self.c))
 
     @property
     def rot(self) -> int:

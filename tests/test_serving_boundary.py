@@ -295,3 +295,12 @@ def test_a_cache_follows_its_fields(monkeypatch):
     c.v_exp = torch.zeros(5, 2, 16, dtype=torch.uint8)
     call(c, _native.RA_E4M3)
     assert (c.heads, c.d) == (2, 64)
+
+
+def test_a_rotation_plan_stays_as_it_is():
+    """The calls hold its address, and a gradient needs the forward's angles."""
+    a, b = ra.new_rope([1.0] * 4), ra.new_rope([0.5] * 8)
+    with pytest.raises(AttributeError):
+        a.c = b.c
+    c = ctypes.cast(a.ref, ctypes.POINTER(_native.RaRopeC)).contents
+    assert a.rot == c.rot == 8
