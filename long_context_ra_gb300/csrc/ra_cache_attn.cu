@@ -401,11 +401,6 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 // -> 96.2 us; eight parts in flight take 98 registers: 100.3 us).
 constexpr int kJoinWarps = 8;
 
-template <typename E, int kSplit>
-struct Join {
-  static constexpr int kStep = kJoinWarps / kSplit;  // rows at a time
-};
-
 // A unit that has parts: false where the block has none to join.
 struct Shared {
   int64_t q0;   // row of the unit's first row in q, out, lse
@@ -453,7 +448,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __shared__ DivisionShared sh;
   __shared__ float4 sums[kJoinWarps][kCols][32];
   __shared__ float sum_l[kJoinWarps];
-  using J = Join<E, kSplit>;
+  constexpr int kStep = kJoinWarps / kSplit;  // rows at a time
   constexpr int kParts = 4;
   const PagedArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -468,7 +463,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const uint32_t quads = c.d / 4;
   wait_for_parts();
   const int begin = blockIdx.x * block_rows, end = min(some, begin + block_rows);
-  for (int first = begin; first < end; first += J::kStep) {
+  for (int first = begin; first < end; first += kStep) {
     const int local = first + warp / kSplit;
     const bool shared = local < end;
     float ms = -INFINITY, l = 0.f;
@@ -664,7 +659,7 @@ cudaError_t tree_join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t 
 
 template <typename E, int kSplit, int kCols>
 cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-  using J = Join<E, kSplit>;
+  constexpr int kStep = kJoinWarps / kSplit;
   const int64_t rows = head_rows(a) < p.rows ? head_rows(a) : p.rows;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -672,12 +667,12 @@ cudaError_t join_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   // A block waits for its parts, so it takes rows one after another only where
   // there would be more blocks than the SMs hold at once.
-  const int64_t steps = (rows + J::kStep - 1) / J::kStep;
+  const int64_t steps = (rows + kStep - 1) / kStep;
   const int64_t units = static_cast<int64_t>(a.c.B) * p.div.units, borders = p.div.ctas - 1;
   const bool by_unit = units <= borders;
   const int64_t held = static_cast<int64_t>(device_sm_count()) * 8;
   const int64_t passes = (steps * (by_unit ? units : borders) + held - 1) / held;
-  const int block_rows = static_cast<int>(passes) * J::kStep;
+  const int block_rows = static_cast<int>(passes) * kStep;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + block_rows - 1) / block_rows),
                      static_cast<unsigned>(by_unit ? units : borders));
   cfg.blockDim = dim3(kJoinWarps * 32);
@@ -702,7 +697,6 @@ cudaError_t launch_ffma_t(const CacheAttnArgs& a, int ctas, cudaStream_t s) {
   p.div.units = a.c.heads * p.row_tiles;
   p.div.tile = F::kTile;
   p.div.ctas = ctas;
-  p.div.min_run = 1;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

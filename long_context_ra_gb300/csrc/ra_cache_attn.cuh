@@ -6,7 +6,6 @@
 
 namespace ra {
 
-constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
 
 // One launch's plan: how many query rows a unit holds and how its key tiles
@@ -48,6 +47,19 @@ __device__ __forceinline__ bool sees(const CacheAttnArgs& a, const SeqInfo& s, i
   if (j >= s.cnt) return false;
   if (!a.mask) return j <= t;
   return a.mask[b * a.mask_stride + static_cast<int64_t>(t) * a.c.T + j] != 0;
+}
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(at));
+  return x;
 }
 
 // CTAs of the kernels, which fix the size of the workspace.

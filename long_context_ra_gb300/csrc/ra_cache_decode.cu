@@ -87,24 +87,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
                "r"(real ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 8 : 0)
-               : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 x;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "r"(at));
-  return x;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
   uint2 x;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at));
@@ -630,7 +618,6 @@ cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s)
   p.div.units = a.c.heads * p.row_tiles;
   p.div.tile = kTile;
   p.div.ctas = kDecodeCtas;
-  p.div.min_run = 1;
   if (a.c.d == 128) return k8 ? launch_t<true, 128>(a, p, s) : launch_t<false, 128>(a, p, s);
   return k8 ? launch_t<true, 64>(a, p, s) : launch_t<false, 64>(a, p, s);
 }

@@ -184,21 +184,9 @@ __device__ __forceinline__ int piece_row(int x, int pc) {
   return D == 128 ? x ^ (pc / 4) : (pc / 4) * (kRows / 2) + (x ^ (pc / 4));
 }
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 8 : 0)
-               : "memory");
-}
 // One arrival on `bar` when this thread's cp.async so far have landed.
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 x;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "r"(at));
-  return x;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -1171,7 +1159,6 @@ cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s) {
   p.row_tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
   p.div.units = a.c.heads * p.row_tiles;
   p.div.ctas = kTreeCtas;
-  p.div.min_run = 1;
   if (a.c.d == 128) return k8 ? by_rows<true, 128>(a, p, s) : by_rows<false, 128>(a, p, s);
   return k8 ? by_rows<true, 64>(a, p, s) : by_rows<false, 64>(a, p, s);
 }

@@ -226,7 +226,7 @@ __device__ __forceinline__ void load_weight(const NormSide& s, const LanePlace<k
 template <typename E, int kP, int kLanes, bool kInterleaved>
 __global__ void __launch_bounds__(kForwardThreads) norm_rope_kernel(const __grid_constant__ NormArgs a,
                                                              int run) {
-  constexpr int kAhead = (sizeof(E) * kP >= 32 ? 2 : 4);
+  constexpr int kAhead = 4;
   const int l = threadIdx.x % kLanes;
   const int64_t token =
       static_cast<int64_t>(blockIdx.x) * (kForwardThreads / kLanes) + threadIdx.x / kLanes;

@@ -86,37 +86,10 @@ __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float* x) {
   }
 }
 
-// 8 consecutive elements as floats, and back.
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const __nv_fp8_e4m3* p, float* x) {
-  const uint2 a = *reinterpret_cast<const uint2*>(p);
-  unpack_e4m3x4(a.x, x);
-  unpack_e4m3x4(a.y, x + 4);
-}
+// 8 consecutive floats.
 __device__ __forceinline__ void store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // kV consecutive elements of a row as they lie in memory: loaded with wide
@@ -199,7 +172,6 @@ struct Division {
   int units;     // per sequence: key heads x row tiles
   int tile;      // keys per tile
   int ctas;
-  int min_run;   // tiles a CTA takes at least
 };
 
 __device__ __forceinline__ int64_t tiles_of(const SeqInfo& s, const Division& v) {
@@ -211,8 +183,7 @@ __device__ __forceinline__ int64_t seq_tiles(const PagedArgs& c, const Division&
 }
 
 __device__ __forceinline__ int64_t run_length(const Division& v, int64_t total) {
-  const int64_t per = (total + v.ctas - 1) / v.ctas;
-  return per < v.min_run ? v.min_run : per;
+  return (total + v.ctas - 1) / v.ctas;
 }
 
 // Shared scratch of the block-wide sums below.
