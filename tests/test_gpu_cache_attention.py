@@ -312,3 +312,37 @@ def test_nan_at_weight_zero_in_another_part(T, dtype, held, d):
     or blocks may work on: their states are joined with weight 0."""
     check_weight_zero([(0, 40), (40, 0), (5, 2990), (2990, 5), (100, 164), (64, 2999), (2999, 2998),
                        (2998, 3000)], T, dtype, held, d)
+
+
+LONG = [
+    ([0], None, 300, 4, 2, 64),                    # a prompt without a context
+    ([77, -1, 500], [257, 3, 140], 257, 4, 2, 16),  # chunks of two prompts, 514 rows a head
+    ([33], None, 520, 3, 3, 128),
+]
+
+
+@pytest.mark.parametrize("dtype,held,d", TYPES)
+@pytest.mark.parametrize("shape", LONG)
+def test_chunks_of_a_prompt(shape, dtype, held, d):
+    """More new tokens than a tile has rows."""
+    lens, count, T, Hq, heads, page = shape
+    q, cache, table, ln, cnt = make(lens, count, T, Hq, heads, page, d, dtype, held, 18)
+    got = ra.ra_cache_attention(q, cache, table.to(DEV), ln, cnt)
+    assert ra.ra_last_device_status() == 0
+    check(got, q, cache, table, lens, count, None)
+
+
+@pytest.mark.parametrize("dtype,held,d", TYPES[3:] + TYPES[:1])
+@pytest.mark.parametrize("at", [0, 127, 150, 256])
+def test_a_new_value_that_is_not_finite_in_a_chunk(at, dtype, held, d):
+    """It reaches the tokens from its own on, in its column, and no bit of the
+    ones before, whichever tile of rows they are in."""
+    lens, T, Hq, heads, page, column = [100, 0], 257, 4, 2, 32, 9
+    q, cache, table, ln, _ = make(lens, None, T, Hq, heads, page, d, dtype, held, 19)
+    want = ra.ra_cache_attention(q, cache, table.to(DEV), ln)
+    bad = with_value(cache, table, [(b, n + at) for b, n in enumerate(lens)], 1, column, math.nan)
+    out, lse = ra.ra_cache_attention(q, bad, table.to(DEV), ln)
+    assert out[:, 2:, at:, column].isnan().all()
+    same = torch.ones(out.shape, dtype=torch.bool, device=DEV)
+    same[:, 2:, at:, column] = False
+    assert torch.equal(out[same], want[0][same]) and torch.equal(lse, want[1])
