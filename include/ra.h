@@ -386,7 +386,10 @@ RA_API ra_status ra_backward_block(const void* q, const void* k, const void* v, 
  *   interleaved  0: pair i = elements (i, i + rot / 2); 1: (2i, 2i + 1).
  *   turns        round(frac(inv_freq / 2 pi) 2^64): the angle in turns is the
  *                fraction of position * turns / 2^64, an integer product that
- *                wraps, so far positions lose no precision.
+ *                wraps.  It is off by |position| 2^-65 turns at most (2^-64
+ *                for |inv_freq| >= 2^16) beside the rounding of the fraction
+ *                to fp32: nothing that fp32 shows up to positions of 2^39,
+ *                3e-6 radian at 2^44.
  */
 typedef struct ra_rope {
   int32_t rot;
@@ -507,7 +510,9 @@ typedef struct ra_cache {
  * that is read and written again keeps its values.  Infinities saturate to
  * 448 * 2^e; NaN stays NaN.  (Magnitudes from 1.9375 * 2^127 on round up to
  * 2^128, which reads back as infinity.)
- *   k, v  [B, heads, T, d] of `dtype`, strides as in ra_qk_norm_rope.
+ *   k, v  [B, heads, T, d] of `dtype`, read through strides as in
+ *         ra_qk_norm_rope, but 16-byte aligned and with strides that are
+ *         multiples of 16 bytes (8 bf16 or 4 f32 elements).
  * Tokens of one call must go to different places: sequences that share a
  * page may share only pages that the call does not write.  lens is not
  * advanced.
@@ -524,7 +529,8 @@ RA_API ra_status ra_cache_write(const ra_cache* cache, const void* k, const int6
  * ra_cache_read -- positions first .. first + n - 1 of every sequence, in
  * `dtype` (the cache's type, or RA_F32 / RA_BF16 for an RA_E4M3 cache): the
  * visiting blocks of ra_fold, or the K/V of a prompt that is continued.
- *   k, v  [B, heads, n, d], dense, written; rows at or behind lens are 0.
+ *   k, v  [B, heads, n, d], dense, 16-byte aligned, written; rows at or behind
+ *         lens are 0.
  * Values are exact (RA_E4M3 into RA_BF16 too, but where a value is below
  * bf16's normal range).
  * Errors as ra_cache_write.
@@ -541,8 +547,9 @@ RA_API ra_status ra_cache_read(const ra_cache* cache, const int32_t* table, int3
  * mask[t][j], in the online-softmax form of ra_forward ("Ring Attention:
  * the math", section "The online-softmax identity that makes streaming
  * legal"); tau = 1 / sqrt(d).
- *   q     [B, Hq, T, d] of `dtype`, dense; Hq a multiple of cache->heads:
- *         query head h reads key head h / (Hq / heads).
+ *   q     [B, Hq, T, d] of `dtype`, dense, 16-byte aligned as out is; Hq a
+ *         multiple of cache->heads: query head h reads key head
+ *         h / (Hq / heads).
  *   mask  uint8 [T, T] per sequence, mask_stride bytes apart (0: one for
  *         all); non-zero: seen.  NULL: j <= t.
  *   out   [B, Hq, T, d] of `dtype`;  lse [B, Hq, T] fp32.  Rows that see no

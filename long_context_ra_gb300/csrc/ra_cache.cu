@@ -13,6 +13,13 @@
 // (four: 69).  Reads take 8 (16: 154 us instead of 125 for 131072 positions of
 // 8 heads out of 8 bits; a lane then stores 32 bytes in two instructions, each
 // of which fills half of a line) and four rows ahead (eight: 127, two: 140).
+// Both choices were measured with bf16 rows and an 8-bit cache.  With the others
+// a lane moves 32 or 64 bytes in steps of 16, in half lines; one sequence, 8
+// heads of 128, us by graph replay and the bytes' floor:
+//   53248 written   bf16 to 8 bits 53 (48), to bf16 75 (64); f32 to 8 bits 89
+//                   (80), to f32 158 (128)
+//   131072 read     8 bits to bf16 123 (119), bf16 160 (158); 8 bits to f32 265
+//                   (198), f32 341 (316)
 
 #include "ra_paged.cuh"
 

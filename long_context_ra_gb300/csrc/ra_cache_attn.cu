@@ -768,9 +768,10 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dt
                         : (held == RA_E4M3 ? launch_ffma<__nv_fp8_e4m3, 4>(a, s) : launch_ffma<float, 4>(a, s));
   // The decode kernel reads a key head once per 16 query rows, the tree kernel
   // once per 256.  Up to 16 rows the former is ahead throughout.  With 17 to 32
-  // rows it still is over 8-bit caches, which the tree kernel has to widen
-  // (16 sequences of 16384, 8 heads, 32 rows: 190 against 242 us; bf16: 331
-  // against 182).
+  // rows it still is over 8-bit caches at d = 128, which the tree kernel has to
+  // widen (8 heads, 32 rows, 16 sequences of 16384: 192 against 227 us, 2 of
+  // 60000: 102 against 115; bf16: 331 against 183 for the former), and even at d =
+  // 64 (141 against 133, 72 against 73).
   const int most = held == RA_E4M3 ? 2 * kDecodeRows : kDecodeRows;
   if (head_rows(a) > most) return launch_cache_tree(a, held == RA_E4M3, s);
   return launch_cache_decode(a, held == RA_E4M3, s);

@@ -15,7 +15,8 @@
 // own, and the two states are joined at the end of the unit.  Four tiles are
 // held while two streams are at work, so at d = 128 those are of 64 keys, which
 // leaves room for tiles on their way; at d = 64 128 keys fit (2 sequences of
-// 60000, 8 heads, 32 rows: 72 -> 56 us, out of 8 bits 103 -> 84).
+// 60000, 8 heads, 64 rows: 82 -> 61 us, out of 8 bits 99 -> 80; 58 and 78 with
+// the later steps).
 //
 // Warp roles (640 threads, 96 registers each at launch):
 //   warps 0-3, 4-7   softmax of stream 0, 1                            (112)
@@ -31,7 +32,7 @@
 // page that does not exist is a box behind the view, which TMA fills with
 // zeros.  bf16 tiles land as operands.  Only value tiles that hold drafts or
 // the end of the sequence pass through warp 12, which clears the rows behind
-// the end.  8-bit tiles land in a raw ring and become bf16 in warps 12-15,
+// the end.  8-bit tiles land in a raw ring and become bf16 in warps 12-19,
 // with the row's scale inside: code * 2^e has 4 significant bits, so it is
 // exact in bf16 for values above 2^-126, and neither the scores nor the
 // probabilities need to know the scale.

@@ -16,8 +16,10 @@
 // pairs of floats (fma.rn.f32x2): with single ones the backward was bound by
 // its instructions.
 //
-// The angle is exact for any position: pos * turns wraps modulo 2^64 and its
-// upper half is the signed fraction of a turn.
+// pos * turns wraps modulo 2^64 as the angle does, and its upper half is the
+// signed fraction of a turn.  turns is off by 2^-65 at most (2^-64 from 2^16
+// radians on), so the angle is by |pos| 2^-65 turns beside fp32's own rounding
+// of the fraction (2^-26): as good as fp32 can tell up to positions of 2^39.
 //
 // Measured, 32768 tokens of 32 + 8 heads of 128, bf16: forward 110 us (671 MB,
 // 89 % of the copy rate; with 4-element pieces and one head ahead 219), backward
