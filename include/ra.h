@@ -560,7 +560,9 @@ RA_API ra_status ra_cache_read(const ra_cache* cache, const int32_t* table, int3
  *              overlap on the GPU, captured ones too, need their own.
  * An element that is not finite, in a key or value row that a query does
  * not see, does not reach that query's result.  Of a value row that it sees,
- * it makes that column of the result infinite or NaN.
+ * it makes that column of the result infinite or NaN.  Sums are fp32 before
+ * they are divided by l: |v| times 2^8 times the keys of a row has to stay
+ * below 2^128.
  * Types: RA_BF16 inputs over an RA_BF16 or RA_E4M3 cache run on the tensor
  * cores (d in {64, 128}); RA_F32 inputs over an RA_F32 or RA_E4M3 cache on
  * the FFMA path (any d the cache may have).
