@@ -583,6 +583,132 @@ RA_API int64_t ra_cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t
                                                   int32_t T, int32_t d);
 
 /*
+ * Pages that several sequences hold.  A table has, beside `lens`,
+ *   ref   int32 [pages] holders of each page: how many rows of tables have it
+ *         among their held columns; 0: free.  All zeros at first.
+ *   held  int32 [B] leading columns of each row that hold a page, 0 .. width;
+ *         the columns behind hold -1.
+ * One table and its counts serve the caches of every layer.  What these calls
+ * meet outside the table or the pages (a page number, a source, a context
+ * that is not held) is left out, and ra_last_device_status returns
+ * RA_ERR_PAGE once.  Calls that share ref or a table run one after the other.
+ *
+ * ra_pages_fork -- new rows that continue sequences: row i of the new table
+ * holds the pages of sequence source[i]'s tokens (the first
+ * ceil(lens / page) columns), whose counts rise by one, and has its length.
+ * source[i] < 0, or one with lens < 0: an empty row with lens_out = -1.  A
+ * step of a beam search is a fork into a second table and a release of the
+ * first; samples of one prompt are forks of one row.
+ *   source     int32 [n], any of 0 .. B - 1, each as often as it is wanted.
+ *   table_out  int32 [n, width], held_out, lens_out int32 [n]: written; they
+ *              may not overlap table, held, lens.
+ *   page       rows of a page, as ra_cache has it.
+ * Errors: RA_ERR_INVALID_ARG (null pointer, negative size, overlap),
+ * RA_ERR_UNSUPPORTED (page; B x width or n x width over 2^31 - 1),
+ * RA_ERR_MISALIGNED, RA_ERR_ARCH, RA_ERR_CUDA.
+ */
+RA_API ra_status ra_pages_fork(int32_t* ref, int64_t pages, const int32_t* table, const int32_t* held,
+                               const int32_t* lens, int32_t width, int32_t page, int32_t B, const int32_t* source,
+                               int32_t n, int32_t* table_out, int32_t* held_out, int32_t* lens_out,
+                               ra_stream_t stream);
+
+/*
+ * ra_pages_reserve -- room for the next count (0 .. T; NULL: T) tokens of every
+ * sequence.  Columns up to ceil((lens + count) / page) get free pages.  Where
+ * the first new token falls into a page that other rows hold too, a free page
+ * takes its place, and (src, dst) name the page whose rows have to be copied
+ * (ra_cache_copy, for every layer's cache); the last of its holders, if all of
+ * them ask, keeps it.  The lowest free page numbers are given out in the order
+ * (sequence, column).
+ *   granted   int32 [B], written: the new tokens that have room (count, or 0):
+ *             the `count` of the calls that follow.
+ *   src, dst  int32 [B], written: pages to copy, -1 for none.
+ * All or nothing: with too few free pages every granted is 0, nothing else
+ * changes, and ra_last_device_status returns RA_ERR_PAGE.  So it does, for
+ * that sequence alone, where a sequence would pass the table's width, does not
+ * hold its context, or shares a page behind the one of its next token
+ * (ra_pages_trim gives those back).  lens < 0: takes no part.
+ * Errors: as ra_pages_fork; RA_ERR_UNSUPPORTED for more than 8192 sequences.
+ */
+RA_API ra_status ra_pages_reserve(int32_t* ref, int64_t pages, int32_t* table, int32_t* held, const int32_t* lens,
+                                  const int32_t* count, int32_t width, int32_t page, int32_t B, int32_t T,
+                                  int32_t* granted, int32_t* src, int32_t* dst, ra_stream_t stream);
+
+/*
+ * ra_pages_trim -- give back the pages behind every sequence's tokens: held
+ * becomes ceil(lens / page) where it was more, the columns behind it -1, and
+ * their pages' counts fall by one.  lens < 0, or lens NULL: all pages of the
+ * sequence, or of every one (it has ended).
+ * Errors: as ra_pages_fork.
+ */
+RA_API ra_status ra_pages_trim(int32_t* ref, int64_t pages, int32_t* table, int32_t* held, const int32_t* lens,
+                               int32_t width, int32_t page, int32_t B, ra_stream_t stream);
+
+/*
+ * ra_cache_copy -- page dst[i] becomes a copy of page src[i] (K, V and
+ * exponents), i < n; a pair with a negative number is passed over, one with a
+ * number outside the cache too, with RA_ERR_PAGE as above.  The pages of dst
+ * are different ones, and none of them is in src.
+ * Errors: as ra_cache_write.
+ */
+RA_API ra_status ra_cache_copy(const ra_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
+                               ra_stream_t stream);
+
+/*
+ * ra_cache_compact -- move the kept ones of a sequence's newest tokens
+ * together: for j < kept the rows at position lens + path[j] go to position
+ * lens + j.  path (int32 [B, T]) rises from token to token, as that of
+ * ra_verify_drafts does; at the first entry that does not, or is T or more, the
+ * sequence's moves end, with RA_ERR_PAGE as above.  kept int32 [B], 0 .. T;
+ * lens < 0: takes no part.  lens is not advanced.  Positions lens .. lens +
+ * T - 1 of a sequence lie in pages of its own.
+ * Errors: as ra_cache_write.
+ */
+RA_API ra_status ra_cache_compact(const ra_cache* cache, const int32_t* table, int32_t width, const int32_t* lens,
+                                  const int32_t* path, const int32_t* kept, int32_t B, int32_t T,
+                                  ra_stream_t stream);
+
+/*
+ * ra_verify_drafts -- which drafted tokens stay, and the token that follows
+ * them, such that what comes out is distributed as the model's own samples.
+ * A sequence's nodes 0 .. count - 1 are tokens in the order of the attention
+ * call: node 0 is the newest token that is settled already, node t > 0 is a
+ * draft that follows node parent[t] < t.  At a node (from node 0 on) its drafts
+ * x_1, x_2, .. (in order of t) are tried, with p, q the node's rows of probs
+ * and draft_probs, r_0 = p and s_0 = 1:
+ *     x_k stays if u_k q(x_k) s_{k-1} < r_{k-1}(x_k); it is the next node;
+ *     else r_k = max(r_{k-1} - s_{k-1} q, 0), s_k = sum of r_k.
+ * Where none is left, the next token is the first i with r(0) + .. + r(i) >
+ * u_0 (r(0) + .. + r(V - 1)) (r = p where nothing is left of r; the last i
+ * with r(i) > 0 where rounding leaves none).
+ *   probs        [B, T, V] of `dtype`: row t is the model's distribution of
+ *                the token after node t.  Elements are >= 0; rows add up to 1.
+ *   draft_probs  likewise: row t is what the drafts below node t were drawn
+ *                from, each by itself.  NULL: drafts were chosen, not drawn
+ *                (q = 1 at the draft); r_k is then r_{k-1} without x_k.
+ *   tokens       int64 [B, T].  parent  int32 [B, T], or NULL: a chain (t - 1).
+ *                A node whose token is not in 0 .. V - 1 or whose parent is not
+ *                in 0 .. t - 1 is no draft (entry 0 is not looked at).
+ *   count        int32 [B], 0 .. T, or NULL (T).  0: takes no part.
+ *   uniform      fp32 [B, T] in [0, 1): u_t of node t; u_0 is that of the next
+ *                token.
+ *   path         int32 [B, T], written: the nodes that stay, 0 first, rising;
+ *                -1 behind them.
+ *   kept         int32 [B], written: their number (0: takes no part).
+ *   token        int64 [B], written: the next token; -1 where the sequence
+ *                takes no part or the row's sum is not positive and finite.
+ * Decisions are those of the formulas in real numbers but for a relative
+ * 2^-40 or so around their borders.
+ * probs and draft_probs are 16-byte aligned.  T <= 1024, V <= 2^31 - 1.
+ * Errors: RA_ERR_INVALID_ARG (null pointer, negative size, T or V < 1, bad
+ * dtype), RA_ERR_UNSUPPORTED, RA_ERR_MISALIGNED, RA_ERR_ARCH, RA_ERR_CUDA.
+ */
+RA_API ra_status ra_verify_drafts(const void* probs, const void* draft_probs, const int64_t* tokens,
+                                  const int32_t* parent, const int32_t* count, const float* uniform, int32_t* path,
+                                  int32_t* kept, int64_t* token, int32_t B, int32_t T, int64_t V, ra_dtype dtype,
+                                  ra_stream_t stream);
+
+/*
  * ra_state_init -- set a state to empty: m = -inf, l = 0, o = 0 ("Ring
  * Attention: the math", section "Accumulation math, step by step": "state = (m
  * = -inf, l = 0, o = 0)").

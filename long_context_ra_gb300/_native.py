@@ -83,6 +83,12 @@ PROTOTYPES = {
     "ra_cache_attention": (_I32, [_P, _P, _P, _I32, _P, _P, _P, _I64, _P, _P, _P, _I64, _I32,
                                   _I32, _I32, _I32, _P]),
     "ra_cache_attention_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32]),
+    "ra_pages_fork": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P]),
+    "ra_pages_reserve": (_I32, [_P, _I64, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "ra_pages_trim": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _P]),
+    "ra_cache_copy": (_I32, [_P, _P, _P, _I32, _P]),
+    "ra_cache_compact": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _P]),
+    "ra_verify_drafts": (_I32, [_P] * 9 + [_I32, _I32, _I64, _I32, _P]),
     "ra_state_init": (_I32, [_SP, _P]),
     "ra_fold": (_I32, [_SP, _P, _P, _P, _I64, _I64, _I32, _P]),
     "ra_merge": (_I32, [_SP, _I32, _P, _P, _I32, _P]),

@@ -81,6 +81,50 @@ cudaError_t launch_cache_write(const CacheCopyArgs& a, ra_dtype dense, ra_dtype 
 cudaError_t launch_cache_read(const CacheCopyArgs& a, ra_dtype dense, ra_dtype held,
                               cudaStream_t s);
 
+// Rows of page numbers, and how many rows hold each page.
+struct PageTableArgs {
+  int32_t* ref;  // [pages]
+  int64_t pages;
+  int32_t* table;  // [B, width]
+  int32_t* held;   // [B] columns that hold a page
+  const int32_t* lens;
+  int32_t width, B;
+  int32_t page_shift;
+  int* status;
+};
+
+// Sequences of one reservation: five bytes of shared memory each.
+constexpr int kReserveSequences = 8192;
+
+cudaError_t launch_pages_fork(const PageTableArgs& a, const int32_t* source, int32_t n, int32_t* table_out,
+                              int32_t* held_out, int32_t* lens_out, cudaStream_t s);
+cudaError_t launch_pages_reserve(const PageTableArgs& a, const int32_t* count, int32_t T, int32_t* granted,
+                                 int32_t* src, int32_t* dst, cudaStream_t s);
+cudaError_t launch_pages_trim(const PageTableArgs& a, cudaStream_t s);
+cudaError_t launch_cache_copy(const PagedArgs& c, ra_dtype held, const int32_t* src, const int32_t* dst, int32_t n,
+                              cudaStream_t s);
+// The kept tokens of a sequence are c.count.
+cudaError_t launch_cache_compact(const PagedArgs& c, ra_dtype held, const int32_t* path, cudaStream_t s);
+
+// Drafts of one call: their tokens, parents and probabilities lie in shared memory.
+constexpr int kVerifyNodes = 1024;
+
+struct VerifyArgs {
+  const void* probs;  // [B, T, V]
+  const void* draft;  // the same, or NULL
+  const int64_t* tokens;
+  const int32_t* parent;  // NULL: t - 1
+  const int32_t* count;   // NULL: T
+  const float* uniform;
+  int32_t* path;
+  int32_t* kept;
+  int64_t* token;
+  int32_t B, T;
+  int64_t V;
+};
+
+cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s);
+
 struct CacheAttnArgs {
   PagedArgs c;
   const void* q;  // [B, Hq, T, d]

@@ -126,6 +126,30 @@ ra_status check_cache(const ra_cache* cache, const int32_t* table, int32_t width
   return RA_OK;
 }
 
+// A type that fits the cache, where a call has no tensors beside it.
+ra_dtype own_dtype(const ra_cache* cache) { return cache && cache->dtype != RA_E4M3 ? cache->dtype : RA_F32; }
+
+// A table of pages and their counts.
+ra_status check_pages(int32_t* ref, int64_t pages, const int32_t* table, const int32_t* held, const int32_t* lens,
+                      int32_t width, int32_t page, int32_t B, bool lens_needed, PageTableArgs* a) {
+  if (pages < 0 || width < 0 || page < 1 || B < 0) return RA_ERR_INVALID_ARG;
+  if (page < 8 || page > 1024 || (page & (page - 1)) != 0) return RA_ERR_UNSUPPORTED;
+  if (pages > INT32_MAX || static_cast<int64_t>(B) * width > INT32_MAX) return RA_ERR_UNSUPPORTED;
+  if (B > 0 && (!held || (lens_needed && !lens) || (width > 0 && !table) || (pages > 0 && !ref)))
+    return RA_ERR_INVALID_ARG;
+  if (!aligned(ref, 4) || !aligned(table, 4) || !aligned(held, 4) || !aligned(lens, 4)) return RA_ERR_MISALIGNED;
+  *a = PageTableArgs{};
+  a->ref = ref;
+  a->pages = pages;
+  a->table = const_cast<int32_t*>(table);
+  a->held = const_cast<int32_t*>(held);
+  a->lens = lens;
+  a->width = width;
+  a->B = B;
+  while ((1 << a->page_shift) < page) ++a->page_shift;
+  return RA_OK;
+}
+
 }  // namespace
 }  // namespace ra
 
@@ -341,6 +365,106 @@ RA_API ra_status ra_cache_attention(const void* q, const ra_cache* cache, const 
   a.wait_limit = wait_limit();
   a.stall_cta = stall_cta();
   return launched(launch_cache_attention(a, dtype, cache->dtype, cu(stream)));
+}
+
+RA_API ra_status ra_pages_fork(int32_t* ref, int64_t pages, const int32_t* table, const int32_t* held,
+                               const int32_t* lens, int32_t width, int32_t page, int32_t B, const int32_t* source,
+                               int32_t n, int32_t* table_out, int32_t* held_out, int32_t* lens_out,
+                               ra_stream_t stream) {
+  RA_TRACE("ra_pages_fork");
+  PageTableArgs a;
+  ra_status st = check_pages(ref, pages, table, held, lens, width, page, B, true, &a);
+  if (st != RA_OK) return st;
+  if (n < 0) return RA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(n) * width > INT32_MAX) return RA_ERR_UNSUPPORTED;
+  if (!aligned(source, 4) || !aligned(table_out, 4) || !aligned(held_out, 4) || !aligned(lens_out, 4))
+    return RA_ERR_MISALIGNED;
+  if (n == 0) return RA_OK;
+  if (!source || (width > 0 && !table_out) || !held_out || !lens_out) return RA_ERR_INVALID_ARG;
+  // a new row that lies over an old one would be read as it is written
+  const int32_t *t0 = table, *t1 = table + static_cast<int64_t>(B) * width;
+  if (width > 0 && B > 0 && table_out < t1 && t0 < table_out + static_cast<int64_t>(n) * width)
+    return RA_ERR_INVALID_ARG;
+  if (B > 0 && ((held_out < held + B && held < held_out + n) || (lens_out < lens + B && lens < lens_out + n)))
+    return RA_ERR_INVALID_ARG;
+  if ((st = device_ready(&a.status)) != RA_OK) return st;
+  return launched(launch_pages_fork(a, source, n, table_out, held_out, lens_out, cu(stream)));
+}
+
+RA_API ra_status ra_pages_reserve(int32_t* ref, int64_t pages, int32_t* table, int32_t* held, const int32_t* lens,
+                                  const int32_t* count, int32_t width, int32_t page, int32_t B, int32_t T,
+                                  int32_t* granted, int32_t* src, int32_t* dst, ra_stream_t stream) {
+  RA_TRACE("ra_pages_reserve");
+  PageTableArgs a;
+  ra_status st = check_pages(ref, pages, table, held, lens, width, page, B, true, &a);
+  if (st != RA_OK) return st;
+  if (T < 0) return RA_ERR_INVALID_ARG;
+  if (B > kReserveSequences) return RA_ERR_UNSUPPORTED;
+  if (!aligned(count, 4) || !aligned(granted, 4) || !aligned(src, 4) || !aligned(dst, 4)) return RA_ERR_MISALIGNED;
+  if (B == 0) return RA_OK;
+  if (!granted || !src || !dst) return RA_ERR_INVALID_ARG;
+  if ((st = device_ready(&a.status)) != RA_OK) return st;
+  return launched(launch_pages_reserve(a, count, T, granted, src, dst, cu(stream)));
+}
+
+RA_API ra_status ra_pages_trim(int32_t* ref, int64_t pages, int32_t* table, int32_t* held, const int32_t* lens,
+                               int32_t width, int32_t page, int32_t B, ra_stream_t stream) {
+  RA_TRACE("ra_pages_trim");
+  PageTableArgs a;
+  ra_status st = check_pages(ref, pages, table, held, lens, width, page, B, false, &a);
+  if (st != RA_OK) return st;
+  if (B == 0) return RA_OK;
+  if ((st = device_ready(&a.status)) != RA_OK) return st;
+  return launched(launch_pages_trim(a, cu(stream)));
+}
+
+RA_API ra_status ra_cache_copy(const ra_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
+                               ra_stream_t stream) {
+  RA_TRACE("ra_cache_copy");
+  PagedArgs c;
+  if (n < 0) return RA_ERR_INVALID_ARG;
+  ra_status st = check_cache(cache, nullptr, 0, nullptr, 0, 0, own_dtype(cache), &c);
+  if (st != RA_OK) return st;
+  if (!aligned(src, 4) || !aligned(dst, 4)) return RA_ERR_MISALIGNED;
+  if (n == 0) return RA_OK;
+  if (!src || !dst) return RA_ERR_INVALID_ARG;
+  if ((st = device_ready(&c.status)) != RA_OK) return st;
+  return launched(launch_cache_copy(c, cache->dtype, src, dst, n, cu(stream)));
+}
+
+RA_API ra_status ra_cache_compact(const ra_cache* cache, const int32_t* table, int32_t width, const int32_t* lens,
+                                  const int32_t* path, const int32_t* kept, int32_t B, int32_t T,
+                                  ra_stream_t stream) {
+  RA_TRACE("ra_cache_compact");
+  PagedArgs c;
+  ra_status st = check_cache(cache, table, width, lens, B, T, own_dtype(cache), &c);
+  if (st != RA_OK) return st;
+  if (!aligned(path, 4) || !aligned(kept, 4)) return RA_ERR_MISALIGNED;
+  if (B == 0 || T == 0) return RA_OK;
+  if (!path || !kept) return RA_ERR_INVALID_ARG;
+  if ((st = device_ready(&c.status)) != RA_OK) return st;
+  c.count = kept;
+  return launched(launch_cache_compact(c, cache->dtype, path, cu(stream)));
+}
+
+RA_API ra_status ra_verify_drafts(const void* probs, const void* draft_probs, const int64_t* tokens,
+                                  const int32_t* parent, const int32_t* count, const float* uniform, int32_t* path,
+                                  int32_t* kept, int64_t* token, int32_t B, int32_t T, int64_t V, ra_dtype dtype,
+                                  ra_stream_t stream) {
+  RA_TRACE("ra_verify_drafts");
+  if (B < 0 || T < 1 || V < 1) return RA_ERR_INVALID_ARG;
+  if (dtype != RA_F32 && dtype != RA_BF16) return RA_ERR_INVALID_ARG;
+  if (T > kVerifyNodes || V > INT32_MAX || B > (1 << 24)) return RA_ERR_UNSUPPORTED;
+  if (!aligned(probs, 16) || !aligned(draft_probs, 16) || !aligned(tokens, 8) || !aligned(token, 8) ||
+      !aligned(parent, 4) || !aligned(count, 4) || !aligned(uniform, 4) || !aligned(path, 4) || !aligned(kept, 4))
+    return RA_ERR_MISALIGNED;
+  if (B == 0) return RA_OK;
+  if (!probs || !tokens || !uniform || !path || !kept || !token) return RA_ERR_INVALID_ARG;
+  int* status = nullptr;
+  const ra_status st = device_ready(&status);
+  if (st != RA_OK) return st;
+  const VerifyArgs a{probs, draft_probs, tokens, parent, count, uniform, path, kept, token, B, T, V};
+  return launched(launch_verify(a, dtype == RA_BF16, cu(stream)));
 }
 
 }  // extern "C"

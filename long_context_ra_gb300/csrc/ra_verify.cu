@@ -1,0 +1,437 @@
+// Verification of drafted tokens against a model's distributions.
+//
+// At a node with distribution p, drafts x_1, x_2, .. were drawn from q (row of
+// the same node), independently of one another.  With r_0 = p, s_0 = 1:
+//   x_k stays iff u_k q(x_k) s_{k-1} < r_{k-1}(x_k); else
+//   r_k = max(r_{k-1} - s_{k-1} q, 0),  s_k = sum of r_k.
+// What stays is distributed as p whatever q is.  Since q is the same for all of
+// a node's drafts, r_k = max(p - c q, 0) with c = s_0 + .. + s_{k-1}: nothing
+// of a row has to be kept between its passes.  Drafts that were chosen, not
+// drawn (no q), count as drawn with probability 1: r_k is p without the refused
+// tokens.  The walk ends at a node all of whose drafts are refused; its next
+// token is the first i with r(0) + .. + r(i) > u_0 sum r.
+//
+// Bound by the bytes of the rows at which sequences stop (V of p and of q),
+// and for few sequences by the chain decide - sum - search.  A cluster of CTAs
+// takes a sequence, each a part of the row; all walk the tree alike from the
+// drafts' own probabilities, which are gathered at the start by one thread
+// each, and read a row only where they need its sum.
+//
+// Decisions have to be those of the definition next to a border as well, and a
+// border lies in every 1 / V of the unit interval: sums of fp32 would move 1 %
+// of them.  FP64 adds at 1/64 of the rate of fp32, which would bound the pass;
+// a lane sums into a pair of floats (error-free sums, 2^-47), and 64 bits take
+// over across lanes.
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "ra_internal.h"
+#include "ra_serve.h"
+
+namespace ra {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMostCtas = 8;  // of a cluster
+
+// h + l, |l| at most half a step of h.
+struct Pair {
+  float h, l;
+  __device__ double value() const { return static_cast<double>(h) + l; }
+  // += (x, e), both without error but for the last places of l
+  __device__ void add(float x, float e) {
+    const float s = __fadd_rn(h, x);
+    const float z = __fsub_rn(s, h);
+    const float err = __fadd_rn(__fsub_rn(h, __fsub_rn(s, z)), __fsub_rn(x, z));
+    h = s;
+    l = __fadd_rn(l, __fadd_rn(err, e));
+  }
+};
+
+// max(p - c q, 0) as a pair; NaN stays NaN.
+__device__ __forceinline__ Pair rest_of(float p, float q, Pair c) {
+  const float m = __fmul_rn(c.h, q);
+  const float me = __fmaf_rn(c.l, q, __fmaf_rn(c.h, q, -m));
+  const float s = __fsub_rn(p, m);
+  const float z = __fsub_rn(s, p);
+  const float err = __fsub_rn(__fsub_rn(p, __fsub_rn(s, z)), __fadd_rn(m, z));
+  const float e = __fsub_rn(err, me);
+  return __fadd_rn(s, e) <= 0.f ? Pair{0.f, 0.f} : Pair{s, e};
+}
+
+template <typename E>
+struct Piece {  // 16 bytes of a row
+  static constexpr int kN = 16 / sizeof(E);
+  uint4 w;
+  __device__ float get(int i) const {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    if (sizeof(E) == 4) return __uint_as_float(x[i % 4]);
+    return __uint_as_float(i & 1 ? x[(i / 2) % 4] & 0xffff0000u : x[(i / 2) % 4] << 16);
+  }
+};
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// A node's row, in pieces that lie on 16 bytes: element i of the row is place
+// i + shift, and places outside the row hold nothing.
+template <typename E, bool kDraft>
+struct Row {
+  const E* p;
+  const E* q;
+  int64_t V;
+  int shift;
+  Pair c;
+  const int32_t* refused;  // tokens that are out (without q)
+  int n_refused;
+
+  __device__ int64_t pieces() const { return (V + shift + Piece<E>::kN - 1) / Piece<E>::kN; }
+
+  __device__ __forceinline__ Piece<E> load(const E* row, int64_t v) const {
+    constexpr int kN = Piece<E>::kN;
+    const int64_t first = v * kN - shift;
+    if (first >= 0 && first + kN <= V) {
+      Piece<E> x;
+      x.w = __ldg(reinterpret_cast<const uint4*>(row + first));
+      return x;
+    }
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if (first + i < 0 || first + i >= V) continue;
+      const uint32_t bits = __float_as_uint(as_float(row[first + i]));
+      if (sizeof(E) == 4)
+        w[i % 4] = bits;
+      else
+        w[(i / 2) % 4] |= i & 1 ? bits : bits >> 16;
+    }
+    return Piece<E>{make_uint4(w[0], w[1], w[2], w[3])};
+  }
+
+  // f(i, rest) for the elements of piece v, whose bytes are x and y
+  template <typename F>
+  __device__ __forceinline__ void each(int64_t v, const Piece<E>& x, const Piece<E>& y, F f) const {
+    constexpr int kN = Piece<E>::kN;
+    uint32_t out = 0;  // bit i: element i was refused
+    if (!kDraft)
+      for (int z = 0; z < n_refused; ++z) {
+        const int64_t place = refused[z] + shift;
+        if (place / kN == v) out |= 1u << (place % kN);
+      }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      Pair r{x.get(i), 0.f};
+      if (kDraft) r = rest_of(x.get(i), y.get(i), c);
+      if (!kDraft && ((out >> i) & 1u)) r = Pair{0.f, 0.f};
+      f(i, r);
+    }
+  }
+
+  // The sum of pieces first, first + step, .. below last.
+  __device__ __forceinline__ Pair sum(int64_t first, int64_t last, int step) const {
+    constexpr int kAhead = kDraft ? 2 : 4;
+    Pair s{0.f, 0.f};
+    for (int64_t v = first; v < last; v += kAhead * step) {
+      Piece<E> x[kAhead], y[kAhead];
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z)
+        if (v + z * step < last) {
+          x[z] = load(p, v + z * step);
+          if (kDraft) y[z] = load(q, v + z * step);
+        }
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z)
+        if (v + z * step < last) each(v + z * step, x[z], y[z], [&](int, Pair r) { s.add(r.h, r.l); });
+    }
+    return s;
+  }
+};
+
+__device__ __forceinline__ double sum_lanes(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ double scan_lanes(double x) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// The first i with before + part[0] + .. + part[i] > target, or the last with
+// part[i] > 0 where rounding leaves none; `before` becomes the sum ahead of it.
+__device__ __forceinline__ int crossing(const double* part, int n, double target, double& before) {
+  double at = before, ahead = before;
+  int last = -1;
+  for (int i = 0; i < n; ++i) {
+    if (part[i] > 0.0) {
+      last = i;
+      ahead = at;
+      if (at + part[i] > target) break;
+    }
+    at += part[i];
+  }
+  before = ahead;
+  return last;
+}
+// The same for a value per lane.
+__device__ __forceinline__ int crossing_lane(double mine, double target, double& before) {
+  const double upto = before + scan_lanes(mine);
+  const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
+  const uint32_t past = __ballot_sync(0xffffffffu, mine > 0.0 && upto > target);
+  const int at = past ? __ffs(past) - 1 : 31 - __clz(some);
+  const double ahead = __shfl_sync(0xffffffffu, upto - mine, max(at, 0));
+  before = ahead;
+  return at;
+}
+
+template <typename E, bool kDraft>
+__global__ void __launch_bounds__(kThreads)
+    verify_kernel(const __grid_constant__ VerifyArgs a) {
+  extern __shared__ int32_t parent[];                        // [T]
+  int32_t* tokens = parent + a.T;                            // [T]
+  int32_t* refused = tokens + a.T;                           // [T]
+  float* us = reinterpret_cast<float*>(refused + a.T);       // [T]
+  float* ps = us + a.T;                                      // [T] p of the parent's row at the token
+  float* qs = ps + a.T;                                      // [T]
+  __shared__ double warp_sums[kWarps], cta_sums[2][kMostCtas], cta_sum[2];
+  __shared__ int next_draft;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
+  const int b = blockIdx.x / ctas;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int count = max(0, min(a.count ? a.count[b] : a.T, a.T));
+  const int64_t row0 = static_cast<int64_t>(b) * a.T;
+  int32_t* path = a.path + row0;
+  if (count == 0) {
+    if (rank == 0) {
+      for (int t = threadIdx.x; t < a.T; t += kThreads) path[t] = -1;
+      if (threadIdx.x == 0) {
+        a.kept[b] = 0;
+        a.token[b] = -1;
+      }
+    }
+    return;  // the whole cluster
+  }
+
+  // ---- the drafts and their own probabilities; -1: not a node of the tree
+  for (int t = threadIdx.x; t < count; t += kThreads) {
+    const int above = a.parent ? a.parent[row0 + t] : t - 1;
+    const int64_t x = a.tokens[row0 + t];
+    const bool good = t > 0 && above >= 0 && above < t && x >= 0 && x < a.V;
+    parent[t] = good ? above : -1;
+    tokens[t] = static_cast<int32_t>(good ? x : 0);
+    us[t] = a.uniform[row0 + t];
+    const int64_t at = (row0 + above) * a.V + x;
+    ps[t] = good ? as_float(static_cast<const E*>(a.probs)[at]) : 0.f;
+    qs[t] = good && kDraft ? as_float(static_cast<const E*>(a.draft)[at]) : 1.f;
+  }
+  __syncthreads();
+
+  Row<E, kDraft> row;
+  row.V = a.V;
+  row.refused = refused;
+  auto enter = [&](int node) {
+    const int64_t at = (row0 + node) * a.V;
+    row.p = static_cast<const E*>(a.probs) + at;
+    row.q = static_cast<const E*>(kDraft ? a.draft : a.probs) + at;
+    row.shift = static_cast<int>(at % Piece<E>::kN);
+    row.c = Pair{0.f, 0.f};
+    row.n_refused = 0;
+  };
+  // The row's sum, of every CTA's part and warp's part of it.
+  int turn = 0;
+  int64_t w0 = 0, w1 = 0;  // this warp's pieces
+  auto row_sum = [&]() {
+    const int64_t n = row.pieces();
+    const int64_t each = (n + ctas * kWarps - 1) / (ctas * kWarps);
+    w0 = min(n, (rank * kWarps + warp) * each);
+    w1 = min(n, w0 + each);
+    const double mine = sum_lanes(row.sum(w0 + lane, w1, 32).value());
+    __syncthreads();
+    if (lane == 0) warp_sums[warp] = mine;
+    __syncthreads();
+    turn ^= 1;
+    if (threadIdx.x == 0) {
+      double s = 0.0;
+      for (int i = 0; i < kWarps; ++i) s += warp_sums[i];
+      cta_sum[turn] = s;
+    }
+    cluster.sync();
+    if (static_cast<int>(threadIdx.x) < ctas)
+      cta_sums[turn][threadIdx.x] = *cluster.map_shared_rank(&cta_sum[turn], threadIdx.x);
+    __syncthreads();
+    double s = 0.0;
+    for (int i = 0; i < ctas; ++i) s += cta_sums[turn][i];
+    return s;
+  };
+
+  // ---- the walk, alike in every thread
+  int node = 0, kept = 1, t = 0;
+  double total = 1.0, scale = 0.0;  // of what is left of the row; c
+  double whole = -1.0;              // without q: the sum of the node's row, once it is known
+  double gone = 0.0;                // without q: that of the refused tokens
+  bool known = true;                // total is up to date
+  enter(0);
+  if (rank == 0 && threadIdx.x == 0) path[0] = 0;
+  while (true) {
+    // the next draft below `node`
+    if (warp == 0) {
+      int found = count;
+      for (int t0 = t + 1; t0 < count; t0 += 32) {
+        const uint32_t here = __ballot_sync(0xffffffffu, t0 + lane < count && parent[t0 + lane] == node);
+        if (here) {
+          found = t0 + __ffs(here) - 1;
+          break;
+        }
+      }
+      if (lane == 0) next_draft = found;
+    }
+    __syncthreads();
+    t = next_draft;
+    __syncthreads();
+    if (t >= count) break;
+    if (!known) {
+      if (kDraft) {
+        total = row_sum();
+      } else {
+        if (whole < 0.0) {
+          const int n = row.n_refused;
+          row.n_refused = 0;
+          whole = row_sum();
+          row.n_refused = n;
+        }
+        total = whole - gone;
+      }
+      known = true;
+    }
+    const double p = ps[t], q = qs[t];
+    double rest = p;
+    bool again = false;  // a token that was refused before
+    if (kDraft) {
+      rest = fmax(p - scale * q, 0.0);
+    } else {
+      for (int i = 0; i < row.n_refused; ++i) again = again || refused[i] == tokens[t];
+      if (again) rest = 0.0;
+    }
+    if (us[t] * q * total < rest) {
+      if (rank == 0 && threadIdx.x == 0) path[kept] = t;
+      ++kept;
+      node = t;
+      enter(node);
+      total = 1.0;
+      scale = gone = 0.0;
+      whole = -1.0;
+      known = true;
+      continue;
+    }
+    if (kDraft) {
+      scale += total;
+      row.c.h = static_cast<float>(scale);
+      row.c.l = static_cast<float>(scale - row.c.h);
+    } else if (!again) {
+      __syncthreads();
+      if (threadIdx.x == 0) refused[row.n_refused] = tokens[t];
+      __syncthreads();
+      ++row.n_refused;
+      gone += p;
+    }
+    known = false;
+  }
+
+  // ---- the next token
+  total = row_sum();
+  if (!(total > 0.0)) {  // nothing is left: p itself
+    row.c = Pair{0.f, 0.f};
+    row.n_refused = 0;
+    total = row_sum();
+  }
+  const bool some = total > 0.0 && total < INFINITY;
+  if (rank == 0) {
+    for (int i = kept + threadIdx.x; i < a.T; i += kThreads) path[i] = -1;
+    if (threadIdx.x == 0) {
+      a.kept[b] = kept;
+      if (!some) a.token[b] = -1;
+    }
+  }
+  if (some) {
+    const double target = us[0] * total;
+    double before = 0.0;
+    // CTA, warp, a lane's run of pieces, piece, element
+    if (crossing(cta_sums[turn], ctas, target, before) == rank &&
+        crossing(warp_sums, kWarps, target, before) == warp) {
+      const int64_t run = (w1 - w0 + 31) / 32;
+      const int64_t mine = min(w1, w0 + lane * run);
+      int at = crossing_lane(row.sum(mine, min(w1, mine + run), 1).value(), target, before);
+      // the pieces of that run, 32 at a time, up to those that pass the target
+      const int64_t r0 = min(w1, w0 + at * run), r1 = min(w1, r0 + run);
+      int64_t v0 = r0;
+      double sofar = before;
+      for (int64_t i = r0; i < r1; i += 32) {
+        const double all = sum_lanes(i + lane < r1 ? row.sum(i + lane, i + lane + 1, 1).value() : 0.0);
+        if (all > 0.0) {
+          v0 = i;
+          before = sofar;
+          if (sofar + all > target) break;
+        }
+        sofar += all;
+      }
+      at = crossing_lane(v0 + lane < r1 ? row.sum(v0 + lane, v0 + lane + 1, 1).value() : 0.0, target, before);
+      if (at >= 0 && lane == at) {
+        const int64_t v = v0 + at;
+        const Piece<E> x = row.load(row.p, v), y = row.load(row.q, v);
+        int64_t found = -1;
+        bool past = false;
+        Pair sum{0.f, 0.f};
+        row.each(v, x, y, [&](int i, Pair r) {
+          if (!past && r.h + r.l > 0.f) {
+            found = v * Piece<E>::kN - row.shift + i;
+            sum.add(r.h, r.l);
+            past = before + sum.value() > target;
+          }
+        });
+        a.token[b] = found;
+      }
+    }
+  }
+  cluster.sync();  // no CTA's sums go while another reads them
+}
+
+template <typename E, bool kDraft>
+cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
+  // All clusters at once on the SMs, four CTAs on each: more CTAs shorten a
+  // sequence's chain, waves lengthen it.
+  int ctas = kMostCtas;
+  while (ctas > 1 && static_cast<int64_t>(a.B) * ctas > 4 * device_sm_count()) ctas /= 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.T) * 24;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<E, kDraft>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s) {
+  if (bf16) return a.draft ? launch_t<__nv_bfloat16, true>(a, s) : launch_t<__nv_bfloat16, false>(a, s);
+  return a.draft ? launch_t<float, true>(a, s) : launch_t<float, false>(a, s);
+}
+
+}  // namespace ra

@@ -1,5 +1,6 @@
 """The calls around the attention: norm and rotation of queries and keys, the
-paged K/V cache, and attention of new tokens over it (``include/ra.h``).
+paged K/V cache, attention of new tokens over it, forks of sequences and their
+pages, and the verification of drafts (``include/ra.h``).
 
 As in the package's other calls, the functions only marshal arguments.  All
 tensors of a call are on the current CUDA device; a call with tensors of
@@ -403,3 +404,135 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
         _dtype_code(q), _on_stream(stream, index))
     _check(res, "ra_cache_attention")
     return out, lse
+
+
+# ------------------------------------------------------ pages that are shared
+def _table(ref, table, held, lens, index):
+    """Addresses and sizes of a table and its counts: (ref, pages, table, held,
+    lens, width, B)."""
+    if table.dim() != 2 or ref.dim() != 1:
+        raise ValueError("table must be [B, width] and ref [pages]")
+    B, width = table.shape
+    return (_dev(ref, index, torch.int32, what="ref"), ref.shape[0],
+            _dev(table, index, torch.int32, what="table"), _dev(held, index, torch.int32, (B,), "held"),
+            None if lens is None else _dev(lens, index, torch.int32, (B,), "lens"), width, B)
+
+
+def ra_pages_fork(ref, table, held, lens, source, page: int, table_out=None, held_out=None,
+                  lens_out=None, stream=None):
+    """Rows that continue sequences source [n] (int32; < 0: an empty row):
+    they hold the same pages, whose counts in ref rise.  Returns (table_out
+    [n, width], held_out [n], lens_out [n])."""
+    index = _here(table)
+    r, pages, tab, hl, ln, width, B = _table(ref, table, held, lens, index)
+    n = source.shape[0]
+    if table_out is None or held_out is None or lens_out is None:
+        with _on(stream):
+            if table_out is None:
+                table_out = torch.empty((n, width), device=table.device, dtype=torch.int32)
+            if held_out is None:
+                held_out = torch.empty(n, device=table.device, dtype=torch.int32)
+            if lens_out is None:
+                lens_out = torch.empty(n, device=table.device, dtype=torch.int32)
+    res = _native.lib().ra_pages_fork(
+        r, pages, tab, hl, ln, width, page, B, _dev(source, index, torch.int32, (n,), "source"), n,
+        _dev(table_out, index, torch.int32, (n, width), "table_out"),
+        _dev(held_out, index, torch.int32, (n,), "held_out"),
+        _dev(lens_out, index, torch.int32, (n,), "lens_out"), _on_stream(stream, index))
+    _check(res, "ra_pages_fork")
+    return table_out, held_out, lens_out
+
+
+def ra_pages_reserve(ref, table, held, lens, page: int, T: int, count=None, granted=None, src=None,
+                     dst=None, stream=None):
+    """Room for count[b] (None: T) new tokens of every sequence: table, held
+    and ref are updated.  Returns (granted, src, dst), int32 [B] each: the new
+    tokens that have room (the `count` of the calls that follow), and the pages
+    that ra_cache_copy has to copy in every layer's cache before they are
+    written."""
+    index = _here(table)
+    r, pages, tab, hl, ln, width, B = _table(ref, table, held, lens, index)
+    if granted is None or src is None or dst is None:
+        with _on(stream):
+            granted, src, dst = (torch.empty(B, device=table.device, dtype=torch.int32) if t is None
+                                 else t for t in (granted, src, dst))
+    res = _native.lib().ra_pages_reserve(
+        r, pages, tab, hl, ln, None if count is None else _dev(count, index, torch.int32, (B,), "count"),
+        width, page, B, T, _dev(granted, index, torch.int32, (B,), "granted"),
+        _dev(src, index, torch.int32, (B,), "src"), _dev(dst, index, torch.int32, (B,), "dst"),
+        _on_stream(stream, index))
+    _check(res, "ra_pages_reserve")
+    return granted, src, dst
+
+
+def ra_pages_trim(ref, table, held, lens, page: int, stream=None) -> None:
+    """Give back the pages behind lens[b] tokens (all of them for lens[b] < 0,
+    and of every sequence for lens=None): table, held and ref are updated."""
+    index = _here(table)
+    r, pages, tab, hl, ln, width, B = _table(ref, table, held, lens, index)
+    res = _native.lib().ra_pages_trim(r, pages, tab, hl, ln, width, page, B, _on_stream(stream, index))
+    _check(res, "ra_pages_trim")
+
+
+def ra_cache_copy(cache: RaCache, src, dst, stream=None) -> RaCache:
+    """Page dst[i] becomes a copy of page src[i] (int32 [n]; pairs with a
+    negative number are passed over)."""
+    index = _here(src)
+    c = cache.found(index)
+    n = src.shape[0]
+    res = _native.lib().ra_cache_copy(c.ref, _dev(src, index, torch.int32, (n,), "src"),
+                                      _dev(dst, index, torch.int32, (n,), "dst"), n,
+                                      _on_stream(stream, index))
+    _check(res, "ra_cache_copy")
+    return cache
+
+
+def ra_cache_compact(cache: RaCache, table, lens, path, kept, stream=None) -> RaCache:
+    """Move the kept new tokens together: the rows at position lens[b] +
+    path[b, j] go to lens[b] + j, j < kept[b] (path int32 [B, T], rising, as
+    ra_verify_drafts returns it).  lens is not advanced."""
+    B, T = path.shape
+    index = _here(path)
+    c = cache.found(index)
+    tab, width, ln, _ = _sequences(table, lens, None, B, index)
+    res = _native.lib().ra_cache_compact(c.ref, tab, width, ln,
+                                         _dev(path, index, torch.int32, (B, T), "path"),
+                                         _dev(kept, index, torch.int32, (B,), "kept"), B, T,
+                                         _on_stream(stream, index))
+    _check(res, "ra_cache_compact")
+    return cache
+
+
+# ------------------------------------------------------- verification of drafts
+def ra_verify_drafts(probs, tokens, uniform, parent=None, draft_probs=None, count=None, path=None,
+                     kept=None, token=None, stream=None):
+    """Which drafts stay, and the token after them.  probs [B, T, V]: the
+    model's distribution after node t (float32 or bfloat16, rows that add up to
+    1); node 0 is the newest settled token, tokens [B, T] (int64) the drafts,
+    parent [B, T] (int32; None: a chain) the node that each follows;
+    draft_probs: what they were drawn from (None: they were chosen); uniform
+    [B, T] float32 in [0, 1).  Returns (path [B, T] int32: the nodes that stay,
+    -1 behind them; kept [B] int32: their number, node 0 counted; token [B]
+    int64)."""
+    B, T, V = probs.shape
+    index = _here(probs)
+    if path is None or kept is None or token is None:
+        with _on(stream):
+            if path is None:
+                path = torch.empty((B, T), device=probs.device, dtype=torch.int32)
+            if kept is None:
+                kept = torch.empty(B, device=probs.device, dtype=torch.int32)
+            if token is None:
+                token = torch.empty(B, device=probs.device, dtype=torch.int64)
+    res = _native.lib().ra_verify_drafts(
+        _dev(probs, index, what="probs"),
+        None if draft_probs is None else _dev(draft_probs, index, probs.dtype, (B, T, V), "draft_probs"),
+        _dev(tokens, index, torch.int64, (B, T), "tokens"),
+        None if parent is None else _dev(parent, index, torch.int32, (B, T), "parent"),
+        None if count is None else _dev(count, index, torch.int32, (B,), "count"),
+        _dev(uniform, index, torch.float32, (B, T), "uniform"),
+        _dev(path, index, torch.int32, (B, T), "path"), _dev(kept, index, torch.int32, (B,), "kept"),
+        _dev(token, index, torch.int64, (B,), "token"), B, T, V, _dtype_code(probs),
+        _on_stream(stream, index))
+    _check(res, "ra_verify_drafts")
+    return path, kept, token
