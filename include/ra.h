@@ -583,6 +583,34 @@ RA_API int64_t ra_cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t
                                                   int32_t T, int32_t d);
 
 /*
+ * ra_cache_attention_shared -- ra_cache_attention for sequences that share
+ * prefixes: samples or beams of one context, requests behind one instruction.
+ * A prefix is read, and its products are taken, once for a group's queries.
+ *   shared  int32 [B]: shared[b] > 0 says that the first shared[b] tokens of
+ *           sequence b are those of the sequence before it (the next lower one
+ *           that takes part, lens >= 0); else a group begins at b.  The first
+ *           one's entry is not looked at.  A group has the smallest of its
+ *           entries and lengths in common, cut to whole tiles and pages; that
+ *           part is read through the table row of its first sequence, whether
+ *           the others hold the same pages or equal copies.
+ * Result, other arguments, limits and errors as ra_cache_attention, whose
+ * rounding differs where states are joined; RA_ERR_INVALID_ARG also for a NULL
+ * `shared`.  Nothing is shared (each sequence reads its own pages, and equal
+ * contents give an equal result) where a key head has more than 128 (RA_F32: 16)
+ * query rows of a sequence, or half as many in a batch too small for the larger
+ * units, and where B is above 2048.
+ */
+RA_API ra_status ra_cache_attention_shared(const void* q, const ra_cache* cache, const int32_t* table,
+                                           int32_t width, const int32_t* lens, const int32_t* shared,
+                                           const int32_t* count, const uint8_t* mask, int64_t mask_stride,
+                                           void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                                           int32_t B, int32_t Hq, int32_t T, ra_dtype dtype, ra_stream_t stream);
+
+/* Scratch bytes ra_cache_attention_shared needs (-1 for invalid sizes). */
+RA_API int64_t ra_cache_attention_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,
+                                                         int32_t d);
+
+/*
  * Pages that several sequences hold.  A table has, beside `lens`,
  *   ref   int32 [pages] holders of each page: how many rows of tables have it
  *         among their held columns; 0: free.  All zeros at first.

@@ -28,7 +28,8 @@ __all__ = ["RaError", "RaState", "ra_forward", "ra_forward_causal", "ra_forward_
            "RaCache", "RaRope", "new_cache", "new_rope", "ra_qk_norm_rope",
            "ra_qk_norm_rope_backward", "ra_qk_norm_rope_backward_workspace_bytes",
            "ra_cache_write", "ra_cache_read", "ra_cache_attention",
-           "ra_cache_attention_workspace_bytes", "ra_pages_fork", "ra_pages_reserve",
+           "ra_cache_attention_workspace_bytes", "ra_cache_attention_shared",
+           "ra_cache_attention_shared_workspace_bytes", "ra_pages_fork", "ra_pages_reserve",
            "ra_pages_trim", "ra_cache_copy", "ra_cache_compact", "ra_verify_drafts"]
 
 
@@ -360,6 +361,7 @@ def ra_watchdog_config(wait_cycles: int = 0, stall_cta: int = -1) -> None:
 
 
 from .serving import (RaCache, RaRope, new_cache, new_rope, ra_cache_attention,  # noqa: E402
+                      ra_cache_attention_shared, ra_cache_attention_shared_workspace_bytes,
                       ra_cache_attention_workspace_bytes, ra_cache_compact, ra_cache_copy,
                       ra_cache_read, ra_cache_write, ra_pages_fork, ra_pages_reserve,
                       ra_pages_trim, ra_qk_norm_rope, ra_qk_norm_rope_backward,

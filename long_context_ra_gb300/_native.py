@@ -83,6 +83,9 @@ PROTOTYPES = {
     "ra_cache_attention": (_I32, [_P, _P, _P, _I32, _P, _P, _P, _I64, _P, _P, _P, _I64, _I32,
                                   _I32, _I32, _I32, _P]),
     "ra_cache_attention_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32]),
+    "ra_cache_attention_shared": (_I32, [_P, _P, _P, _I32, _P, _P, _P, _P, _I64, _P, _P, _P, _I64,
+                                         _I32, _I32, _I32, _I32, _P]),
+    "ra_cache_attention_shared_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32]),
     "ra_pages_fork": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P]),
     "ra_pages_reserve": (_I32, [_P, _I64, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
     "ra_pages_trim": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _P]),

@@ -59,9 +59,9 @@ struct Ffma {
   static int smem(int d) { return (kRows * d + kTile * (2 * d + 4)) * 4; }
 };
 
-template <typename H, typename F>
+template <typename H, typename F, typename A>
 __global__ void __launch_bounds__(F::kThreads, F::kCtas)
-    cache_attn_ffma_kernel(const __grid_constant__ CacheAttnArgs a,
+    cache_attn_ffma_kernel(const __grid_constant__ A a,
                            const __grid_constant__ AttnPlan p) {
   constexpr bool k8 = sizeof(H) == 1;
   constexpr int kRW = F::kRW, kKL = F::kKL, kTile = F::kTile, kPairs = F::kPairs;
@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
   __shared__ int64_t key_row[2][kTile];
   __shared__ float4 probs[F::kWarps][F::kWarpKeys][kRW / 2];  // (p, p, p', p') of two rows
   __shared__ float states[F::kWarps][kRW][2];
-  const PagedArgs& c = a.c;
+  constexpr bool kShared = IsShared<A>::value;
+  const auto& c = paged(a);
   const int d = c.d, ld = d + 4;
   float* qs = reinterpret_cast<float*>(smem4);  // [kRows][d]
   float* ks = qs + F::kRows * d;                // [kTile][ld]
@@ -80,11 +81,22 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
   const int64_t rows = head_rows(a);
 
   allow_join();
+  wait_for_plan(a);
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   UnitWalk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
     const int head = u.unit / p.row_tiles;
     const int64_t r0 = static_cast<int64_t>(u.unit % p.row_tiles) * F::kRows;
+    // row `local` of a unit over a stretch
+    [[maybe_unused]] auto member = [&](int local) {
+      if constexpr (kShared) return MemberRow(a, c.list[u.b], u.unit, 0, local);
+    };
+    auto is_row = [&](int local) {
+      if constexpr (kShared)
+        return member(local).q >= 0;
+      else
+        return r0 + local < rows;
+    };
     // q, out, lse row of row 0 of the unit
     const int64_t q0 = (static_cast<int64_t>(u.b) * c.heads + head) * rows + r0;
     const int64_t keys = u.seq.keys(), context = u.seq.len;
@@ -101,19 +113,35 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     const float* q = static_cast<const float*>(a.q) + q0 * d;
     for (int i = threadIdx.x * 4; i < F::kRows * d; i += F::kThreads * 4) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r0 + i / d < rows) x = *reinterpret_cast<const float4*>(q + i);
+      if constexpr (kShared) {
+        const int64_t at = member(i / d).q;
+        if (at >= 0) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at * d + i % d);
+      } else if (r0 + i / d < rows) {
+        x = *reinterpret_cast<const float4*>(q + i);
+      }
       const float t = a.scale_log2;
       *reinterpret_cast<float4*>(qs + i) = make_float4(x.x * t, x.y * t, x.z * t, x.w * t);
     }
     float m[kRW], l[kRW];
     uint64_t o[kRW][kPairs];  // columns 2 lane, 2 lane + 1 of every 64
     int t[kRW];
+    // a row's sequence and the new tokens that it may see (stretches: per row)
+    int mask_b[kShared ? kRW : 1], cnt[kShared ? kRW : 1];
+    auto seq_of = [&](int r) { return SeqInfo{u.seq.len, kShared ? cnt[r % (kShared ? kRW : 1)] : u.seq.cnt}; };
+    auto b_of = [&](int r) { return kShared ? mask_b[r % (kShared ? kRW : 1)] : u.b; };
 #pragma unroll
     for (int r = 0; r < kRW; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
-      const int64_t row = r0 + rg * kRW + r;
-      t[r] = row < rows ? static_cast<int>(row % c.T) : c.T;
+      if constexpr (kShared) {
+        const MemberRow y = member(rg * kRW + r);
+        t[r] = y.t;
+        mask_b[r] = y.b;
+        cnt[r] = y.cnt;
+      } else {
+        const int64_t row = r0 + rg * kRW + r;
+        t[r] = row < rows ? static_cast<int>(row % c.T) : c.T;
+      }
 #pragma unroll
       for (int x = 0; x < kPairs; ++x) o[r][x] = 0ull;
     }
@@ -171,7 +199,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         }
       }
       const bool clean = !__syncthreads_or(bad);
-      if (r0 + rg * kRW >= rows) continue;  // no row of this warp's
+      if (!is_row(rg * kRW)) continue;  // no row of this warp's
       // ---- scores of keys lane, lane + 32 of the warp's part of the tile
       const float* kw = ks + (kg * F::kWarpKeys + lane) * ld;
       const float* qw = qs + rg * kRW * d;
@@ -214,7 +242,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
           const bool here = at[kg * F::kWarpKeys + lane + 32 * z] >= 0;
 #pragma unroll
           for (int r = 0; r < kRW; ++r)
-            if (!here || !sees(a, u.seq, u.b, t[r], pos)) s[r][z] = -INFINITY;
+            if (!here || !sees(a, seq_of(r), b_of(r), t[r], pos)) s[r][z] = -INFINITY;
         }
       }
       // ---- reference, probabilities
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
           float2* pr = reinterpret_cast<float2*>(probs[warp][lane + 32 * z]);
 #pragma unroll
           for (int r = 0; r < kRW; ++r)
-            if (!here || !sees(a, u.seq, u.b, t[r], pos)) pr[r] = make_float2(-0.f, -0.f);
+            if (!here || !sees(a, seq_of(r), b_of(r), t[r], pos)) pr[r] = make_float2(-0.f, -0.f);
         }
       }
       __syncwarp();
@@ -330,7 +358,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 #pragma unroll
     for (int r = 0; r < kRW; ++r) {
       const int local = rg * kRW + r;
-      if (r0 + local >= rows) continue;
+      if (!is_row(local)) continue;
       if (F::kKG > 1) {
         float ms = m[r];
 #pragma unroll
@@ -357,15 +385,32 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         m[r] = ms;
         l[r] = ls;
       }
-      const bool dead = t[r] >= u.seq.cnt;  // no query: an empty state
+      const bool dead = t[r] >= seq_of(r).cnt;  // no query: an empty state
       if (dead) {
         m[r] = -INFINITY;
         l[r] = 0.f;
       }
-      const bool whole = u.whole();
-      const float f = l[r] == 0.f ? 0.f : whole ? 1.f / l[r] : 1.f;
+      const bool whole = u.whole(), finish = whole && !kShared;
+      const float f = l[r] == 0.f ? 0.f : finish ? 1.f / l[r] : 1.f;
       const int slot = u.slot(blockIdx.x);
-      float* dst = whole ? static_cast<float*>(a.out) + (q0 + local) * d
+      if constexpr (kShared) {
+        if (whole) {
+          const int64_t q_row = member(local).q;
+#pragma unroll
+          for (int x = 0; x < kPairs; ++x) {
+            const int col = 2 * lane + 64 * x;
+            if (col < d)
+              *reinterpret_cast<uint64_t*>(a.whole_o + (col / 4 * a.all_rows + q_row) * 4 + col % 4) =
+                  dead ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f, f));
+          }
+          if (lane == 0) {
+            a.whole_ml[2 * q_row] = m[r];
+            a.whole_ml[2 * q_row + 1] = l[r];
+          }
+          continue;
+        }
+      }
+      float* dst = finish ? static_cast<float*>(a.out) + (q0 + local) * d
                          : slot_o(a, p, slot) + static_cast<int64_t>(local) * d;
 #pragma unroll
       for (int x = 0; x < kPairs; ++x)
@@ -373,7 +418,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
           *reinterpret_cast<uint64_t*>(dst + 2 * lane + 64 * x) =
               dead ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f, f));
       if (lane == 0) {
-        if (whole) {
+        if (finish) {
           a.lse[q0 + local] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2F;
         } else {
           float* ml = slot_ml(a, p, slot) + 2 * local;
@@ -689,33 +734,85 @@ cudaError_t join_s(const CacheAttnArgs& a, const AttnPlan& p, bool bf16, cudaStr
   return bf16 ? join_t<__nv_bfloat16, kSplit, 2>(a, p, s) : join_t<float, kSplit, 2>(a, p, s);
 }
 
-template <typename H, typename F>
-cudaError_t launch_ffma_t(const CacheAttnArgs& a, int ctas, cudaStream_t s) {
-  AttnPlan p;
-  p.rows = F::kRows;
-  p.row_tiles = static_cast<int>((head_rows(a) + F::kRows - 1) / F::kRows);
-  p.div.units = a.c.heads * p.row_tiles;
-  p.div.tile = F::kTile;
-  p.div.ctas = ctas;
+template <typename H, typename F, typename A>
+cudaError_t launch_ffma_kernel(const A& a, const AttnPlan& p, cudaStream_t s) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
     const int most = F::smem(RA_MAX_HEAD_DIM);
-    e = cudaFuncSetAttribute(cache_attn_ffma_kernel<H, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(cache_attn_ffma_kernel<H, F, A>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              most < kFfmaSmem ? most : kFfmaSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  cache_attn_ffma_kernel<H, F><<<p.div.ctas, F::kThreads, F::smem(a.c.d), s>>>(a, p);
-  e = cudaGetLastError();
+  if constexpr (IsShared<A>::value)
+    return launch_behind(cache_attn_ffma_kernel<H, F, A>, dim3(p.div.ctas), F::kThreads, F::smem(a.c.d), s, a, p);
+  cache_attn_ffma_kernel<H, F, A><<<p.div.ctas, F::kThreads, F::smem(a.c.d), s>>>(a, p);
+  return cudaGetLastError();
+}
+
+template <int NC>
+struct FfmaSet {
+  using F4 = Ffma<4, 1, 1, 4, NC>;
+  using F8 = Ffma<4, 1, 2, 2, NC>;
+  using F16 = Ffma<4, 1, 4, 1, NC>;
+  using F64 = Ffma<8, 2, 8, 1, NC>;
+};
+template <typename F>
+SharedShape shape_of(int ctas) {
+  return SharedShape{F::kTile, F::kRows, F::kRows, ctas, false};
+}
+
+template <typename H, int NC, typename A>
+cudaError_t by_ffma_kernel(const A& a, const AttnPlan& p, SharedKernel k, cudaStream_t s) {
+  using S = FfmaSet<NC>;
+  switch (k) {
+    case SharedKernel::kFfma4: return launch_ffma_kernel<H, typename S::F4>(a, p, s);
+    case SharedKernel::kFfma8: return launch_ffma_kernel<H, typename S::F8>(a, p, s);
+    case SharedKernel::kFfma16: return launch_ffma_kernel<H, typename S::F16>(a, p, s);
+    default: return launch_ffma_kernel<H, typename S::F64>(a, p, s);
+  }
+}
+
+template <typename A>
+cudaError_t by_ffma_type(const A& a, const AttnPlan& p, SharedKernel k, bool k8, cudaStream_t s) {
+  if (a.c.d <= 128)
+    return k8 ? by_ffma_kernel<__nv_fp8_e4m3, 2>(a, p, k, s) : by_ffma_kernel<float, 2>(a, p, k, s);
+  return k8 ? by_ffma_kernel<__nv_fp8_e4m3, 4>(a, p, k, s) : by_ffma_kernel<float, 4>(a, p, k, s);
+}
+
+cudaError_t launch_ffma(const CacheAttnArgs& a, bool k8, cudaStream_t s) {
+  const SharedKernel k = ffma_kernel(head_rows(a), a.c.d);
+  const SharedShape f = ffma_shape(k);
+  AttnPlan p;
+  p.rows = f.rows;
+  p.row_tiles = static_cast<int>((head_rows(a) + f.rows - 1) / f.rows);
+  p.div.units = a.c.heads * p.row_tiles;
+  p.div.tile = f.tile;
+  p.div.ctas = f.ctas;
+  const cudaError_t e = by_ffma_type(a, p, k, k8, s);
   return e == cudaSuccess ? launch_cache_attn_join(a, p, false, s) : e;
 }
 
-template <typename H, int NC>
-cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
-  const int64_t rows = head_rows(a);
+}  // namespace
+
+SharedShape ffma_shape(SharedKernel k) {
+  using S = FfmaSet<2>;  // the columns per lane change none of it
+  switch (k) {
+    case SharedKernel::kFfma4: return shape_of<S::F4>(kFfmaCtas);
+    case SharedKernel::kFfma8: return shape_of<S::F8>(kFfmaCtas);
+    case SharedKernel::kFfma16: return shape_of<S::F16>(kFfmaCtas);
+    default: return shape_of<S::F64>(kFfmaCtas / 2);
+  }
+}
+
+cudaError_t launch_shared_ffma(const SharedAttnArgs& a, const AttnPlan& p, SharedKernel k, bool k8, cudaStream_t s) {
+  return by_ffma_type(a, p, k, k8, s);
+}
+
+SharedKernel ffma_kernel(int64_t rows, int d) {
   // The smallest group of rows that holds a head's, with as many warps on the
   // keys as leave room for three CTAs on an SM.  Groups of 64 rows feed more
   // products from a read, but groups of 16 keep four CTAs on an SM and none of
@@ -724,19 +821,14 @@ cudaError_t launch_ffma(const CacheAttnArgs& a, cudaStream_t s) {
   // 43 / 135 124, 64 rows 41 48 / 181 143; d = 128, 64 rows 58 84 / 279 285, 96
   // rows 76 107 / 408 502, 128 rows 92 119 / 548 530; d = 176, 40 rows 93 96 / 456
   // 322; one tile of d = 240, 18 rows 22 49).
-  const int few = a.c.d > 128 ? 32 : a.c.d > 64 ? 96 : 48;
-  using F4 = Ffma<4, 1, 1, 4, NC>;
-  using F8 = Ffma<4, 1, 2, 2, NC>;
-  using F16 = Ffma<4, 1, 4, 1, NC>;
-  using F64 = Ffma<8, 2, 8, 1, NC>;
+  const int few = d > 128 ? 32 : d > 64 ? 96 : 48;
+  using S = FfmaSet<2>;  // the columns per lane take no shared memory
   constexpr int third = kFfmaSmem / 3;
-  if (rows <= 4 && F4::smem(a.c.d) <= third) return launch_ffma_t<H, F4>(a, kFfmaCtas, s);
-  if (rows <= 8 && F8::smem(a.c.d) <= third) return launch_ffma_t<H, F8>(a, kFfmaCtas, s);
-  if (rows <= few || F64::smem(a.c.d) > kFfmaSmem) return launch_ffma_t<H, F16>(a, kFfmaCtas, s);
-  return launch_ffma_t<H, F64>(a, kFfmaCtas / 2, s);
+  if (rows <= 4 && S::F4::smem(d) <= third) return SharedKernel::kFfma4;
+  if (rows <= 8 && S::F8::smem(d) <= third) return SharedKernel::kFfma8;
+  if (rows <= few || S::F64::smem(d) > kFfmaSmem) return SharedKernel::kFfma16;
+  return SharedKernel::kFfma64;
 }
-
-}  // namespace
 
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,
                                    cudaStream_t s) {
@@ -763,9 +855,7 @@ cudaError_t launch_cache_tree_join(const CacheAttnArgs& a, const AttnPlan& p, cu
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dtype held,
                                    cudaStream_t s) {
-  if (dense == RA_F32)
-    return a.c.d <= 128 ? (held == RA_E4M3 ? launch_ffma<__nv_fp8_e4m3, 2>(a, s) : launch_ffma<float, 2>(a, s))
-                        : (held == RA_E4M3 ? launch_ffma<__nv_fp8_e4m3, 4>(a, s) : launch_ffma<float, 4>(a, s));
+  if (dense == RA_F32) return launch_ffma(a, held == RA_E4M3, s);
   // The decode kernel reads a key head once per 16 query rows, the tree kernel
   // once per 256.  Up to 16 rows the former is ahead throughout.  With 17 to 32
   // rows it still is over 8-bit caches at d = 128, which the tree kernel has to

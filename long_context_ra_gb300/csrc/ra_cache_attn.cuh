@@ -18,6 +18,49 @@ struct AttnPlan {
   int row_tiles;  // units per (sequence, key head)
 };
 
+// A launch over stretches.  A unit's rows are those of its members' queries of
+// one key head, `tile_members` sequences to a tile of rows: row i of tile t
+// belongs to member t tile_members + i / rows1.  Every unit leaves a state, of
+// a part in its slot as above, of a whole unit in `whole_ml`, `whole_o` at the
+// query row's own place: [rows][2] and [d / 4][rows][4].
+struct SharedAttnArgs : CacheAttnArgs {
+  SharedPaged stretches;
+  float* whole_ml;
+  float* whole_o;
+  int64_t all_rows;  // of q
+  int32_t rows1;     // of one sequence and key head
+  int32_t tile_members;
+};
+
+__host__ __device__ __forceinline__ const PagedArgs& paged(const CacheAttnArgs& a) { return a.c; }
+__host__ __device__ __forceinline__ const SharedPaged& paged(const SharedAttnArgs& a) { return a.stretches; }
+
+template <typename A>
+struct IsShared {
+  static constexpr bool value = false;
+};
+template <>
+struct IsShared<SharedAttnArgs> {
+  static constexpr bool value = true;
+};
+
+// A row of a unit over a stretch.
+struct MemberRow {
+  int64_t q;  // its row in q, or -1
+  int b;      // its sequence
+  int t;      // its token
+  int cnt;    // the new tokens of its sequence
+  __device__ __forceinline__ MemberRow(const SharedAttnArgs& a, const Stretch& s, int head, int tile, int i) {
+    const int m = i / a.rows1, w = i % a.rows1, member = tile * a.tile_members + m;
+    const bool real = m < a.tile_members && member < s.members;
+    b = s.b0 + member;
+    t = w % a.c.T;
+    cnt = real ? sequence(a.c, b).cnt : 0;
+    q = real ? (static_cast<int64_t>(b) * a.c.heads + head) * a.rows1 + w : -1;
+  }
+  __device__ __forceinline__ bool live() const { return t < cnt; }
+};
+
 // Query rows of one key head: g heads x T tokens, token fastest, which is
 // the order they have in q, out and lse.
 __host__ __device__ __forceinline__ int64_t head_rows(const CacheAttnArgs& a) {
@@ -30,6 +73,12 @@ __device__ __forceinline__ float* slot_ml(const CacheAttnArgs& a, const AttnPlan
 __device__ __forceinline__ float* slot_o(const CacheAttnArgs& a, const AttnPlan& p, int slot) {
   return a.ws + static_cast<int64_t>(2 * p.div.ctas) * p.rows * 2 +
          static_cast<int64_t>(slot) * p.rows * a.c.d;
+}
+
+// Where a kernel works out of what the one before it has written.
+__device__ __forceinline__ void wait_for_plan(const CacheAttnArgs&) {}
+__device__ __forceinline__ void wait_for_plan(const SharedAttnArgs&) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The join is launched while the kernel that writes the parts still runs
@@ -70,6 +119,37 @@ constexpr int kTreeCtas = 152;  // one per SM
 
 cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s);
 cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s);
+
+// How a kernel takes stretches: key tile, rows of a unit and of a row tile,
+// CTAs, and whether its parts' o is [d / 4][rows][4].
+enum class SharedKernel { kDecode, kTreeOne, kTreeTwo, kFfma4, kFfma8, kFfma16, kFfma64 };
+struct SharedShape {
+  int tile, rows, tile_rows, ctas;
+  bool quads;
+};
+SharedShape decode_shape();
+SharedShape tree_shape(int d, bool two);
+SharedShape ffma_shape(SharedKernel k);
+SharedKernel ffma_kernel(int64_t rows, int d);
+cudaError_t launch_shared_decode(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s);
+cudaError_t launch_shared_tree(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s);
+cudaError_t launch_shared_ffma(const SharedAttnArgs& a, const AttnPlan& p, SharedKernel k, bool k8, cudaStream_t s);
+
+// A launch that may begin before the one before it on the stream has ended.
+template <typename... K, typename... X>
+cudaError_t launch_behind(void (*kernel)(K...), dim3 grid, int threads, int smem, cudaStream_t s, X... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // Joins the parts of the units that several CTAs shared.
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,

@@ -170,21 +170,23 @@ __device__ __forceinline__ void each_value_tile(const uint32_t (&w)[4][kWords], 
   }
 }
 
-template <bool k8, int D>
+template <bool k8, int D, typename A>
 __global__ void __launch_bounds__(kThreads, 2)
-    cache_decode_kernel(const __grid_constant__ CacheAttnArgs a,
+    cache_decode_kernel(const __grid_constant__ A a,
                         const __grid_constant__ AttnPlan p) {
   using S = Shape<k8, D>;
   // whole lines: a base that is only 16-byte aligned costs 5 % (238 us, not 227)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ DivisionShared sh;
-  const PagedArgs& c = a.c;
+  constexpr bool kShared = IsShared<A>::value;
+  const auto& c = paged(a);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStage);
   const int64_t rows = head_rows(a);
 
   allow_join();
+  wait_for_plan(a);
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   UnitWalk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
@@ -199,12 +201,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     // 32) rows); lane i holds granule base * per + i.
     const int gshift = min(c.page_shift, 5), per = kChunk >> gshift;
     int pg = -1, nx = -1;
+    const int32_t* table = pages_of(c, u.b);
+    const int columns = columns_of(c, u.b);
     auto pages = [&](int base) {
       const int chunk = base + lane / per;
       const int64_t at = key0 + static_cast<int64_t>(chunk) * kTile + ((lane % per) << gshift);
       if (chunk >= n || at >= keys) return -1;
       const int64_t col = at >> c.page_shift;
-      const int page = col < c.width ? c.table[static_cast<int64_t>(u.b) * c.width + col] : -1;
+      const int page = col < columns ? table[col] : -1;
       if (page >= 0 && page < c.pages) return page;
       flag_page(c.status);
       return -1;
@@ -283,13 +287,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- queries as A fragments, in the order in which K rows are read
     uint32_t qf[D / 16][4];
     float scale[2];
-    int tq[2];
+    int tq[2], mask_b[2];  // a row's token and sequence
+    SeqInfo seq[2];        // the context and new tokens that it may see
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t row = r0 + g + 8 * h;
-      const bool real = row < rows;
-      tq[h] = real ? static_cast<int>(row % c.T) : c.T;
-      const uint8_t* src = static_cast<const uint8_t*>(a.q) + (q0 + g + 8 * h) * D * 2;
+      bool real;
+      int64_t at;
+      if constexpr (kShared) {
+        const MemberRow r(a, c.list[u.b], u.unit, 0, g + 8 * h);
+        real = r.q >= 0;
+        at = r.q;
+        tq[h] = r.t;
+        mask_b[h] = r.b;
+        seq[h] = SeqInfo{u.seq.len, r.cnt};
+      } else {
+        const int64_t row = r0 + g + 8 * h;
+        real = row < rows;
+        at = q0 + g + 8 * h;
+        tq[h] = real ? static_cast<int>(row % c.T) : c.T;
+        mask_b[h] = u.b;
+        seq[h] = u.seq;
+      }
+      const uint8_t* src = static_cast<const uint8_t*>(a.q) + at * D * 2;
       uint32_t amax = 0;
 #pragma unroll
       for (int st = 0; st < D / 16; ++st) {
@@ -395,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const int j = x / 4, z = x % 4;
-          if (((out >> j) & 1u) || !sees(a, u.seq, u.b, tq[z / 2], pos + 8 * j + 2 * t + z % 2)) {
+          if (((out >> j) & 1u) || !sees(a, seq[z / 2], mask_b[z / 2], tq[z / 2], pos + 8 * j + 2 * t + z % 2)) {
             seen &= ~(1u << x);
             s[j][z] = -INFINITY;
           }
@@ -523,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      const bool dead = tq[h] >= u.seq.cnt;  // no query: an empty state
+      const bool dead = tq[h] >= seq[h].cnt;  // no query: an empty state
       if (dead) {
         m[h] = -INFINITY;
         l[h] = 0.f;
@@ -543,7 +562,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     {
       const int r = threadIdx.x / 8, x0 = (threadIdx.x % 8) * 4;
-      if (r0 + r < rows) {
+      bool here = r0 + r < rows;
+      int64_t q_row = 0;  // its place in q (stretches)
+      if constexpr (kShared) {
+        q_row = MemberRow(a, c.list[u.b], u.unit, 0, r).q;
+        here = q_row >= 0;
+      }
+      if (here) {
         float ms = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) ms = fmaxf(ms, jm[2 * (w * kRows + r)]);
@@ -555,14 +580,16 @@ __global__ void __launch_bounds__(kThreads, 2)
           f[w] = lw == 0.f ? 0.f : exp2f(jm[2 * (w * kRows + r)] - ref);
           ls += f[w] * lw;
         }
-        const bool whole = u.whole();
-        const float fin = whole ? (ls == 0.f ? 0.f : 1.f / ls) : 1.f;
+        const bool whole = u.whole(), finish = whole && !kShared;
+        const float fin = finish ? (ls == 0.f ? 0.f : 1.f / ls) : 1.f;
         const int slot = u.slot(blockIdx.x);
         if (threadIdx.x % 8 == 0) {
-          if (whole) {
+          if (finish) {
             a.lse[q0 + r] = ls == 0.f ? -INFINITY : (ms + log2f(ls)) * kLn2F;
           } else {
             float* ml = slot_ml(a, p, slot) + 2 * r;
+            if constexpr (kShared)
+              if (whole) ml = a.whole_ml + 2 * q_row;
             ml[0] = ms;
             ml[1] = ls;
           }
@@ -579,12 +606,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             v[2] = fmaf(f[w], y.z, v[2]);
             v[3] = fmaf(f[w], y.w, v[3]);
           }
-          if (whole) {
+          if (finish) {
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (q0 + r) * D + 32 * x + x0) =
                 make_uint2(pack_bf16x2(v[0] * fin, v[1] * fin), pack_bf16x2(v[2] * fin, v[3] * fin));
           } else {
-            *reinterpret_cast<float4*>(slot_o(a, p, slot) + r * D + 32 * x + x0) =
-                make_float4(v[0], v[1], v[2], v[3]);
+            float4* dst = reinterpret_cast<float4*>(slot_o(a, p, slot) + r * D + 32 * x + x0);
+            if constexpr (kShared)
+              if (whole) dst = reinterpret_cast<float4*>(a.whole_o) + (8 * x + x0 / 4) * a.all_rows + q_row;
+            *dst = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
       }
@@ -593,22 +622,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <bool k8, int D>
-cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+template <bool k8, int D, typename A>
+cudaError_t launch_t(const A& a, const AttnPlan& p, cudaStream_t s) {
   using S = Shape<k8, D>;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(cache_decode_kernel<k8, D>,
+    e = cudaFuncSetAttribute(cache_decode_kernel<k8, D, A>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  cache_decode_kernel<k8, D><<<p.div.ctas, kThreads, S::kSmem, s>>>(a, p);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_cache_attn_join(a, p, true, s) : e;
+  if constexpr (IsShared<A>::value) {
+    return launch_behind(cache_decode_kernel<k8, D, A>, dim3(p.div.ctas), kThreads, S::kSmem, s, a, p);
+  } else {
+    cache_decode_kernel<k8, D, A><<<p.div.ctas, kThreads, S::kSmem, s>>>(a, p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_cache_attn_join(a, p, true, s) : e;
+  }
+}
+
+template <typename A>
+cudaError_t by_type(const A& a, const AttnPlan& p, bool k8, cudaStream_t s) {
+  if (a.c.d == 128) return k8 ? launch_t<true, 128>(a, p, s) : launch_t<false, 128>(a, p, s);
+  return k8 ? launch_t<true, 64>(a, p, s) : launch_t<false, 64>(a, p, s);
 }
 
 }  // namespace
@@ -620,8 +659,13 @@ cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s)
   p.div.units = a.c.heads * p.row_tiles;
   p.div.tile = kTile;
   p.div.ctas = kDecodeCtas;
-  if (a.c.d == 128) return k8 ? launch_t<true, 128>(a, p, s) : launch_t<false, 128>(a, p, s);
-  return k8 ? launch_t<true, 64>(a, p, s) : launch_t<false, 64>(a, p, s);
+  return by_type(a, p, k8, s);
+}
+
+SharedShape decode_shape() { return SharedShape{kTile, kRows, kRows, kDecodeCtas, false}; }
+
+cudaError_t launch_shared_decode(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s) {
+  return by_type(a, p, k8, s);
 }
 
 }  // namespace ra

@@ -302,14 +302,14 @@ __device__ __noinline__ uint32_t seen_word(const CacheAttnArgs& a, const SeqInfo
 
 // Which of columns x .. x + 31 of the drafts that query t sees in the walk's
 // part hold a value that is not finite (a bit each).
-template <bool k8, int D>
-__device__ __noinline__ uint32_t poisoned_columns(const CacheAttnArgs& a, const UnitWalk& u, int head,
+template <bool k8, int D, typename A>
+__device__ __noinline__ uint32_t poisoned_columns(const A& a, const UnitWalk& u, int b, int head,
                                                   int t, int x, int tile) {
-  const PagedArgs& c = a.c;
+  const auto& c = paged(a);
   uint32_t bad = 0;
   const int64_t end = min(u.last * tile, u.seq.keys());
   for (int64_t pos = max(u.first * tile, u.seq.len); pos < end; ++pos) {
-    if (!sees(a, u.seq, u.b, t, pos)) continue;
+    if (!sees(a, u.seq, b, t, pos)) continue;
     int64_t row = cache_row(c, u.b, pos);
     if (row < 0) continue;
     row += static_cast<int64_t>(head) << c.page_shift;
@@ -364,12 +364,22 @@ struct Unit {
   }
 };
 
-template <bool k8, int D, bool kTwo>
+// Whether a unit has rows in its second tile.
+__device__ __forceinline__ bool second_tile(const CacheAttnArgs& a, const AttnPlan& p, const UnitWalk& u,
+                                            int64_t rows) {
+  return Unit(a, p, u, rows).r0 + 128 < rows;
+}
+__device__ __forceinline__ bool second_tile(const SharedAttnArgs& a, const AttnPlan&, const UnitWalk& u, int64_t) {
+  return a.stretches.list[u.b].members > a.tile_members;
+}
+
+template <bool k8, int D, bool kTwo, typename A>
 __global__ void __launch_bounds__(kThreads, 1)
-    cache_tree_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ AttnPlan p,
+    cache_tree_kernel(const __grid_constant__ A a, const __grid_constant__ AttnPlan p,
                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const __grid_constant__ CUtensorMap tq) {
   using L = Layout<k8, D, kTwo>;
+  constexpr bool kShared = IsShared<A>::value;
   constexpr int kS = L::kStages, kKeys = L::kKeys, kN = kKeys / 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -380,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Abort ab{tmem_holder + 1, a.c.status, a.wait_limit > 0 ? a.wait_limit : kWaitLimit};
   volatile uint32_t* poison = reinterpret_cast<volatile uint32_t*>(gbase + L::kPoison);
   DivisionShared& sh = *reinterpret_cast<DivisionShared*>(gbase + L::kDivision);
-  const PagedArgs& c = a.c;
+  const auto& c = paged(a);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t rows = head_rows(a);
 
@@ -414,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(base + L::kMisc, kTmemCols);
     tmem_relinquish();
   }
+  wait_for_plan(a);
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   tc_fence_before();
   __syncthreads();
@@ -427,8 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The unit's queries, in the order of widen16: in place, a piece stays in
     // its thread.
     auto order_queries = [&](const UnitWalk& w, uint32_t ord) {
-      const Unit un(a, p, w, rows);
-      const uint32_t end = base + L::kQ0 + (kTwo && un.r0 + 128 < rows ? 2 : 1) * L::kQTile;
+      const uint32_t end = base + L::kQ0 + (kTwo && second_tile(a, p, w, rows) ? 2 : 1) * L::kQTile;
       if (!wait_warp(bars.q_raw(), ord & 1u, ab)) return false;
 #pragma unroll 1
       for (uint32_t at = base + L::kQ0 + tid * 16; at < end; at += 4 * 256 * 16) {
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     static_assert(!k8 || L::kQTile % (4 * 256 * 16) == 0, "whole rounds of the queries");
     UnitWalk w;
-    w.start_found(p.div, sh, run);
+    w.start_found(c, p.div, sh, run);
     if (k8) {
       Ring in, out;  // raw stages; operand stages
       constexpr int kTeams = 256 / L::kTeam;
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t behind = static_cast<int32_t>((c.pages > 0 ? c.pages * c.heads : 1));
     const uint64_t map_k = reinterpret_cast<uint64_t>(&tk), map_v = reinterpret_cast<uint64_t>(&tv);
     UnitWalk w;
-    w.start_found(p.div, sh, run);
+    w.start_found(c, p.div, sh, run);
     Ring r;
     uint32_t ktiles = 0;
     // a bit per stage: loaded, to arrive at raw_full, and the phase of that
@@ -608,14 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the first tile with drafts or the end
       const int border =
           static_cast<int>(min(max(w.seq.len / kKeys - w.first, int64_t{0}), static_cast<int64_t>(n)));
-      const int32_t* row_of_table = c.table + static_cast<int64_t>(w.b) * c.width;
+      const int32_t* row_of_table = pages_of(c, w.b);
+      const uint32_t columns = static_cast<uint32_t>(columns_of(c, w.b));
       // this lane's page of a tile: its number, -1 for one that is missing,
       // -2 for none
       auto look_up = [&](int tile) {
         const uint32_t pos = pos0 + static_cast<uint32_t>(tile) * kKeys + box * page_rows;
         if (!mine || tile >= n || pos >= keys) return -2;
         const uint32_t col = pos >> c.page_shift;
-        return col < static_cast<uint32_t>(c.width) ? max(__ldg(row_of_table + col), -1) : -1;
+        return col < columns ? max(__ldg(row_of_table + col), -1) : -1;
       };
       int page = -2, ahead = look_up(0);  // of the last key tile loaded; of the next
       int32_t z = 0, zv = 0;              // its TMA coordinate; that of the value tile to come
@@ -696,18 +707,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // product that nobody reads.
       const uint32_t bar = k8 ? bars.q_raw() : bars.q_full();
       UnitWalk w;
-      w.start_found(p.div, sh, run);
+      w.start_found(c, p.div, sh, run);
       uint32_t ord = 0;
       for (; !w.done(); ++ord, w.next(c, p.div)) {
         if (!wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) break;
         if (lane == 0) {
-          const Unit un(a, p, w, rows);
-          const bool two = kTwo && un.r0 + 128 < rows;
-          mbar_arrive_expect_tx(bar, (two ? 2 : 1) * L::kQTile);
+          const bool two = kTwo && second_tile(a, p, w, rows);
+          if constexpr (kShared) {
+            // all rows of a tile's members; rows of others, and what is left of the tile, nobody reads
+            const int b0 = c.list[w.b].b0;
+            const uint32_t box = 128u * a.rows1 * a.tile_members;
+            mbar_arrive_expect_tx(bar, (two ? 2 : 1) * (D / 64) * box);
 #pragma unroll 1
-          for (int x = 0; x < (two ? 2 : 1) * (D / 64); ++x)
-            tma_load_2d(base + L::kQ0 + x * L::kQBox, &tq, x % (D / 64) * 64,
-                        static_cast<int32_t>(un.q0) + x / (D / 64) * 128, bar);
+            for (int x = 0; x < (two ? 2 : 1) * (D / 64); ++x)
+              tma_load_4d(base + L::kQ0 + x * L::kQBox, &tq, x % (D / 64) * 64, 0, w.unit,
+                          b0 + x / (D / 64) * a.tile_members, bar);
+          } else {
+            const Unit un(a, p, w, rows);
+            mbar_arrive_expect_tx(bar, (two ? 2 : 1) * L::kQTile);
+#pragma unroll 1
+            for (int x = 0; x < (two ? 2 : 1) * (D / 64); ++x)
+              tma_load_2d(base + L::kQ0 + x * L::kQBox, &tq, x % (D / 64) * 64,
+                          static_cast<int32_t>(un.q0) + x / (D / 64) * 128, bar);
+          }
         }
         __syncwarp();
       }
@@ -730,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return s;
       };
-      for (u.start_found(p.div, sh, run); ok && !u.done(); u.next(c, p.div), ++unit) {
+      for (u.start_found(c, p.div, sh, run); ok && !u.done(); u.next(c, p.div), ++unit) {
         const int n = static_cast<int>(u.last - u.first);
         ok = wait1(bars.q_full(), unit & 1u, ab);
         if (!ok) break;
@@ -741,8 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (kTwo) {
-          const Unit un(a, p, u, rows);
-          const bool two = un.r0 + 128 < rows;
+          const bool two = second_tile(a, p, u, rows);
           uint64_t dk = dK + desc_step(sk * L::kTile);
           issue_qk<D, kKeys>(tS0, dQ0, dk);
           mma_commit(bars.s_full(0));
@@ -857,23 +878,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, no = 0, unit = 0, xc = 0, kt = 0;     // phases; K tiles before the unit
     bool ok = true;
     UnitWalk& u = reinterpret_cast<UnitWalk*>(gbase + L::kWalks)[warp];
-    if (lane == 0) u.start_found(p.div, sh, run);
+    if (lane == 0) u.start_found(c, p.div, sh, run);
     __syncwarp();
     while (ok && !u.done()) {
       const int n = static_cast<int>(u.last - u.first);
       // the first tile of this part that holds drafts or the end
       const int border = static_cast<int>(
           min(max(u.seq.len / kKeys - u.first, int64_t{0}), static_cast<int64_t>(n)));
-      int tok;
-      bool active, exists;
-      {
+      int tok, mask_b;   // the row's token and sequence
+      int64_t q_row;     // its place in q (stretches)
+      SeqInfo seq;       // context and new tokens that it may see
+      bool exists;
+      const bool active = kTwo ? t == 0 || second_tile(a, p, u, rows) : t == 0 || n > 1;
+      if constexpr (kShared) {
+        const MemberRow r(a, c.list[u.b], u.unit, kTwo ? t : 0, row);
+        tok = r.t;
+        mask_b = r.b;
+        q_row = r.q;
+        exists = r.q >= 0;
+        seq = SeqInfo{u.seq.len, r.cnt};
+      } else {
         const Unit un(a, p, u, rows);
-        active = kTwo ? (t == 0 || un.r0 + 128 < rows) : (t == 0 || n > 1);
         const int64_t lrow = un.r0 + (kTwo ? t * 128 : 0) + row;  // row within the key head
         exists = lrow < rows;
         tok = exists ? static_cast<int>(lrow % c.T) : c.T;
+        mask_b = u.b;
+        q_row = 0;
+        seq = u.seq;
       }
-      const bool live = tok < u.seq.cnt;
+      const bool live = tok < seq.cnt;
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_ref = -INFINITY, l = 0.f;
       if (active) {
@@ -892,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int w = 0; w < kN; ++w) {
                 const uint32_t seen =
-                    seen_word(a, u.seq, u.b, tok, (u.first + it) * kKeys + 32 * w, left >> (4 * w));
+                    seen_word(a, seq, mask_b, tok, (u.first + it) * kKeys + 32 * w, left >> (4 * w));
                 uint32_t s[32];
                 __syncwarp();
                 tmem_ld32(tS + 32 * w, s);
@@ -998,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float f0 = 1.f, f1 = 0.f;  // weights of this stream's and the other's sums
       if (kTwo ? active : t == 0 || exchange) {
         const Unit un(a, p, u, rows);
-        const bool whole = u.whole();
+        const bool whole = u.whole(), finish = whole && !kShared;
         const int slot = u.slot(blockIdx.x);
         const int local = (kTwo ? t * 128 : 0) + row;
         const int first = exchange ? t * (D / 2) : 0;
@@ -1050,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(bars.x_empty(1 - t));
             ++xc;
           }
-          if (i == 0 && whole) inv = l == 0.f ? 0.f : 1.f / l;
+          if (i == 0 && finish) inv = l == 0.f ? 0.f : 1.f / l;
           // A row without a query may hold anything.  Of one that sees no key, or
           // a stream that it sees none of, the sums are 0; a weight of 0
           // multiplies all the same, since sums may be NaN.
@@ -1068,12 +1101,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (poisoned && live) {
             // elements of drafts that were left out because they are not finite
-            const uint32_t bad = poisoned_columns<k8, D>(a, u, un.head, tok, x, kKeys);
+            const uint32_t bad = poisoned_columns<k8, D>(a, u, mask_b, un.head, tok, x, kKeys);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if ((bad >> e) & 1u) r[e] = 0x7fffffffu;
           }
-          if (whole) {
+          if (finish) {
             uint4 y[4];  // 8 columns each
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -1093,12 +1126,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               a.lse[un.q0 + local] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * kLn2F;
           } else if (exists) {
             float4* dst = reinterpret_cast<float4*>(slot_o(a, p, slot)) + x / 4 * p.rows + local;
+            int64_t pitch = p.rows;
+            if constexpr (kShared) {
+              if (whole) {
+                pitch = a.all_rows;
+                dst = reinterpret_cast<float4*>(a.whole_o) + x / 4 * pitch + q_row;
+              }
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[e * p.rows] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+              dst[e * pitch] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
                                             __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-            if (x == 0)
-              *reinterpret_cast<float2*>(slot_ml(a, p, slot) + 2 * local) = make_float2(m_ref, l);
+            if (x == 0) {
+              float* ml = slot_ml(a, p, slot) + 2 * local;
+              if constexpr (kShared)
+                if (whole) ml = a.whole_ml + 2 * q_row;
+              *reinterpret_cast<float2*>(ml) = make_float2(m_ref, l);
+            }
           }
         }
         tc_fence_before();
@@ -1120,15 +1164,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool k8, int D, bool kTwo>
-cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
+template <bool k8, int D, bool kTwo, typename A>
+cudaError_t launch_t(const A& a, const AttnPlan& plan, cudaStream_t s) {
   using L = Layout<k8, D, kTwo>;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(cache_tree_kernel<k8, D, kTwo>,
+    e = cudaFuncSetAttribute(cache_tree_kernel<k8, D, kTwo, A>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
@@ -1136,19 +1180,31 @@ cudaError_t launch_t(const CacheAttnArgs& a, const AttnPlan& plan, cudaStream_t 
   CUtensorMap tk, tv, tq;
   const int rows = (1 << a.c.page_shift) < L::kKeys ? 1 << a.c.page_shift : L::kKeys;
   if (!encode_pages(&tk, a.c.pages > 0 ? a.c.k : a.q, a.c, rows, k8) ||
-      !encode_pages(&tv, a.c.pages > 0 ? a.c.v : a.q, a.c, rows, k8) ||
-      !encode_rows(&tq, a.q, static_cast<int64_t>(a.c.B) * a.Hq * a.c.T, D))
+      !encode_pages(&tv, a.c.pages > 0 ? a.c.v : a.q, a.c, rows, k8))
     return cudaErrorUnknown;
   AttnPlan p = plan;
   p.div.tile = L::kKeys;
-  cache_tree_kernel<k8, D, kTwo><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv, tq);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? launch_cache_tree_join(a, p, s) : e;
+  if constexpr (IsShared<A>::value) {
+    if (!encode_members(&tq, a.q, a.c.B, a.c.heads, a.rows1, D, a.tile_members)) return cudaErrorUnknown;
+    return launch_behind(cache_tree_kernel<k8, D, kTwo, A>, dim3(p.div.ctas), kThreads, L::kSmem, s, a, p, tk, tv,
+                         tq);
+  } else {
+    if (!encode_rows(&tq, a.q, static_cast<int64_t>(a.c.B) * a.Hq * a.c.T, D)) return cudaErrorUnknown;
+    cache_tree_kernel<k8, D, kTwo, A><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv, tq);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_cache_tree_join(a, p, s) : e;
+  }
 }
 
-template <bool k8, int D>
-cudaError_t by_rows(const CacheAttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-  return p.rows == 256 ? launch_t<k8, D, true>(a, p, s) : launch_t<k8, D, false>(a, p, s);
+template <bool k8, int D, typename A>
+cudaError_t by_rows(const A& a, const AttnPlan& p, cudaStream_t s) {
+  return p.rows == 256 ? launch_t<k8, D, true, A>(a, p, s) : launch_t<k8, D, false, A>(a, p, s);
+}
+
+template <typename A>
+cudaError_t by_type(const A& a, const AttnPlan& p, bool k8, cudaStream_t s) {
+  if (a.c.d == 128) return k8 ? by_rows<true, 128>(a, p, s) : by_rows<false, 128>(a, p, s);
+  return k8 ? by_rows<true, 64>(a, p, s) : by_rows<false, 64>(a, p, s);
 }
 
 }  // namespace
@@ -1160,8 +1216,15 @@ cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s) {
   p.row_tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
   p.div.units = a.c.heads * p.row_tiles;
   p.div.ctas = kTreeCtas;
-  if (a.c.d == 128) return k8 ? by_rows<true, 128>(a, p, s) : by_rows<false, 128>(a, p, s);
-  return k8 ? by_rows<true, 64>(a, p, s) : by_rows<false, 64>(a, p, s);
+  return by_type(a, p, k8, s);
+}
+
+SharedShape tree_shape(int d, bool two) {
+  return SharedShape{two || d == 64 ? 128 : 64, two ? 256 : 128, 128, kTreeCtas, true};
+}
+
+cudaError_t launch_shared_tree(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s) {
+  return by_type(a, p, k8, s);
 }
 
 }  // namespace ra

@@ -15,13 +15,44 @@ namespace ra {
 // A timeout, whose results are invalid, is not replaced.
 __device__ __forceinline__ void flag_page(int* status) { atomicCAS(status, 0, kStatusPage); }
 
+// A stretch of keys that some rows of queries see, as the attention over
+// shared prefixes divides a batch: the positions from column `skip` of row
+// `row` of the table on, seen by `members` sequences from b0 on.  Of a prefix
+// len is its length and cnt 0; of a sequence's own part they are the tokens and
+// new tokens behind the prefix.
+struct Stretch {
+  int32_t len, cnt;
+  int32_t row, skip;
+  int32_t b0, members;
+};
+
+// The stretches of one launch, in the place of a batch's sequences.
+struct SharedPaged : PagedArgs {
+  const Stretch* list;
+  const int64_t* at;      // key tiles (of one unit) before each stretch
+  const int64_t* totals;  // tiles of all; the number of stretches
+};
+
+// The page numbers of a sequence, and how many there can be.
+__device__ __forceinline__ const int32_t* pages_of(const PagedArgs& c, int b) {
+  return c.table + static_cast<int64_t>(b) * c.width;
+}
+__device__ __forceinline__ const int32_t* pages_of(const SharedPaged& c, int b) {
+  return c.table + static_cast<int64_t>(c.list[b].row) * c.width + c.list[b].skip;
+}
+__device__ __forceinline__ int columns_of(const PagedArgs& c, int) { return c.width; }
+__device__ __forceinline__ int columns_of(const SharedPaged& c, int b) {
+  return max(c.width - c.list[b].skip, 0);
+}
+
 // Row of head 0 of position `pos` of sequence b in the cache (add
 // h << page_shift for head h), or -1, with the status word set, for a
 // position or page outside the cache.
-__device__ __forceinline__ int64_t cache_row(const PagedArgs& c, int b, int64_t pos) {
+template <typename P>
+__device__ __forceinline__ int64_t cache_row(const P& c, int b, int64_t pos) {
   const int64_t col = pos >> c.page_shift;
-  if (col < c.width) {
-    const int64_t page = c.table[static_cast<int64_t>(b) * c.width + col];
+  if (col < columns_of(c, b)) {
+    const int64_t page = pages_of(c, b)[col];
     if (page >= 0 && page < c.pages)
       return ((page * c.heads) << c.page_shift) + (pos & ((int64_t{1} << c.page_shift) - 1));
   }
@@ -43,6 +74,10 @@ __device__ __forceinline__ SeqInfo sequence(const PagedArgs& c, int b) {
   s.len = len < 0 ? 0 : len;
   s.cnt = len < 0 ? 0 : max(0, min(cnt, c.T));
   return s;
+}
+
+__device__ __forceinline__ SeqInfo sequence(const SharedPaged& c, int b) {
+  return SeqInfo{c.list[b].len, c.list[b].cnt};
 }
 
 // 2^(e - 127) of an exponent byte.
@@ -182,6 +217,20 @@ __device__ __forceinline__ int64_t seq_tiles(const PagedArgs& c, const Division&
   return tiles_of(sequence(c, b), v);
 }
 
+// Of a stretch there may be none.
+__device__ __forceinline__ int64_t tiles_of(const PagedArgs&, const SeqInfo& s, const Division& v) {
+  return tiles_of(s, v);
+}
+__device__ __forceinline__ int64_t tiles_of(const SharedPaged&, const SeqInfo& s, const Division& v) {
+  return (s.keys() + v.tile - 1) / v.tile;
+}
+// On to a sequence with tiles, where there is one.
+__device__ __forceinline__ int with_tiles(const PagedArgs&, int b) { return b; }
+__device__ __forceinline__ int with_tiles(const SharedPaged& c, int b) {
+  while (sequence(c, b).keys() == 0) ++b;
+  return b;
+}
+
 __device__ __forceinline__ int64_t run_length(const Division& v, int64_t total) {
   return (total + v.ctas - 1) / v.ctas;
 }
@@ -284,6 +333,33 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
   return min(run, all - begin);
 }
 
+// The same for stretches, whose tiles have been added up: every warp looks for
+// the last stretch that begins at or before the run.
+__device__ __forceinline__ int64_t division_start(const SharedPaged& c, const Division& v, int cta,
+                                                  DivisionShared& sh) {
+  const int64_t all = c.totals[0] * v.units;
+  const int n = static_cast<int>(c.totals[1]);
+  const int64_t run = run_length(v, all);
+  const int64_t begin = cta * run;
+  if (begin < all) {
+    const int lane = threadIdx.x % 32;
+    int found = 0;
+    for (int i = 0; i < n; i += 32) {
+      const uint32_t here = __ballot_sync(0xffffffffu, i + lane < n && c.at[i + lane] * v.units <= begin);
+      if (here == 0u) break;
+      found = i + 31 - __clz(here);
+    }
+    if (lane == 0) {  // of every warp: all write the same
+      sh.b = found;
+      sh.seq = sequence(c, found);
+      sh.off = begin - c.at[found] * v.units;
+      sh.run = run;
+    }
+  }
+  __syncthreads();
+  return begin >= all ? 0 : min(run, all - begin);
+}
+
 // Tiles (of one unit) of the sequences before b, and of all.  All threads of
 // the block take part.
 __device__ __forceinline__ void division_before(const PagedArgs& c, const Division& v, int b,
@@ -319,40 +395,47 @@ struct UnitWalk {
   int64_t tiles, first, last;  // of the unit; this CTA's part [first, last)
   int unit;
 
-  __device__ void start(const PagedArgs& c, const Division& v, const DivisionShared& sh,
-                        int64_t n) {
+  template <typename P>
+  __device__ void start(const P& c, const Division& v, const DivisionShared& sh, int64_t n) {
     left = n;
     b = sh.b;
     off = sh.off;
     if (left > 0) load(c, v);
   }
   // The same without a load: the sequence is the one that division_start found.
-  __device__ void start_found(const Division& v, const DivisionShared& sh, int64_t n) {
+  template <typename P>
+  __device__ void start_found(const P& c, const Division& v, const DivisionShared& sh, int64_t n) {
     left = n;
     b = sh.b;
     off = sh.off;
     seq = sh.seq;
-    if (left > 0) set(v);
+    if (left > 0) set(c, v);
   }
   __device__ bool done() const { return left <= 0; }
-  __device__ void load(const PagedArgs& c, const Division& v) {
+  template <typename P>
+  __device__ void load(const P& c, const Division& v) {
     seq = sequence(c, b);
-    set(v);
+    set(c, v);
   }
-  __device__ void set(const Division& v) {
-    tiles = tiles_of(seq, v);
+  template <typename P>
+  __device__ void set(const P& c, const Division& v) {
+    tiles = tiles_of(c, seq, v);
     unit = static_cast<int>(off / tiles);
     first = off - unit * tiles;
     last = min(tiles, first + left);
   }
-  __device__ void next(const PagedArgs& c, const Division& v) {
+  template <typename P>
+  __device__ void next(const P& c, const Division& v) {
     left -= last - first;
     off += last - first;
     if (off == tiles * v.units) {
       ++b;
       off = 0;
     }
-    if (left > 0) load(c, v);
+    if (left > 0) {
+      if (off == 0) b = with_tiles(c, b);
+      load(c, v);
+    }
   }
   __device__ bool whole() const { return first == 0 && last == tiles; }
   // Slot of a part that is not the whole unit.

@@ -66,6 +66,9 @@ struct PagedArgs {
 bool encode_pages(CUtensorMap* map, const void* ptr, const PagedArgs& c, int box_rows, bool bytes);
 // TMA view of dense bf16 rows [rows, d] with boxes of 128 rows of 64 columns, swizzled alike.
 bool encode_rows(CUtensorMap* map, const void* ptr, int64_t rows, int d);
+// TMA view of bf16 queries [B, heads, rows, d] with boxes of all rows of one head of `members`
+// sequences, 64 columns, swizzled alike.
+bool encode_members(CUtensorMap* map, const void* ptr, int B, int heads, int rows, int d, int members);
 
 struct CacheCopyArgs {
   PagedArgs c;
@@ -141,6 +144,11 @@ struct CacheAttnArgs {
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, ra_dtype dense, ra_dtype held,
                                    cudaStream_t s);
+// `shared` [B]: tokens that a sequence has in common with the one before it.
+cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t* shared, ra_dtype dense,
+                                          ra_dtype held, cudaStream_t s);
+int64_t cache_attention_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,
+                                               int32_t d);
 int64_t cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,
                                         int32_t d);
 

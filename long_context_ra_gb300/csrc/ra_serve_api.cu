@@ -126,6 +126,40 @@ ra_status check_cache(const ra_cache* cache, const int32_t* table, int32_t width
   return RA_OK;
 }
 
+// Arguments of the attention calls; `a` keeps q = NULL where nothing is to be done.
+ra_status check_attention(const void* q, const ra_cache* cache, const int32_t* table, int32_t width,
+                          const int32_t* lens, const int32_t* count, const uint8_t* mask, int64_t mask_stride,
+                          void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                          int64_t (*wanted)(int32_t, int32_t, int32_t, int32_t, int32_t), int32_t B, int32_t Hq,
+                          int32_t T, ra_dtype dtype, CacheAttnArgs* a) {
+  ra_status st = check_cache(cache, table, width, lens, B, T, dtype, &a->c);
+  if (st != RA_OK) return st;
+  if (Hq < 0 || Hq % cache->heads != 0) return RA_ERR_INVALID_ARG;
+  if (mask && mask_stride != 0 && mask_stride < static_cast<int64_t>(T) * T)
+    return RA_ERR_INVALID_ARG;
+  if (dtype == RA_BF16 && cache->d != 64 && cache->d != 128) return RA_ERR_UNSUPPORTED;
+  if (Hq > kMaxHeads || static_cast<int64_t>(B) * Hq * T > kMaxTokens) return RA_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(count, 4) ||
+      !aligned(workspace, 256))
+    return RA_ERR_MISALIGNED;
+  if (B == 0 || Hq == 0 || T == 0) return RA_OK;
+  if (!q || !out || !lse || !workspace) return RA_ERR_INVALID_ARG;
+  if (workspace_bytes < wanted(B, Hq, cache->heads, T, cache->d)) return RA_ERR_INVALID_ARG;
+  if ((st = device_ready(&a->c.status)) != RA_OK) return st;
+  a->c.count = count;
+  a->q = q;
+  a->mask = mask;
+  a->mask_stride = mask_stride;
+  a->out = out;
+  a->lse = lse;
+  a->ws = static_cast<float*>(workspace);
+  a->Hq = Hq;
+  a->scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(cache->d)));
+  a->wait_limit = wait_limit();
+  a->stall_cta = stall_cta();
+  return RA_OK;
+}
+
 // A type that fits the cache, where a call has no tensors beside it.
 ra_dtype own_dtype(const ra_cache* cache) { return cache && cache->dtype != RA_E4M3 ? cache->dtype : RA_F32; }
 
@@ -338,33 +372,31 @@ RA_API ra_status ra_cache_attention(const void* q, const ra_cache* cache, const 
                                     ra_stream_t stream) {
   RA_TRACE("ra_cache_attention");
   CacheAttnArgs a{};
-  ra_status st = check_cache(cache, table, width, lens, B, T, dtype, &a.c);
-  if (st != RA_OK) return st;
-  if (Hq < 0 || Hq % cache->heads != 0) return RA_ERR_INVALID_ARG;
-  if (mask && mask_stride != 0 && mask_stride < static_cast<int64_t>(T) * T)
-    return RA_ERR_INVALID_ARG;
-  if (dtype == RA_BF16 && cache->d != 64 && cache->d != 128) return RA_ERR_UNSUPPORTED;
-  if (Hq > kMaxHeads || static_cast<int64_t>(B) * Hq * T > kMaxTokens) return RA_ERR_UNSUPPORTED;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(count, 4) ||
-      !aligned(workspace, 256))
-    return RA_ERR_MISALIGNED;
-  if (B == 0 || Hq == 0 || T == 0) return RA_OK;
-  if (!q || !out || !lse || !workspace) return RA_ERR_INVALID_ARG;
-  if (workspace_bytes < cache_attention_workspace_bytes(B, Hq, cache->heads, T, cache->d))
-    return RA_ERR_INVALID_ARG;
-  if ((st = device_ready(&a.c.status)) != RA_OK) return st;
-  a.c.count = count;
-  a.q = q;
-  a.mask = mask;
-  a.mask_stride = mask_stride;
-  a.out = out;
-  a.lse = lse;
-  a.ws = static_cast<float*>(workspace);
-  a.Hq = Hq;
-  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(cache->d)));
-  a.wait_limit = wait_limit();
-  a.stall_cta = stall_cta();
-  return launched(launch_cache_attention(a, dtype, cache->dtype, cu(stream)));
+  const ra_status st = check_attention(q, cache, table, width, lens, count, mask, mask_stride, out, lse, workspace,
+                                       workspace_bytes, cache_attention_workspace_bytes, B, Hq, T, dtype, &a);
+  return st != RA_OK || !a.q ? st : launched(launch_cache_attention(a, dtype, cache->dtype, cu(stream)));
+}
+
+RA_API int64_t ra_cache_attention_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,
+                                                         int32_t d) {
+  if (B < 0 || Hq < 0 || heads < 1 || T < 0 || d < 1 || d > RA_MAX_HEAD_DIM || Hq % heads != 0)
+    return -1;
+  return cache_attention_shared_workspace_bytes(B, Hq, heads, T, d);
+}
+
+RA_API ra_status ra_cache_attention_shared(const void* q, const ra_cache* cache, const int32_t* table,
+                                           int32_t width, const int32_t* lens, const int32_t* shared,
+                                           const int32_t* count, const uint8_t* mask, int64_t mask_stride,
+                                           void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                                           int32_t B, int32_t Hq, int32_t T, ra_dtype dtype, ra_stream_t stream) {
+  RA_TRACE("ra_cache_attention_shared");
+  CacheAttnArgs a{};
+  if (!shared && B > 0 && Hq > 0 && T > 0) return RA_ERR_INVALID_ARG;
+  if (!aligned(shared, 4)) return RA_ERR_MISALIGNED;
+  const ra_status st = check_attention(q, cache, table, width, lens, count, mask, mask_stride, out, lse, workspace,
+                                       workspace_bytes, cache_attention_shared_workspace_bytes, B, Hq, T, dtype, &a);
+  if (st != RA_OK || !a.q) return st;
+  return launched(launch_cache_attention_shared(a, shared, dtype, cache->dtype, cu(stream)));
 }
 
 RA_API ra_status ra_pages_fork(int32_t* ref, int64_t pages, const int32_t* table, const int32_t* held,

@@ -373,6 +373,25 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
     or [T, T] for all sequences; None: j <= t).  Hq is a multiple of the
     cache's heads.  `workspace` (uint8, ra_cache_attention_workspace_bytes) is
     allocated when not given.  Returns (out [B, Hq, T, d], lse [B, Hq, T])."""
+    return _attend(None, q, cache, table, lens, count, mask, out, lse, workspace, stream)
+
+
+def ra_cache_attention_shared_workspace_bytes(B: int, Hq: int, heads: int, T: int, d: int) -> int:
+    return int(_native.lib().ra_cache_attention_shared_workspace_bytes(B, Hq, heads, T, d))
+
+
+def ra_cache_attention_shared(q, cache: RaCache, table, lens, shared, count=None, mask=None, out=None,
+                              lse=None, workspace=None, stream=None):
+    """ra_cache_attention for sequences that share prefixes, each read once for
+    all of them: shared [B] (int32) > 0 are the tokens that sequence b has in
+    common with the one before it (the next lower one with lens >= 0), else a
+    group begins at b.  `workspace`: ra_cache_attention_shared_workspace_bytes."""
+    if shared is None:
+        raise ValueError("shared must be an int32 tensor [B]")
+    return _attend(shared, q, cache, table, lens, count, mask, out, lse, workspace, stream)
+
+
+def _attend(shared, q, cache, table, lens, count, mask, out, lse, workspace, stream):
     B, Hq, T, d = q.shape
     index = _here(q)
     c = cache.found(index)
@@ -387,6 +406,9 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
             mp = _dev(mask, index, shape=(T, T), what="mask")
         else:
             mp, ms = _dev(mask, index, shape=(B, T, T), what="mask"), T * T
+    lib = _native.lib()
+    size = lib.ra_cache_attention_workspace_bytes if shared is None else \
+        lib.ra_cache_attention_shared_workspace_bytes
     if out is None or lse is None or workspace is None:
         with _on(stream):
             if out is None:
@@ -394,15 +416,19 @@ def ra_cache_attention(q, cache: RaCache, table, lens, count=None, mask=None, ou
             if lse is None:
                 lse = torch.empty((B, Hq, T), device=q.device, dtype=torch.float32)
             if workspace is None:
-                n = ra_cache_attention_workspace_bytes(B, Hq, c.heads, T, d)
-                workspace = torch.empty(max(n, 0), device=q.device, dtype=torch.uint8)
-    res = _native.lib().ra_cache_attention(
-        _dev(q, index, shape=(B, Hq, T, d), what="q"), c.ref, tab, width, ln, cnt, mp, ms,
-        _dev(out, index, q.dtype, (B, Hq, T, d), "out"),
-        _dev(lse, index, torch.float32, (B, Hq, T), "lse"),
-        _dev(workspace, index, torch.uint8, what="workspace"), workspace.numel(), B, Hq, T,
-        _dtype_code(q), _on_stream(stream, index))
-    _check(res, "ra_cache_attention")
+                workspace = torch.empty(max(int(size(B, Hq, c.heads, T, d)), 0), device=q.device,
+                                        dtype=torch.uint8)
+    rest = (cnt, mp, ms, _dev(out, index, q.dtype, (B, Hq, T, d), "out"),
+            _dev(lse, index, torch.float32, (B, Hq, T), "lse"),
+            _dev(workspace, index, torch.uint8, what="workspace"), workspace.numel(), B, Hq, T,
+            _dtype_code(q), _on_stream(stream, index))
+    qp = _dev(q, index, shape=(B, Hq, T, d), what="q")
+    if shared is None:
+        _check(lib.ra_cache_attention(qp, c.ref, tab, width, ln, *rest), "ra_cache_attention")
+    else:
+        res = lib.ra_cache_attention_shared(qp, c.ref, tab, width, ln,
+                                            _dev(shared, index, torch.int32, (B,), "shared"), *rest)
+        _check(res, "ra_cache_attention_shared")
     return out, lse
 
 

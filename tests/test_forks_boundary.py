@@ -159,3 +159,36 @@ def test_binding_refuses_host_tensors(monkeypatch):
         ra.ra_pages_trim(i, t, i, None, 16)
     with pytest.raises(ValueError):
         ra.ra_verify_drafts(torch.zeros(1, 2, 3), torch.zeros(1, 2, dtype=torch.int64), torch.zeros(1, 2))
+
+
+def attend(L, c, q=A, table=A, width=4, lens=A, shared=A, count=None, mask=None, ms=0, out=A, lse=A, ws=A, n=None,
+           B=3, Hq=4, T=2, dt=BF16):
+    if n is None:
+        n = max(0, L.ra_cache_attention_shared_workspace_bytes(B, max(Hq, 0), 1, max(T, 0), 64))
+    return L.ra_cache_attention_shared(q, ctypes.byref(c) if c else None, table, width, lens, shared, count, mask,
+                                       ms, out, lse, ws, n, B, Hq, T, dt, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), INV), (dict(out=None), INV), (dict(lse=None), INV), (dict(ws=None), INV), (dict(n=64), INV),
+    (dict(Hq=3), INV), (dict(Hq=-2), INV), (dict(mask=A, ms=3), INV), (dict(B=-1), INV), (dict(T=-1), INV),
+    (dict(lens=None), INV), (dict(table=None), INV), (dict(shared=None), INV), (dict(dt=E4M3), INV),
+    (dict(dt=F32), UNS), (dict(q=A + 8), MIS), (dict(out=A + 8), MIS), (dict(ws=A + 16), MIS), (dict(shared=A + 2), MIS),
+    (dict(count=A + 2), MIS), (dict(T=0), OK), (dict(Hq=0), OK), (dict(B=0, lens=None, table=None, shared=None), OK),
+    (dict(), ARCH), (dict(mask=A, ms=4), ARCH),
+])
+def test_shared_attention_rules(L, kw, code):
+    assert attend(L, cache(), **kw) == code
+
+
+def test_shared_attention_of_other_caches(L):
+    assert attend(L, None) == INV
+    assert attend(L, cache(d=80)) == UNS
+    assert attend(L, cache(d=80, dt=F32), dt=F32, n=1 << 40) == ARCH
+    w, plain = L.ra_cache_attention_shared_workspace_bytes, L.ra_cache_attention_workspace_bytes
+    assert w(-1, 4, 2, 1, 64) == -1 and w(1, 3, 2, 1, 64) == -1 and w(1, 4, 0, 1, 64) == -1
+    assert w(1, 4, 2, 1, 264) == -1
+    for sizes in ((1, 4, 2, 1, 64), (96, 32, 8, 1, 128), (3000, 8, 8, 1, 64), (8, 32, 8, 300, 128)):
+        assert w(*sizes) >= plain(*sizes)
+    with pytest.raises(ValueError):
+        ra.ra_cache_attention_shared(None, None, None, None, None)
