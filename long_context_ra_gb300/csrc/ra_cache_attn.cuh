@@ -38,10 +38,12 @@ __host__ __device__ __forceinline__ const SharedPaged& paged(const SharedAttnArg
 template <typename A>
 struct IsShared {
   static constexpr bool value = false;
+  using Walk = UnitWalk;
 };
 template <>
 struct IsShared<SharedAttnArgs> {
   static constexpr bool value = true;
+  using Walk = StretchWalk;
 };
 
 // A row of a unit over a stretch.

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   allow_join();
   wait_for_plan(a);
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
-  UnitWalk u;
+  typename IsShared<A>::Walk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
     const int head = u.unit / p.row_tiles;
     const int64_t r0 = static_cast<int64_t>(u.unit % p.row_tiles) * kRows;

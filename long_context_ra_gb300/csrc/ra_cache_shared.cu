@@ -22,15 +22,16 @@
 namespace ra {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;    // at most
 constexpr int kPlanSequences = 2048;  // 20 bytes of shared memory each
 constexpr int kTile = 128;            // a multiple of every kernel's key tile
+constexpr int kLeadKeys = 512;        // keys that take a CTA as long as a unit's start and end
 
 // The plan in the workspace.
 struct Plan {
   Stretch* list[2];   // [B] prefixes; [B] own parts, one per sequence
-  int64_t* at[2];     // tiles before each
-  int64_t* totals;    // [2][2] tiles of all; stretches
+  int64_t* at[2];     // lengths before each
+  int64_t* totals;    // [2][2] length of all; stretches
   int32_t* lot;       // [B] the prefix stretch that a sequence is a member of, or -1
 };
 
@@ -39,6 +40,7 @@ struct PlanArgs {
   const int32_t* shared;
   Plan plan;
   int tile[2];      // keys per tile of the two launches
+  int lead[2];
   int granule;      // a common part is a multiple of it
   int members;      // sequences of a lot
 };
@@ -58,7 +60,7 @@ __device__ __forceinline__ longlong2 scan_two(longlong2 x, longlong2* warps, lon
   __syncthreads();
   if (lane == 31) warps[warp] = x;
   __syncthreads();
-  const longlong2 w = scan(warps[lane]);
+  const longlong2 w = scan(lane * 32 < static_cast<int>(blockDim.x) ? warps[lane] : longlong2{0, 0});
   all.x = __shfl_sync(0xffffffffu, w.x, 31);
   all.y = __shfl_sync(0xffffffffu, w.y, 31);
   const int64_t bx = __shfl_sync(0xffffffffu, w.x, max(warp - 1, 0)), by = __shfl_sync(0xffffffffu, w.y, max(warp - 1, 0));
@@ -78,13 +80,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   int32_t* last = first + G;
   int32_t* lots = last + G;      // [G] live sequences, then the first lot
   allow_join();
-  for (int i = tid; i < G; i += kPlanThreads) {
+  for (int i = tid; i < G; i += blockDim.x) {
     common[i] = INT32_MAX;
     first[i] = B;
     last[i] = -1;
     lots[i] = 0;
   }
-  const int each = (B + kPlanThreads - 1) / kPlanThreads;
+  const int each = (B + blockDim.x - 1) / blockDim.x;
   const int b0 = min(B, tid * each), b1 = min(B, b0 + each);
   // ---- groups: one begins where a live sequence shares nothing
   longlong2 sum{0, 0}, all;
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     common[g] = part;
     lots[g] = n;
     sum.x += n;
-    sum.y += static_cast<int64_t>(n) * (part / a.tile[0]);
+    sum.y += n * stretch_length(part / a.tile[0], a.lead[0]);
   }
   longlong2 before = scan_two(sum, warps, all);
   before.x -= sum.x;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       a.plan.list[0][before.x] = Stretch{common[g], 0, first[g], 0, b, min(a.members, last[g] + 1 - b)};
       a.plan.at[0][before.x] = before.y;
       before.x += 1;
-      before.y += common[g] / a.tile[0];
+      before.y += stretch_length(common[g] / a.tile[0], a.lead[0]);
     }
   }
   if (tid == 0) {
@@ -143,16 +145,16 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     const int part = c.lens[b] >= 0 ? common[group[b]] : 0;
     return Stretch{static_cast<int32_t>(s.len) - part, s.cnt, b, part >> c.page_shift, b, 1};
   };
-  auto tiles = [&](const Stretch& s) {
-    return (static_cast<int64_t>(s.len) + s.cnt + a.tile[1] - 1) / a.tile[1];
+  auto length = [&](const Stretch& s) {
+    return stretch_length(stretch_tiles(SeqInfo{s.len, s.cnt}, a.tile[1]), a.lead[1]);
   };
-  for (int b = b0; b < b1; ++b) sum.x += tiles(own(b));
+  for (int b = b0; b < b1; ++b) sum.x += length(own(b));
   int64_t own_at = scan_two(sum, warps, all).x - sum.x;
   for (int b = b0; b < b1; ++b) {
     const Stretch s = own(b);
     a.plan.list[1][b] = s;
     a.plan.at[1][b] = own_at;
-    own_at += tiles(s);
+    own_at += length(s);
     const int g = group[b];
     a.plan.lot[b] = c.lens[b] >= 0 && common[g] > 0 ? lots[g] + (b - first[g]) / a.members : -1;
   }
@@ -173,7 +175,7 @@ struct Side {
   const float4* part_o;    // a slot's rows x d / 4 quads
   const float2* whole_ml;
   const float4* whole_o;
-  int rows, ctas, tile, tile_members, tile_rows;
+  int rows, ctas, tile, lead, tile_members, tile_rows;
   int row_step, quad_step;  // of a slot's quads
 };
 
@@ -189,16 +191,20 @@ constexpr int kJoinThreads = 128;
 constexpr int kQuads = 2;
 constexpr int kParts = 4;
 
-template <typename E>
+template <typename E, int kSplit>
 __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_constant__ JoinArgs j) {
+  constexpr int kItems = kJoinThreads / 32 / kSplit;  // of a block
+  __shared__ float4 sums[kSplit > 1 ? kJoinThreads / 32 : 1][kQuads][32];
+  __shared__ float2 sum_ml[kSplit > 1 ? kJoinThreads / 32 : 1][32];
   const CacheAttnArgs& a = j.a;
   const PagedArgs& c = a.c;
   const int quads = c.d / 4, slices = quads / kQuads;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kSplit;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + warp / kSplit;
   const int quad = static_cast<int>(item % slices) * kQuads;
-  const int64_t row = item / slices * 32 + threadIdx.x % 32;
+  const int64_t row = item / slices * 32 + lane;
+  const bool here = row < j.all_rows;
   wait_for_parts();
-  if (row >= j.all_rows) return;
   const int w = static_cast<int>(row % j.rows1);  // within its sequence and key head
   const int head = static_cast<int>(row / j.rows1 % c.heads);
   const int b = static_cast<int>(row / j.rows1 / c.heads);
@@ -211,16 +217,16 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
 #pragma unroll
     for (int h = 0; h < kQuads; ++h) o[h] = make_float4(o[h].x * f, o[h].y * f, o[h].z * f, o[h].w * f);
   };
-  if (w % c.T < sequence(c, b).cnt) {
+  if (here && w % c.T < sequence(c, b).cnt) {
 #pragma unroll 1
     for (int z = 0; z < 2; ++z) {
       const Side& s = j.side[z];
       const int v = z == 0 ? j.lot[b] : b;
       if (v < 0) continue;
       const Stretch st = s.list[v];
-      const int64_t tiles = (static_cast<int64_t>(st.len) + st.cnt + s.tile - 1) / s.tile;
+      const int64_t tiles = stretch_tiles(SeqInfo{st.len, st.cnt}, s.tile);
       const int64_t run = (s.totals[0] * c.heads + s.ctas - 1) / s.ctas;
-      const int64_t u0 = s.at[v] * c.heads + head * tiles;
+      const int64_t u0 = s.at[v] * c.heads + head * stretch_length(tiles, s.lead);
       const int c0 = static_cast<int>(u0 / run), c1 = static_cast<int>((u0 + tiles - 1) / run);
       const int member = b - st.b0;
       const int local = member / s.tile_members * s.tile_rows + member % s.tile_members * j.rows1 + w;
@@ -228,7 +234,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
       const float2* ml_at = whole ? s.whole_ml + row : s.part_ml + local;
       const float4* o_at = whole ? s.whole_o + quad * j.all_rows + row : s.part_o + quad * s.quad_step + local * s.row_step;
       const int64_t quad_step = whole ? j.all_rows : s.quad_step;
-      for (int i = c0; i <= c1; i += kParts) {
+      // the own part's few by the last warp, the prefix's from the first on
+      for (int i = c0 + (z == 0 ? sub : kSplit - 1 - sub) * kParts; i <= c1; i += kParts * kSplit) {
         float2 ml[kParts];
         float4 y[kParts][kQuads];
 #pragma unroll
@@ -261,6 +268,33 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
       }
     }
   }
+  if (kSplit > 1) {
+#pragma unroll
+    for (int h = 0; h < kQuads; ++h) sums[warp][h][lane] = o[h];
+    sum_ml[warp][lane] = make_float2(m, l);
+    __syncthreads();
+    if (sub != 0) return;
+    float top = m;
+#pragma unroll
+    for (int z = 1; z < kSplit; ++z) top = fmaxf(top, sum_ml[warp + z][lane].x);
+    if (top > m && m > -INFINITY) scale(exp2f(m - top));
+    m = top;
+#pragma unroll
+    for (int z = 1; z < kSplit; ++z) {
+      const float2 ml = sum_ml[warp + z][lane];
+      const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
+      l = fmaf(f, ml.y, l);
+#pragma unroll
+      for (int h = 0; h < kQuads; ++h) {
+        const float4 y = sums[warp + z][h][lane];
+        o[h].x = fmaf(f, y.x, o[h].x);
+        o[h].y = fmaf(f, y.y, o[h].y);
+        o[h].z = fmaf(f, y.z, o[h].z);
+        o[h].w = fmaf(f, y.w, o[h].w);
+      }
+    }
+  }
+  if (!here) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   E* dst = static_cast<E*>(a.out) + row * c.d + 4 * quad;
   if constexpr (sizeof(E) == 4) {
@@ -280,6 +314,13 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
     *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
   }
   if (quad == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
+}
+
+template <typename E, int kSplit>
+cudaError_t join(const JoinArgs& j, int64_t items, cudaStream_t s) {
+  constexpr int kItems = kJoinThreads / 32 / kSplit;
+  const dim3 grid(static_cast<unsigned>((items + kItems - 1) / kItems));
+  return launch_behind(shared_join_kernel<E, kSplit>, grid, kJoinThreads, 0, s, j);
 }
 
 // ------------------------------------------------------------ the workspace
@@ -356,12 +397,14 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
     pl.plan.list[z] = reinterpret_cast<Stretch*>(take(B * sizeof(Stretch)));
     pl.plan.at[z] = reinterpret_cast<int64_t*>(take(B * 8));
     pl.tile[z] = shape[z].tile;
+    pl.lead[z] = kLeadKeys / shape[z].tile;
   }
   pl.plan.lot = reinterpret_cast<int32_t*>(take(B * 4));
   const int page = 1 << a.c.page_shift;
   pl.granule = page > kTile ? page : kTile;
   pl.members = static_cast<int>(members);
-  shared_plan_kernel<<<1, kPlanThreads, B * 20 + 16, s>>>(pl);
+  const int threads = B < kPlanThreads ? (B + 31) / 32 * 32 : kPlanThreads;  // fewer warps are quicker
+  shared_plan_kernel<<<1, threads, B * 20 + 16, s>>>(pl);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
@@ -378,6 +421,7 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
     g.stretches.list = pl.plan.list[z];
     g.stretches.at = pl.plan.at[z];
     g.stretches.totals = pl.plan.totals + 2 * z;
+    g.stretches.lead = pl.lead[z];
     g.whole_o = reinterpret_cast<float*>(ws + r.whole[z]);
     g.whole_ml = g.whole_o + round256(j.all_rows * a.c.d * 4) / 4;
     g.all_rows = j.all_rows;
@@ -406,15 +450,18 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
                      p.rows,
                      p.div.ctas,
                      p.div.tile,
+                     pl.lead[z],
                      g.tile_members,
                      shape[z].tile_rows,
                      shape[z].quads ? 1 : a.c.d / 4,
                      shape[z].quads ? p.rows : 1};
   }
+  // Four warps to a row's parts where those of a single group may be many.
   const int64_t items = (j.all_rows + 31) / 32 * (a.c.d / 4 / kQuads);
-  const dim3 grid(static_cast<unsigned>((items + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
-  return dense == RA_BF16 ? launch_behind(shared_join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, s, j)
-                          : launch_behind(shared_join_kernel<float>, grid, kJoinThreads, 0, s, j);
+  const int64_t units = a.c.heads * ((B + members - 1) / members);
+  const bool many = shape[0].ctas > 8 * units;
+  if (dense == RA_BF16) return many ? join<__nv_bfloat16, 4>(j, items, s) : join<__nv_bfloat16, 1>(j, items, s);
+  return many ? join<float, 4>(j, items, s) : join<float, 1>(j, items, s);
 }
 
 }  // namespace ra

@@ -118,7 +118,7 @@ struct Layout {
   static constexpr int kDivision = kLeftOut + 128;
   // walks of the 8 softmax warps: in shared memory, not in registers
   static constexpr int kWalks = (kDivision + static_cast<int>(sizeof(DivisionShared)) + 15) / 16 * 16;
-  static constexpr int kBytes = kWalks + 8 * static_cast<int>(sizeof(UnitWalk));
+  static constexpr int kBytes = kWalks + 8 * static_cast<int>(sizeof(StretchWalk));  // the larger of the two
   static constexpr int kSmem = kBytes + 1024;  // slack for 1024-byte alignment
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kRawStages + kStages <= 24, "rings");
@@ -302,8 +302,8 @@ __device__ __noinline__ uint32_t seen_word(const CacheAttnArgs& a, const SeqInfo
 
 // Which of columns x .. x + 31 of the drafts that query t sees in the walk's
 // part hold a value that is not finite (a bit each).
-template <bool k8, int D, typename A>
-__device__ __noinline__ uint32_t poisoned_columns(const A& a, const UnitWalk& u, int b, int head,
+template <bool k8, int D, typename A, typename W>
+__device__ __noinline__ uint32_t poisoned_columns(const A& a, const W& u, int b, int head,
                                                   int t, int x, int tile) {
   const auto& c = paged(a);
   uint32_t bad = 0;
@@ -357,7 +357,8 @@ struct Unit {
   int head;
   int64_t r0;  // first query row of the unit within its key head
   int64_t q0;  // its row in q, out, lse
-  __device__ Unit(const CacheAttnArgs& a, const AttnPlan& p, const UnitWalk& u, int64_t rows) {
+  template <typename W>
+  __device__ Unit(const CacheAttnArgs& a, const AttnPlan& p, const W& u, int64_t rows) {
     head = u.unit / p.row_tiles;
     r0 = static_cast<int64_t>(u.unit % p.row_tiles) * p.rows;
     q0 = (static_cast<int64_t>(u.b) * a.c.heads + head) * rows + r0;
@@ -369,7 +370,7 @@ __device__ __forceinline__ bool second_tile(const CacheAttnArgs& a, const AttnPl
                                             int64_t rows) {
   return Unit(a, p, u, rows).r0 + 128 < rows;
 }
-__device__ __forceinline__ bool second_tile(const SharedAttnArgs& a, const AttnPlan&, const UnitWalk& u, int64_t) {
+__device__ __forceinline__ bool second_tile(const SharedAttnArgs& a, const AttnPlan&, const StretchWalk& u, int64_t) {
   return a.stretches.list[u.b].members > a.tile_members;
 }
 
@@ -380,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tq) {
   using L = Layout<k8, D, kTwo>;
   constexpr bool kShared = IsShared<A>::value;
+  using Walk = typename IsShared<A>::Walk;
   constexpr int kS = L::kStages, kKeys = L::kKeys, kN = kKeys / 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x - kHandWarp * 32;
     // The unit's queries, in the order of widen16: in place, a piece stays in
     // its thread.
-    auto order_queries = [&](const UnitWalk& w, uint32_t ord) {
+    auto order_queries = [&](const Walk& w, uint32_t ord) {
       const uint32_t end = base + L::kQ0 + (kTwo && second_tile(a, p, w, rows) ? 2 : 1) * L::kQTile;
       if (!wait_warp(bars.q_raw(), ord & 1u, ab)) return false;
 #pragma unroll 1
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     static_assert(!k8 || L::kQTile % (4 * 256 * 16) == 0, "whole rounds of the queries");
-    UnitWalk w;
+    Walk w;
     w.start_found(c, p.div, sh, run);
     if (k8) {
       Ring in, out;  // raw stages; operand stages
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t in_page = (1u << c.page_shift) - 1u;
     const int32_t behind = static_cast<int32_t>((c.pages > 0 ? c.pages * c.heads : 1));
     const uint64_t map_k = reinterpret_cast<uint64_t>(&tk), map_v = reinterpret_cast<uint64_t>(&tv);
-    UnitWalk w;
+    Walk w;
     w.start_found(c, p.div, sh, run);
     Ring r;
     uint32_t ktiles = 0;
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Rows behind the head's belong to other heads or are zeros: rows of the
       // product that nobody reads.
       const uint32_t bar = k8 ? bars.q_raw() : bars.q_full();
-      UnitWalk w;
+      Walk w;
       w.start_found(c, p.div, sh, run);
       uint32_t ord = 0;
       for (; !w.done(); ++ord, w.next(c, p.div)) {
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring r;
       uint32_t unit = 0, np0 = 0, np1 = 0;  // units; P tiles taken per stream
       bool ok = true, any = false;
-      UnitWalk u;
+      Walk u;
       // wait for the next stage of the ring: its index, or -1
       auto take = [&]() {
         if (!wait1(bars.kv_full(r.stage), r.phase, ab)) return -1;
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* xml = xo + 2 * 128 * 33;                        // [2][128][2]
     uint32_t ns = 0, no = 0, unit = 0, xc = 0, kt = 0;     // phases; K tiles before the unit
     bool ok = true;
-    UnitWalk& u = reinterpret_cast<UnitWalk*>(gbase + L::kWalks)[warp];
+    Walk& u = reinterpret_cast<Walk*>(gbase + L::kWalks)[warp];
     if (lane == 0) u.start_found(c, p.div, sh, run);
     __syncwarp();
     while (ok && !u.done()) {

@@ -29,8 +29,9 @@ struct Stretch {
 // The stretches of one launch, in the place of a batch's sequences.
 struct SharedPaged : PagedArgs {
   const Stretch* list;
-  const int64_t* at;      // key tiles (of one unit) before each stretch
-  const int64_t* totals;  // tiles of all; the number of stretches
+  const int64_t* at;      // length (of one unit) before each stretch
+  const int64_t* totals;  // length of all; the number of stretches
+  int32_t lead;           // tiles that a unit's start and end are reckoned as
 };
 
 // The page numbers of a sequence, and how many there can be.
@@ -217,19 +218,12 @@ __device__ __forceinline__ int64_t seq_tiles(const PagedArgs& c, const Division&
   return tiles_of(sequence(c, b), v);
 }
 
-// Of a stretch there may be none.
-__device__ __forceinline__ int64_t tiles_of(const PagedArgs&, const SeqInfo& s, const Division& v) {
-  return tiles_of(s, v);
-}
-__device__ __forceinline__ int64_t tiles_of(const SharedPaged&, const SeqInfo& s, const Division& v) {
-  return (s.keys() + v.tile - 1) / v.tile;
-}
-// On to a sequence with tiles, where there is one.
-__device__ __forceinline__ int with_tiles(const PagedArgs&, int b) { return b; }
-__device__ __forceinline__ int with_tiles(const SharedPaged& c, int b) {
-  while (sequence(c, b).keys() == 0) ++b;
-  return b;
-}
+// Tiles of a stretch, of which there may be none, and the length that a unit of
+// it takes in the division: its tiles and `lead` more that stand for its start
+// and end.  (Units of a tile each otherwise fill a run that takes many times as
+// long as one of whole tiles: 96 sequences of 0 to 2000 own tokens 175 us.)
+__device__ __forceinline__ int64_t stretch_tiles(const SeqInfo& s, int tile) { return (s.keys() + tile - 1) / tile; }
+__device__ __forceinline__ int64_t stretch_length(int64_t tiles, int lead) { return tiles > 0 ? tiles + lead : 0; }
 
 __device__ __forceinline__ int64_t run_length(const Division& v, int64_t total) {
   return (total + v.ctas - 1) / v.ctas;
@@ -333,7 +327,7 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
   return min(run, all - begin);
 }
 
-// The same for stretches, whose tiles have been added up: every warp looks for
+// The same for stretches, whose lengths have been added up: every warp looks for
 // the last stretch that begins at or before the run.
 __device__ __forceinline__ int64_t division_start(const SharedPaged& c, const Division& v, int cta,
                                                   DivisionShared& sh) {
@@ -351,7 +345,6 @@ __device__ __forceinline__ int64_t division_start(const SharedPaged& c, const Di
     }
     if (lane == 0) {  // of every warp: all write the same
       sh.b = found;
-      sh.seq = sequence(c, found);
       sh.off = begin - c.at[found] * v.units;
       sh.run = run;
     }
@@ -395,50 +388,95 @@ struct UnitWalk {
   int64_t tiles, first, last;  // of the unit; this CTA's part [first, last)
   int unit;
 
-  template <typename P>
-  __device__ void start(const P& c, const Division& v, const DivisionShared& sh, int64_t n) {
+  __device__ void start(const PagedArgs& c, const Division& v, const DivisionShared& sh, int64_t n) {
     left = n;
     b = sh.b;
     off = sh.off;
     if (left > 0) load(c, v);
   }
   // The same without a load: the sequence is the one that division_start found.
-  template <typename P>
-  __device__ void start_found(const P& c, const Division& v, const DivisionShared& sh, int64_t n) {
+  __device__ void start_found(const PagedArgs&, const Division& v, const DivisionShared& sh, int64_t n) {
     left = n;
     b = sh.b;
     off = sh.off;
     seq = sh.seq;
-    if (left > 0) set(c, v);
+    if (left > 0) set(v);
   }
   __device__ bool done() const { return left <= 0; }
-  template <typename P>
-  __device__ void load(const P& c, const Division& v) {
+  __device__ void load(const PagedArgs& c, const Division& v) {
     seq = sequence(c, b);
-    set(c, v);
+    set(v);
   }
-  template <typename P>
-  __device__ void set(const P& c, const Division& v) {
-    tiles = tiles_of(c, seq, v);
+  __device__ void set(const Division& v) {
+    tiles = tiles_of(seq, v);
     unit = static_cast<int>(off / tiles);
     first = off - unit * tiles;
     last = min(tiles, first + left);
   }
-  template <typename P>
-  __device__ void next(const P& c, const Division& v) {
+  __device__ void next(const PagedArgs& c, const Division& v) {
     left -= last - first;
     off += last - first;
     if (off == tiles * v.units) {
       ++b;
       off = 0;
     }
-    if (left > 0) {
-      if (off == 0) b = with_tiles(c, b);
-      load(c, v);
-    }
+    if (left > 0) load(c, v);
   }
   __device__ bool whole() const { return first == 0 && last == tiles; }
   // Slot of a part that is not the whole unit.
+  __device__ int slot(int cta) const { return 2 * cta + (first == 0 ? 1 : 0); }
+};
+
+// The same over stretches: off and left count lengths, of which `lead` at a
+// unit's end are no tiles.  A part without a tile is passed over.
+struct StretchWalk {
+  int64_t left, off, step, span;
+  int b;
+  SeqInfo seq;
+  int64_t tiles, first, last;
+  int unit;
+
+  __device__ void start(const SharedPaged& c, const Division& v, const DivisionShared& sh, int64_t n) {
+    left = n;
+    b = sh.b;
+    off = sh.off;
+    settle(c, v);
+  }
+  __device__ void start_found(const SharedPaged& c, const Division& v, const DivisionShared& sh, int64_t n) {
+    start(c, v, sh, n);
+  }
+  __device__ bool done() const { return left <= 0; }
+  __device__ void settle(const SharedPaged& c, const Division& v) {
+    while (left > 0) {
+      seq = sequence(c, b);
+      tiles = stretch_tiles(seq, v.tile);
+      span = stretch_length(tiles, c.lead);
+      if (span == 0) {
+        ++b;
+        continue;
+      }
+      unit = static_cast<int>(off / span);
+      const int64_t from = off - unit * span;
+      step = min(span - from, left);
+      first = min(from, tiles);
+      last = min(from + step, tiles);
+      if (first < last) return;
+      pass(v);
+    }
+  }
+  __device__ void pass(const Division& v) {
+    left -= step;
+    off += step;
+    if (off == span * v.units) {
+      ++b;
+      off = 0;
+    }
+  }
+  __device__ void next(const SharedPaged& c, const Division& v) {
+    pass(v);
+    settle(c, v);
+  }
+  __device__ bool whole() const { return first == 0 && last == tiles; }
   __device__ int slot(int cta) const { return 2 * cta + (first == 0 ? 1 : 0); }
 };
 
