@@ -215,15 +215,12 @@ bool encode_rows(CUtensorMap* map, const void* ptr, int64_t rows, int d) {
   return get_encoder() == RA_OK && make_map(map, ptr, rows, d) == RA_OK;
 }
 
-bool encode_members(CUtensorMap* map, const void* ptr, int B, int heads, int rows, int d, int members) {
+bool encode_single_rows(CUtensorMap* map, const void* ptr, int64_t rows, int d) {
   if (get_encoder() != RA_OK) return false;
-  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(B)};
-  const cuuint64_t strides[3] = {row, row * rows, row * rows * heads};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, static_cast<cuuint32_t>(members)};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
+  const cuuint32_t box[2] = {64, 1}, estr[2] = {1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

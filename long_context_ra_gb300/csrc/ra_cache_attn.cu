@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     const int64_t r0 = static_cast<int64_t>(u.unit % p.row_tiles) * F::kRows;
     // row `local` of a unit over a stretch
     [[maybe_unused]] auto member = [&](int local) {
-      if constexpr (kShared) return MemberRow(a, c.list[u.b], u.unit, 0, local);
+      if constexpr (kShared) return MemberRow(a, c.list[u.b], u.unit, local);
     };
     auto is_row = [&](int local) {
       if constexpr (kShared)
@@ -396,16 +396,17 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
       if constexpr (kShared) {
         if (whole) {
           const int64_t q_row = member(local).q;
+          const int side = c.list[u.b].first < 0;
 #pragma unroll
           for (int x = 0; x < kPairs; ++x) {
             const int col = 2 * lane + 64 * x;
             if (col < d)
-              *reinterpret_cast<uint64_t*>(a.whole_o + (col / 4 * a.all_rows + q_row) * 4 + col % 4) =
+              *reinterpret_cast<uint64_t*>(a.whole_o[side] + (col / 4 * a.all_rows + q_row) * 4 + col % 4) =
                   dead ? 0ull : mul_f32x2(o[r][x], pack_f32x2(f, f));
           }
           if (lane == 0) {
-            a.whole_ml[2 * q_row] = m[r];
-            a.whole_ml[2 * q_row + 1] = l[r];
+            a.whole_ml[side][2 * q_row] = m[r];
+            a.whole_ml[side][2 * q_row + 1] = l[r];
           }
           continue;
         }
@@ -762,7 +763,7 @@ struct FfmaSet {
 };
 template <typename F>
 SharedShape shape_of(int ctas) {
-  return SharedShape{F::kTile, F::kRows, F::kRows, ctas, false};
+  return SharedShape{F::kTile, F::kRows, ctas, false};
 }
 
 template <typename H, int NC, typename A>

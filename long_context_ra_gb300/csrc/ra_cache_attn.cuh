@@ -18,18 +18,17 @@ struct AttnPlan {
   int row_tiles;  // units per (sequence, key head)
 };
 
-// A launch over stretches.  A unit's rows are those of its members' queries of
-// one key head, `tile_members` sequences to a tile of rows: row i of tile t
-// belongs to member t tile_members + i / rows1.  Every unit leaves a state, of
-// a part in its slot as above, of a whole unit in `whole_ml`, `whole_o` at the
-// query row's own place: [rows][2] and [d / 4][rows][4].
+// A launch over stretches, whose units' rows come from several sequences.
+// Every unit leaves a state, of a part in its slot as above, of a whole unit in
+// `whole_ml`, `whole_o` at the query row's own place: [rows][2] and [d / 4][rows][4],
+// for prefixes and own parts apart.
 struct SharedAttnArgs : CacheAttnArgs {
   SharedPaged stretches;
-  float* whole_ml;
-  float* whole_o;
+  const int32_t* rows_of;  // query rows of the prefixes: sequence x rows1 + row
+  float* whole_ml[2];
+  float* whole_o[2];
   int64_t all_rows;  // of q
   int32_t rows1;     // of one sequence and key head
-  int32_t tile_members;
 };
 
 __host__ __device__ __forceinline__ const PagedArgs& paged(const CacheAttnArgs& a) { return a.c; }
@@ -52,15 +51,19 @@ struct MemberRow {
   int b;      // its sequence
   int t;      // its token
   int cnt;    // the new tokens of its sequence
-  __device__ __forceinline__ MemberRow(const SharedAttnArgs& a, const Stretch& s, int head, int tile, int i) {
-    const int m = i / a.rows1, w = i % a.rows1, member = tile * a.tile_members + m;
-    const bool real = m < a.tile_members && member < s.members;
-    b = s.b0 + member;
+  __device__ __forceinline__ MemberRow(const SharedAttnArgs& a, const Stretch& s, int head, int i) {
+    const bool real = i < s.rows;
+    const int at = row(a, s, real ? i : 0);
+    b = at / a.rows1;
+    const int w = at % a.rows1;
     t = w % a.c.T;
     cnt = real ? sequence(a.c, b).cnt : 0;
     q = real ? (static_cast<int64_t>(b) * a.c.heads + head) * a.rows1 + w : -1;
   }
-  __device__ __forceinline__ bool live() const { return t < cnt; }
+  // sequence x rows1 + row: below 2^31, as rows of q are
+  static __device__ __forceinline__ int row(const SharedAttnArgs& a, const Stretch& s, int i) {
+    return s.first >= 0 ? a.rows_of[s.first + i] : ~s.first * a.rows1 + i;
+  }
 };
 
 // Query rows of one key head: g heads x T tokens, token fastest, which is
@@ -105,6 +108,11 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool re
                "r"(real ? 8 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 x;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -122,11 +130,11 @@ constexpr int kTreeCtas = 152;  // one per SM
 cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s);
 cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s);
 
-// How a kernel takes stretches: key tile, rows of a unit and of a row tile,
-// CTAs, and whether its parts' o is [d / 4][rows][4].
+// How a kernel takes stretches: key tile, rows of a unit, CTAs, and whether its
+// parts' o is [d / 4][rows][4].
 enum class SharedKernel { kDecode, kTreeOne, kTreeTwo, kFfma4, kFfma8, kFfma16, kFfma64 };
 struct SharedShape {
-  int tile, rows, tile_rows, ctas;
+  int tile, rows, ctas;
   bool quads;
 };
 SharedShape decode_shape();

@@ -84,11 +84,6 @@ struct Shape {
   }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
-               : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
 __device__ __forceinline__ void cp_wait() {
@@ -294,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool real;
       int64_t at;
       if constexpr (kShared) {
-        const MemberRow r(a, c.list[u.b], u.unit, 0, g + 8 * h);
+        const MemberRow r(a, c.list[u.b], u.unit, g + 8 * h);
         real = r.q >= 0;
         at = r.q;
         tq[h] = r.t;
@@ -565,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool here = r0 + r < rows;
       int64_t q_row = 0;  // its place in q (stretches)
       if constexpr (kShared) {
-        q_row = MemberRow(a, c.list[u.b], u.unit, 0, r).q;
+        q_row = MemberRow(a, c.list[u.b], u.unit, r).q;
         here = q_row >= 0;
       }
       if (here) {
@@ -589,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           } else {
             float* ml = slot_ml(a, p, slot) + 2 * r;
             if constexpr (kShared)
-              if (whole) ml = a.whole_ml + 2 * q_row;
+              if (whole) ml = a.whole_ml[c.list[u.b].first < 0] + 2 * q_row;
             ml[0] = ms;
             ml[1] = ls;
           }
@@ -612,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           } else {
             float4* dst = reinterpret_cast<float4*>(slot_o(a, p, slot) + r * D + 32 * x + x0);
             if constexpr (kShared)
-              if (whole) dst = reinterpret_cast<float4*>(a.whole_o) + (8 * x + x0 / 4) * a.all_rows + q_row;
+              if (whole) dst = reinterpret_cast<float4*>(a.whole_o[c.list[u.b].first < 0]) + (8 * x + x0 / 4) * a.all_rows + q_row;
             *dst = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
@@ -662,7 +657,7 @@ cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s)
   return by_type(a, p, k8, s);
 }
 
-SharedShape decode_shape() { return SharedShape{kTile, kRows, kRows, kDecodeCtas, false}; }
+SharedShape decode_shape() { return SharedShape{kTile, kRows, kDecodeCtas, false}; }
 
 cudaError_t launch_shared_decode(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s) {
   return by_type(a, p, k8, s);

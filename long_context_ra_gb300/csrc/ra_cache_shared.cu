@@ -4,16 +4,17 @@
 //
 // With (m, l, o) the online-softmax state of a row over a set of keys, the
 // state over all keys is the join of that over the prefix and that over the
-// rest, so the two can be worked on by launches of unlike shape: the prefix by
-// the rows of up to tile x members sequences at once, which puts a decode step
-// on the tensor cores; a sequence's own part as before.  Both run the kernels
-// of ra_cache_attention over a list of stretches (ra_paged.cuh), so that
-// pages, types, masks, the division of ragged work and the parts of shared
-// units are theirs.  Four launches, each behind the one before:
-//   plan     one block: groups, their common tokens, the two lists
-//   prefix   one stretch per group and lot of members
-//   own      one stretch per sequence
-//   join     every query row from its states, in order
+// rest, so the two can be worked on by units of unlike shape: the prefix by the
+// new tokens' rows of all of a group's sequences, laid end to end and cut into
+// lots, which puts a decode step on the tensor cores; a sequence's own part as
+// before.  Both run the kernels of ra_cache_attention over a list of stretches
+// (ra_paged.cuh), so that pages, types, masks, the division of ragged work and
+// the parts of shared units are theirs.  Each launch begins behind the one before:
+//   plan      one block: groups, their common tokens, the rows, the stretches
+//   prefixes  a stretch per lot of a group
+//   own parts a stretch per sequence (in one launch with the prefixes where the
+//             same kernel takes both)
+//   join      every query row from its states, in order
 // A group's common part is cut to whole key tiles and pages, so no tile of it
 // holds a draft or an end, and a sequence's own part begins at a page.
 
@@ -23,26 +24,36 @@ namespace ra {
 namespace {
 
 constexpr int kPlanThreads = 1024;    // at most
-constexpr int kPlanSequences = 2048;  // 20 bytes of shared memory each
+constexpr int kPlanSequences = 2048;  // 32 bytes of shared memory each
 constexpr int kTile = 128;            // a multiple of every kernel's key tile
+constexpr int kRuns = 9;              // lengths of a run that are tried
 constexpr int kLeadKeys = 512;        // keys that take a CTA as long as a unit's start and end
 
-// The plan in the workspace.
+// Where a sequence's rows are among the lots: row r of its live ones is row
+// (rel + r) of lot `lot` on (-1: its group has nothing in common).
+struct Place {
+  int32_t lot, rel;
+};
+
+// The plan in the workspace.  List 1 may be the same as list 0, behind it.
 struct Plan {
-  Stretch* list[2];   // [B] prefixes; [B] own parts, one per sequence
-  int64_t* at[2];     // lengths before each
-  int64_t* totals;    // [2][2] length of all; stretches
-  int32_t* lot;       // [B] the prefix stretch that a sequence is a member of, or -1
+  Stretch* list[2];
+  int64_t* totals;   // [2][3] length of all, stretches, run; then the first own stretch in its list
+  Place* places;     // [B]
+  int32_t* rows_of;  // [B rows1]
 };
 
 struct PlanArgs {
   PagedArgs c;
   const int32_t* shared;
   Plan plan;
-  int tile[2];      // keys per tile of the two launches
+  int tile[2];   // keys per tile of the two kinds of stretches
   int lead[2];
-  int granule;      // a common part is a multiple of it
-  int members;      // sequences of a lot
+  int ctas[2];
+  int granule;   // a common part is a multiple of it
+  int lot_rows;  // query rows of a lot
+  int group;     // query heads of a key head
+  bool one_list;
 };
 
 // Inclusive scan of two values per thread over the block; `all`: the sums.
@@ -71,96 +82,159 @@ __device__ __forceinline__ longlong2 scan_two(longlong2 x, longlong2* warps, lon
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int32_t smem[];
   __shared__ longlong2 warps[32];
+  __shared__ int runs[kRuns], again;
   const PagedArgs& c = a.c;
   const int B = c.B, tid = threadIdx.x;
   const int G = B + 1;           // groups: 0 for live sequences ahead of the first that shares nothing
   int32_t* group = smem;         // [B] group of each sequence
-  int32_t* common = group + B;   // [G] tokens in common, then the shared part
-  int32_t* first = common + G;   // [G] its first and last live sequence
-  int32_t* last = first + G;
-  int32_t* lots = last + G;      // [G] live sequences, then the first lot
+  int32_t* row_at = group + B;   // [B] its first live row among those of the lots
+  int32_t* len = row_at + B;     // [B] lens
+  int32_t* cnt = len + B;        // [B] new tokens
+  int32_t* common = cnt + B;     // [G] tokens in common, then the shared part
+  int32_t* first = common + G;   // [G] its first live sequence
+  int32_t* rows = first + G;     // [G] live rows
+  int32_t* lots = rows + G;      // [G] live sequences, then the first lot
   allow_join();
+  if (tid < kRuns) runs[tid] = 0;
+  if (tid == 0) again = 0;
   for (int i = tid; i < G; i += blockDim.x) {
     common[i] = INT32_MAX;
     first[i] = B;
-    last[i] = -1;
+    rows[i] = 0;
     lots[i] = 0;
   }
   const int each = (B + blockDim.x - 1) / blockDim.x;
   const int b0 = min(B, tid * each), b1 = min(B, b0 + each);
+  const int g1 = b0 < B && b1 == B ? G : b1;  // this thread's groups: b0 .. g1 - 1
   // ---- groups: one begins where a live sequence shares nothing
   longlong2 sum{0, 0}, all;
-  for (int b = b0; b < b1; ++b) sum.x += c.lens[b] >= 0 && a.shared[b] <= 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = c.lens[b], t = c.count ? c.count[b] : c.T;
+    len[b] = n;
+    cnt[b] = n < 0 ? 0 : max(0, min(t, c.T));
+    if (n >= 0 && t > c.T) flag_page(c.status);
+    group[b] = a.shared[b];
+    sum.x += n >= 0 && group[b] <= 0;
+  }
   int64_t at = scan_two(sum, warps, all).x - sum.x;
   for (int b = b0; b < b1; ++b) {
-    const bool live = c.lens[b] >= 0;
-    at += live && a.shared[b] <= 0;
-    const int g = static_cast<int>(at);
-    group[b] = g;
-    if (live) {
-      atomicMin(first + g, b);
-      atomicMax(last + g, b);
-      atomicAdd(lots + g, 1);
-      if (c.count && c.count[b] > c.T) flag_page(c.status);
+    at += len[b] >= 0 && group[b] <= 0;
+    if (len[b] >= 0) {
+      atomicMin(first + at, b);
+      atomicAdd(lots + at, 1);
     }
+    row_at[b] = group[b];  // for the moment
+    group[b] = static_cast<int>(at);
   }
   __syncthreads();
   for (int b = b0; b < b1; ++b)
-    if (c.lens[b] >= 0) atomicMin(common + group[b], b == first[group[b]] ? c.lens[b] : min(c.lens[b], a.shared[b]));
+    if (len[b] >= 0) atomicMin(common + group[b], b == first[group[b]] ? len[b] : min(len[b], row_at[b]));
   __syncthreads();
-  // ---- their shared parts and lots of members
-  const int g1 = b0 < B && b1 == B ? G : b1;
+  for (int g = b0; g < g1; ++g) common[g] = lots[g] > 1 ? max(common[g], 0) / a.granule * a.granule : 0;
+  __syncthreads();
+  // ---- rows that see a prefix
+  sum = longlong2{0, 0};
+  auto live_rows = [&](int b) { return common[group[b]] > 0 ? cnt[b] * a.group : 0; };
+  for (int b = b0; b < b1; ++b) {
+    const int n = live_rows(b);
+    sum.x += n;
+    if (n > 0) atomicAdd(rows + group[b], n);
+  }
+  int row = static_cast<int>(scan_two(sum, warps, all).x - sum.x);
+  const int rows_all = static_cast<int>(all.x);
+  for (int b = b0; b < b1; ++b) {
+    row_at[b] = row;
+    row += live_rows(b);
+  }
+  __syncthreads();
+  // ---- lengths: of a lot's units, and of a sequence's own
+  auto lots_of = [&](int g) { return common[g] > 0 ? (rows[g] + a.lot_rows - 1) / a.lot_rows : 0; };
+  auto lot_length = [&](int g) { return c.heads * stretch_length(common[g] / a.tile[0], a.lead[0]); };
+  auto part = [&](int b) { return cnt[b] > 0 ? common[group[b]] : 0; };
+  auto own = [&](int b) { return cnt[b] > 0 ? len[b] - part(b) : 0; };  // without new tokens: nothing
+  auto length = [&](int b) {
+    return c.heads * stretch_length(stretch_tiles(SeqInfo{own(b), cnt[b]}, a.tile[1]), a.lead[1]);
+  };
+  sum = longlong2{0, 0};
+  for (int g = b0; g < g1; ++g) sum.x += lots_of(g) * lot_length(g);
+  for (int b = b0; b < b1; ++b) sum.y += length(b);
+  const longlong2 own_before = scan_two(sum, warps, all);
+  int64_t own_at = own_before.y - sum.y;
+  const int64_t own_all = all.y, total = all.x + (a.one_list ? own_all : 0);
+  // ---- the run of a CTA.  Lots of a group read the same keys: where they begin
+  // at runs' starts they do so at the same time, out of L2 (9 lots of 65536 keys,
+  // 8 heads: 2.5 GB from memory without).  The smallest run, up to an eighth
+  // above the even one, with which every lot can take whole runs.
+  const int64_t even = (total + a.ctas[0] - 1) / a.ctas[0];
+  for (int g = b0; g < g1; ++g) {
+    const int n = lots_of(g);
+    if (n > 1) again = 1;
+    if (n > 0)
+      for (int i = 0; i < kRuns; ++i) {
+        const int64_t run = even + even * i / (8 * (kRuns - 1));
+        atomicAdd(&runs[i], static_cast<int>(n * ((lot_length(g) + run - 1) / run)));
+      }
+  }
+  __syncthreads();
+  int64_t run = even;
+  bool aligned = false;
+  for (int i = 0; i < kRuns && again && !aligned; ++i) {
+    const int64_t r = even + even * i / (8 * (kRuns - 1));
+    aligned = runs[i] + (a.one_list ? (own_all + r - 1) / r : 0) <= a.ctas[0];
+    if (aligned) run = r;
+  }
+  // ---- lots
+  auto lot_room = [&](int g) { return aligned ? (lot_length(g) + run - 1) / run * run : lot_length(g); };
   sum = longlong2{0, 0};
   for (int g = b0; g < g1; ++g) {
-    const int part = lots[g] > 1 ? max(common[g], 0) / a.granule * a.granule : 0;
-    const int n = part > 0 ? (last[g] - first[g] + a.members) / a.members : 0;
-    common[g] = part;
-    lots[g] = n;
-    sum.x += n;
-    sum.y += n * stretch_length(part / a.tile[0], a.lead[0]);
+    sum.x += lots_of(g);
+    sum.y += lots_of(g) * lot_room(g);
   }
   longlong2 before = scan_two(sum, warps, all);
   before.x -= sum.x;
   before.y -= sum.y;
   for (int g = b0; g < g1; ++g) {
-    const int n = lots[g];
+    const int n = lots_of(g);
     lots[g] = static_cast<int>(before.x);
     for (int i = 0; i < n; ++i) {
-      const int b = first[g] + i * a.members;
-      a.plan.list[0][before.x] = Stretch{common[g], 0, first[g], 0, b, min(a.members, last[g] + 1 - b)};
-      a.plan.at[0][before.x] = before.y;
+      a.plan.list[0][before.x] = Stretch{common[g], 0, first[g], 0, row_at[first[g]] + i * a.lot_rows,
+                                         min(a.lot_rows, rows[g] - i * a.lot_rows), before.y, lot_room(g)};
       before.x += 1;
-      before.y += stretch_length(common[g] / a.tile[0], a.lead[0]);
+      before.y += lot_room(g);
     }
   }
-  if (tid == 0) {
-    a.plan.totals[0] = all.y;
-    a.plan.totals[1] = all.x;
-  }
+  const longlong2 prefixes = all;
   __syncthreads();
   // ---- own parts
-  sum = longlong2{0, 0};
-  auto own = [&](int b) {
-    const SeqInfo s = sequence(c, b);
-    const int part = c.lens[b] >= 0 ? common[group[b]] : 0;
-    return Stretch{static_cast<int32_t>(s.len) - part, s.cnt, b, part >> c.page_shift, b, 1};
-  };
-  auto length = [&](const Stretch& s) {
-    return stretch_length(stretch_tiles(SeqInfo{s.len, s.cnt}, a.tile[1]), a.lead[1]);
-  };
-  for (int b = b0; b < b1; ++b) sum.x += length(own(b));
-  int64_t own_at = scan_two(sum, warps, all).x - sum.x;
+  Stretch* list = a.one_list ? a.plan.list[0] + prefixes.x : a.plan.list[1];
+  if (a.one_list) own_at += prefixes.y;
   for (int b = b0; b < b1; ++b) {
-    const Stretch s = own(b);
-    a.plan.list[1][b] = s;
-    a.plan.at[1][b] = own_at;
-    own_at += length(s);
+    list[b] = Stretch{own(b), cnt[b], b, part(b) >> c.page_shift, ~b, a.group * c.T, own_at, length(b)};
+    own_at += length(b);
     const int g = group[b];
-    a.plan.lot[b] = c.lens[b] >= 0 && common[g] > 0 ? lots[g] + (b - first[g]) / a.members : -1;
+    a.plan.places[b] = part(b) > 0 ? Place{lots[g], row_at[b] - row_at[first[g]]} : Place{-1, 0};
   }
   if (tid == 0) {
-    a.plan.totals[2] = all.x;
-    a.plan.totals[3] = B;
+    a.plan.totals[0] = prefixes.y + (a.one_list ? own_all : 0);
+    a.plan.totals[1] = prefixes.x + (a.one_list ? B : 0);
+    a.plan.totals[2] = run;
+    a.plan.totals[3] = own_all;
+    a.plan.totals[4] = B;
+    a.plan.totals[5] = (own_all + a.ctas[1] - 1) / a.ctas[1];
+    a.plan.totals[6] = a.one_list ? prefixes.x : 0;
+  }
+  // ---- the query rows of the lots: heads of a sequence one after another, its new tokens only
+  for (int r = tid; r < rows_all; r += blockDim.x) {
+    int lo = 0, hi = B - 1;  // the last sequence whose rows begin at or before r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (row_at[mid] <= r)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int j = r - row_at[lo], n = cnt[lo];
+    a.plan.rows_of[r] = lo * a.group * c.T + j / n * c.T + j % n;
   }
 }
 
@@ -169,22 +243,22 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
 // of states laid out a column quad of all rows at a time.
 struct Side {
   const Stretch* list;
-  const int64_t* at;
-  const int64_t* totals;
+  const int64_t* run;
   const float2* part_ml;   // [slots][rows]
   const float4* part_o;    // a slot's rows x d / 4 quads
   const float2* whole_ml;
   const float4* whole_o;
-  int rows, ctas, tile, lead, tile_members, tile_rows;
+  int rows, tile, lead;
   int row_step, quad_step;  // of a slot's quads
 };
 
 struct JoinArgs {
   CacheAttnArgs a;
   Side side[2];
-  const int32_t* lot;
+  const Place* places;
+  const int64_t* first_own;  // stretch of sequence 0 in side 1's list
   int64_t all_rows;
-  int32_t rows1;
+  int32_t rows1, lot_rows;
 };
 
 constexpr int kJoinThreads = 128;
@@ -217,19 +291,21 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
 #pragma unroll
     for (int h = 0; h < kQuads; ++h) o[h] = make_float4(o[h].x * f, o[h].y * f, o[h].z * f, o[h].w * f);
   };
-  if (here && w % c.T < sequence(c, b).cnt) {
+  const int cnt = here ? sequence(c, b).cnt : 0;
+  if (w % c.T < cnt) {
+    const Place place = j.places[b];
 #pragma unroll 1
     for (int z = 0; z < 2; ++z) {
       const Side& s = j.side[z];
-      const int v = z == 0 ? j.lot[b] : b;
-      if (v < 0) continue;
+      if (z == 0 && place.lot < 0) continue;
+      const int rel = place.rel + w / c.T * cnt + w % c.T;
+      const int v = z == 0 ? place.lot + rel / j.lot_rows : b + static_cast<int>(*j.first_own);
+      const int local = z == 0 ? rel % j.lot_rows : w;
       const Stretch st = s.list[v];
       const int64_t tiles = stretch_tiles(SeqInfo{st.len, st.cnt}, s.tile);
-      const int64_t run = (s.totals[0] * c.heads + s.ctas - 1) / s.ctas;
-      const int64_t u0 = s.at[v] * c.heads + head * stretch_length(tiles, s.lead);
+      const int64_t run = *s.run;
+      const int64_t u0 = st.at + head * stretch_length(tiles, s.lead);
       const int c0 = static_cast<int>(u0 / run), c1 = static_cast<int>((u0 + tiles - 1) / run);
-      const int member = b - st.b0;
-      const int local = member / s.tile_members * s.tile_rows + member % s.tile_members * j.rows1 + w;
       const bool whole = c0 == c1;
       const float2* ml_at = whole ? s.whole_ml + row : s.part_ml + local;
       const float4* o_at = whole ? s.whole_o + quad * j.all_rows + row : s.part_o + quad * s.quad_step + local * s.row_step;
@@ -326,6 +402,10 @@ cudaError_t join(const JoinArgs& j, int64_t items, cudaStream_t s) {
 // ------------------------------------------------------------ the workspace
 constexpr int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
+// A group has two sequences at least, and all its lots but one are full; the
+// smallest lots have 4 rows.
+int64_t lots_at_most(int64_t B, int64_t rows1) { return B / 2 + (B * rows1 + 3) / 4; }
+
 struct Room {
   int64_t plan, parts[2], whole[2], end;
 };
@@ -334,10 +414,11 @@ struct Room {
 Room room(int32_t B, int64_t rows1, int32_t heads, int32_t d) {
   const int64_t all = B * rows1 * heads;
   const int64_t slots = 2ll * (B * rows1 > 16 ? kTreeCtas * 256 : kFfmaCtas * 16);
-  const int64_t own = 2ll * (rows1 > 16 ? kTreeCtas * 128 : kFfmaCtas * 16);
+  const int64_t own = 2ll * kFfmaCtas * 16;  // one launch takes both above 16 rows of a sequence
   Room r;
   r.plan = 0;
-  r.parts[0] = round256(static_cast<int64_t>(B) * (2 * sizeof(Stretch) + 2 * 8 + 4) + 4 * 8 + 5 * 256);
+  r.parts[0] = round256(static_cast<int64_t>(B) * (2 * sizeof(Stretch) + sizeof(Place)) + all / heads * 4 +
+                        lots_at_most(B, rows1) * sizeof(Stretch) + 7 * 8 + 5 * 256);
   r.parts[1] = r.parts[0] + round256(slots * (d + 2) * 4);
   r.whole[0] = r.parts[1] + round256(own * (d + 2) * 4);
   r.whole[1] = r.whole[0] + round256(all * (d + 2) * 4 + 256);
@@ -355,110 +436,125 @@ int64_t cache_attention_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t he
 
 cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t* shared, ra_dtype dense,
                                           ra_dtype held, cudaStream_t s) {
-  const int64_t rows1 = head_rows(a), stacked = a.c.B * rows1;
+  const int B = a.c.B;
+  const int64_t rows1 = head_rows(a), stacked = B * rows1;
   const bool k8 = held == RA_E4M3;
-  // The kernel for a lot's rows, by all rows that there may be, and the one for
-  // a sequence's own.
+  // The kernel for lots, by all rows that there may be, and the one for a
+  // sequence's own.
   SharedKernel kernel[2];
   SharedShape shape[2];
   if (dense == RA_F32) {
-    for (int z = 0; z < 2; ++z) {
-      kernel[z] = ffma_kernel(z == 0 ? stacked : rows1, a.c.d);
-      shape[z] = ffma_shape(kernel[z]);
-    }
+    for (int z = 0; z < 2; ++z) kernel[z] = ffma_kernel(z == 0 ? stacked : rows1, a.c.d);
   } else {
     kernel[0] = stacked > 128 ? SharedKernel::kTreeTwo : stacked > kDecodeRows ? SharedKernel::kTreeOne
                                                                               : SharedKernel::kDecode;
-    kernel[1] = rows1 > kDecodeRows ? SharedKernel::kTreeOne : SharedKernel::kDecode;
-    for (int z = 0; z < 2; ++z)
-      shape[z] = kernel[z] == SharedKernel::kDecode ? decode_shape()
-                                                    : tree_shape(a.c.d, kernel[z] == SharedKernel::kTreeTwo);
+    kernel[1] = rows1 > kDecodeRows ? kernel[0] : SharedKernel::kDecode;
   }
-  const int64_t tile_members = rows1 > 0 ? shape[0].tile_rows / rows1 : 0;
-  const int64_t members = tile_members * (shape[0].rows / shape[0].tile_rows);
+  for (int z = 0; z < 2; ++z)
+    shape[z] = kernel[z] == SharedKernel::kDecode                                            ? decode_shape()
+               : kernel[z] == SharedKernel::kTreeOne || kernel[z] == SharedKernel::kTreeTwo
+                   ? tree_shape(a.c.d, kernel[z] == SharedKernel::kTreeTwo)
+                   : ffma_shape(kernel[z]);
   // Nothing to gain where a unit has no room for a second sequence's rows.
-  if (a.c.B < 2 || a.c.B > kPlanSequences || members < 2 || rows1 > shape[1].rows)
+  if (B < 2 || B > kPlanSequences || 2 * rows1 > shape[0].rows || rows1 > shape[1].rows)
     return launch_cache_attention(a, dense, held, s);
 
-  const int B = a.c.B;
   const Room r = room(B, rows1, a.c.heads, a.c.d);
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.ws);
   PlanArgs pl;
   pl.c = a.c;
   pl.shared = shared;
+  pl.one_list = kernel[0] == kernel[1];
+  pl.lot_rows = shape[0].rows;
+  pl.group = a.Hq / a.c.heads;
   uint8_t* at = ws + r.plan;
   auto take = [&](int64_t bytes) {
     uint8_t* x = at;
     at += round256(bytes);
     return x;
   };
-  pl.plan.totals = reinterpret_cast<int64_t*>(take(4 * 8));
+  pl.plan.totals = reinterpret_cast<int64_t*>(take(7 * 8));
   for (int z = 0; z < 2; ++z) {
-    pl.plan.list[z] = reinterpret_cast<Stretch*>(take(B * sizeof(Stretch)));
-    pl.plan.at[z] = reinterpret_cast<int64_t*>(take(B * 8));
+    const int64_t n = z == 0 ? B + lots_at_most(B, rows1) : B;
+    pl.plan.list[z] = reinterpret_cast<Stretch*>(take(n * sizeof(Stretch)));
     pl.tile[z] = shape[z].tile;
     pl.lead[z] = kLeadKeys / shape[z].tile;
+    pl.ctas[z] = shape[z].ctas;
   }
-  pl.plan.lot = reinterpret_cast<int32_t*>(take(B * 4));
+  pl.plan.places = reinterpret_cast<Place*>(take(B * sizeof(Place)));
+  pl.plan.rows_of = reinterpret_cast<int32_t*>(take(stacked * 4));
   const int page = 1 << a.c.page_shift;
   pl.granule = page > kTile ? page : kTile;
-  pl.members = static_cast<int>(members);
-  const int threads = B < kPlanThreads ? (B + 31) / 32 * 32 : kPlanThreads;  // fewer warps are quicker
-  shared_plan_kernel<<<1, threads, B * 20 + 16, s>>>(pl);
-  cudaError_t e = cudaGetLastError();
+  // fewer warps are quicker, where they do not have many rows each
+  const int64_t want = B > stacked / 8 ? B : stacked / 8;
+  const int threads = want < kPlanThreads ? static_cast<int>((want + 31) / 32 * 32) : kPlanThreads;
+  const int smem = B * 32 + 16;
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kPlanSequences * 32 + 16);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  shared_plan_kernel<<<1, threads, smem, s>>>(pl);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
   JoinArgs j;
   j.a = a;
-  j.lot = pl.plan.lot;
+  j.places = pl.plan.places;
+  j.first_own = pl.plan.totals + 6;
   j.all_rows = static_cast<int64_t>(B) * a.c.heads * rows1;
   j.rows1 = static_cast<int32_t>(rows1);
+  j.lot_rows = pl.lot_rows;
+  SharedAttnArgs g;
+  static_cast<CacheAttnArgs&>(g) = a;
+  static_cast<PagedArgs&>(g.stretches) = a.c;
+  g.rows_of = pl.plan.rows_of;
+  g.all_rows = j.all_rows;
+  g.rows1 = j.rows1;
   for (int z = 0; z < 2; ++z) {
-    SharedAttnArgs g;
-    static_cast<CacheAttnArgs&>(g) = a;
-    g.ws = reinterpret_cast<float*>(ws + r.parts[z]);
-    static_cast<PagedArgs&>(g.stretches) = a.c;
-    g.stretches.list = pl.plan.list[z];
-    g.stretches.at = pl.plan.at[z];
-    g.stretches.totals = pl.plan.totals + 2 * z;
-    g.stretches.lead = pl.lead[z];
-    g.whole_o = reinterpret_cast<float*>(ws + r.whole[z]);
-    g.whole_ml = g.whole_o + round256(j.all_rows * a.c.d * 4) / 4;
-    g.all_rows = j.all_rows;
-    g.rows1 = j.rows1;
-    g.tile_members = static_cast<int32_t>(z == 0 ? tile_members : 1);
+    g.whole_o[z] = reinterpret_cast<float*>(ws + r.whole[z]);
+    g.whole_ml[z] = g.whole_o[z] + round256(j.all_rows * a.c.d * 4) / 4;
+  }
+  for (int z = 0; z < 2; ++z) {
+    const int l = pl.one_list ? 0 : z;  // the list, and the launch, of this side
+    g.ws = reinterpret_cast<float*>(ws + r.parts[l]);
+    g.stretches.list = pl.plan.list[l];
+    g.stretches.totals = pl.plan.totals + 3 * l;
+    g.stretches.lead = pl.lead[l];
     AttnPlan p;
     p.div = Division{a.c.heads, shape[z].tile, shape[z].ctas};
     p.rows = shape[z].rows;
     p.row_tiles = 1;
-    if (kernel[z] == SharedKernel::kDecode)
-      e = launch_shared_decode(g, p, k8, s);
-    else if (kernel[z] == SharedKernel::kTreeOne || kernel[z] == SharedKernel::kTreeTwo)
-      e = launch_shared_tree(g, p, k8, s);
-    else
-      e = launch_shared_ffma(g, p, kernel[z], k8, s);
-    if (e != cudaSuccess) return e;
-    const float* parts = g.ws;
+    if (z == l) {
+      if (kernel[z] == SharedKernel::kDecode)
+        e = launch_shared_decode(g, p, k8, s);
+      else if (kernel[z] == SharedKernel::kTreeOne || kernel[z] == SharedKernel::kTreeTwo)
+        e = launch_shared_tree(g, p, k8, s);
+      else
+        e = launch_shared_ffma(g, p, kernel[z], k8, s);
+      if (e != cudaSuccess) return e;
+    }
     const int64_t slots = 2ll * p.div.ctas;
     j.side[z] = Side{g.stretches.list,
-                     g.stretches.at,
-                     g.stretches.totals,
-                     reinterpret_cast<const float2*>(parts),
-                     reinterpret_cast<const float4*>(parts + slots * p.rows * 2),
-                     reinterpret_cast<const float2*>(g.whole_ml),
-                     reinterpret_cast<const float4*>(g.whole_o),
+                     g.stretches.totals + 2,
+                     reinterpret_cast<const float2*>(g.ws),
+                     reinterpret_cast<const float4*>(g.ws + slots * p.rows * 2),
+                     reinterpret_cast<const float2*>(g.whole_ml[z]),
+                     reinterpret_cast<const float4*>(g.whole_o[z]),
                      p.rows,
-                     p.div.ctas,
                      p.div.tile,
                      pl.lead[z],
-                     g.tile_members,
-                     shape[z].tile_rows,
                      shape[z].quads ? 1 : a.c.d / 4,
                      shape[z].quads ? p.rows : 1};
   }
   // Four warps to a row's parts where those of a single group may be many.
   const int64_t items = (j.all_rows + 31) / 32 * (a.c.d / 4 / kQuads);
-  const int64_t units = a.c.heads * ((B + members - 1) / members);
+  const int64_t units = a.c.heads * ((stacked + pl.lot_rows - 1) / pl.lot_rows);
   const bool many = shape[0].ctas > 8 * units;
   if (dense == RA_BF16) return many ? join<__nv_bfloat16, 4>(j, items, s) : join<__nv_bfloat16, 1>(j, items, s);
   return many ? join<float, 4>(j, items, s) : join<float, 1>(j, items, s);

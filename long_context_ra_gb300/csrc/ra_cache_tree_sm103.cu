@@ -371,7 +371,7 @@ __device__ __forceinline__ bool second_tile(const CacheAttnArgs& a, const AttnPl
   return Unit(a, p, u, rows).r0 + 128 < rows;
 }
 __device__ __forceinline__ bool second_tile(const SharedAttnArgs& a, const AttnPlan&, const StretchWalk& u, int64_t) {
-  return a.stretches.list[u.b].members > a.tile_members;
+  return a.stretches.list[u.b].rows > 128;
 }
 
 template <bool k8, int D, bool kTwo, typename A>
@@ -704,7 +704,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     // ================= MMA issuer, query loader (and an idle warp) =================
     setmaxnreg_inc<kRegsMain>();
-    if (warp == kQueryWarp) {
+    if (kShared && warp == kQueryWarp) {
+      // Rows of several sequences, four to a lane and load; what is left of a tile
+      // repeats the last one: rows that nobody reads.
+      if constexpr (kShared) {
+        const uint32_t bar = k8 ? bars.q_raw() : bars.q_full();
+        Walk w;
+        w.start_found(c, p.div, sh, run);
+        uint32_t ord = 0;
+        for (; !w.done(); ++ord, w.next(c, p.div)) {
+          const Stretch s = c.list[w.b];
+          const int tiles = kTwo && s.rows > 128 ? 2 : 1;
+          int32_t y[2][4];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int at = MemberRow::row(a, s, min(x / 4 * 128 + lane * 4 + x % 4, s.rows - 1));
+            y[x / 4][x % 4] = (at / a.rows1 * c.heads + w.unit) * a.rows1 + at % a.rows1;
+          }
+          if (!wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar, tiles * L::kQTile);
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 2 * (D / 64); ++x)
+            if (x / (D / 64) < tiles)
+              tma_gather4(base + L::kQ0 + x * L::kQBox + lane * 512, &tq, x % (D / 64) * 64, y[x / (D / 64)], bar);
+        }
+        if (ord > 0) wait_drain(bar, (ord - 1u) & 1u);  // lands before the CTA goes, in any case
+      }
+    } else if (warp == kQueryWarp) {
       // Rows behind the head's belong to other heads or are zeros: rows of the
       // product that nobody reads.
       const uint32_t bar = k8 ? bars.q_raw() : bars.q_full();
@@ -714,24 +741,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; !w.done(); ++ord, w.next(c, p.div)) {
         if (!wait_warp(bars.q_empty(), (ord & 1u) ^ 1u, ab)) break;
         if (lane == 0) {
-          const bool two = kTwo && second_tile(a, p, w, rows);
-          if constexpr (kShared) {
-            // all rows of a tile's members; rows of others, and what is left of the tile, nobody reads
-            const int b0 = c.list[w.b].b0;
-            const uint32_t box = 128u * a.rows1 * a.tile_members;
-            mbar_arrive_expect_tx(bar, (two ? 2 : 1) * (D / 64) * box);
+          const Unit un(a, p, w, rows);
+          const bool two = kTwo && un.r0 + 128 < rows;
+          mbar_arrive_expect_tx(bar, (two ? 2 : 1) * L::kQTile);
 #pragma unroll 1
-            for (int x = 0; x < (two ? 2 : 1) * (D / 64); ++x)
-              tma_load_4d(base + L::kQ0 + x * L::kQBox, &tq, x % (D / 64) * 64, 0, w.unit,
-                          b0 + x / (D / 64) * a.tile_members, bar);
-          } else {
-            const Unit un(a, p, w, rows);
-            mbar_arrive_expect_tx(bar, (two ? 2 : 1) * L::kQTile);
-#pragma unroll 1
-            for (int x = 0; x < (two ? 2 : 1) * (D / 64); ++x)
-              tma_load_2d(base + L::kQ0 + x * L::kQBox, &tq, x % (D / 64) * 64,
-                          static_cast<int32_t>(un.q0) + x / (D / 64) * 128, bar);
-          }
+          for (int x = 0; x < (two ? 2 : 1) * (D / 64); ++x)
+            tma_load_2d(base + L::kQ0 + x * L::kQBox, &tq, x % (D / 64) * 64,
+                        static_cast<int32_t>(un.q0) + x / (D / 64) * 128, bar);
         }
         __syncwarp();
       }
@@ -893,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool exists;
       const bool active = kTwo ? t == 0 || second_tile(a, p, u, rows) : t == 0 || n > 1;
       if constexpr (kShared) {
-        const MemberRow r(a, c.list[u.b], u.unit, kTwo ? t : 0, row);
+        const MemberRow r(a, c.list[u.b], u.unit, (kTwo ? t * 128 : 0) + row);
         tok = r.t;
         mask_b = r.b;
         q_row = r.q;
@@ -1132,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kShared) {
               if (whole) {
                 pitch = a.all_rows;
-                dst = reinterpret_cast<float4*>(a.whole_o) + x / 4 * pitch + q_row;
+                dst = reinterpret_cast<float4*>(a.whole_o[c.list[u.b].first < 0]) + x / 4 * pitch + q_row;
               }
             }
 #pragma unroll
@@ -1142,7 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x == 0) {
               float* ml = slot_ml(a, p, slot) + 2 * local;
               if constexpr (kShared)
-                if (whole) ml = a.whole_ml + 2 * q_row;
+                if (whole) ml = a.whole_ml[c.list[u.b].first < 0] + 2 * q_row;
               *reinterpret_cast<float2*>(ml) = make_float2(m_ref, l);
             }
           }
@@ -1187,7 +1203,7 @@ cudaError_t launch_t(const A& a, const AttnPlan& plan, cudaStream_t s) {
   AttnPlan p = plan;
   p.div.tile = L::kKeys;
   if constexpr (IsShared<A>::value) {
-    if (!encode_members(&tq, a.q, a.c.B, a.c.heads, a.rows1, D, a.tile_members)) return cudaErrorUnknown;
+    if (!encode_single_rows(&tq, a.q, static_cast<int64_t>(a.c.B) * a.Hq * a.c.T, D)) return cudaErrorUnknown;
     return launch_behind(cache_tree_kernel<k8, D, kTwo, A>, dim3(p.div.ctas), kThreads, L::kSmem, s, a, p, tk, tv,
                          tq);
   } else {
@@ -1222,7 +1238,7 @@ cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s) {
 }
 
 SharedShape tree_shape(int d, bool two) {
-  return SharedShape{two || d == 64 ? 128 : 64, two ? 256 : 128, 128, kTreeCtas, true};
+  return SharedShape{two || d == 64 ? 128 : 64, two ? 256 : 128, kTreeCtas, true};
 }
 
 cudaError_t launch_shared_tree(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s) {

@@ -17,20 +17,22 @@ __device__ __forceinline__ void flag_page(int* status) { atomicCAS(status, 0, kS
 
 // A stretch of keys that some rows of queries see, as the attention over
 // shared prefixes divides a batch: the positions from column `skip` of row
-// `row` of the table on, seen by `members` sequences from b0 on.  Of a prefix
-// len is its length and cnt 0; of a sequence's own part they are the tokens and
-// new tokens behind the prefix.
+// `row` of the table on.  Of a prefix len is its length and cnt 0, and the query
+// rows that see it are entries first .. first + rows - 1 of a list; of a
+// sequence's own part they are the tokens and new tokens behind the prefix, and
+// the rows are those of sequence ~first.
 struct Stretch {
   int32_t len, cnt;
   int32_t row, skip;
-  int32_t b0, members;
+  int32_t first, rows;
+  int64_t at;      // of its units in the division
+  int64_t length;  // that they take in it
 };
 
 // The stretches of one launch, in the place of a batch's sequences.
 struct SharedPaged : PagedArgs {
   const Stretch* list;
-  const int64_t* at;      // length (of one unit) before each stretch
-  const int64_t* totals;  // length of all; the number of stretches
+  const int64_t* totals;  // length of all; the number of stretches; the length of a CTA's run
   int32_t lead;           // tiles that a unit's start and end are reckoned as
 };
 
@@ -331,21 +333,20 @@ __device__ __forceinline__ int64_t division_start(const PagedArgs& c, const Divi
 // the last stretch that begins at or before the run.
 __device__ __forceinline__ int64_t division_start(const SharedPaged& c, const Division& v, int cta,
                                                   DivisionShared& sh) {
-  const int64_t all = c.totals[0] * v.units;
+  const int64_t all = c.totals[0], run = c.totals[2];
   const int n = static_cast<int>(c.totals[1]);
-  const int64_t run = run_length(v, all);
   const int64_t begin = cta * run;
   if (begin < all) {
     const int lane = threadIdx.x % 32;
     int found = 0;
     for (int i = 0; i < n; i += 32) {
-      const uint32_t here = __ballot_sync(0xffffffffu, i + lane < n && c.at[i + lane] * v.units <= begin);
+      const uint32_t here = __ballot_sync(0xffffffffu, i + lane < n && c.list[i + lane].at <= begin);
       if (here == 0u) break;
       found = i + 31 - __clz(here);
     }
     if (lane == 0) {  // of every warp: all write the same
       sh.b = found;
-      sh.off = begin - c.at[found] * v.units;
+      sh.off = begin - c.list[found].at;
       sh.run = run;
     }
   }
@@ -428,9 +429,10 @@ struct UnitWalk {
 };
 
 // The same over stretches: off and left count lengths, of which `lead` at a
-// unit's end are no tiles.  A part without a tile is passed over.
+// unit's end, and what is left of a stretch's length behind its units, are no
+// tiles.  A part without a tile is passed over.
 struct StretchWalk {
-  int64_t left, off, step, span;
+  int64_t left, off, step, length;
   int b;
   SeqInfo seq;
   int64_t tiles, first, last;
@@ -450,30 +452,28 @@ struct StretchWalk {
     while (left > 0) {
       seq = sequence(c, b);
       tiles = stretch_tiles(seq, v.tile);
-      span = stretch_length(tiles, c.lead);
-      if (span == 0) {
+      length = c.list[b].length;
+      if (off >= length) {
         ++b;
+        off = 0;
         continue;
       }
+      const int64_t span = stretch_length(tiles, c.lead);
       unit = static_cast<int>(off / span);
       const int64_t from = off - unit * span;
-      step = min(span - from, left);
+      step = min((unit < v.units ? span * (unit + 1) : length) - off, left);
       first = min(from, tiles);
-      last = min(from + step, tiles);
+      last = unit < v.units ? min(from + step, tiles) : first;
       if (first < last) return;
-      pass(v);
+      pass();
     }
   }
-  __device__ void pass(const Division& v) {
+  __device__ void pass() {
     left -= step;
     off += step;
-    if (off == span * v.units) {
-      ++b;
-      off = 0;
-    }
   }
   __device__ void next(const SharedPaged& c, const Division& v) {
-    pass(v);
+    pass();
     settle(c, v);
   }
   __device__ bool whole() const { return first == 0 && last == tiles; }

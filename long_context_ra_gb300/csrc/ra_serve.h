@@ -66,9 +66,8 @@ struct PagedArgs {
 bool encode_pages(CUtensorMap* map, const void* ptr, const PagedArgs& c, int box_rows, bool bytes);
 // TMA view of dense bf16 rows [rows, d] with boxes of 128 rows of 64 columns, swizzled alike.
 bool encode_rows(CUtensorMap* map, const void* ptr, int64_t rows, int d);
-// TMA view of bf16 queries [B, heads, rows, d] with boxes of all rows of one head of `members`
-// sequences, 64 columns, swizzled alike.
-bool encode_members(CUtensorMap* map, const void* ptr, int B, int heads, int rows, int d, int members);
+// The same with boxes of one row, for loads that gather rows.
+bool encode_single_rows(CUtensorMap* map, const void* ptr, int64_t rows, int d);
 
 struct CacheCopyArgs {
   PagedArgs c;
