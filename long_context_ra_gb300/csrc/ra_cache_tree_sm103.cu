@@ -86,6 +86,11 @@ constexpr int kLoadWarp = 9;
 constexpr int kHandWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;
+// Stretches: how far above the largest score the reference is put when it moves.
+// Any reference gives the same l and o; one that moves costs the tile's softmax
+// a pass over O, and the largest of some 10^4 scores is further above that of a
+// first tile than kRescaleLog2 where key rows are of unlike length.
+constexpr float kHeadroom = 16.0f;
 
 template <bool k8, int D, bool kTwo>
 struct Layout {
@@ -977,8 +982,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   v[e] = fmax3(v[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + 8 + e]));
               mx = fmax3(mx, fmax3(v[0], v[1], v[2]), fmax3(fmax3(v[3], v[4], v[5]), v[6], v[7]));
             }
-            const float m_new = mx * a.scale_log2;
+            float m_new = mx * a.scale_log2;
             const bool need = m_new > m_ref + kRescaleLog2;
+            if (kShared) m_new += kHeadroom;
             if (__any_sync(0xffffffffu, need)) {
               const float alpha = need ? ex2(m_ref - m_new) : 1.f;
               if (o_valid) {
