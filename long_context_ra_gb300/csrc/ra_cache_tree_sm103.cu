@@ -244,7 +244,8 @@ __device__ __forceinline__ void widen16(const uint4& w4, uint32_t e, uint32_t (&
 }
 
 template <int D, int kKeys>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
+__device__ __forceinline__ void issue_qk(bool leader, uint32_t d_tmem, uint64_t dq, uint64_t dk) {
+  if (!leader) return;
   constexpr uint32_t idesc = idesc_bf16_f32(kBM, kKeys, false);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
@@ -253,8 +254,9 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t dq, uint64_t 
 }
 
 template <int D, int kKeys>
-__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t dv,
+__device__ __forceinline__ void issue_pv(bool leader, uint32_t d_tmem, uint32_t p_tmem, uint64_t dv,
                                          uint32_t accumulate) {
+  if (!leader) return;
   constexpr uint32_t idesc = idesc_bf16_f32(kBM, D, true);
   mma_bf16_ts(d_tmem, p_tmem, dv, idesc, accumulate);
 #pragma unroll
@@ -757,7 +759,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (ord > 0) wait_drain(bar, (ord - 1u) & 1u);  // lands before the CTA goes, in any case
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
+      // The whole warp walks along; one lane issues.
+      const bool leader = elect_one();
+      auto commit = [&](uint32_t bar) {
+        if (leader) mma_commit(bar);
+      };
       const uint64_t dQ0 = desc_sw128(base + L::kQ0, 16, 1024);
       const uint64_t dQ1 = desc_sw128(base + L::kQ1, 16, 1024);
       const uint64_t dK = desc_sw128(base + L::kKV, 16, 1024);
@@ -769,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk u;
       // wait for the next stage of the ring: its index, or -1
       auto take = [&]() {
-        if (!wait1(bars.kv_full(r.stage), r.phase, ab)) return -1;
+        if (!wait_warp(bars.kv_full(r.stage), r.phase, ab)) return -1;
         const int s = r.stage;
         r.step<kS>();
         tc_fence_after();
@@ -777,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (u.start_found(c, p.div, sh, run); ok && !u.done(); u.next(c, p.div), ++unit) {
         const int n = static_cast<int>(u.last - u.first);
-        ok = wait1(bars.q_full(), unit & 1u, ab);
+        ok = wait_warp(bars.q_full(), unit & 1u, ab);
         if (!ok) break;
         any = true;
         int sk = take();
@@ -788,23 +795,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kTwo) {
           const bool two = second_tile(a, p, u, rows);
           uint64_t dk = dK + desc_step(sk * L::kTile);
-          issue_qk<D, kKeys>(tS0, dQ0, dk);
-          mma_commit(bars.s_full(0));
+          issue_qk<D, kKeys>(leader, tS0, dQ0, dk);
+          commit(bars.s_full(0));
           if (two) {
-            issue_qk<D, kKeys>(tS1, dQ1, dk);
-            mma_commit(bars.s_full(1));
+            issue_qk<D, kKeys>(leader, tS1, dQ1, dk);
+            commit(bars.s_full(1));
           }
-          mma_commit(bars.kv_empty(sk));
-          if (n == 1) mma_commit(bars.q_empty());
+          commit(bars.kv_empty(sk));
+          if (n == 1) commit(bars.q_empty());
           for (int it = 0; it < n; ++it) {
             const int sv = take();
-            if (sv < 0 || !wait1(bars.p_full(0), np0++ & 1u, ab)) {
+            if (sv < 0 || !wait_warp(bars.p_full(0), np0++ & 1u, ab)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint64_t dv = dV + desc_step(sv * L::kTile);
-            issue_pv<D, kKeys>(tO0, tS0, dv, it > 0);
+            issue_pv<D, kKeys>(leader, tO0, tS0, dv, it > 0);
             const bool more = it + 1 < n;
             if (more) {
               sk = take();
@@ -813,77 +820,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               dk = dK + desc_step(sk * L::kTile);
-              issue_qk<D, kKeys>(tS0, dQ0, dk);
-              mma_commit(bars.s_full(0));
+              issue_qk<D, kKeys>(leader, tS0, dQ0, dk);
+              commit(bars.s_full(0));
             }
             if (two) {
-              if (!wait1(bars.p_full(1), np1++ & 1u, ab)) {
+              if (!wait_warp(bars.p_full(1), np1++ & 1u, ab)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              issue_pv<D, kKeys>(tO1, tS1, dv, it > 0);
+              issue_pv<D, kKeys>(leader, tO1, tS1, dv, it > 0);
             }
-            mma_commit(bars.kv_empty(sv));
+            commit(bars.kv_empty(sv));
             if (more) {
               if (two) {
-                issue_qk<D, kKeys>(tS1, dQ1, dk);
-                mma_commit(bars.s_full(1));
+                issue_qk<D, kKeys>(leader, tS1, dQ1, dk);
+                commit(bars.s_full(1));
               }
-              mma_commit(bars.kv_empty(sk));
-              if (it + 2 == n) mma_commit(bars.q_empty());  // the last scores
+              commit(bars.kv_empty(sk));
+              if (it + 2 == n) commit(bars.q_empty());  // the last scores
             }
           }
           if (ok) {
-            mma_commit(bars.o_full(0));
-            if (two) mma_commit(bars.o_full(1));
+            commit(bars.o_full(0));
+            if (two) commit(bars.o_full(1));
           }
         } else {
-          issue_qk<D, kKeys>(tS0, dQ0, dK + desc_step(sk * L::kTile));
-          mma_commit(bars.s_full(0));
-          mma_commit(bars.kv_empty(sk));
+          issue_qk<D, kKeys>(leader, tS0, dQ0, dK + desc_step(sk * L::kTile));
+          commit(bars.s_full(0));
+          commit(bars.kv_empty(sk));
           if (n > 1) {
             sk = take();
             if (sk < 0) {
               ok = false;
               break;
             }
-            issue_qk<D, kKeys>(tS1, dQ0, dK + desc_step(sk * L::kTile));
-            mma_commit(bars.s_full(1));
-            mma_commit(bars.kv_empty(sk));
+            issue_qk<D, kKeys>(leader, tS1, dQ0, dK + desc_step(sk * L::kTile));
+            commit(bars.s_full(1));
+            commit(bars.kv_empty(sk));
           }
-          if (n <= 2) mma_commit(bars.q_empty());
+          if (n <= 2) commit(bars.q_empty());
           for (int it = 0; it < n; ++it) {
             const int t = it & 1;
             const int sv = take();
-            if (sv < 0 || !wait1(bars.p_full(t), (t ? np1++ : np0++) & 1u, ab)) {
+            if (sv < 0 || !wait_warp(bars.p_full(t), (t ? np1++ : np0++) & 1u, ab)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint32_t tS = t ? tS1 : tS0;
-            issue_pv<D, kKeys>(t ? tO1 : tO0, tS, dV + desc_step(sv * L::kTile), it > 1);
-            mma_commit(bars.kv_empty(sv));
+            issue_pv<D, kKeys>(leader, t ? tO1 : tO0, tS, dV + desc_step(sv * L::kTile), it > 1);
+            commit(bars.kv_empty(sv));
             if (it + 2 < n) {
               sk = take();
               if (sk < 0) {
                 ok = false;
                 break;
               }
-              issue_qk<D, kKeys>(tS, dQ0, dK + desc_step(sk * L::kTile));
-              mma_commit(bars.s_full(t));
-              mma_commit(bars.kv_empty(sk));
-              if (it + 3 == n) mma_commit(bars.q_empty());  // the last scores
+              issue_qk<D, kKeys>(leader, tS, dQ0, dK + desc_step(sk * L::kTile));
+              commit(bars.s_full(t));
+              commit(bars.kv_empty(sk));
+              if (it + 3 == n) commit(bars.q_empty());  // the last scores
             }
           }
           if (ok) {
-            mma_commit(bars.o_full(0));
-            if (n > 1) mma_commit(bars.o_full(1));
+            commit(bars.o_full(0));
+            if (n > 1) commit(bars.o_full(1));
           }
         }
       }
       if (!ok && any) {
-        mma_commit(bars.drain());
+        commit(bars.drain());
         wait_drain(bars.drain(), 0);
       }
     }
