@@ -126,9 +126,19 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     uint64_t o[kRW][kPairs];  // columns 2 lane, 2 lane + 1 of every 64
     int t[kRW];
     // a row's sequence and the new tokens that it may see (stretches: per row)
-    int mask_b[kShared ? kRW : 1], cnt[kShared ? kRW : 1];
-    auto seq_of = [&](int r) { return SeqInfo{u.seq.len, kShared ? cnt[r % (kShared ? kRW : 1)] : u.seq.cnt}; };
-    auto b_of = [&](int r) { return kShared ? mask_b[r % (kShared ? kRW : 1)] : u.b; };
+    [[maybe_unused]] int mask_b[kRW], cnt[kRW];
+    auto seq_of = [&](int r) {
+      if constexpr (kShared)
+        return SeqInfo{u.seq.len, cnt[r]};
+      else
+        return u.seq;
+    };
+    auto b_of = [&](int r) {
+      if constexpr (kShared)
+        return mask_b[r];
+      else
+        return u.b;
+    };
 #pragma unroll
     for (int r = 0; r < kRW; ++r) {
       m[r] = -INFINITY;
@@ -763,7 +773,7 @@ struct FfmaSet {
 };
 template <typename F>
 SharedShape shape_of(int ctas) {
-  return SharedShape{F::kTile, F::kRows, ctas, false};
+  return SharedShape{F::kTile, F::kRows, ctas, 512 / F::kTile, false};
 }
 
 template <typename H, int NC, typename A>

@@ -130,11 +130,12 @@ constexpr int kTreeCtas = 152;  // one per SM
 cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s);
 cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s);
 
-// How a kernel takes stretches: key tile, rows of a unit, CTAs, and whether its
-// parts' o is [d / 4][rows][4].
+// How a kernel takes stretches: key tile, rows of a unit, CTAs, the tiles that
+// take a CTA as long as a unit's start and end, and whether its parts' o is
+// [d / 4][rows][4].
 enum class SharedKernel { kDecode, kTreeOne, kTreeTwo, kFfma4, kFfma8, kFfma16, kFfma64 };
 struct SharedShape {
-  int tile, rows, ctas;
+  int tile, rows, ctas, lead;
   bool quads;
 };
 SharedShape decode_shape();

@@ -657,7 +657,7 @@ cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s)
   return by_type(a, p, k8, s);
 }
 
-SharedShape decode_shape() { return SharedShape{kTile, kRows, kDecodeCtas, false}; }
+SharedShape decode_shape() { return SharedShape{kTile, kRows, kDecodeCtas, 1024 / kTile, false}; }
 
 cudaError_t launch_shared_decode(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s) {
   return by_type(a, p, k8, s);

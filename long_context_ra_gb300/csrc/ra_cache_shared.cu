@@ -27,7 +27,6 @@ constexpr int kPlanThreads = 1024;    // at most
 constexpr int kPlanSequences = 2048;  // 32 bytes of shared memory each
 constexpr int kTile = 128;            // a multiple of every kernel's key tile
 constexpr int kRuns = 9;              // lengths of a run that are tried
-constexpr int kLeadKeys = 512;        // keys that take a CTA as long as a unit's start and end
 
 // Where a sequence's rows are among the lots: row r of its live ones is row
 // (rel + r) of lot `lot` on (-1: its group has nothing in common).
@@ -47,7 +46,7 @@ struct PlanArgs {
   PagedArgs c;
   const int32_t* shared;
   Plan plan;
-  int tile[2];   // keys per tile of the two kinds of stretches
+  int tile_shift[2];  // log2 of the keys per tile of the two kinds of stretches
   int lead[2];
   int ctas[2];
   int granule;   // a common part is a multiple of it
@@ -149,11 +148,14 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   __syncthreads();
   // ---- lengths: of a lot's units, and of a sequence's own
   auto lots_of = [&](int g) { return common[g] > 0 ? (rows[g] + a.lot_rows - 1) / a.lot_rows : 0; };
-  auto lot_length = [&](int g) { return c.heads * stretch_length(common[g] / a.tile[0], a.lead[0]); };
+  auto lot_length = [&](int g) {
+    return c.heads * stretch_length(common[g] >> a.tile_shift[0], a.lead[0]);
+  };
   auto part = [&](int b) { return cnt[b] > 0 ? common[group[b]] : 0; };
   auto own = [&](int b) { return cnt[b] > 0 ? len[b] - part(b) : 0; };  // without new tokens: nothing
   auto length = [&](int b) {
-    return c.heads * stretch_length(stretch_tiles(SeqInfo{own(b), cnt[b]}, a.tile[1]), a.lead[1]);
+    const int64_t keys = static_cast<int64_t>(own(b)) + cnt[b];
+    return c.heads * stretch_length((keys + (1 << a.tile_shift[1]) - 1) >> a.tile_shift[1], a.lead[1]);
   };
   sum = longlong2{0, 0};
   for (int g = b0; g < g1; ++g) sum.x += lots_of(g) * lot_length(g);
@@ -166,29 +168,34 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   // 8 heads: 2.5 GB from memory without).  The smallest run, up to an eighth
   // above the even one, with which every lot can take whole runs.
   const int64_t even = (total + a.ctas[0] - 1) / a.ctas[0];
+  const uint32_t even32 = static_cast<uint32_t>(even);
+  auto candidate = [&](int i) { return even32 + even32 / (8 * (kRuns - 1)) * i; };
+  const bool small = total < (int64_t{1} << 31);  // the products below stay in 32 bits
   for (int g = b0; g < g1; ++g) {
     const int n = lots_of(g);
     if (n > 1) again = 1;
-    if (n > 0)
-      for (int i = 0; i < kRuns; ++i) {
-        const int64_t run = even + even * i / (8 * (kRuns - 1));
-        atomicAdd(&runs[i], static_cast<int>(n * ((lot_length(g) + run - 1) / run)));
-      }
+    if (n > 0 && small)
+      for (int i = 0; i < kRuns; ++i)
+        atomicAdd(&runs[i], n * static_cast<int>((static_cast<uint32_t>(lot_length(g)) + candidate(i) - 1) / candidate(i)));
   }
   __syncthreads();
   int64_t run = even;
   bool aligned = false;
-  for (int i = 0; i < kRuns && again && !aligned; ++i) {
-    const int64_t r = even + even * i / (8 * (kRuns - 1));
-    aligned = runs[i] + (a.one_list ? (own_all + r - 1) / r : 0) <= a.ctas[0];
+  for (int i = 0; i < kRuns && again && small && !aligned; ++i) {
+    const uint32_t r = candidate(i);
+    aligned = runs[i] + (a.one_list ? (static_cast<uint32_t>(own_all) + r - 1) / r : 0u) <= static_cast<uint32_t>(a.ctas[0]);
     if (aligned) run = r;
   }
   // ---- lots
-  auto lot_room = [&](int g) { return aligned ? (lot_length(g) + run - 1) / run * run : lot_length(g); };
+  auto lot_room = [&](int g) {
+    const int64_t n = lot_length(g);
+    return aligned ? (static_cast<uint32_t>(n + run - 1) / static_cast<uint32_t>(run)) * run : n;
+  };
   sum = longlong2{0, 0};
   for (int g = b0; g < g1; ++g) {
-    sum.x += lots_of(g);
-    sum.y += lots_of(g) * lot_room(g);
+    const int n = lots_of(g);
+    sum.x += n;
+    if (n > 0) sum.y += n * lot_room(g);
   }
   longlong2 before = scan_two(sum, warps, all);
   before.x -= sum.x;
@@ -196,11 +203,12 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   for (int g = b0; g < g1; ++g) {
     const int n = lots_of(g);
     lots[g] = static_cast<int>(before.x);
+    const int64_t room = n > 0 ? lot_room(g) : 0;
     for (int i = 0; i < n; ++i) {
       a.plan.list[0][before.x] = Stretch{common[g], 0, first[g], 0, row_at[first[g]] + i * a.lot_rows,
-                                         min(a.lot_rows, rows[g] - i * a.lot_rows), before.y, lot_room(g)};
+                                         min(a.lot_rows, rows[g] - i * a.lot_rows), before.y, room};
       before.x += 1;
-      before.y += lot_room(g);
+      before.y += room;
     }
   }
   const longlong2 prefixes = all;
@@ -477,8 +485,9 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
   for (int z = 0; z < 2; ++z) {
     const int64_t n = z == 0 ? B + lots_at_most(B, rows1) : B;
     pl.plan.list[z] = reinterpret_cast<Stretch*>(take(n * sizeof(Stretch)));
-    pl.tile[z] = shape[z].tile;
-    pl.lead[z] = kLeadKeys / shape[z].tile;
+    pl.tile_shift[z] = 0;
+    while ((1 << pl.tile_shift[z]) < shape[z].tile) ++pl.tile_shift[z];
+    pl.lead[z] = shape[z].lead;
     pl.ctas[z] = shape[z].ctas;
   }
   pl.plan.places = reinterpret_cast<Place*>(take(B * sizeof(Place)));
@@ -486,7 +495,7 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
   const int page = 1 << a.c.page_shift;
   pl.granule = page > kTile ? page : kTile;
   // fewer warps are quicker, where they do not have many rows each
-  const int64_t want = B > stacked / 8 ? B : stacked / 8;
+  const int64_t want = B > stacked / 4 ? B : stacked / 4;
   const int threads = want < kPlanThreads ? static_cast<int>((want + 31) / 32 * 32) : kPlanThreads;
   const int smem = B * 32 + 16;
   static thread_local int configured_device = -1;

@@ -74,18 +74,23 @@ namespace {
 using namespace ptx;
 using namespace sm103;
 
-constexpr int kThreads = 640;
-constexpr uint32_t kRegs = 96;        // per thread at launch
-constexpr uint32_t kRegsMain = 112;   // softmax, MMA issuer, loader
-constexpr uint32_t kRegsHand = 72;    // queries, conversion
-static_assert(3 * 128 * kRegsMain + 2 * 128 * kRegsHand == kThreads * kRegs,
-              "register split must equal the launch's register total");
-constexpr int kMmaWarp = 11;
-constexpr int kQueryWarp = 10;
-constexpr int kLoadWarp = 9;
-constexpr int kHandWarp = 12;
+// kWide: nothing is converted, and the softmax warps hold a row's scores of a
+// tile in registers.
+template <bool kWide>
+struct Roles {
+  static constexpr int kThreads = kWide ? 384 : 640;
+  static constexpr uint32_t kRegs = kWide ? 168 : 96;       // per thread at launch
+  static constexpr uint32_t kRegsSoftmax = kWide ? 200 : 112;
+  static constexpr uint32_t kRegsMain = kWide ? 104 : 112;   // MMA issuer, loader
+  static constexpr uint32_t kRegsHand = kWide ? 104 : 72;    // queries, conversion
+  static constexpr int kLoadWarp = kWide ? 8 : 9;
+  static constexpr int kQueryWarp = 10;
+  static constexpr int kMmaWarp = kWide ? 9 : 11;
+  static constexpr int kHandWarp = kWide ? 11 : 12;
+  static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsMain + (kWide ? 0 : 2 * 128 * kRegsHand) == kThreads * kRegs,
+                "register split must equal the launch's register total");
+};
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.0f;
 // Stretches: how far above the largest score the reference is put when it moves.
 // Any reference gives the same l and o; one that moves costs the tile's softmax
 // a pass over O, and the largest of some 10^4 scores is further above that of a
@@ -372,6 +377,95 @@ struct Unit {
   }
 };
 
+// What a softmax thread's row is.
+struct RowFacts {
+  int tok, b;   // its token and sequence
+  int64_t q;    // its place in q (stretches)
+  SeqInfo seq;  // context and new tokens that it may see
+  bool exists;
+};
+
+// The tiles of a unit in the wide form's softmax: a thread holds its row's 128
+// scores in registers.  A function of its own, so that what the unit's end needs
+// is saved once, not in the loop: local memory there takes the products'
+// bandwidth to shared memory (a tile then takes 4020 clocks, 3360 with two passes
+// over TMEM, X here).
+struct WideTiles {
+  uint32_t s_full, p_full, tS, tO;
+  int n, border, kt;
+  uint32_t ns;
+  bool warp_live;
+};
+template <int D, typename A, typename W>
+__device__ __noinline__ float2 wide_tiles(const A& a, const W& u, const WideTiles w, const Abort ab,
+                                          const uint8_t* left_out, int row, int keys) {
+  float m_ref = -INFINITY, l = 0.f;
+  const float scale = a.scale_log2;
+  const uint64_t scale2 = pack_f32x2(scale, scale);
+  uint32_t phase = w.ns;
+#pragma unroll 1
+  for (int it = 0; it < w.n; ++it) {
+    if (!wait_warp(w.s_full, phase++ & 1u, ab)) break;
+    tc_fence_after();
+    if (w.warp_live) {
+      const uint32_t left = *reinterpret_cast<const volatile uint32_t*>(left_out + ((w.kt + it) & 31) * 4);
+      if (it >= w.border || left != 0u) {  // scores that are not seen become -inf in TMEM
+        const Stretch st = paged(a).list[u.b];
+        const MemberRow r(a, st, u.unit, row);
+#pragma unroll 1
+        for (int x = 0; x < kBN / 32; ++x) {
+          const uint32_t seen = seen_word(a, SeqInfo{u.seq.len, r.cnt}, r.b, r.t, (u.first + it) * keys + 32 * x,
+                                          left >> (4 * x));
+          uint32_t y[32];
+          __syncwarp();
+          tmem_ld32(w.tS + 32 * x, y);
+          tmem_ld_wait();
+          reg_fence(y, 32);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((seen >> e) & 1u)) y[e] = __float_as_uint(-INFINITY);
+          tmem_st32(w.tS + 32 * x, y);
+        }
+        tmem_st_wait();
+      }
+      uint32_t s[kBN];
+#pragma unroll
+      for (int x = 0; x < kBN; x += 32) tmem_ld32(w.tS + x, s + x);
+      tmem_ld_wait();
+      reg_fence(s, kBN);
+      float m_new = row_max(s) * scale;
+      const bool need = m_new > m_ref + kRescaleLog2;
+      if (__any_sync(0xffffffffu, need)) {
+        m_new += kHeadroom;
+        const float alpha = need ? ex2(m_ref - m_new) : 1.f;
+        if (it > 0) {
+#pragma unroll 1
+          for (int x = 0; x < D; x += 16) {
+            uint32_t o[16];
+            tmem_ld16(w.tO + x, o);
+            tmem_ld_wait();
+            reg_fence(o, 16);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(w.tO + x, o);
+          }
+          tmem_st_wait();
+        }
+        if (need) {
+          l *= alpha;
+          m_ref = m_new;
+        }
+      }
+      const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+      l += exp_store(s, scale2, pack_f32x2(neg, neg), w.tS);
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    mbar_arrive(w.p_full);
+  }
+  return make_float2(m_ref, l);
+}
+
 // Whether a unit has rows in its second tile.
 __device__ __forceinline__ bool second_tile(const CacheAttnArgs& a, const AttnPlan& p, const UnitWalk& u,
                                             int64_t rows) {
@@ -381,14 +475,31 @@ __device__ __forceinline__ bool second_tile(const SharedAttnArgs& a, const AttnP
   return a.stretches.list[u.b].rows > 128;
 }
 
+// The form of a launch: over stretches of two tiles of rows the wide one.
+template <bool k8, bool kTwo, typename A>
+struct Form {
+  static constexpr bool kWide = !k8 && kTwo && IsShared<A>::value;
+};
+template <uint32_t kFrom, uint32_t kTo>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (kTo > kFrom)
+    setmaxnreg_inc<kTo>();
+  else
+    setmaxnreg_dec<kTo>();
+}
+
 template <bool k8, int D, bool kTwo, typename A>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<Form<k8, kTwo, A>::kWide>::kThreads, 1)
     cache_tree_kernel(const __grid_constant__ A a, const __grid_constant__ AttnPlan p,
                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const __grid_constant__ CUtensorMap tq) {
   using L = Layout<k8, D, kTwo>;
   constexpr bool kShared = IsShared<A>::value;
   using Walk = typename IsShared<A>::Walk;
+  constexpr bool kWide = Form<k8, kTwo, A>::kWide;
+  using Ro = Roles<kWide>;
+  constexpr int kMmaWarp = Ro::kMmaWarp, kQueryWarp = Ro::kQueryWarp, kLoadWarp = Ro::kLoadWarp,
+                kHandWarp = Ro::kHandWarp;
   constexpr int kS = L::kStages, kKeys = L::kKeys, kN = kKeys / 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -442,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kHandWarp) {
     // ================= queries, conversion =================
-    setmaxnreg_dec<kRegsHand>();
+    set_registers<Ro::kRegs, Ro::kRegsHand>();
     const int tid = threadIdx.x - kHandWarp * 32;
     // The unit's queries, in the order of widen16: in place, a piece stays in
     // its thread.
@@ -599,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kLoadWarp) {
     // ================= loader =================
-    setmaxnreg_inc<kRegsMain>();
+    set_registers<Ro::kRegs, Ro::kRegsMain>();
     const int page_rows = min(1 << c.page_shift, kKeys);  // of a box
     const int boxes = kKeys / page_rows;
     constexpr int kHalves = k8 ? 1 : D / 64;
@@ -710,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 8) {
     // ================= MMA issuer, query loader (and an idle warp) =================
-    setmaxnreg_inc<kRegsMain>();
+    set_registers<Ro::kRegs, Ro::kRegsMain>();
     if (kShared && warp == kQueryWarp) {
       // Rows of several sequences, four to a lane and load; what is left of a tile
       // repeats the last one: rows that nobody reads.
@@ -896,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ================= softmax =================
-    setmaxnreg_inc<kRegsMain>();
+    set_registers<Ro::kRegs, Ro::kRegsSoftmax>();
     const int t = warp / 4, wq = warp % 4;
     const int row = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -915,31 +1026,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the first tile of this part that holds drafts or the end
       const int border = static_cast<int>(
           min(max(u.seq.len / kKeys - u.first, int64_t{0}), static_cast<int64_t>(n)));
-      int tok, mask_b;   // the row's token and sequence
-      int64_t q_row;     // its place in q (stretches)
-      SeqInfo seq;       // context and new tokens that it may see
-      bool exists;
       const bool active = kTwo ? t == 0 || second_tile(a, p, u, rows) : t == 0 || n > 1;
-      if constexpr (kShared) {
-        const MemberRow r(a, c.list[u.b], u.unit, (kTwo ? t * 128 : 0) + row);
-        tok = r.t;
-        mask_b = r.b;
-        q_row = r.q;
-        exists = r.q >= 0;
-        seq = SeqInfo{u.seq.len, r.cnt};
-      } else {
-        const Unit un(a, p, u, rows);
-        const int64_t lrow = un.r0 + (kTwo ? t * 128 : 0) + row;  // row within the key head
-        exists = lrow < rows;
-        tok = exists ? static_cast<int>(lrow % c.T) : c.T;
-        mask_b = u.b;
-        q_row = 0;
-        seq = u.seq;
-      }
-      const bool live = tok < seq.cnt;
+      // What a thread's row is.  The wide form, whose loop has no registers to
+      // spare, works it out again where it is needed.
+      auto row_facts = [&]() {
+        RowFacts f;
+        if constexpr (kShared) {
+          const MemberRow r(a, c.list[u.b], u.unit, (kTwo ? t * 128 : 0) + row);
+          f = RowFacts{r.t, r.b, r.q, SeqInfo{u.seq.len, r.cnt}, r.q >= 0};
+        } else {
+          const Unit un(a, p, u, rows);
+          const int64_t lrow = un.r0 + (kTwo ? t * 128 : 0) + row;  // row within the key head
+          f.exists = lrow < rows;
+          f.tok = f.exists ? static_cast<int>(lrow % c.T) : c.T;
+          f.b = u.b;
+          f.q = 0;
+          f.seq = u.seq;
+        }
+        return f;
+      };
+      RowFacts facts = row_facts();
+      const bool live = facts.tok < facts.seq.cnt;
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_ref = -INFINITY, l = 0.f;
-      if (active) {
+      if constexpr (kWide) {
+        if (active) {
+          const WideTiles w{bars.s_full(t), bars.p_full(t), tS, tO, n, border, static_cast<int>(kt), ns, warp_live};
+          const float2 ml = wide_tiles<D>(a, u, w, ab, gbase + L::kLeftOut, (kTwo ? t * 128 : 0) + row, kKeys);
+          m_ref = ml.x;
+          l = ml.y;
+          ns += static_cast<uint32_t>(n);
+          ok = *ab.flag == 0u && wait_warp(bars.o_full(t), no++ & 1u, ab);
+          if (!ok) break;
+          tc_fence_after();
+        }
+      } else if (active) {
         bool o_valid = false;
         for (int it = kTwo ? 0 : t; it < n; it += kTwo ? 1 : 2) {
           if (!wait_warp(bars.s_full(t), ns++ & 1u, ab)) {
@@ -955,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int w = 0; w < kN; ++w) {
                 const uint32_t seen =
-                    seen_word(a, seq, mask_b, tok, (u.first + it) * kKeys + 32 * w, left >> (4 * w));
+                    seen_word(a, facts.seq, facts.b, facts.tok, (u.first + it) * kKeys + 32 * w, left >> (4 * w));
                 uint32_t s[32];
                 __syncwarp();
                 tmem_ld32(tS + 32 * w, s);
@@ -1050,6 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       kt += static_cast<uint32_t>(n);
+      if (kWide) facts = row_facts();
       if (!live) {
         m_ref = -INFINITY;
         l = 0.f;
@@ -1132,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (poisoned && live) {
             // elements of drafts that were left out because they are not finite
-            const uint32_t bad = poisoned_columns<k8, D>(a, u, mask_b, un.head, tok, x, kKeys);
+            const uint32_t bad = poisoned_columns<k8, D>(a, u, facts.b, un.head, facts.tok, x, kKeys);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if ((bad >> e) & 1u) r[e] = 0x7fffffffu;
@@ -1153,15 +1275,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (un.r0 + local - lane % 4 + e < rows) dst[e * (D / 8)] = y[e];
-            if (x == 0 && exists)
+            if (x == 0 && facts.exists)
               a.lse[un.q0 + local] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * kLn2F;
-          } else if (exists) {
+          } else if (facts.exists) {
             float4* dst = reinterpret_cast<float4*>(slot_o(a, p, slot)) + x / 4 * p.rows + local;
             int64_t pitch = p.rows;
             if constexpr (kShared) {
               if (whole) {
                 pitch = a.all_rows;
-                dst = reinterpret_cast<float4*>(a.whole_o[c.list[u.b].first < 0]) + x / 4 * pitch + q_row;
+                dst = reinterpret_cast<float4*>(a.whole_o[c.list[u.b].first < 0]) + x / 4 * pitch + facts.q;
               }
             }
 #pragma unroll
@@ -1171,7 +1293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x == 0) {
               float* ml = slot_ml(a, p, slot) + 2 * local;
               if constexpr (kShared)
-                if (whole) ml = a.whole_ml[c.list[u.b].first < 0] + 2 * q_row;
+                if (whole) ml = a.whole_ml[c.list[u.b].first < 0] + 2 * facts.q;
               *reinterpret_cast<float2*>(ml) = make_float2(m_ref, l);
             }
           }
@@ -1198,6 +1320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool k8, int D, bool kTwo, typename A>
 cudaError_t launch_t(const A& a, const AttnPlan& plan, cudaStream_t s) {
   using L = Layout<k8, D, kTwo>;
+  constexpr int kThreads = Roles<Form<k8, kTwo, A>::kWide>::kThreads;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1251,7 +1374,8 @@ cudaError_t launch_cache_tree(const CacheAttnArgs& a, bool k8, cudaStream_t s) {
 }
 
 SharedShape tree_shape(int d, bool two) {
-  return SharedShape{two || d == 64 ? 128 : 64, two ? 256 : 128, kTreeCtas, true};
+  const int tile = two || d == 64 ? 128 : 64;
+  return SharedShape{tile, two ? 256 : 128, kTreeCtas, 768 / tile, true};
 }
 
 cudaError_t launch_shared_tree(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s) {
