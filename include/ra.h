@@ -598,7 +598,8 @@ RA_API int64_t ra_cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t
  * `shared`.  Nothing is shared (each sequence reads its own pages, and equal
  * contents give an equal result) where a key head has more than 128 (RA_F32: 16)
  * query rows of a sequence, or half as many in a batch too small for the larger
- * units, and where B is above 2048.
+ * units, where B is above 2048, and where the whole table of B - 1 sequences
+ * stands for less than 160 MiB of the cache, which are read again as fast.
  */
 RA_API ra_status ra_cache_attention_shared(const void* q, const ra_cache* cache, const int32_t* table,
                                            int32_t width, const int32_t* lens, const int32_t* shared,

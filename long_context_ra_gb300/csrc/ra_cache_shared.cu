@@ -26,6 +26,12 @@ namespace {
 constexpr int kPlanThreads = 1024;    // at most
 constexpr int kPlanSequences = 2048;  // 32 bytes of shared memory each
 constexpr int kTile = 128;            // a multiple of every kernel's key tile
+// Bytes of repeated prefixes below which they are read again: some 30 us at the
+// rate of the decode kernel.  (us shared, not shared: 3 sequences of 1100, 2 heads
+// of 64, 20.7 12.5; 4 of 16384, 8 heads of 128, bf16, 203 MB, 50 50; 16 of 4096,
+// 260 MB, 44 42; 64 of 1024, 297 MB, 52 53; 16 of 16384, 1 GB, 60 108; out of 8 bits
+// 101 MB 50 48, 149 MB 59 58, 507 MB 58 114; f32 162 MB 81 75, 127 MB 77 84.)
+constexpr int64_t kWorthSharing = 160ll << 20;
 constexpr int kRuns = 9;              // lengths of a run that are tried
 
 // Where a sequence's rows are among the lots: row r of its live ones is row
@@ -463,8 +469,12 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
                : kernel[z] == SharedKernel::kTreeOne || kernel[z] == SharedKernel::kTreeTwo
                    ? tree_shape(a.c.d, kernel[z] == SharedKernel::kTreeTwo)
                    : ffma_shape(kernel[z]);
-  // Nothing to gain where a unit has no room for a second sequence's rows.
-  if (B < 2 || B > kPlanSequences || 2 * rows1 > shape[0].rows || rows1 > shape[1].rows)
+  // Nothing to gain where a unit has no room for a second sequence's rows, or
+  // where all that the table could have in common takes less time to read again
+  // than the plan and the join take.
+  const int64_t element = held == RA_F32 ? 4 : held == RA_BF16 ? 2 : 1;
+  const int64_t again = ((static_cast<int64_t>(B - 1) * a.c.width) << a.c.page_shift) * a.c.heads * 2 * a.c.d * element;
+  if (B < 2 || B > kPlanSequences || 2 * rows1 > shape[0].rows || rows1 > shape[1].rows || again < kWorthSharing)
     return launch_cache_attention(a, dense, held, s);
 
   const Room r = room(B, rows1, a.c.heads, a.c.d);

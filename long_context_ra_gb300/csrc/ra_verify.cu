@@ -152,9 +152,13 @@ struct Row {
   }
 };
 
-__device__ __forceinline__ double sum_lanes(double x) {
+// The sum of the lanes' pairs, in every lane.
+__device__ __forceinline__ Pair sum_lanes(Pair x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, x.h, o), l = __shfl_xor_sync(0xffffffffu, x.l, o);
+    x.add(h, l);
+  }
   return x;
 }
 __device__ __forceinline__ double scan_lanes(double x) {
@@ -167,35 +171,32 @@ __device__ __forceinline__ double scan_lanes(double x) {
   return x;
 }
 
-// The first i with before + part[0] + .. + part[i] > target, or the last with
-// part[i] > 0 where rounding leaves none; `before` becomes the sum ahead of it.
-__device__ __forceinline__ int crossing(const double* part, int n, double target, double& before) {
-  double at = before, ahead = before;
-  int last = -1;
-  for (int i = 0; i < n; ++i) {
-    if (part[i] > 0.0) {
-      last = i;
-      ahead = at;
-      if (at + part[i] > target) break;
-    }
-    at += part[i];
-  }
-  before = ahead;
-  return last;
-}
-// The same for a value per lane.
-__device__ __forceinline__ int crossing_lane(double mine, double target, double& before) {
+// The first of 32 lanes' values with before + part[0] + .. + part[i] > target, or
+// the last that is above 0 where rounding leaves none (-1: none is); `before`
+// becomes the sum ahead of it.
+__device__ __forceinline__ int crossing(double mine, double target, double& before) {
   const double upto = before + scan_lanes(mine);
   const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
   const uint32_t past = __ballot_sync(0xffffffffu, mine > 0.0 && upto > target);
   const int at = past ? __ffs(past) - 1 : 31 - __clz(some);
-  const double ahead = __shfl_sync(0xffffffffu, upto - mine, max(at, 0));
-  before = ahead;
+  before = __shfl_sync(0xffffffffu, upto - mine, max(at, 0));
   return at;
 }
 
+// What the walk asks of the block: a row's sum, for the next decision or, at the
+// end, for the next token.
+struct Ask {
+  int node, n_refused;
+  Pair c;
+  bool last;
+};
+
+// A warp takes its pieces of a row in up to kParts parts, whose sums by lanes it
+// leaves in shared memory, so that the search goes on inside one of them.
+constexpr int kParts = 8;
+
 template <typename E, bool kDraft>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
   extern __shared__ int32_t parent[];                        // [T]
   int32_t* tokens = parent + a.T;                            // [T]
@@ -203,8 +204,9 @@ __global__ void __launch_bounds__(kThreads)
   float* us = reinterpret_cast<float*>(refused + a.T);       // [T]
   float* ps = us + a.T;                                      // [T] p of the parent's row at the token
   float* qs = ps + a.T;                                      // [T]
-  __shared__ double warp_sums[kWarps], cta_sums[2][kMostCtas], cta_sum[2];
-  __shared__ int next_draft;
+  __shared__ float2 parts[kWarps][kParts][32];
+  __shared__ double warp_sums[kWarps], cta_sums[kMostCtas], cta_sum[2], row_total;
+  __shared__ Ask ask;
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
   const int b = blockIdx.x / ctas;
@@ -240,25 +242,30 @@ __global__ void __launch_bounds__(kThreads)
   Row<E, kDraft> row;
   row.V = a.V;
   row.refused = refused;
-  auto enter = [&](int node) {
-    const int64_t at = (row0 + node) * a.V;
+  // The row's sum, and in every CTA the sums of its parts.
+  int turn = 0;
+  int64_t w0 = 0, w1 = 0, each = 0;  // this warp's pieces; of a part
+  auto row_sum = [&](const Ask& x) {
+    const int64_t at = (row0 + x.node) * a.V;
     row.p = static_cast<const E*>(a.probs) + at;
     row.q = static_cast<const E*>(kDraft ? a.draft : a.probs) + at;
     row.shift = static_cast<int>(at % Piece<E>::kN);
-    row.c = Pair{0.f, 0.f};
-    row.n_refused = 0;
-  };
-  // The row's sum, of every CTA's part and warp's part of it.
-  int turn = 0;
-  int64_t w0 = 0, w1 = 0;  // this warp's pieces
-  auto row_sum = [&]() {
+    row.c = x.c;
+    row.n_refused = x.n_refused;
     const int64_t n = row.pieces();
-    const int64_t each = (n + ctas * kWarps - 1) / (ctas * kWarps);
-    w0 = min(n, (rank * kWarps + warp) * each);
-    w1 = min(n, w0 + each);
-    const double mine = sum_lanes(row.sum(w0 + lane, w1, 32).value());
-    __syncthreads();
-    if (lane == 0) warp_sums[warp] = mine;
+    const int64_t of_warp = (n + ctas * kWarps - 1) / (ctas * kWarps);
+    w0 = min(n, (rank * kWarps + warp) * of_warp);
+    w1 = min(n, w0 + of_warp);
+    each = (of_warp + kParts * 32 - 1) / (kParts * 32) * 32;  // whole rounds of the warp
+    Pair all{0.f, 0.f};
+    for (int i = 0; i < kParts; ++i) {
+      const int64_t first = min(w1, w0 + i * each);
+      const Pair part = row.sum(first + lane, min(w1, first + each), 32);
+      parts[warp][i][lane] = make_float2(part.h, part.l);
+      all.add(part.h, part.l);
+    }
+    all = sum_lanes(all);
+    if (lane == 0) warp_sums[warp] = all.value();
     __syncthreads();
     turn ^= 1;
     if (threadIdx.x == 0) {
@@ -268,124 +275,149 @@ __global__ void __launch_bounds__(kThreads)
     }
     cluster.sync();
     if (static_cast<int>(threadIdx.x) < ctas)
-      cta_sums[turn][threadIdx.x] = *cluster.map_shared_rank(&cta_sum[turn], threadIdx.x);
+      cta_sums[threadIdx.x] = *cluster.map_shared_rank(&cta_sum[turn], threadIdx.x);
     __syncthreads();
-    double s = 0.0;
-    for (int i = 0; i < ctas; ++i) s += cta_sums[turn][i];
-    return s;
+    if (threadIdx.x == 0) {
+      double s = 0.0;
+      for (int i = 0; i < ctas; ++i) s += cta_sums[i];
+      row_total = s;
+    }
+    __syncthreads();
   };
 
-  // ---- the walk, alike in every thread
-  int node = 0, kept = 1, t = 0;
+  // ---- the walk, by the first warp of every CTA alike (64-bit arithmetic is slow:
+  // by all warps a decision took 1 us)
+  int node = 0, kept = 1, t = 0, n_refused = 0;
   double total = 1.0, scale = 0.0;  // of what is left of the row; c
-  double whole = -1.0;              // without q: the sum of the node's row, once it is known
-  double gone = 0.0;                // without q: that of the refused tokens
-  bool known = true;                // total is up to date
-  enter(0);
+  double whole = -1.0, gone = 0.0;  // without q: the sum of the node's row, once it is known; of the refused
+  bool known = true, summing = false;
   if (rank == 0 && threadIdx.x == 0) path[0] = 0;
   while (true) {
-    // the next draft below `node`
     if (warp == 0) {
-      int found = count;
-      for (int t0 = t + 1; t0 < count; t0 += 32) {
-        const uint32_t here = __ballot_sync(0xffffffffu, t0 + lane < count && parent[t0 + lane] == node);
-        if (here) {
-          found = t0 + __ffs(here) - 1;
+      if (summing) {
+        if (!kDraft) whole = row_total;
+        total = kDraft ? row_total : whole - gone;
+        known = true;
+      }
+      while (true) {
+        // the next draft below `node`; one that waited for a sum is still at t
+        if (!summing) {
+          int found = count;
+          for (int t0 = t + 1; t0 < count; t0 += 32) {
+            const uint32_t here = __ballot_sync(0xffffffffu, t0 + lane < count && parent[t0 + lane] == node);
+            if (here) {
+              found = t0 + __ffs(here) - 1;
+              break;
+            }
+          }
+          t = found;
+        }
+        summing = false;
+        if (t >= count) break;
+        if (!known && !kDraft && whole >= 0.0) {
+          total = whole - gone;
+          known = true;
+        }
+        if (!known) {
+          summing = true;
           break;
         }
-      }
-      if (lane == 0) next_draft = found;
-    }
-    __syncthreads();
-    t = next_draft;
-    __syncthreads();
-    if (t >= count) break;
-    if (!known) {
-      if (kDraft) {
-        total = row_sum();
-      } else {
-        if (whole < 0.0) {
-          const int n = row.n_refused;
-          row.n_refused = 0;
-          whole = row_sum();
-          row.n_refused = n;
+        const double p = ps[t], q = qs[t];
+        double rest = p;
+        bool again = false;  // a token that was refused before
+        if (kDraft) {
+          rest = fmax(p - scale * q, 0.0);
+        } else {
+          for (int i = 0; i < n_refused; ++i) again = again || refused[i] == tokens[t];
+          if (again) rest = 0.0;
         }
-        total = whole - gone;
+        if (us[t] * q * total < rest) {
+          if (rank == 0 && lane == 0) path[kept] = t;
+          ++kept;
+          node = t;
+          n_refused = 0;
+          total = 1.0;
+          scale = gone = 0.0;
+          whole = -1.0;
+          known = true;
+          continue;
+        }
+        known = false;
+        if (kDraft) {
+          scale += total;
+        } else if (!again) {
+          if (lane == 0) refused[n_refused] = tokens[t];
+          __syncwarp();
+          ++n_refused;
+          gone += p;
+        }
       }
-      known = true;
+      if (lane == 0) {
+        const float h = static_cast<float>(scale);
+        // for a decision without q the whole row is summed once, the refused with it
+        ask = Ask{node, summing && !kDraft ? 0 : n_refused, Pair{h, static_cast<float>(scale - h)}, !summing};
+      }
     }
-    const double p = ps[t], q = qs[t];
-    double rest = p;
-    bool again = false;  // a token that was refused before
-    if (kDraft) {
-      rest = fmax(p - scale * q, 0.0);
-    } else {
-      for (int i = 0; i < row.n_refused; ++i) again = again || refused[i] == tokens[t];
-      if (again) rest = 0.0;
-    }
-    if (us[t] * q * total < rest) {
-      if (rank == 0 && threadIdx.x == 0) path[kept] = t;
-      ++kept;
-      node = t;
-      enter(node);
-      total = 1.0;
-      scale = gone = 0.0;
-      whole = -1.0;
-      known = true;
-      continue;
-    }
-    if (kDraft) {
-      scale += total;
-      row.c.h = static_cast<float>(scale);
-      row.c.l = static_cast<float>(scale - row.c.h);
-    } else if (!again) {
-      __syncthreads();
-      if (threadIdx.x == 0) refused[row.n_refused] = tokens[t];
-      __syncthreads();
-      ++row.n_refused;
-      gone += p;
-    }
-    known = false;
+    __syncthreads();
+    const Ask x = ask;
+    row_sum(x);
+    if (x.last) break;
   }
 
   // ---- the next token
-  total = row_sum();
-  if (!(total > 0.0)) {  // nothing is left: p itself
-    row.c = Pair{0.f, 0.f};
-    row.n_refused = 0;
-    total = row_sum();
+  if (!(row_total > 0.0)) {  // nothing is left: p itself
+    const Ask x{ask.node, 0, Pair{0.f, 0.f}, true};
+    row_sum(x);
   }
-  const bool some = total > 0.0 && total < INFINITY;
-  if (rank == 0) {
-    for (int i = kept + threadIdx.x; i < a.T; i += kThreads) path[i] = -1;
-    if (threadIdx.x == 0) {
+  const double all = row_total;
+  const bool some = all > 0.0 && all < INFINITY;
+  if (rank == 0 && warp == 0) {
+    for (int i = kept + lane; i < a.T; i += 32) path[i] = -1;
+    if (lane == 0) {
       a.kept[b] = kept;
       if (!some) a.token[b] = -1;
     }
   }
   if (some) {
-    const double target = us[0] * total;
-    double before = 0.0;
-    // CTA, warp, a lane's run of pieces, piece, element
-    if (crossing(cta_sums[turn], ctas, target, before) == rank &&
-        crossing(warp_sums, kWarps, target, before) == warp) {
-      const int64_t run = (w1 - w0 + 31) / 32;
-      const int64_t mine = min(w1, w0 + lane * run);
-      int at = crossing_lane(row.sum(mine, min(w1, mine + run), 1).value(), target, before);
-      // the pieces of that run, 32 at a time, up to those that pass the target
-      const int64_t r0 = min(w1, w0 + at * run), r1 = min(w1, r0 + run);
+    // CTA, warp, part, piece, element: the first warp finds the warp
+    __shared__ int found_warp;
+    __shared__ double found_before;
+    const double target = us[0] * all;
+    if (warp == 0) {
+      double before = 0.0;
+      int w = -1;
+      if (crossing(lane < ctas ? cta_sums[lane] : 0.0, target, before) == rank)
+        w = crossing(lane < kWarps ? warp_sums[lane] : 0.0, target, before);
+      if (lane == 0) {
+        found_warp = w;
+        found_before = before;
+      }
+    }
+    __syncthreads();
+    if (found_warp == warp) {
+      double before = found_before;
+      // a lane adds up the lanes' sums of a part
+      double mine = 0.0;
+      if (lane < kParts) {
+        Pair s{0.f, 0.f};
+        for (int i = 0; i < 32; ++i) s.add(parts[warp][lane][i].x, parts[warp][lane][i].y);
+        mine = s.value();
+      }
+      const int part = max(crossing(mine, target, before), 0);
+      const int64_t r0 = min(w1, w0 + part * each), r1 = min(w1, r0 + each);
+      // its pieces, 32 at a time, up to those that pass the target
       int64_t v0 = r0;
       double sofar = before;
       for (int64_t i = r0; i < r1; i += 32) {
-        const double all = sum_lanes(i + lane < r1 ? row.sum(i + lane, i + lane + 1, 1).value() : 0.0);
-        if (all > 0.0) {
+        const double sum = sum_lanes(row.sum(i + lane, min(r1, i + lane + 1), 1)).value();
+        if (sum > 0.0) {
           v0 = i;
           before = sofar;
-          if (sofar + all > target) break;
+          if (sofar + sum > target) break;
         }
-        sofar += all;
+        sofar += sum;
       }
-      at = crossing_lane(v0 + lane < r1 ? row.sum(v0 + lane, v0 + lane + 1, 1).value() : 0.0, target, before);
+      const int at = crossing(row.sum(v0 + lane, min(r1, v0 + lane + 1), 1).value(), target, before);
       if (at >= 0 && lane == at) {
         const int64_t v = v0 + at;
         const Piece<E> x = row.load(row.p, v), y = row.load(row.q, v);
@@ -408,10 +440,10 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename E, bool kDraft>
 cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
-  // All clusters at once on the SMs, four CTAs on each: more CTAs shorten a
+  // All clusters at once on the SMs, two CTAs on each: more CTAs shorten a
   // sequence's chain, waves lengthen it.
   int ctas = kMostCtas;
-  while (ctas > 1 && static_cast<int64_t>(a.B) * ctas > 4 * device_sm_count()) ctas /= 2;
+  while (ctas > 1 && static_cast<int64_t>(a.B) * ctas > 2 * device_sm_count()) ctas /= 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = ctas;
@@ -424,6 +456,17 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  static_assert(kVerifyNodes * 24 + kWarps * kParts * 32 * 8 <= 64 * 1024, "shared memory");
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(verify_kernel<E, kDraft>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kVerifyNodes * 24);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
   return cudaLaunchKernelEx(&cfg, verify_kernel<E, kDraft>, a);
 }
 

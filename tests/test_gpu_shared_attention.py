@@ -25,6 +25,15 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
 
 
+def wide(table, cache):
+    """The table with columns of no page behind: as large as one must be for
+    prefixes to be shared rather than read again."""
+    _, heads, page, d = cache.k.shape
+    column = (table.shape[0] - 1) * page * heads * 2 * d * cache.k.element_size()
+    more = (160 << 20) // max(column, 1) + 1
+    return torch.cat([table, torch.full((table.shape[0], more), -1, dtype=torch.int32)], 1).to(DEV)
+
+
 def make(groups, count, T, Hq, heads, page, d, dtype, held, seed, same_pages=True):
     """groups: (prefix, [own context tokens of each sequence; None: lens = -1]).
     The prefix of a group is the same in all of its sequences: whole pages are
@@ -89,9 +98,15 @@ SHAPES = [
 def test_causal(shape, dtype, held, d):
     groups, count, T, Hq, heads, page = SHAPES[shape]
     q, cache, table, lens, shared, cnt = make(groups, count, T, Hq, heads, page, d, dtype, held, 1)
-    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared, cnt)
+    got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared, cnt)
     assert ra.ra_last_device_status() == 0
     check(got, q, cache, table, lens, count, None)
+    # a small table: each reads its own pages, as without sharing
+    if (len(lens) - 1) * table.shape[1] * page * heads * 2 * d * cache.k.element_size() >= 160 << 20:
+        return
+    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared, cnt)
+    want = ra.ra_cache_attention(q, cache, table.to(DEV), i32(lens), cnt)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @pytest.mark.parametrize("dtype,held,d", TYPES)
@@ -103,7 +118,7 @@ def test_tree(shape, one_mask, dtype, held, d):
     mask = tree(1, T, 3)[0] if one_mask else tree(len(lens), T, 3)
     if not one_mask and len(lens) > 2:
         mask[2] = False                      # new tokens that see the context alone
-    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared, cnt, mask.to(DEV))
+    got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared, cnt, mask.to(DEV))
     assert ra.ra_last_device_status() == 0
     check(got, q, cache, table, lens, count, mask)
 
@@ -118,13 +133,13 @@ def test_the_common_part_is_the_first_ones(dtype, held, d, T):
     result stays, so they are not read."""
     groups = [(300, [5, 90, 3, 8, 0])]
     q, cache, table, lens, shared, _ = make(groups, None, T, 2, 1, 16, d, dtype, held, 4, same_pages=False)
-    want = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+    want = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
     check(want, q, cache, table, lens, None, None)
     for b in range(1, len(lens)):
         for p in table[b, :256 // 16].tolist():
             cache.v.view(torch.uint8)[p] = 0x7f
             cache.k.view(torch.uint8)[p] = 0x7f
-    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+    got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
@@ -139,11 +154,11 @@ def test_entries_of_all_kinds(dtype, held, d, T):
                     [-5, -1, 0, 512, 0, 0, 0], [0] * 7):
         if max(entries) > 1000:  # more than is in common would be wrong: only where the lengths cut it
             entries = [min(e, 512 if b < 4 else 400) if e > 1000 else e for b, e in enumerate(entries)]
-        got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), i32(entries))
+        got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), i32(entries))
         check(got, q, cache, table, lens, None, None)
     one = [(512, [0, 0])]
     q, cache, table, lens, shared, _ = make(one, None, T, 2, 1, 32, d, dtype, held, 6)
-    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), i32([0, 1 << 30]))  # cut by lens
+    got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), i32([0, 1 << 30]))  # cut by lens
     check(got, q, cache, table, lens, None, None)
     assert plain[0].isfinite().all()
 
@@ -156,7 +171,7 @@ def test_many_sequences(dtype, held, d, T):
         own = [b % 3 for b in range(B)]
         groups = [(128, own[:1500]), (0, own[1500:1700]), (260, own[1700:])]
         q, cache, table, lens, shared, _ = make(groups, None, T, 1, 1, 128, d, dtype, held, 7)
-        got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+        got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
         want = ra.ra_cache_attention(q, cache, table.to(DEV), i32(lens))
         some = list(range(0, B, 97)) + [1499, 1500, 1699, 1700, B - 1]
         assert ra.ra_last_device_status() == 0
@@ -170,11 +185,11 @@ def test_values_that_are_not_finite_in_a_prefix(dtype, held, d, T):
     its column only."""
     groups = [(300, [5, 70, 0]), (0, [400]), (290, [3, 9])]
     q, cache, table, lens, shared, _ = make(groups, None, T, 4, 2, 16, d, dtype, held, 8)
-    want = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+    want = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
     for at in (0, 255, 256, 285):
         places = [(b, at) for b in range(6)]
         bad = with_value(cache, table, places, 1, 7, math.nan)
-        got = ra.ra_cache_attention_shared(q, bad, table.to(DEV), i32(lens), shared)
+        got = ra.ra_cache_attention_shared(q, bad, wide(table, bad), i32(lens), shared)
         check_one_column(got, want, 2, 1, 7, lens, None, T)
 
 
@@ -191,9 +206,9 @@ def test_weights_of_0_between_prefix_and_rest(dtype, held, d, T):
         k[:, :, top] = 8
         ra.ra_cache_write(cache, k, v, table.to(DEV), i32([0] * 3), i32([x + T for x in lens]))
         q = torch.full_like(q, 4.0)
-        want = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+        want = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
         bad = with_value(cache, table, [(b, at) for b in range(3)], 0, 7, math.nan)
-        got = ra.ra_cache_attention_shared(q, bad, table.to(DEV), i32(lens), shared)
+        got = ra.ra_cache_attention_shared(q, bad, wide(table, bad), i32(lens), shared)
         check_one_column(got, want, 2, 0, 7, lens, None, T)
 
 
@@ -205,11 +220,11 @@ def test_drafts_that_are_not_seen(dtype, held, d, T):
     q, cache, table, lens, shared, _ = make(groups, None, T, 2, 1, 16, d, dtype, held, 10)
     mask = tree(3, T, 7)
     mask[:, 1:, 0] = False
-    want = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared, None, mask.to(DEV))
+    want = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared, None, mask.to(DEV))
     for t in (cache.k, cache.v):
         for b, n in enumerate(lens):
             t[int(table[b, n // 16]), :, n % 16] = torch.full((1, d), math.nan, device=DEV).to(held)
-    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared, None, mask.to(DEV))
+    got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared, None, mask.to(DEV))
     assert torch.equal(got[0][:, :, 1:], want[0][:, :, 1:]) and torch.equal(got[1][:, :, 1:], want[1][:, :, 1:])
     assert not got[0][:, :, 0].isfinite().any()
 
@@ -222,20 +237,20 @@ def test_bad_pages(dtype, held, d, T):
     q, cache, table, lens, shared, _ = make(groups, None, T, 2, 1, 16, d, dtype, held, 11)
     bad = table.clone()
     bad[:, 3], bad[1, 33] = cache.k.shape[0] + 5, -1
-    got = ra.ra_cache_attention_shared(q, cache, bad.to(DEV), i32(lens), shared)
+    got = ra.ra_cache_attention_shared(q, cache, wide(bad, cache), i32(lens), shared)
     assert ra.ra_last_device_status() == _native.RA_ERR_PAGE
     want = ra.ra_cache_attention(q, cache, bad.to(DEV), i32(lens))
     assert ra.ra_last_device_status() == _native.RA_ERR_PAGE
     torch.testing.assert_close(got[0].float(), want[0].float(), atol=2e-2, rtol=2.0 ** -6)
     torch.testing.assert_close(got[1], want[1], atol=1e-4, rtol=1e-5)
     # a table that is too short for the sequences
-    got = ra.ra_cache_attention_shared(q, cache, table[:, :20].contiguous().to(DEV), i32(lens), shared)
+    got = ra.ra_cache_attention_shared(q, cache, wide(table[:, :20], cache), i32(lens), shared)
     assert ra.ra_last_device_status() == _native.RA_ERR_PAGE
     want = ra.ra_cache_attention(q, cache, table[:, :20].contiguous().to(DEV), i32(lens))
     torch.testing.assert_close(got[1], want[1], atol=1e-4, rtol=1e-5)
     # a count above T
     ra.ra_last_device_status()
-    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared, i32([T, T + 1, T]))
+    got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared, i32([T, T + 1, T]))
     assert ra.ra_last_device_status() == _native.RA_ERR_PAGE
     check(got, q, cache, table, lens, None, None)
 
@@ -245,10 +260,10 @@ def test_repeats_and_does_not_depend_on_the_workspace(dtype, held, d, T):
     groups = [(3000, [5, 700, 0, 9]), (800, [3, 9])]
     q, cache, table, lens, shared, _ = make(groups, None, T, 4, 2, 64, d, dtype, held, 12)
     n = ra.ra_cache_attention_shared_workspace_bytes(6, 4, 2, T, d)
-    first = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+    first = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
     for fill in (0, 255):
         ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
-        again = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared, workspace=ws)
+        again = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared, workspace=ws)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
@@ -256,7 +271,7 @@ def test_repeats_and_does_not_depend_on_the_workspace(dtype, held, d, T):
 def test_graph_follows_lengths_and_entries(dtype, held, d, T):
     groups = [(640, [50, 60, 70]), (0, [10]), (512, [9, 8])]
     q, cache, table, lens, shared, _ = make(groups, None, T, 2, 1, 32, d, dtype, held, 13)
-    tab, ln, sh = table.to(DEV), i32(lens), shared.clone()
+    tab, ln, sh = wide(table, cache), i32(lens), shared.clone()
     out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
     ws = torch.empty(ra.ra_cache_attention_shared_workspace_bytes(6, 2, 1, T, d), dtype=torch.uint8, device=DEV)
     ra.ra_cache_attention_shared(q, cache, tab, ln, sh, out=out, lse=lse, workspace=ws)
@@ -280,10 +295,10 @@ def test_a_wait_that_runs_out_is_said():
     q, cache, table, lens, shared, _ = make(groups, None, 33, 2, 1, 64, 128, torch.bfloat16, torch.bfloat16, 14)
     try:
         ra.ra_watchdog_config(1 << 20, 0)
-        ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+        ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
         assert ra.ra_last_device_status() == _native.RA_ERR_TIMEOUT
     finally:
         ra.ra_watchdog_config(0, -1)
-    got = ra.ra_cache_attention_shared(q, cache, table.to(DEV), i32(lens), shared)
+    got = ra.ra_cache_attention_shared(q, cache, wide(table, cache), i32(lens), shared)
     assert ra.ra_last_device_status() == 0
     check(got, q, cache, table, lens, None, None)
