@@ -116,6 +116,10 @@ __device__ __forceinline__ int scan_block(int x, int* warps, int& all) {
   return x + (warp > 0 ? before : 0);
 }
 
+// A thread has the sequences tid, tid + 1024, .. and keeps what it has read of
+// them: the block spends its time on chains of loads.
+constexpr int kEach = kReserveSequences / kReserveThreads;
+
 __global__ void __launch_bounds__(kReserveThreads)
     pages_reserve_kernel(const __grid_constant__ PageTableArgs a, const int32_t* count, int T, int32_t* granted,
                          int32_t* src, int32_t* dst) {
@@ -124,74 +128,88 @@ __global__ void __launch_bounds__(kReserveThreads)
   __shared__ int warps[32];
   const int tid = threadIdx.x;
   const int64_t in_page = (int64_t{1} << a.page_shift) - 1;
-  auto tokens = [&](int b) { return max(0, min(count ? count[b] : T, T)); };
-  auto first_page = [&](int b) {  // of the first new token
-    return a.table[static_cast<int64_t>(b) * a.width + (a.lens[b] >> a.page_shift)];
+  // f(b, i) for this thread's sequences, the i-th of them
+  auto mine = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int b = tid + i * kReserveThreads;
+      if (i * kReserveThreads >= a.B) break;
+      if (b < a.B) f(b, i);
+    }
   };
+  int len[kEach], tokens[kEach], held[kEach], page[kEach];  // page: of the first new token, where others hold it too
+  uint8_t st[kEach];
 
   // ---- who asks, and for how much
-  for (int b = tid; b < a.B; b += kReserveThreads) {
-    const int64_t len = a.lens[b];
-    const int n = tokens(b);
-    uint8_t st = kAsksNothing;
+  mine([&](int b, int i) {
+    len[i] = a.lens[b];
+    tokens[i] = count ? count[b] : T;
+    held[i] = held_columns(a, b);
+  });
+  bool leaving = false;
+  mine([&](int b, int i) {
     int need = 0;
-    if (len >= 0 && n > 0) {
-      const int held = held_columns(a, b);
-      const int64_t last = columns_of(a, len + n);
-      bool good = last <= a.width && columns_of(a, len) <= held;
-      bool shared = false;
+    st[i] = kAsksNothing;
+    page[i] = -1;
+    if (len[i] >= 0 && tokens[i] > T) flag_page(a.status);
+    tokens[i] = max(0, min(tokens[i], T));
+    if (len[i] >= 0 && tokens[i] > 0) {
+      const int64_t last = columns_of(a, static_cast<int64_t>(len[i]) + tokens[i]);
+      bool good = last <= a.width && columns_of(a, len[i]) <= held[i];
       if (good) {
         const int32_t* row = a.table + static_cast<int64_t>(b) * a.width;
-        const int first = static_cast<int>(len >> a.page_shift);
-        for (int c = first; c < min(static_cast<int64_t>(held), last); ++c) {
+        const int first = len[i] >> a.page_shift;
+        for (int c = first; c < min(static_cast<int64_t>(held[i]), last); ++c) {
           const int p = row[c];
           const int r = a_page(a, p) ? a.ref[p] : 0;
-          if (r > 1 && c == first) shared = true;
+          if (r > 1 && c == first) page[i] = p;
           good = good && r >= 1 && (r == 1 || c == first);
         }
       }
       if (good) {
-        st = shared ? kLeaves : kAsks;
-        need = static_cast<int>(max(last - held, int64_t{0}));
+        st[i] = page[i] >= 0 ? kLeaves : kAsks;
+        need = static_cast<int>(max(last - held[i], int64_t{0}));
+        leaving = leaving || st[i] == kLeaves;
       } else {
         flag_page(a.status);
       }
     }
-    if (len >= 0 && count && count[b] > T) flag_page(a.status);
-    state[b] = st;
     upto[b] = need;
     src[b] = -1;
     dst[b] = -1;
-  }
-  __syncthreads();
-  for (int b = tid; b < a.B; b += kReserveThreads)
-    if (state[b] == kLeaves) atomicSub(a.ref + first_page(b), 1);
-  __syncthreads();
-  for (int b = tid; b < a.B; b += kReserveThreads)
-    if (state[b] == kLeaves) {
-      int32_t* r = a.ref + first_page(b);
-      if (__ldcg(r) <= 0) atomicMin(r, -(b + 1));
-    }
-  __syncthreads();
-  for (int b = tid; b < a.B; b += kReserveThreads)
-    if (state[b] == kLeaves) {
-      if (__ldcg(a.ref + first_page(b)) == -(b + 1))
-        state[b] = kKeeps;
+  });
+  if (__syncthreads_or(leaving)) {  // (all counts have been read)
+    mine([&](int, int i) {
+      if (st[i] == kLeaves) atomicSub(a.ref + page[i], 1);
+    });
+    __syncthreads();
+    mine([&](int b, int i) {
+      if (st[i] == kLeaves && __ldcg(a.ref + page[i]) <= 0) atomicMin(a.ref + page[i], -(b + 1));
+    });
+    __syncthreads();
+    mine([&](int b, int i) {
+      if (st[i] != kLeaves) return;
+      if (__ldcg(a.ref + page[i]) == -(b + 1))
+        st[i] = kKeeps;
       else
         upto[b] += 1;
-    }
+    });
+    __syncthreads();
+    mine([&](int, int i) {
+      if (st[i] == kKeeps) a.ref[page[i]] = 1;
+    });
+  }
+  mine([&](int b, int i) { state[b] = st[i]; });
   __syncthreads();
-  for (int b = tid; b < a.B; b += kReserveThreads)
-    if (state[b] == kKeeps) a.ref[first_page(b)] = 1;
 
   // ---- upto: an inclusive scan, a run of sequences per thread
   int total;  // below 2^31: B rows of the table
   {
     const int each = (a.B + kReserveThreads - 1) / kReserveThreads;
     const int b0 = min(a.B, tid * each), b1 = min(a.B, b0 + each);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += upto[b];
-    int at = scan_block(mine, warps, total) - mine;
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += upto[b];
+    int at = scan_block(sum, warps, total) - sum;
     for (int b = b0; b < b1; ++b) {
       at += upto[b];
       upto[b] = at;
@@ -199,34 +217,40 @@ __global__ void __launch_bounds__(kReserveThreads)
   }
   __syncthreads();
 
-  // ---- free pages in rising order, f(page, rank) for those below `total`
-  auto each_free = [&](auto f) {
-    int before = 0;
-    for (int64_t p0 = 0; p0 < a.pages && before < total; p0 += kReserveThreads * kScan) {
-      const int64_t p = p0 + tid * kScan;
-      uint32_t free_bits = 0;
+  // ---- free pages in rising order, f(page, rank) for those below `total`.  The
+  // second walk has the first round's pages still in hand.
+  uint32_t first_free = 0;
+  int first_rank = 0, first_all = 0;
+  auto look = [&](int64_t p0, int& rank, int& all) {
+    const int64_t p = p0 + tid * kScan;
+    uint32_t bits = 0;
 #pragma unroll
-      for (int i = 0; i < kScan; ++i)
-        if (p + i < a.pages && __ldcg(a.ref + p + i) == 0) free_bits |= 1u << i;
-      int all;
-      int rank = before + scan_block(__popc(free_bits), warps, all) - __popc(free_bits);
-      for (; free_bits; free_bits &= free_bits - 1, ++rank)
-        if (rank < total) f(p + __ffs(free_bits) - 1, rank);
-      before += all;
-    }
-    return before;
+    for (int i = 0; i < kScan; ++i)
+      if (p + i < a.pages && __ldcg(a.ref + p + i) == 0) bits |= 1u << i;
+    rank = scan_block(__popc(bits), warps, all) - __popc(bits);
+    return bits;
   };
-  const bool enough = each_free([](int64_t, int) {}) >= total;
-  __syncthreads();
+  constexpr int64_t kRound = static_cast<int64_t>(kReserveThreads) * kScan;
+  bool enough = total == 0;
+  if (!enough) {
+    first_free = look(0, first_rank, first_all);
+    int found = first_all;
+    for (int64_t p0 = kRound; p0 < a.pages && found < total; p0 += kRound) {
+      int rank, all;
+      look(p0, rank, all);
+      found += all;
+    }
+    enough = found >= total;
+  }
   if (!enough) {  // all or nothing
     if (tid == 0) flag_page(a.status);
-    for (int b = tid; b < a.B; b += kReserveThreads) {
-      if (state[b] == kLeaves) atomicAdd(a.ref + first_page(b), 1);
+    mine([&](int b, int i) {
+      if (st[i] == kLeaves) atomicAdd(a.ref + page[i], 1);
       granted[b] = 0;
-    }
+    });
     return;
   }
-  each_free([&](int64_t page, int rank) {
+  auto give = [&](int page_number, int rank) {
     int lo = 0, hi = a.B - 1;  // the first sequence with upto > rank
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -237,26 +261,35 @@ __global__ void __launch_bounds__(kReserveThreads)
     }
     int j = rank - (lo > 0 ? upto[lo - 1] : 0);
     int32_t* row = a.table + static_cast<int64_t>(lo) * a.width;
-    a.ref[page] = 1;
+    a.ref[page_number] = 1;
     if (state[lo] == kLeaves && j-- == 0) {
-      const int first = a.lens[lo] >> a.page_shift;
-      if (a.lens[lo] & in_page) {  // tokens of the context lie in it
+      const int at = a.lens[lo], first = at >> a.page_shift;
+      if (at & in_page) {  // tokens of the context lie in it
         src[lo] = row[first];
-        dst[lo] = static_cast<int32_t>(page);
+        dst[lo] = page_number;
       }
-      row[first] = static_cast<int32_t>(page);
+      row[first] = page_number;
       return;
     }
-    row[held_columns(a, lo) + j] = static_cast<int32_t>(page);
-  });
-  __syncthreads();
-  for (int b = tid; b < a.B; b += kReserveThreads) {
-    const bool asks = state[b] != kAsksNothing;
-    granted[b] = asks ? tokens(b) : 0;
+    row[held_columns(a, lo) + j] = page_number;
+  };
+  int before = 0;
+  for (int64_t p0 = 0; p0 < a.pages && before < total; p0 += kRound) {
+    int rank = first_rank, all = first_all;
+    uint32_t bits = first_free;
+    if (p0 > 0) bits = look(p0, rank, all);
+    for (rank += before; bits && rank < total; bits &= bits - 1, ++rank)
+      give(static_cast<int>(p0 + tid * kScan + __ffs(bits) - 1), rank);
+    before += all;
+  }
+  __syncthreads();  // the columns that were held have been read
+  mine([&](int b, int i) {
+    const bool asks = st[i] != kAsksNothing;
+    granted[b] = asks ? tokens[i] : 0;
     if (asks)
       a.held[b] = static_cast<int32_t>(
-          max(static_cast<int64_t>(held_columns(a, b)), columns_of(a, static_cast<int64_t>(a.lens[b]) + tokens(b))));
-  }
+          max(static_cast<int64_t>(held[i]), columns_of(a, static_cast<int64_t>(len[i]) + tokens[i])));
+  });
 }
 
 // ------------------------------------------------------------------- copy
