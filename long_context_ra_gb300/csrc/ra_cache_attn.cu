@@ -81,7 +81,6 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
   const int64_t rows = head_rows(a);
 
   allow_join();
-  wait_for_plan(a);
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   typename IsShared<A>::Walk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
@@ -758,8 +757,6 @@ cudaError_t launch_ffma_kernel(const A& a, const AttnPlan& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  if constexpr (IsShared<A>::value)
-    return launch_behind(cache_attn_ffma_kernel<H, F, A>, dim3(p.div.ctas), F::kThreads, F::smem(a.c.d), s, a, p);
   cache_attn_ffma_kernel<H, F, A><<<p.div.ctas, F::kThreads, F::smem(a.c.d), s>>>(a, p);
   return cudaGetLastError();
 }

@@ -80,12 +80,6 @@ __device__ __forceinline__ float* slot_o(const CacheAttnArgs& a, const AttnPlan&
          static_cast<int64_t>(slot) * p.rows * a.c.d;
 }
 
-// Where a kernel works out of what the one before it has written.
-__device__ __forceinline__ void wait_for_plan(const CacheAttnArgs&) {}
-__device__ __forceinline__ void wait_for_plan(const SharedAttnArgs&) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // The join is launched while the kernel that writes the parts still runs
 // (programmatic dependent launch): the kernel allows it at its start, the join
 // works out where its rows lie and then waits for the kernel's end.
@@ -138,29 +132,13 @@ struct SharedShape {
   int tile, rows, ctas, lead;
   bool quads;
 };
-SharedShape decode_shape();
+SharedShape decode_shape(bool k8);
 SharedShape tree_shape(int d, bool two);
 SharedShape ffma_shape(SharedKernel k);
 SharedKernel ffma_kernel(int64_t rows, int d);
 cudaError_t launch_shared_decode(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s);
 cudaError_t launch_shared_tree(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s);
 cudaError_t launch_shared_ffma(const SharedAttnArgs& a, const AttnPlan& p, SharedKernel k, bool k8, cudaStream_t s);
-
-// A launch that may begin before the one before it on the stream has ended.
-template <typename... K, typename... X>
-cudaError_t launch_behind(void (*kernel)(K...), dim3 grid, int threads, int smem, cudaStream_t s, X... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 // Joins the parts of the units that several CTAs shared.
 cudaError_t launch_cache_attn_join(const CacheAttnArgs& a, const AttnPlan& p, bool bf16,

@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t rows = head_rows(a);
 
   allow_join();
-  wait_for_plan(a);
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   typename IsShared<A>::Walk u;
   for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
@@ -630,13 +629,12 @@ cudaError_t launch_t(const A& a, const AttnPlan& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  if constexpr (IsShared<A>::value) {
-    return launch_behind(cache_decode_kernel<k8, D, A>, dim3(p.div.ctas), kThreads, S::kSmem, s, a, p);
-  } else {
-    cache_decode_kernel<k8, D, A><<<p.div.ctas, kThreads, S::kSmem, s>>>(a, p);
-    e = cudaGetLastError();
+  cache_decode_kernel<k8, D, A><<<p.div.ctas, kThreads, S::kSmem, s>>>(a, p);
+  e = cudaGetLastError();
+  if constexpr (IsShared<A>::value)
+    return e;
+  else
     return e == cudaSuccess ? launch_cache_attn_join(a, p, true, s) : e;
-  }
 }
 
 template <typename A>
@@ -657,7 +655,7 @@ cudaError_t launch_cache_decode(const CacheAttnArgs& a, bool k8, cudaStream_t s)
   return by_type(a, p, k8, s);
 }
 
-SharedShape decode_shape() { return SharedShape{kTile, kRows, kDecodeCtas, 1024 / kTile, false}; }
+SharedShape decode_shape(bool k8) { return SharedShape{kTile, kRows, kDecodeCtas, k8 ? 6 : 8, false}; }
 
 cudaError_t launch_shared_decode(const SharedAttnArgs& a, const AttnPlan& p, bool k8, cudaStream_t s) {
   return by_type(a, p, k8, s);

@@ -9,7 +9,9 @@
 // lots, which puts a decode step on the tensor cores; a sequence's own part as
 // before.  Both run the kernels of ra_cache_attention over a list of stretches
 // (ra_paged.cuh), so that pages, types, masks, the division of ragged work and
-// the parts of shared units are theirs.  Each launch begins behind the one before:
+// the parts of shared units are theirs.  The launches, one behind the other (one
+// that may begin ahead of its turn takes SMs from the one before it: 64 samples of
+// 16384 tokens 93 us where all may, 78 where none does):
 //   plan      one block: groups, their common tokens, the rows, the stretches
 //   prefixes  a stretch per lot of a group
 //   own parts a stretch per sequence (in one launch with the prefixes where the
@@ -26,11 +28,14 @@ namespace {
 constexpr int kPlanThreads = 1024;    // at most
 constexpr int kPlanSequences = 2048;  // 32 bytes of shared memory each
 constexpr int kTile = 128;            // a multiple of every kernel's key tile
-// Bytes of repeated prefixes below which they are read again: some 30 us at the
-// rate of the decode kernel.  (us shared, not shared: 3 sequences of 1100, 2 heads
-// of 64, 20.7 12.5; 4 of 16384, 8 heads of 128, bf16, 203 MB, 50 50; 16 of 4096,
-// 260 MB, 44 42; 64 of 1024, 297 MB, 52 53; 16 of 16384, 1 GB, 60 108; out of 8 bits
-// 101 MB 50 48, 149 MB 59 58, 507 MB 58 114; f32 162 MB 81 75, 127 MB 77 84.)
+// Bytes of repeated prefixes below which they are read again: some 25 us at the
+// rate of the decode kernel, which plan, second launch and join take.  (us shared,
+// not shared, tails of 100.  bf16, 8 heads of 128: 4 sequences of 8192, 102 MB, 36
+// 36; 4 of 16384, 203 MB, 42 50; 16 of 4096, 260 MB, 48 42; 64 of 1024, 297 MB, 61
+// 54; 16 of 8192, 511 MB, 49 63; 64 of 16384, 77 341.  Out of 8 bits: 4 of 8192, 51 MB,
+// 38 36; 4 of 16384, 101 MB, 42 48; 16 of 4096, 130 MB, 52 46; 64 of 2048, 281 MB, 66
+// 83.  2 heads of 64: 64 of 8192, 268 MB, 46 44.  f32, 4 heads of 80: 4 of 8192,
+// 64 MB, 50 50; 16 of 2048, 84 MB, 59 46; 16 of 4096, 162 MB, 67 75.)
 constexpr int64_t kWorthSharing = 160ll << 20;
 constexpr int kRuns = 9;              // lengths of a run that are tried
 
@@ -99,7 +104,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   int32_t* first = common + G;   // [G] its first live sequence
   int32_t* rows = first + G;     // [G] live rows
   int32_t* lots = rows + G;      // [G] live sequences, then the first lot
-  allow_join();
   if (tid < kRuns) runs[tid] = 0;
   if (tid == 0) again = 0;
   for (int i = tid; i < G; i += blockDim.x) {
@@ -292,7 +296,6 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
   const int quad = static_cast<int>(item % slices) * kQuads;
   const int64_t row = item / slices * 32 + lane;
   const bool here = row < j.all_rows;
-  wait_for_parts();
   const int w = static_cast<int>(row % j.rows1);  // within its sequence and key head
   const int head = static_cast<int>(row / j.rows1 % c.heads);
   const int b = static_cast<int>(row / j.rows1 / c.heads);
@@ -410,7 +413,8 @@ template <typename E, int kSplit>
 cudaError_t join(const JoinArgs& j, int64_t items, cudaStream_t s) {
   constexpr int kItems = kJoinThreads / 32 / kSplit;
   const dim3 grid(static_cast<unsigned>((items + kItems - 1) / kItems));
-  return launch_behind(shared_join_kernel<E, kSplit>, grid, kJoinThreads, 0, s, j);
+  shared_join_kernel<E, kSplit><<<grid, kJoinThreads, 0, s>>>(j);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------ the workspace
@@ -465,7 +469,7 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
     kernel[1] = rows1 > kDecodeRows ? kernel[0] : SharedKernel::kDecode;
   }
   for (int z = 0; z < 2; ++z)
-    shape[z] = kernel[z] == SharedKernel::kDecode                                            ? decode_shape()
+    shape[z] = kernel[z] == SharedKernel::kDecode                                            ? decode_shape(k8)
                : kernel[z] == SharedKernel::kTreeOne || kernel[z] == SharedKernel::kTreeTwo
                    ? tree_shape(a.c.d, kernel[z] == SharedKernel::kTreeTwo)
                    : ffma_shape(kernel[z]);
@@ -574,7 +578,7 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
   // Four warps to a row's parts where those of a single group may be many.
   const int64_t items = (j.all_rows + 31) / 32 * (a.c.d / 4 / kQuads);
   const int64_t units = a.c.heads * ((stacked + pl.lot_rows - 1) / pl.lot_rows);
-  const bool many = shape[0].ctas > 8 * units;
+  const bool many = shape[0].ctas > 16 * units;
   if (dense == RA_BF16) return many ? join<__nv_bfloat16, 4>(j, items, s) : join<__nv_bfloat16, 1>(j, items, s);
   return many ? join<float, 4>(j, items, s) : join<float, 1>(j, items, s);
 }

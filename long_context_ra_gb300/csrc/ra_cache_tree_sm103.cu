@@ -544,7 +544,6 @@ __global__ void __launch_bounds__(Roles<Form<k8, kTwo, A>::kWide>::kThreads, 1)
     tmem_alloc(base + L::kMisc, kTmemCols);
     tmem_relinquish();
   }
-  wait_for_plan(a);
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   tc_fence_before();
   __syncthreads();
@@ -1340,8 +1339,8 @@ cudaError_t launch_t(const A& a, const AttnPlan& plan, cudaStream_t s) {
   p.div.tile = L::kKeys;
   if constexpr (IsShared<A>::value) {
     if (!encode_single_rows(&tq, a.q, static_cast<int64_t>(a.c.B) * a.Hq * a.c.T, D)) return cudaErrorUnknown;
-    return launch_behind(cache_tree_kernel<k8, D, kTwo, A>, dim3(p.div.ctas), kThreads, L::kSmem, s, a, p, tk, tv,
-                         tq);
+    cache_tree_kernel<k8, D, kTwo, A><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv, tq);
+    return cudaGetLastError();
   } else {
     if (!encode_rows(&tq, a.q, static_cast<int64_t>(a.c.B) * a.Hq * a.c.T, D)) return cudaErrorUnknown;
     cache_tree_kernel<k8, D, kTwo, A><<<p.div.ctas, kThreads, L::kSmem, s>>>(a, p, tk, tv, tq);

@@ -36,8 +36,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;  // of a cluster
 
 // h + l, |l| at most half a step of h.
@@ -195,9 +193,10 @@ struct Ask {
 // leaves in shared memory, so that the search goes on inside one of them.
 constexpr int kParts = 8;
 
-template <typename E, bool kDraft>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename E, bool kDraft, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ int32_t parent[];                        // [T]
   int32_t* tokens = parent + a.T;                            // [T]
   int32_t* refused = tokens + a.T;                           // [T]
@@ -438,12 +437,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster.sync();  // no CTA's sums go while another reads them
 }
 
-template <typename E, bool kDraft>
-cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
-  // All clusters at once on the SMs, two CTAs on each: more CTAs shorten a
-  // sequence's chain, waves lengthen it.
-  int ctas = kMostCtas;
-  while (ctas > 1 && static_cast<int64_t>(a.B) * ctas > 2 * device_sm_count()) ctas /= 2;
+template <typename E, bool kDraft, int kThreads>
+cudaError_t launch_k(const VerifyArgs& a, int ctas, cudaStream_t s) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = ctas;
@@ -456,18 +451,32 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  static_assert(kVerifyNodes * 24 + kWarps * kParts * 32 * 8 <= 64 * 1024, "shared memory");
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(verify_kernel<E, kDraft>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(verify_kernel<E, kDraft, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kVerifyNodes * 24);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  return cudaLaunchKernelEx(&cfg, verify_kernel<E, kDraft>, a);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<E, kDraft, kThreads>, a);
+}
+
+template <typename E, bool kDraft>
+cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
+  // All clusters at once on the SMs, 1024 threads on each: few sequences take
+  // CTAs of more threads, many of fewer (which spread more evenly over the SMs),
+  // and only then fewer CTAs.  (V = 131072, fp32: 64 sequences 27 us with 256
+  // threads, 31 with 128; 128 sequences 39 with 128, 41 with 4 CTAs of 512; 512 of
+  // 32768 39 and 50.)
+  const int64_t held = static_cast<int64_t>(device_sm_count()) * 1024;
+  int ctas = kMostCtas;
+  if (static_cast<int64_t>(a.B) * ctas * 512 <= held) return launch_k<E, kDraft, 512>(a, ctas, s);
+  if (static_cast<int64_t>(a.B) * ctas * 256 <= held) return launch_k<E, kDraft, 256>(a, ctas, s);
+  while (ctas > 1 && static_cast<int64_t>(a.B) * ctas * 128 > held) ctas /= 2;
+  return launch_k<E, kDraft, 128>(a, ctas, s);
 }
 
 }  // namespace
