@@ -183,7 +183,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   allow_join();
   const int64_t run = division_start(c, p.div, blockIdx.x, sh);
   typename IsShared<A>::Walk u;
-  for (u.start(c, p.div, sh, run); !u.done(); u.next(c, p.div)) {
+  u.start(c, p.div, sh, run);
+
+  // ---- page numbers.  A chunk lies in `per` pages (granules of min(page,
+  // 32) rows); lane i holds granule base * per + i.  A unit's first are looked up
+  // before the one ahead of it is joined.
+  const int gshift = min(c.page_shift, 5), per = kChunk >> gshift;
+  auto look_up = [&](const typename IsShared<A>::Walk& w, int base) {
+    const int chunk = base + lane / per;
+    const int64_t at = (w.first + chunk) * kTile + warp * kChunk + ((lane % per) << gshift);
+    if (w.first + chunk >= w.last || at >= w.seq.keys()) return -1;
+    const int64_t col = at >> c.page_shift;
+    const int page = col < columns_of(c, w.b) ? pages_of(c, w.b)[col] : -1;
+    if (page >= 0 && page < c.pages) return page;
+    flag_page(c.status);
+    return -1;
+  };
+  const int batch = 32 / per;  // chunks whose pages the lanes hold
+  int pg = -1, nx = -1;
+  if (!u.done()) {
+    pg = look_up(u, 0);
+    nx = look_up(u, batch);
+  }
+  while (!u.done()) {
     const int head = u.unit / p.row_tiles;
     const int64_t r0 = static_cast<int64_t>(u.unit % p.row_tiles) * kRows;
     const int64_t q0 = (static_cast<int64_t>(u.b) * c.heads + head) * rows + r0;
@@ -191,23 +213,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n = static_cast<int>(u.last - u.first);  // chunks of this warp
     const int64_t key0 = u.first * kTile + warp * kChunk;
 
-    // ---- page numbers.  A chunk lies in `per` pages (granules of min(page,
-    // 32) rows); lane i holds granule base * per + i.
-    const int gshift = min(c.page_shift, 5), per = kChunk >> gshift;
-    int pg = -1, nx = -1;
-    const int32_t* table = pages_of(c, u.b);
-    const int columns = columns_of(c, u.b);
-    auto pages = [&](int base) {
-      const int chunk = base + lane / per;
-      const int64_t at = key0 + static_cast<int64_t>(chunk) * kTile + ((lane % per) << gshift);
-      if (chunk >= n || at >= keys) return -1;
-      const int64_t col = at >> c.page_shift;
-      const int page = col < columns ? table[col] : -1;
-      if (page >= 0 && page < c.pages) return page;
-      flag_page(c.status);
-      return -1;
-    };
-    const int batch = 32 / per;  // chunks whose pages the lanes hold
     uint32_t left_out = 0;       // of the chunk loaded last: a bit per 8 rows not in the cache
     uint32_t left_ring = 0;      // the same of the chunks under way, 4 bits each, newest lowest
     const int64_t in_page = (int64_t{1} << c.page_shift) - 1;
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool v = m & 1;
       if (!v && i > 0 && i % batch == 0) {
         pg = nx;
-        nx = pages(i + batch);
+        nx = look_up(u, i + batch);
       }
       const int64_t pos = key0 + static_cast<int64_t>(i) * kTile;
       const uint32_t dst = ring + (m % S::kStages) * S::kStage;
@@ -262,8 +267,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!v) left_ring = (left_ring << 4) | left_out;
     };
 
-    pg = pages(0);
-    nx = pages(batch);
 #pragma unroll 1
     for (int m = 0; m < S::kStages - 1; ++m) {
       if (m < 2 * n) issue(m);
@@ -283,8 +286,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     float scale[2];
     int tq[2], mask_b[2];  // a row's token and sequence
     SeqInfo seq[2];        // the context and new tokens that it may see
+    bool two;              // rows 8 .. 15 hold queries too
+    if constexpr (kShared)
+      two = c.list[u.b].rows > 8;
+    else
+      two = rows - r0 > 8;
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) qf[st][1] = qf[st][3] = 0u;
+    scale[1] = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !two) break;
       bool real;
       int64_t at;
       if constexpr (kShared) {
@@ -389,7 +401,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           ks[1] = exp_scale(ek >> 8);
         }
 #pragma unroll
-        for (int z = 0; z < 4; ++z) s[j][z] *= k8 ? scale[z / 2] * ks[z % 2] : scale[z / 2];
+        for (int z = 0; z < 2; ++z) s[j][z] *= k8 ? scale[0] * ks[z] : scale[0];
+        if (two) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) s[j][2 + z] *= k8 ? scale[1] * ks[z] : scale[1];
+        }
       }
       const uint32_t vb = arrive(2 * i + 1);
       float ev[4][2];  // log2 of the V scales of this lane's columns
@@ -408,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const int j = x / 4, z = x % 4;
+          if (z >= 2 && !two) continue;
           if (((out >> j) & 1u) || !sees(a, seq[z / 2], mask_b[z / 2], tq[z / 2], pos + 8 * j + 2 * t + z % 2)) {
             seen &= ~(1u << x);
             s[j][z] = -INFINITY;
@@ -422,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int h = 0; h < 2; ++h) {
         xm[h] = -INFINITY;
         ym[h] = -INFINITY;
+        if (h == 1 && !two) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           xm[h] = fmax3(xm[h], s[j][2 * h], s[j][2 * h + 1]);
@@ -433,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (__any_sync(0xffffffffu, pass)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
           float x = fmaxf(m[h], xm[h]), y = fmaxf(mo[h], ym[h]);
 #pragma unroll
           for (int w = 1; w < 4; w <<= 1) {
@@ -454,6 +473,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t pf[2][4];  // A fragments of the two halves of the chunk
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !two) {
+          pf[0][1] = pf[0][3] = pf[1][1] = pf[1][3] = 0u;
+          break;
+        }
         const float ref = m[h] == -INFINITY ? 0.f : m[h];
         const float refo = mo[h] == -INFINITY ? 0.f : mo[h] - kF16Offset;
 #pragma unroll
@@ -527,6 +550,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
 
+    typename IsShared<A>::Walk following = u;
+    following.next(c, p.div);
+    if (!following.done()) {
+      pg = look_up(following, 0);
+      nx = look_up(following, batch);
+    }
+
     // ---- join the four warps' states
     cp_wait<0>();
     __syncthreads();
@@ -534,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float* jm = js + kWarps * kRows * S::kLd;             // [warp][row][2]
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !two) break;
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       const bool dead = tq[h] >= seq[h].cnt;  // no query: an empty state
@@ -613,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     __syncthreads();
+    u = following;
   }
 }
 
