@@ -20,13 +20,22 @@
 // Decisions have to be those of the definition next to a border as well, and a
 // border lies in every 1 / V of the unit interval: sums of fp32 would move 1 %
 // of them.  FP64 adds at 1/64 of the rate of fp32, which would bound the pass;
-// a lane sums into a pair of floats (error-free sums, 2^-47), and 64 bits take
-// over across lanes.
+// sums are pairs of floats (error-free sums, 2^-47), and 64 bits decide.
+//
+// Measured (fp32 unless said): 128 sequences of 5 drafts, V = 131072, 40 us, of
+// which 134 MB of rows take 20 at the copy rate and the chain of a single sequence
+// some 12; bf16 37 (22 operations an element for the pairs: issue-bound).  One
+// sequence, V = 32768, 16 us.  32 trees of 32 chosen tokens, V = 100003, bf16, 27:
+// a pass over a row for every node of the path that refuses a token, each load,
+// cluster barrier and decision, one behind the other.  There the sums of all warps
+// go to all CTAs ahead of the barrier, and the loads of the parts are under way
+// together (31 us without).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <utility>
 
 #include "ra_internal.h"
 #include "ra_serve.h"
@@ -83,21 +92,21 @@ struct Row {
   const E* p;
   const E* q;
   int64_t V;
-  int shift;
+  int shift, whole;  // pieces from here on do not end in the row
   Pair c;
   const int32_t* refused;  // tokens that are out (without q)
   int n_refused;
 
-  __device__ int64_t pieces() const { return (V + shift + Piece<E>::kN - 1) / Piece<E>::kN; }
+  __device__ int pieces() const { return static_cast<int>((V + shift + Piece<E>::kN - 1) / Piece<E>::kN); }
 
-  __device__ __forceinline__ Piece<E> load(const E* row, int64_t v) const {
+  __device__ __forceinline__ Piece<E> load(const E* row, int v) const {
     constexpr int kN = Piece<E>::kN;
-    const int64_t first = v * kN - shift;
-    if (first >= 0 && first + kN <= V) {
+    if (v >= (shift > 0) && v < whole) {
       Piece<E> x;
-      x.w = __ldg(reinterpret_cast<const uint4*>(row + first));
+      x.w = __ldg(reinterpret_cast<const uint4*>(row - shift) + v);
       return x;
     }
+    const int64_t first = static_cast<int64_t>(v) * kN - shift;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -113,7 +122,7 @@ struct Row {
 
   // f(i, rest) for the elements of piece v, whose bytes are x and y
   template <typename F>
-  __device__ __forceinline__ void each(int64_t v, const Piece<E>& x, const Piece<E>& y, F f) const {
+  __device__ __forceinline__ void each(int v, const Piece<E>& x, const Piece<E>& y, F f) const {
     constexpr int kN = Piece<E>::kN;
     uint32_t out = 0;  // bit i: element i was refused
     if (!kDraft)
@@ -130,23 +139,24 @@ struct Row {
     }
   }
 
-  // The sum of pieces first, first + step, .. below last.
-  __device__ __forceinline__ Pair sum(int64_t first, int64_t last, int step) const {
-    constexpr int kAhead = kDraft ? 2 : 4;
+  // Piece v of the rows, and what it adds to a sum: nothing behind `last`.
+  __device__ __forceinline__ void load(int v, int last, Piece<E>& x, Piece<E>& y) const {
+    if (v >= last) return;
+    x = load(p, v);
+    if (kDraft) y = load(q, v);
+  }
+  __device__ __forceinline__ void add(int v, int last, const Piece<E>& x, const Piece<E>& y, Pair& s) const {
+    if (v < last) each(v, x, y, [&](int, Pair r) { s.add(r.h, r.l); });
+  }
+  __device__ __forceinline__ Pair sum(int v, int last, const Piece<E>& x, const Piece<E>& y) const {
     Pair s{0.f, 0.f};
-    for (int64_t v = first; v < last; v += kAhead * step) {
-      Piece<E> x[kAhead], y[kAhead];
-#pragma unroll
-      for (int z = 0; z < kAhead; ++z)
-        if (v + z * step < last) {
-          x[z] = load(p, v + z * step);
-          if (kDraft) y[z] = load(q, v + z * step);
-        }
-#pragma unroll
-      for (int z = 0; z < kAhead; ++z)
-        if (v + z * step < last) each(v + z * step, x[z], y[z], [&](int, Pair r) { s.add(r.h, r.l); });
-    }
+    add(v, last, x, y, s);
     return s;
+  }
+  __device__ __forceinline__ Pair sum(int v, int last) const {
+    Piece<E> x, y;
+    load(v, last, x, y);
+    return sum(v, last, x, y);
   }
 };
 
@@ -197,6 +207,7 @@ template <typename E, bool kDraft, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
   constexpr int kWarps = kThreads / 32;
+  constexpr int kAhead = kDraft ? 2 : 4;  // rounds of loads under way
   extern __shared__ int32_t parent[];                        // [T]
   int32_t* tokens = parent + a.T;                            // [T]
   int32_t* refused = tokens + a.T;                           // [T]
@@ -204,7 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   float* ps = us + a.T;                                      // [T] p of the parent's row at the token
   float* qs = ps + a.T;                                      // [T]
   __shared__ float2 parts[kWarps][kParts][32];
-  __shared__ double warp_sums[kWarps], cta_sums[kMostCtas], cta_sum[2], row_total;
+  // Every CTA has the sums of all warps of the cluster, those of one row until it
+  // is through with the next.
+  __shared__ float2 warp_sums[2][kMostCtas * kWarps];
+  __shared__ double row_total;
   __shared__ Ask ask;
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
@@ -224,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     return;  // the whole cluster
   }
 
+  auto begun = cluster.barrier_arrive();
   // ---- the drafts and their own probabilities; -1: not a node of the tree
   for (int t = threadIdx.x; t < count; t += kThreads) {
     const int above = a.parent ? a.parent[row0 + t] : t - 1;
@@ -237,51 +252,71 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     qs[t] = good && kDraft ? as_float(static_cast<const E*>(a.draft)[at]) : 1.f;
   }
   __syncthreads();
+  bool met = false;
 
   Row<E, kDraft> row;
   row.V = a.V;
   row.refused = refused;
   // The row's sum, and in every CTA the sums of its parts.
   int turn = 0;
-  int64_t w0 = 0, w1 = 0, each = 0;  // this warp's pieces; of a part
+  int w0 = 0, w1 = 0, each = 0;  // this warp's pieces; of a part
   auto row_sum = [&](const Ask& x) {
     const int64_t at = (row0 + x.node) * a.V;
     row.p = static_cast<const E*>(a.probs) + at;
     row.q = static_cast<const E*>(kDraft ? a.draft : a.probs) + at;
     row.shift = static_cast<int>(at % Piece<E>::kN);
+    row.whole = static_cast<int>((a.V + row.shift) / Piece<E>::kN);
     row.c = x.c;
     row.n_refused = x.n_refused;
-    const int64_t n = row.pieces();
-    const int64_t of_warp = (n + ctas * kWarps - 1) / (ctas * kWarps);
+    const int n = row.pieces();
+    const int of_warp = (n + ctas * kWarps - 1) / (ctas * kWarps);
     w0 = min(n, (rank * kWarps + warp) * of_warp);
     w1 = min(n, w0 + of_warp);
     each = (of_warp + kParts * 32 - 1) / (kParts * 32) * 32;  // whole rounds of the warp
     Pair all{0.f, 0.f};
-    for (int i = 0; i < kParts; ++i) {
-      const int64_t first = min(w1, w0 + i * each);
-      const Pair part = row.sum(first + lane, min(w1, first + each), 32);
+    auto close = [&](int i, Pair part) {
       parts[warp][i][lane] = make_float2(part.h, part.l);
       all.add(part.h, part.l);
+    };
+    if (each == 32) {
+      // a round a part: the loads of some parts under way together
+#pragma unroll 1
+      for (int i = 0; i < kParts; i += kAhead) {
+        Piece<E> p[kAhead], q[kAhead];
+        const int v = w0 + i * 32 + lane;
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z) row.load(v + 32 * z, w1, p[z], q[z]);
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z) close(i + z, row.sum(v + 32 * z, w1, p[z], q[z]));
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kParts; ++i) {
+        const int last = min(w1, w0 + (i + 1) * each);
+        Pair part{0.f, 0.f};
+        for (int v = w0 + i * each + lane; v < last; v += kAhead * 32) {
+          Piece<E> p[kAhead], q[kAhead];
+#pragma unroll
+          for (int z = 0; z < kAhead; ++z) row.load(v + 32 * z, last, p[z], q[z]);
+#pragma unroll
+          for (int z = 0; z < kAhead; ++z) row.add(v + 32 * z, last, p[z], q[z], part);
+        }
+        close(i, part);
+      }
     }
     all = sum_lanes(all);
-    if (lane == 0) warp_sums[warp] = all.value();
-    __syncthreads();
     turn ^= 1;
-    if (threadIdx.x == 0) {
-      double s = 0.0;
-      for (int i = 0; i < kWarps; ++i) s += warp_sums[i];
-      cta_sum[turn] = s;
-    }
+    if (!met) cluster.barrier_wait(std::move(begun));  // every CTA is there to be written to
+    met = true;
+    if (lane < ctas) *cluster.map_shared_rank(&warp_sums[turn][rank * kWarps + warp], lane) = make_float2(all.h, all.l);
     cluster.sync();
-    if (static_cast<int>(threadIdx.x) < ctas)
-      cta_sums[threadIdx.x] = *cluster.map_shared_rank(&cta_sum[turn], threadIdx.x);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      double s = 0.0;
-      for (int i = 0; i < ctas; ++i) s += cta_sums[i];
-      row_total = s;
+    if (warp == 0) {
+      Pair total{0.f, 0.f};
+      for (int i = lane; i < ctas * kWarps; i += 32) total.add(warp_sums[turn][i].x, warp_sums[turn][i].y);
+      total = sum_lanes(total);
+      if (lane == 0) row_total = total.value();
+      __syncwarp();
     }
-    __syncthreads();
   };
 
   // ---- the walk, by the first warp of every CTA alike (64-bit arithmetic is slow:
@@ -362,11 +397,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     row_sum(x);
     if (x.last) break;
   }
+  __syncthreads();
 
   // ---- the next token
   if (!(row_total > 0.0)) {  // nothing is left: p itself
     const Ask x{ask.node, 0, Pair{0.f, 0.f}, true};
     row_sum(x);
+    __syncthreads();
   }
   const double all = row_total;
   const bool some = all > 0.0 && all < INFINITY;
@@ -378,37 +415,37 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     }
   }
   if (some) {
-    // CTA, warp, part, piece, element: the first warp finds the warp
+    // warp, part, piece, element: the first warp finds the warp
     __shared__ int found_warp;
     __shared__ double found_before;
     const double target = us[0] * all;
     if (warp == 0) {
-      double before = 0.0;
-      int w = -1;
-      if (crossing(lane < ctas ? cta_sums[lane] : 0.0, target, before) == rank)
-        w = crossing(lane < kWarps ? warp_sums[lane] : 0.0, target, before);
-      if (lane == 0) {
-        found_warp = w;
-        found_before = before;
-      }
+      // a lane has the sums of some neighbouring warps
+      const int n = ctas * kWarps, of_lane = (n + 31) / 32;
+      auto sum_of = [&](int w) { return w < n ? static_cast<double>(warp_sums[turn][w].x) + warp_sums[turn][w].y : 0.0; };
+      double before = 0.0, mine = 0.0;
+      for (int i = 0; i < of_lane; ++i) mine += sum_of(lane * of_lane + i);
+      int found = max(crossing(mine, target, before), 0) * of_lane;
+      if (of_lane > 1) found += max(crossing(lane < of_lane ? sum_of(found + lane) : 0.0, target, before), 0);
+      if (lane == 0) found_before = before;
+      if (lane == 0) found_warp = found - rank * kWarps;
     }
     __syncthreads();
     if (found_warp == warp) {
       double before = found_before;
-      // a lane adds up the lanes' sums of a part
-      double mine = 0.0;
-      if (lane < kParts) {
-        Pair s{0.f, 0.f};
-        for (int i = 0; i < 32; ++i) s.add(parts[warp][lane][i].x, parts[warp][lane][i].y);
-        mine = s.value();
+      double mine = 0.0;  // a lane's: of a part
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const double sum = sum_lanes(Pair{parts[warp][i][lane].x, parts[warp][i][lane].y}).value();
+        if (lane == i) mine = sum;
       }
       const int part = max(crossing(mine, target, before), 0);
-      const int64_t r0 = min(w1, w0 + part * each), r1 = min(w1, r0 + each);
+      const int r0 = min(w1, w0 + part * each), r1 = min(w1, r0 + each);
       // its pieces, 32 at a time, up to those that pass the target
-      int64_t v0 = r0;
+      int v0 = r0;
       double sofar = before;
-      for (int64_t i = r0; i < r1; i += 32) {
-        const double sum = sum_lanes(row.sum(i + lane, min(r1, i + lane + 1), 1)).value();
+      for (int i = r0; i < r1; i += 32) {
+        const double sum = sum_lanes(row.sum(i + lane, r1)).value();
         if (sum > 0.0) {
           v0 = i;
           before = sofar;
@@ -416,16 +453,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         }
         sofar += sum;
       }
-      const int at = crossing(row.sum(v0 + lane, min(r1, v0 + lane + 1), 1).value(), target, before);
+      const int at = crossing(row.sum(v0 + lane, r1).value(), target, before);
       if (at >= 0 && lane == at) {
-        const int64_t v = v0 + at;
+        const int v = v0 + at;
         const Piece<E> x = row.load(row.p, v), y = row.load(row.q, v);
         int64_t found = -1;
         bool past = false;
         Pair sum{0.f, 0.f};
         row.each(v, x, y, [&](int i, Pair r) {
           if (!past && r.h + r.l > 0.f) {
-            found = v * Piece<E>::kN - row.shift + i;
+            found = static_cast<int64_t>(v) * Piece<E>::kN - row.shift + i;
             sum.add(r.h, r.l);
             past = before + sum.value() > target;
           }
@@ -434,7 +471,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       }
     }
   }
-  cluster.sync();  // no CTA's sums go while another reads them
 }
 
 template <typename E, bool kDraft, int kThreads>
@@ -469,8 +505,8 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   // All clusters at once on the SMs, 1024 threads on each: few sequences take
   // CTAs of more threads, many of fewer (which spread more evenly over the SMs),
   // and only then fewer CTAs.  (V = 131072, fp32: 64 sequences 27 us with 256
-  // threads, 31 with 128; 128 sequences 39 with 128, 41 with 4 CTAs of 512; 512 of
-  // 32768 39 and 50.)
+  // threads, 31 with 128; 128 sequences 40 with 128, 43 with 4 CTAs of 512; 512 of
+  // 32768 41 and 51.)
   const int64_t held = static_cast<int64_t>(device_sm_count()) * 1024;
   int ctas = kMostCtas;
   if (static_cast<int64_t>(a.B) * ctas * 512 <= held) return launch_k<E, kDraft, 512>(a, ctas, s);
