@@ -630,7 +630,7 @@ RA_API int64_t ra_cache_attention_shared_workspace_bytes(int32_t B, int32_t Hq, 
  * first; samples of one prompt are forks of one row.
  *   source     int32 [n], any of 0 .. B - 1, each as often as it is wanted.
  *   table_out  int32 [n, width], held_out, lens_out int32 [n]: written; they
- *              may not overlap table, held, lens.
+ *              overlap neither ref, table, held, lens and source nor one another.
  *   page       rows of a page, as ra_cache has it.
  * Errors: RA_ERR_INVALID_ARG (null pointer, negative size, overlap),
  * RA_ERR_UNSUPPORTED (page; B x width or n x width over 2^31 - 1),
@@ -651,7 +651,8 @@ RA_API ra_status ra_pages_fork(int32_t* ref, int64_t pages, const int32_t* table
  * (sequence, column).
  *   granted   int32 [B], written: the new tokens that have room (count, or 0):
  *             the `count` of the calls that follow.
- *   src, dst  int32 [B], written: pages to copy, -1 for none.
+ *   src, dst  int32 [B], written: pages to copy, -1 for none.  The three overlap
+ *             neither one another nor what is read (granted may be `count`).
  * All or nothing: with too few free pages every granted is 0, nothing else
  * changes, and ra_last_device_status returns RA_ERR_PAGE.  So it does, for
  * that sequence alone, where a sequence would pass the table's width, does not

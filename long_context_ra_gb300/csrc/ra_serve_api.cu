@@ -163,6 +163,15 @@ ra_status check_attention(const void* q, const ra_cache* cache, const int32_t* t
 // A type that fits the cache, where a call has no tensors beside it.
 ra_dtype own_dtype(const ra_cache* cache) { return cache && cache->dtype != RA_E4M3 ? cache->dtype : RA_F32; }
 
+struct Ints {
+  const int32_t* p;
+  int64_t n;
+};
+bool overlap(const Ints& x, const Ints& y) {
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
+  return x.n > 0 && y.n > 0 && x0 < y0 + 4 * y.n && y0 < x0 + 4 * x.n;
+}
+
 // A table of pages and their counts.
 ra_status check_pages(int32_t* ref, int64_t pages, const int32_t* table, const int32_t* held, const int32_t* lens,
                       int32_t width, int32_t page, int32_t B, bool lens_needed, PageTableArgs* a) {
@@ -413,12 +422,12 @@ RA_API ra_status ra_pages_fork(int32_t* ref, int64_t pages, const int32_t* table
     return RA_ERR_MISALIGNED;
   if (n == 0) return RA_OK;
   if (!source || (width > 0 && !table_out) || !held_out || !lens_out) return RA_ERR_INVALID_ARG;
-  // a new row that lies over an old one would be read as it is written
-  const int32_t *t0 = table, *t1 = table + static_cast<int64_t>(B) * width;
-  if (width > 0 && B > 0 && table_out < t1 && t0 < table_out + static_cast<int64_t>(n) * width)
-    return RA_ERR_INVALID_ARG;
-  if (B > 0 && ((held_out < held + B && held < held_out + n) || (lens_out < lens + B && lens < lens_out + n)))
-    return RA_ERR_INVALID_ARG;
+  // what is written would be read by another row's block
+  const Ints out[] = {{table_out, static_cast<int64_t>(n) * width}, {held_out, n}, {lens_out, n}};
+  const Ints in[] = {{ref, pages}, {table, static_cast<int64_t>(B) * width}, {held, B}, {lens, B}, {source, n}};
+  for (const Ints& x : out)
+    for (const Ints& y : in)
+      if (overlap(x, y)) return RA_ERR_INVALID_ARG;
   if ((st = device_ready(&a.status)) != RA_OK) return st;
   return launched(launch_pages_fork(a, source, n, table_out, held_out, lens_out, cu(stream)));
 }

@@ -505,8 +505,8 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   // All clusters at once on the SMs, 1024 threads on each: few sequences take
   // CTAs of more threads, many of fewer (which spread more evenly over the SMs),
   // and only then fewer CTAs.  (V = 131072, fp32: 64 sequences 27 us with 256
-  // threads, 31 with 128; 128 sequences 40 with 128, 43 with 4 CTAs of 512; 512 of
-  // 32768 41 and 51.)
+  // threads, 31 with 128; 128 sequences 40 with 128, 41 with 4 CTAs of 512; 512 of
+  // 32768 41 and 49.)
   const int64_t held = static_cast<int64_t>(device_sm_count()) * 1024;
   int ctas = kMostCtas;
   if (static_cast<int64_t>(a.B) * ctas * 512 <= held) return launch_k<E, kDraft, 512>(a, ctas, s);

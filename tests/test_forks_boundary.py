@@ -65,8 +65,9 @@ def test_fork_rules(L):
     assert fork(L, to=A - 76) == INV
     assert fork(L, to=A + 48) == ARCH
     assert fork(L, to=A - 80) == ARCH
-    assert fork(L, ho=A + 8) == INV and fork(L, ho=A + 12) == ARCH
-    assert fork(L, lo=A - 16) == INV and fork(L, lo=A - 20) == ARCH
+    apart = dict(ref=FAR + 4096, source=FAR + 8192, table=FAR + 12288)
+    assert fork(L, ho=A + 8, **apart) == INV and fork(L, ho=A + 12, **apart) == ARCH
+    assert fork(L, lo=A - 16, **apart) == INV and fork(L, lo=A - 20, **apart) == ARCH
 
 
 def test_reserve_rules(L):
@@ -192,3 +193,14 @@ def test_shared_attention_of_other_caches(L):
         assert w(*sizes) >= plain(*sizes)
     with pytest.raises(ValueError):
         ra.ra_cache_attention_shared(None, None, None, None, None)
+
+
+@pytest.mark.parametrize("out", ["to", "ho", "lo"])
+@pytest.mark.parametrize("near", ["ref", "table", "held", "lens", "source"])
+def test_fork_refuses_what_lies_over_its_inputs(L, out, near):
+    size = dict(ref=10, table=12, held=3, lens=3, source=5)[near]
+    far = {k: A + i * 4096 for i, k in enumerate(("ref", "table", "held", "lens", "source"))}
+    assert fork(L, **far, **{out: far[near] + 4 * (size - 1)}) == INV
+    assert fork(L, **far, **{out: far[near] - 4 * (4 if out != "to" else 19)}) == INV
+    assert fork(L, **far, **{out: far[near] + 4 * size}) == ARCH
+    assert fork(L, **far, **{out: far[near] - 4 * (5 if out != "to" else 20)}) == ARCH
