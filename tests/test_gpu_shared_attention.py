@@ -123,6 +123,19 @@ def test_tree(shape, one_mask, dtype, held, d):
     check(got, q, cache, table, lens, count, mask)
 
 
+@pytest.mark.parametrize("held,d", [(torch.bfloat16, 64), (torch.bfloat16, 128), (E4M3, 64), (E4M3, 128)])
+@pytest.mark.parametrize("Hq,T", [(1, 1), (7, 1), (2, 4), (9, 1), (3, 5), (16, 1), (2, 12)])
+def test_rows_of_a_small_unit(Hq, T, held, d):
+    """1 to 24 rows of a key head: the decode kernel works on one half of its 16 rows or on both."""
+    q, cache, table, lens, shared, cnt = make([(300, [70, 9]), (0, [200, 0, None, 1])], None, T, 2 * Hq, 2, 32, d,
+                                              torch.bfloat16, held, 6)
+    got = ra.ra_cache_attention(q, cache, table.to(DEV), i32(lens))
+    check(got, q, cache, table, lens, None, None)
+    got = ra.ra_cache_attention_shared(q[:2].contiguous(), cache, wide(table[:2], cache), i32(lens[:2]), shared[:2])
+    check(got, q[:2], cache, table[:2], lens[:2], None, None)
+    assert ra.ra_last_device_status() == 0
+
+
 WIDE = [(torch.float32, torch.float32, 80, 1), (torch.bfloat16, torch.bfloat16, 64, 1),
         (torch.bfloat16, torch.bfloat16, 128, 12), (torch.bfloat16, E4M3, 128, 40)]
 
