@@ -32,9 +32,12 @@
 // score passes it by more than 2^8: a vote per chunk instead of a row maximum.
 //
 // Measured, 32 ragged sequences of up to 32768, 8 key heads of 128, 4 queries
-// each: 8-bit cache (1.25 GB) 226 us, 5.5 TB/s, 81 % of the copy rate.  With 64
+// each: 8-bit cache (1.25 GB) 220 us, 5.7 TB/s, 84 % of the copy rate.  With 64
 // keys a chunk it took 348 us, with 32 and V behind all of K 303; the packed
-// conversions made that 230.  Pages of 32 rows and more are alike; smaller ones
+// conversions made that 230, leaving out the second 8 rows where a unit has none
+// 220.  A unit costs some 6 us beside its tiles, of which the look-up of its first
+// pages goes on while the one ahead is joined (96 sequences of up to 2048, 8 key
+// heads, 8 bits: 179 -> 165 us with both).  Pages of 32 rows and more are alike; smaller ones
 // take a look-up per 16-byte piece (32 sequences of 16384, 8 bits: 188 us with
 // pages of 32 to 256, 320 of 8 or 16; bf16 313 and 453).  One sequence of 1000 takes 12 us, most of it the
 // two launches and the chain of look-up, load and join.

@@ -61,13 +61,13 @@ struct PlanArgs {
   int lead[2];
   int ctas[2];
   int granule;   // a common part is a multiple of it
-  int lot_rows;  // query rows of a lot
+  int lot_rows, lot_shift;  // query rows of a lot, and their log2
   int group;     // query heads of a key head
   bool one_list;
 };
 
 // Inclusive scan of two values per thread over the block; `all`: the sums.
-__device__ __forceinline__ longlong2 scan_two(longlong2 x, longlong2* warps, longlong2& all) {
+__device__ __noinline__ longlong2 scan_two(longlong2 x, longlong2* warps, longlong2& all) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   auto scan = [&](longlong2 v) {
 #pragma unroll
@@ -89,6 +89,10 @@ __device__ __forceinline__ longlong2 scan_two(longlong2 x, longlong2* warps, lon
   return x;
 }
 
+// One block that runs through its code once: bound by the loads of that code as
+// much as by the chain of scans, so that loops stay loops and the scan is a
+// function (32 samples, the whole call: 78 us with all of it inlined and unrolled,
+// 75 without).
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int32_t smem[];
   __shared__ longlong2 warps[32];
@@ -106,6 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   int32_t* lots = rows + G;      // [G] live sequences, then the first lot
   if (tid < kRuns) runs[tid] = 0;
   if (tid == 0) again = 0;
+#pragma unroll 1
   for (int i = tid; i < G; i += blockDim.x) {
     common[i] = INT32_MAX;
     first[i] = B;
@@ -117,6 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   const int g1 = b0 < B && b1 == B ? G : b1;  // this thread's groups: b0 .. g1 - 1
   // ---- groups: one begins where a live sequence shares nothing
   longlong2 sum{0, 0}, all;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int n = c.lens[b], t = c.count ? c.count[b] : c.T;
     len[b] = n;
@@ -126,6 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     sum.x += n >= 0 && group[b] <= 0;
   }
   int64_t at = scan_two(sum, warps, all).x - sum.x;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     at += len[b] >= 0 && group[b] <= 0;
     if (len[b] >= 0) {
@@ -136,14 +143,17 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     group[b] = static_cast<int>(at);
   }
   __syncthreads();
+#pragma unroll 1
   for (int b = b0; b < b1; ++b)
     if (len[b] >= 0) atomicMin(common + group[b], b == first[group[b]] ? len[b] : min(len[b], row_at[b]));
   __syncthreads();
+#pragma unroll 1
   for (int g = b0; g < g1; ++g) common[g] = lots[g] > 1 ? max(common[g], 0) / a.granule * a.granule : 0;
   __syncthreads();
   // ---- rows that see a prefix
   sum = longlong2{0, 0};
   auto live_rows = [&](int b) { return common[group[b]] > 0 ? cnt[b] * a.group : 0; };
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int n = live_rows(b);
     sum.x += n;
@@ -151,13 +161,14 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   }
   int row = static_cast<int>(scan_two(sum, warps, all).x - sum.x);
   const int rows_all = static_cast<int>(all.x);
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     row_at[b] = row;
     row += live_rows(b);
   }
   __syncthreads();
   // ---- lengths: of a lot's units, and of a sequence's own
-  auto lots_of = [&](int g) { return common[g] > 0 ? (rows[g] + a.lot_rows - 1) / a.lot_rows : 0; };
+  auto lots_of = [&](int g) { return common[g] > 0 ? (rows[g] + a.lot_rows - 1) >> a.lot_shift : 0; };
   auto lot_length = [&](int g) {
     return c.heads * stretch_length(common[g] >> a.tile_shift[0], a.lead[0]);
   };
@@ -168,7 +179,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     return c.heads * stretch_length((keys + (1 << a.tile_shift[1]) - 1) >> a.tile_shift[1], a.lead[1]);
   };
   sum = longlong2{0, 0};
+#pragma unroll 1
   for (int g = b0; g < g1; ++g) sum.x += lots_of(g) * lot_length(g);
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) sum.y += length(b);
   const longlong2 own_before = scan_two(sum, warps, all);
   int64_t own_at = own_before.y - sum.y;
@@ -181,16 +194,19 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   const uint32_t even32 = static_cast<uint32_t>(even);
   auto candidate = [&](int i) { return even32 + even32 / (8 * (kRuns - 1)) * i; };
   const bool small = total < (int64_t{1} << 31);  // the products below stay in 32 bits
+#pragma unroll 1
   for (int g = b0; g < g1; ++g) {
     const int n = lots_of(g);
     if (n > 1) again = 1;
     if (n > 0 && small)
+#pragma unroll 1
       for (int i = 0; i < kRuns; ++i)
         atomicAdd(&runs[i], n * static_cast<int>((static_cast<uint32_t>(lot_length(g)) + candidate(i) - 1) / candidate(i)));
   }
   __syncthreads();
   int64_t run = even;
   bool aligned = false;
+#pragma unroll 1
   for (int i = 0; i < kRuns && again && small && !aligned; ++i) {
     const uint32_t r = candidate(i);
     aligned = runs[i] + (a.one_list ? (static_cast<uint32_t>(own_all) + r - 1) / r : 0u) <= static_cast<uint32_t>(a.ctas[0]);
@@ -202,6 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     return aligned ? (static_cast<uint32_t>(n + run - 1) / static_cast<uint32_t>(run)) * run : n;
   };
   sum = longlong2{0, 0};
+#pragma unroll 1
   for (int g = b0; g < g1; ++g) {
     const int n = lots_of(g);
     sum.x += n;
@@ -210,10 +227,12 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   longlong2 before = scan_two(sum, warps, all);
   before.x -= sum.x;
   before.y -= sum.y;
+#pragma unroll 1
   for (int g = b0; g < g1; ++g) {
     const int n = lots_of(g);
     lots[g] = static_cast<int>(before.x);
     const int64_t room = n > 0 ? lot_room(g) : 0;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       a.plan.list[0][before.x] = Stretch{common[g], 0, first[g], 0, row_at[first[g]] + i * a.lot_rows,
                                          min(a.lot_rows, rows[g] - i * a.lot_rows), before.y, room};
@@ -226,6 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   // ---- own parts
   Stretch* list = a.one_list ? a.plan.list[0] + prefixes.x : a.plan.list[1];
   if (a.one_list) own_at += prefixes.y;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     list[b] = Stretch{own(b), cnt[b], b, part(b) >> c.page_shift, ~b, a.group * c.T, own_at, length(b)};
     own_at += length(b);
@@ -488,6 +508,8 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
   pl.shared = shared;
   pl.one_list = kernel[0] == kernel[1];
   pl.lot_rows = shape[0].rows;
+  pl.lot_shift = 0;
+  while ((1 << pl.lot_shift) < pl.lot_rows) ++pl.lot_shift;
   pl.group = a.Hq / a.c.heads;
   uint8_t* at = ws + r.plan;
   auto take = [&](int64_t bytes) {

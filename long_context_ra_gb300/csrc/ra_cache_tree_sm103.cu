@@ -18,11 +18,18 @@
 // 60000, 8 heads, 64 rows: 82 -> 61 us, out of 8 bits 99 -> 80; 58 and 78 with
 // the later steps).
 //
-// Warp roles (640 threads, 96 registers each at launch):
+// Over stretches (ra_cache_attention_shared) a unit's rows come from several
+// sequences: the query warp gathers them row by row (tile::gather4).
+//
+// Warp roles (640 threads, 96 registers each at launch; the wide form below has
+// 384 of 168):
 //   warps 0-3, 4-7   softmax of stream 0, 1                            (112)
 //   warp  9          loader: TMA boxes of the key and value tiles      (112)
 //   warp  10         TMA boxes of the queries
-//   warp  11         TMEM allocator, MMA issuer
+//   warp  11         TMEM allocator, MMA issuer: the warp walks along as a whole
+//                    and one lane issues, so that its operands stay in uniform
+//                    registers (24 trees of 32 over 65536: 1087 -> 799 us, with
+//                    a shared context 553 -> 501)
 //   warps 12-19      8-bit cache: conversion, two tiles under way       (72)
 //   (bf16 cache)     warp 12: tiles that end a sequence
 // 3 x 128 x 112 + 2 x 128 x 72 = 61440 = 640 x 96.
@@ -39,16 +46,19 @@
 //
 // Code size sets the pace before anything else: 20 warps in five roles share
 // one instruction cache.  With the score and exponential loops unrolled a tile
-// of 128 keys and 256 rows took 7.3 us; rolled, 3.  Every role is a short loop
+// of 128 keys and 256 rows took 7.3 us; rolled, 3.  (Where nothing is converted and
+// two tiles of rows are at work, over stretches, the wide form has 12 warps, and
+// softmax threads of 200 registers that hold a row's 128 scores of a tile: one
+// pass over TMEM, not two.)  Every role is a short loop
 // in 32-bit arithmetic with the unit's constants taken out: a role of one warp
 // that spends some hundred instructions on an item is slower than the 1.1 us
 // of tensor time that the tile needs.
 //
 // Measured per tile of 128 keys on one SM (152 at work, d = 128): one query
-// tile, bf16 1.6 us (the tile's bytes alone take 1.5 at the copy rate), 8 bits
-// 1.9; two query tiles, bf16 2.0 us, 8 bits 2.35 (without conversion 1.8,
-// without softmax 1.85; 57 % of the issue slots are used).
-// 488 rows over 2^20 keys of 8 heads out of 8 bits: 1.97 ms, 56 % of the tensor
+// tile, bf16 1.4 us (the tile's bytes alone take 1.5 at the copy rate), 8 bits
+// 2.0; two query tiles, bf16 1.7 us, wide 1.2 (the products alone 1.1), 8 bits
+// 2.2.  d = 64: 0.7, 1.1; 1.4, 1.6.
+// 488 rows over 2^20 keys of 8 heads out of 8 bits: 1.88 ms, 59 % of the tensor
 // rate.  A unit costs some 8 us beside its tiles: pipeline start (clocks from
 // the launch: place in the division 2900, queries and first keys 6200, scores
 // 7900, probabilities 10400, first results 12300) and end (5000 for 256 rows'

@@ -22,14 +22,16 @@
 // of them.  FP64 adds at 1/64 of the rate of fp32, which would bound the pass;
 // sums are pairs of floats (error-free sums, 2^-47), and 64 bits decide.
 //
-// Measured (fp32 unless said): 128 sequences of 5 drafts, V = 131072, 40 us, of
+// Measured (fp32 unless said): 128 sequences of 5 drafts, V = 131072, 41 us, of
 // which 134 MB of rows take 20 at the copy rate and the chain of a single sequence
-// some 12; bf16 37 (22 operations an element for the pairs: issue-bound).  One
-// sequence, V = 32768, 16 us.  32 trees of 32 chosen tokens, V = 100003, bf16, 27:
+// some 11; bf16 35 (22 operations an element for the pairs: issue-bound).  One
+// sequence, V = 32768, 14.5 us.  32 trees of 32 chosen tokens, V = 100003, bf16, 25:
 // a pass over a row for every node of the path that refuses a token, each load,
-// cluster barrier and decision, one behind the other.  There the sums of all warps
-// go to all CTAs ahead of the barrier, and the loads of the parts are under way
-// together (31 us without).
+// cluster barrier and decision, one behind the other.  So the sums of all warps go
+// to all CTAs ahead of one barrier, the loads of the parts are under way together
+// (31 -> 27 us), and code that runs once stays short, since it is loaded as it
+// runs: one place that sums a row, the row's ends in a loop (27 -> 25, one sequence
+// 16 -> 14.5).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -106,16 +108,22 @@ struct Row {
       x.w = __ldg(reinterpret_cast<const uint4*>(row - shift) + v);
       return x;
     }
+    // an end of the row, the last element first; few instructions rather than fast:
+    // this stands wherever a piece is loaded
     const int64_t first = static_cast<int64_t>(v) * kN - shift;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (first + i < 0 || first + i >= V) continue;
-      const uint32_t bits = __float_as_uint(as_float(row[first + i]));
-      if (sizeof(E) == 4)
-        w[i % 4] = bits;
-      else
-        w[(i / 2) % 4] |= i & 1 ? bits : bits >> 16;
+#pragma unroll 1
+    for (int i = kN - 1; i >= 0; --i) {
+      const bool real = first + i >= 0 && first + i < V;
+      const uint32_t bits = real ? __float_as_uint(as_float(row[first + i])) : 0u;
+      if (sizeof(E) == 4) {
+        w[3] = w[2], w[2] = w[1], w[1] = w[0], w[0] = bits;
+      } else {
+        w[3] = __funnelshift_l(w[2], w[3], 16);
+        w[2] = __funnelshift_l(w[1], w[2], 16);
+        w[1] = __funnelshift_l(w[0], w[1], 16);
+        w[0] = (w[0] << 16) | (bits >> 16);
+      }
     }
     return Piece<E>{make_uint4(w[0], w[1], w[2], w[3])};
   }
@@ -207,7 +215,7 @@ template <typename E, bool kDraft, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
   constexpr int kWarps = kThreads / 32;
-  constexpr int kAhead = kDraft ? 2 : 4;  // rounds of loads under way
+  constexpr int kAhead = 2;  // rounds of loads under way; 4 are no faster
   extern __shared__ int32_t parent[];                        // [T]
   int32_t* tokens = parent + a.T;                            // [T]
   int32_t* refused = tokens + a.T;                           // [T]
@@ -273,37 +281,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     w0 = min(n, (rank * kWarps + warp) * of_warp);
     w1 = min(n, w0 + of_warp);
     each = (of_warp + kParts * 32 - 1) / (kParts * 32) * 32;  // whole rounds of the warp
-    Pair all{0.f, 0.f};
-    auto close = [&](int i, Pair part) {
-      parts[warp][i][lane] = make_float2(part.h, part.l);
-      all.add(part.h, part.l);
-    };
-    if (each == 32) {
-      // a round a part: the loads of some parts under way together
+    // Loads of some rounds of 32 pieces under way together, those of the next part
+    // too: a row of 10^5 has a few rounds a warp.
+    const int per = each / 32, rounds = (of_warp + 31) / 32;
+    Pair all{0.f, 0.f}, part{0.f, 0.f};
+    int filled = 0, left = per;
 #pragma unroll 1
-      for (int i = 0; i < kParts; i += kAhead) {
-        Piece<E> p[kAhead], q[kAhead];
-        const int v = w0 + i * 32 + lane;
+    for (int r = 0; r < rounds; r += kAhead) {
+      Piece<E> p[kAhead], q[kAhead];
+      const int v = w0 + r * 32 + lane;
 #pragma unroll
-        for (int z = 0; z < kAhead; ++z) row.load(v + 32 * z, w1, p[z], q[z]);
+      for (int z = 0; z < kAhead; ++z) row.load(v + 32 * z, w1, p[z], q[z]);
 #pragma unroll
-        for (int z = 0; z < kAhead; ++z) close(i + z, row.sum(v + 32 * z, w1, p[z], q[z]));
-      }
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < kParts; ++i) {
-        const int last = min(w1, w0 + (i + 1) * each);
-        Pair part{0.f, 0.f};
-        for (int v = w0 + i * each + lane; v < last; v += kAhead * 32) {
-          Piece<E> p[kAhead], q[kAhead];
-#pragma unroll
-          for (int z = 0; z < kAhead; ++z) row.load(v + 32 * z, last, p[z], q[z]);
-#pragma unroll
-          for (int z = 0; z < kAhead; ++z) row.add(v + 32 * z, last, p[z], q[z], part);
+      for (int z = 0; z < kAhead; ++z) {
+        row.add(v + 32 * z, w1, p[z], q[z], part);
+        if (--left == 0) {
+          all.add(part.h, part.l);
+          if (filled < kParts) parts[warp][filled++][lane] = make_float2(part.h, part.l);
+          part = Pair{0.f, 0.f};
+          left = per;
         }
-        close(i, part);
       }
     }
+    all.add(part.h, part.l);
+    for (; filled < kParts; part = Pair{0.f, 0.f}) parts[warp][filled++][lane] = make_float2(part.h, part.l);
     all = sum_lanes(all);
     turn ^= 1;
     if (!met) cluster.barrier_wait(std::move(begun));  // every CTA is there to be written to
@@ -326,8 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   double whole = -1.0, gone = 0.0;  // without q: the sum of the node's row, once it is known; of the refused
   bool known = true, summing = false;
   if (rank == 0 && threadIdx.x == 0) path[0] = 0;
+  bool walking = true, nothing = false;
   while (true) {
-    if (warp == 0) {
+    if (walking && warp == 0) {
       if (summing) {
         if (!kDraft) whole = row_total;
         total = kDraft ? row_total : whole - gone;
@@ -393,18 +395,20 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       }
     }
     __syncthreads();
-    const Ask x = ask;
+    Ask x = ask;
+    if (nothing) {  // is left: p itself
+      x.n_refused = 0;
+      x.c = Pair{0.f, 0.f};
+    }
     row_sum(x);
-    if (x.last) break;
+    if (!x.last) continue;
+    __syncthreads();
+    if (nothing || row_total > 0.0) break;
+    nothing = true;
+    walking = false;
   }
-  __syncthreads();
 
   // ---- the next token
-  if (!(row_total > 0.0)) {  // nothing is left: p itself
-    const Ask x{ask.node, 0, Pair{0.f, 0.f}, true};
-    row_sum(x);
-    __syncthreads();
-  }
   const double all = row_total;
   const bool some = all > 0.0 && all < INFINITY;
   if (rank == 0 && warp == 0) {
@@ -443,17 +447,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       const int r0 = min(w1, w0 + part * each), r1 = min(w1, r0 + each);
       // its pieces, 32 at a time, up to those that pass the target
       int v0 = r0;
-      double sofar = before;
+      double sofar = before, piece = 0.0;  // this lane's of the 32 from v0 on
       for (int i = r0; i < r1; i += 32) {
-        const double sum = sum_lanes(row.sum(i + lane, r1)).value();
+        const Pair here = row.sum(i + lane, r1);
+        const double sum = sum_lanes(here).value();
         if (sum > 0.0) {
           v0 = i;
           before = sofar;
+          piece = here.value();
           if (sofar + sum > target) break;
         }
         sofar += sum;
       }
-      const int at = crossing(row.sum(v0 + lane, r1).value(), target, before);
+      const int at = crossing(piece, target, before);
       if (at >= 0 && lane == at) {
         const int v = v0 + at;
         const Piece<E> x = row.load(row.p, v), y = row.load(row.q, v);
