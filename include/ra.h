@@ -790,8 +790,9 @@ RA_API ra_status ra_merge(const ra_state* partials, int32_t G, void* out, float*
  * ra_watchdog_config -- settings of the bounded waits in the tensor-core
  * kernels (bf16 forward, fold, partial, split and backward calls, and the
  * kernel of ra_cache_attention for more than 16 query rows per key head; 32
- * over an RA_E4M3 cache).  The pages have no counterpart: it belongs to the
- * library's failure detection.
+ * over an RA_E4M3 cache; of ra_cache_attention_shared likewise, and for more
+ * than 16 rows of a batch where it shares).  The pages have no counterpart: it
+ * belongs to the library's failure detection.
  *   wait_cycles  SM clock cycles one wait of a kernel may take before the
  *                kernel gives up: it records RA_ERR_TIMEOUT (read by
  *                ra_last_device_status), lets the copies and products it
@@ -801,7 +802,7 @@ RA_API ra_status ra_merge(const ra_state* partials, int32_t G, void* out, float*
  *                later tensor-core launch (the fold kernel of the forward,
  *                causal, partial, fold and split calls; the dK/dV and dQ
  *                kernels of the backward calls; the many-row kernel of
- *                ra_cache_attention) load no input, so that its
+ *                ra_cache_attention and its _shared) load no input, so that its
  *                waits run out and the call reports RA_ERR_TIMEOUT; the rows
  *                of that CTA are then not written.  -1 (the default) turns
  *                it off.
