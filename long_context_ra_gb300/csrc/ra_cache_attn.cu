@@ -19,7 +19,8 @@
 // whose probabilities are kept twice side by side; 8 rows x 2 keys a lane are
 // 32 paired FFMA for 10 reads of 16 bytes.  Measured: 2 sequences of 4096, 3 key
 // heads of 80, 6 rows each 19 us a call (70 with one warp per row and a tile at
-// a time); 256 rows over 4096 keys of 128: 17 TFLOP/s.
+// a time); 256 rows over 4096 keys of 128: 20 TFLOP/s (17 with divisions to find a
+// piece's key, and one loop over values for tiles of both kinds).
 //
 // A key that a row does not see has p = 0.  In tiles with drafts or the end that
 // hold a value that is not finite it is left out of the sum rather than
@@ -73,6 +74,12 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
   constexpr bool kShared = IsShared<A>::value;
   const auto& c = paged(a);
   const int d = c.d, ld = d + 4;
+  // i / (d / 8) of a tile's pieces as a product: with i < 2^13 and d / 8 <= 2^5 what
+  // the factor is rounded up by stays below the step to the next quotient
+  const int per_key = d / 8;
+  const uint32_t by_key = (1u << 20) / per_key + 1u;
+  static_assert(kTile * RA_MAX_HEAD_DIM / 8 + 4 * F::kThreads <= 8192 && RA_MAX_HEAD_DIM <= 256, "its range");
+  auto key_of = [&](int i) { return static_cast<int>(i * by_key >> 20); };
   float* qs = reinterpret_cast<float*>(smem4);  // [kRows][d]
   float* ks = qs + F::kRows * d;                // [kTile][ld]
   float* vs = ks + kTile * ld;                  // [kTile][d]
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     uint64_t o[kRW][kPairs];  // columns 2 lane, 2 lane + 1 of every 64
     int t[kRW];
     // a row's sequence and the new tokens that it may see (stretches: per row)
-    [[maybe_unused]] int mask_b[kRW], cnt[kRW];
+    [[maybe_unused]] int mask_b[kRW] = {}, cnt[kRW] = {};
     auto seq_of = [&](int r) {
       if constexpr (kShared)
         return SeqInfo{u.seq.len, cnt[r]};
@@ -160,19 +167,20 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
       look_up(tile + 1);
       const bool border = tile * kTile + kTile > context;
       bool bad = false;  // a value that is not finite in a tile that not every row sees
-      for (int i0 = threadIdx.x; i0 < kTile * d / 8; i0 += 4 * F::kThreads) {
+      for (int i0 = threadIdx.x; i0 < kTile * per_key; i0 += 4 * F::kThreads) {
         // four pieces of 8 elements of K and of V are on their way together
         Packed<H, 8> x[4], y[4];
         uint32_t ek[4], ev[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const int i = i0 + z * F::kThreads;
-          const int64_t row = i < kTile * d / 8 ? at[i / (d / 8)] : -1;
+          const int key = key_of(i);
+          const int64_t row = i < kTile * per_key ? at[key] : -1;
           x[z].zero();
           y[z].zero();
           ek[z] = ev[z] = 127;
           if (row >= 0) {
-            const int e = (i % (d / 8)) * 8;
+            const int e = (i - key * per_key) * 8;
             x[z].load(static_cast<const H*>(c.k) + row * d + e);
             y[z].load(static_cast<const H*>(c.v) + row * d + e);
             if (k8) {
@@ -184,8 +192,8 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const int i = i0 + z * F::kThreads;
-          if (i >= kTile * d / 8) break;
-          const int key = i / (d / 8), e = (i % (d / 8)) * 8;
+          if (i >= kTile * per_key) break;
+          const int key = key_of(i), e = (i - key * per_key) * 8;
           float f[8];
           x[z].get(f);
           if (k8) {
@@ -303,16 +311,20 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
       int col[kPairs];
 #pragma unroll
       for (int x = 0; x < kPairs; ++x) col[x] = 2 * lane + 64 * x < d ? 2 * lane + 64 * x : 0;
-#pragma unroll 2
-      for (int key = 0; key < F::kWarpKeys; ++key, vw += d) {
-        ulonglong2 pr[kRW / 2];
+      auto key_probs = [&](int key, ulonglong2 (&pr)[kRW / 2], uint64_t (&vv)[kPairs]) {
 #pragma unroll
         for (int r = 0; r < kRW / 2; ++r) pr[r] = *reinterpret_cast<const ulonglong2*>(&probs[warp][key][r]);
-        uint64_t vv[kPairs];
 #pragma unroll
         for (int x = 0; x < kPairs; ++x)
           if (64 * x < d) vv[x] = *reinterpret_cast<const uint64_t*>(vw + col[x]);
-        if (whole_tile || clean) {
+        vw += d;
+      };
+      if (whole_tile || clean) {
+#pragma unroll 4
+        for (int key = 0; key < F::kWarpKeys; ++key) {
+          ulonglong2 pr[kRW / 2];
+          uint64_t vv[kPairs];
+          key_probs(key, pr, vv);
 #pragma unroll
           for (int x = 0; x < kPairs; ++x)
             if (64 * x < d) {
@@ -322,7 +334,13 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                 o[r + 1][x] = fma_f32x2(pr[r / 2].y, vv[x], o[r + 1][x]);
               }
             }
-        } else {
+        }
+      } else {
+#pragma unroll 1
+        for (int key = 0; key < F::kWarpKeys; ++key) {
+          ulonglong2 pr[kRW / 2];
+          uint64_t vv[kPairs];
+          key_probs(key, pr, vv);
 #pragma unroll
           for (int r = 0; r < kRW; r += 2) {
             // the same for every lane: whether a row sees this key
