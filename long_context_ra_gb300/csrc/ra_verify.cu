@@ -26,8 +26,9 @@
 // which 134 MB of rows take 20 at the copy rate and the chain of a single sequence
 // some 11; bf16 35 (22 operations an element for the pairs: issue-bound).  One
 // sequence, V = 32768, 14.5 us.  32 trees of 32 chosen tokens, V = 100003, bf16, 25:
-// a pass over a row for every node of the path that refuses a token, each load,
-// cluster barrier and decision, one behind the other.  So the sums of all warps go
+// a pass over a row for every node of the path that refuses a token (and one more
+// wherever the refused had 7/8 of what was summed), each load, cluster barrier and
+// decision, one behind the other.  So the sums of all warps go
 // to all CTAs ahead of one barrier, the loads of the parts are under way together
 // (31 -> 27 us), and code that runs once stays short, since it is loaded as it
 // runs: one place that sums a row, the row's ends in a loop (27 -> 25, one sequence
@@ -324,15 +325,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   // by all warps a decision took 1 us)
   int node = 0, kept = 1, t = 0, n_refused = 0;
   double total = 1.0, scale = 0.0;  // of what is left of the row; c
-  double whole = -1.0, gone = 0.0;  // without q: the sum of the node's row, once it is known; of the refused
+  // Without q a refusal only takes its token out, so that a sum serves for the next
+  // one too: what it was when it was taken (< 0: not yet) and what has gone from it
+  // since.  The difference stands while it is at least kKept of the sum, of which it
+  // then keeps all but three bits of the accuracy; where less is left (as of a row
+  // with most of its weight on the refused) the row is summed again without them.
+  constexpr double kKept = 0.125;
+  double whole = -1.0, gone = 0.0;
   bool known = true, summing = false;
   if (rank == 0 && threadIdx.x == 0) path[0] = 0;
   bool walking = true, nothing = false;
   while (true) {
     if (walking && warp == 0) {
       if (summing) {
-        if (!kDraft) whole = row_total;
-        total = kDraft ? row_total : whole - gone;
+        whole = total = row_total;
+        gone = 0.0;
         known = true;
       }
       while (true) {
@@ -352,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         if (t >= count) break;
         if (!known && !kDraft && whole >= 0.0) {
           total = whole - gone;
-          known = true;
+          known = total >= kKept * whole;
         }
         if (!known) {
           summing = true;
@@ -390,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       }
       if (lane == 0) {
         const float h = static_cast<float>(scale);
-        // for a decision without q the whole row is summed once, the refused with it
-        ask = Ask{node, summing && !kDraft ? 0 : n_refused, Pair{h, static_cast<float>(scale - h)}, !summing};
+        ask = Ask{node, n_refused, Pair{h, static_cast<float>(scale - h)}, !summing};
       }
     }
     __syncthreads();
