@@ -714,8 +714,10 @@ RA_API ra_status ra_cache_compact(const ra_cache* cache, const int32_t* table, i
  *   probs        [B, T, V] of `dtype`: row t is the model's distribution of
  *                the token after node t.  Elements are >= 0; rows add up to 1.
  *   draft_probs  likewise: row t is what the drafts below node t were drawn
- *                from, each by itself.  NULL: drafts were chosen, not drawn
- *                (q = 1 at the draft); r_k is then r_{k-1} without x_k.
+ *                from, each by itself; that of a node without drafts, or whose
+ *                first one stays, may hold anything but at the draft.  NULL:
+ *                drafts were chosen, not drawn (q = 1 at the draft); r_k is then
+ *                r_{k-1} without x_k.
  *   tokens       int64 [B, T].  parent  int32 [B, T], or NULL: a chain (t - 1).
  *                A node whose token is not in 0 .. V - 1 or whose parent is not
  *                in 0 .. t - 1 is no draft (entry 0 is not looked at).

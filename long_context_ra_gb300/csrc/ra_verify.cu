@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   auto row_sum = [&](const Ask& x) {
     const int64_t at = (row0 + x.node) * a.V;
     row.p = static_cast<const E*>(a.probs) + at;
-    row.q = static_cast<const E*>(kDraft ? a.draft : a.probs) + at;
+    // where none was refused (c = 0) the rest is p: a node without drafts may have no row of q
+    row.q = static_cast<const E*>(kDraft && x.c.h != 0.f ? a.draft : a.probs) + at;
     row.shift = static_cast<int>(at % Piece<E>::kN);
     row.whole = static_cast<int>((a.V + row.shift) / Piece<E>::kN);
     row.c = x.c;
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     row_sum(x);
     if (!x.last) continue;
     __syncthreads();
-    if (nothing || row_total > 0.0) break;
+    if (nothing || !(row_total <= 0.0)) break;  // (a NaN is no row without a rest)
     nothing = true;
     walking = false;
   }

@@ -11,7 +11,7 @@ import torch
 
 import fork_ref as F
 import long_context_ra_gb300 as ra
-from test_gpu_verify import BORDER, check
+from test_gpu_verify import check, make
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -110,3 +110,35 @@ def test_a_refused_draft_that_is_not_finite(dtype):
     upto = rest.cumsum(-1)
     want = (upto > u[:, :1].double() * upto[:, -1:]).double().argmax(-1)
     assert torch.equal(token, want)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -1.0, 1e30])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tree", [False, True])
+def test_rows_of_draft_probs_that_nothing_was_drawn_from(tree, dtype, value):
+    """A node without drafts has no row of draft_probs: what lies there does not
+    matter, in a chain that stays whole, at the leaves of trees, for a node 0
+    that stands alone."""
+    B, T, V = 20, 6, 301
+    p, q, tokens, parent, u = make(B, T, V, dtype, tree, True, 9)
+    u[:, 1:] *= 0.05
+    count = [T - b % T for b in range(B)]
+    for b in range(B):
+        above = {parent[b, t] if tree else t - 1 for t in range(1, count[b])}
+        for t in set(range(T)) - above:
+            q[b, t] = value
+    path, kept, token = check(p, q, tokens, parent, u, count)
+    assert (kept > 1).any() and (token >= 0).all()
+
+
+def test_a_row_of_draft_probs_that_is_needed():
+    """A NaN in the row that refused a draft was drawn from: no next token."""
+    p, q, tokens, parent, u = make(3, 2, 50, torch.float32, False, True, 2)
+    u[:, 1] = float(ONE)
+    p[:, 0, :] = 1.0 / 50
+    q[:, 0] = torch.softmax(torch.arange(50.0, device=DEV) * 0.1, -1)
+    tokens[:, 1] = 49
+    q[1, 0, 3] = math.nan
+    par = torch.tensor([[-1, 0]] * 3, dtype=torch.int32, device=DEV)
+    path, kept, token = ra.ra_verify_drafts(p, tokens, u, par, q)
+    assert kept.tolist() == [1, 1, 1] and token.tolist()[1] == -1 and min(token.tolist()[::2]) >= 0
