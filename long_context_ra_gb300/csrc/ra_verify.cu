@@ -136,7 +136,7 @@ struct Row {
     uint32_t out = 0;  // bit i: element i was refused
     if (!kDraft)
       for (int z = 0; z < n_refused; ++z) {
-        const int64_t place = refused[z] + shift;
+        const int64_t place = static_cast<int64_t>(refused[z]) + shift;  // passes 32 bits in the longest rows
         if (place / kN == v) out |= 1u << (place % kN);
       }
 #pragma unroll

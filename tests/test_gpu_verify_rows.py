@@ -142,3 +142,16 @@ def test_a_row_of_draft_probs_that_is_needed():
     par = torch.tensor([[-1, 0]] * 3, dtype=torch.int32, device=DEV)
     path, kept, token = ra.ra_verify_drafts(p, tokens, u, par, q)
     assert kept.tolist() == [1, 1, 1] and token.tolist()[1] == -1 and min(token.tolist()[::2]) >= 0
+
+
+def test_the_longest_row():
+    """V = 2^31 - 1: the last token's place in the second row, which begins 14
+    bytes behind a multiple of 16, lies behind 2^31."""
+    V = 2 ** 31 - 1
+    p = torch.zeros(1, 3, V, dtype=torch.bfloat16, device=DEV)
+    p[0, 0, V - 2] = 1.0
+    p[0, 1, V - 1], p[0, 1, V - 3], p[0, 1, 5] = 0.5, 0.25, 0.25
+    tokens = torch.tensor([[0, V - 2, V - 1]], device=DEV)
+    u = torch.tensor([[0.6, 0.5, 0.9]], device=DEV)
+    path, kept, token = ra.ra_verify_drafts(p, tokens, u)
+    assert path.tolist() == [[0, 1, -1]] and kept.tolist() == [2] and token.tolist() == [V - 3]
