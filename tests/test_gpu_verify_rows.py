@@ -155,3 +155,24 @@ def test_the_longest_row():
     u = torch.tensor([[0.6, 0.5, 0.9]], device=DEV)
     path, kept, token = ra.ra_verify_drafts(p, tokens, u)
     assert path.tolist() == [[0, 1, -1]] and kept.tolist() == [2] and token.tolist() == [V - 3]
+
+
+def test_a_long_row_with_a_peak():
+    """Some 2^13 small probabilities behind one that has a good part of the row, in
+    one thread's part of it."""
+    B, T, V = 6, 3, 1 << 26
+    r = np.random.RandomState(3)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    p = torch.zeros(B, T, V, device=DEV)
+    tokens = torch.tensor([[0, 1, 0]], device=DEV).expand(B, T).contiguous()
+    par = torch.tensor([[-1, 0, 0]], dtype=torch.int32, device=DEV).expand(B, T).contiguous()
+    u = torch.full((B, T), float(ONE), device=DEV)
+    for b in range(B):
+        row = torch.exp(torch.randn(V, generator=g, device=DEV))
+        p[b, 0] = row * (0.4 / row.sum(dtype=torch.float64)).float()
+        p[b, 0, 1], p[b, 0, 0] = 0.25, 0.0
+        others = float(p[b, 0].sum(dtype=torch.float64)) - 0.25
+        x, y = beside(others, others, b % 2 == 0, r)
+        p[b, 0, 0], u[b, 2] = float(x), float(y)
+    path, kept, _ = ra.ra_verify_drafts(p, tokens, u, par)
+    assert kept.tolist() == [2, 1] * 3 and path[::2, 1].tolist() == [2] * 3
