@@ -730,7 +730,13 @@ RA_API ra_status ra_cache_compact(const ra_cache* cache, const int32_t* table, i
  *   token        int64 [B], written: the next token; -1 where the sequence
  *                takes no part or the row's sum is not positive and finite.
  * Decisions are those of the formulas in real numbers but for a relative
- * 2^-40 or so around their borders.
+ * 2^-40 or so around their borders (where a node has refused two drawn drafts
+ * and more, 2^-40 or so of the whole row's sum: r_k is a difference of p and q).
+ * The formulas give the model's distribution for u from all of [0, 1).  Numbers
+ * that are multiples of 2^-24, as fp32 generators give them, resolve just
+ * that: a probability comes out with an error below 2^-24, and a token whose
+ * interval of the cumulative sum holds no such multiple does not come out (from
+ * V = 10^5 on, some of the tail's).
  * probs and draft_probs are 16-byte aligned.  T <= 1024, V <= 2^31 - 1.
  * Errors: RA_ERR_INVALID_ARG (null pointer, negative size, T or V < 1, bad
  * dtype), RA_ERR_UNSUPPORTED, RA_ERR_MISALIGNED, RA_ERR_ARCH, RA_ERR_CUDA.

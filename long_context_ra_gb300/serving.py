@@ -537,7 +537,8 @@ def ra_verify_drafts(probs, tokens, uniform, parent=None, draft_probs=None, coun
     1); node 0 is the newest settled token, tokens [B, T] (int64) the drafts,
     parent [B, T] (int32; None: a chain) the node that each follows;
     draft_probs: what they were drawn from (None: they were chosen); uniform
-    [B, T] float32 in [0, 1).  Returns (path [B, T] int32: the nodes that stay,
+    [B, T] float32 in [0, 1), which resolves probabilities to 2^-24.  A row of
+    draft_probs that no draft was drawn from is not read.  Returns (path [B, T] int32: the nodes that stay,
     -1 behind them; kept [B] int32: their number, node 0 counted; token [B]
     int64)."""
     B, T, V = probs.shape
