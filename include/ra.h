@@ -607,7 +607,8 @@ RA_API ra_status ra_cache_attention_shared(const void* q, const ra_cache* cache,
                                            void* out, float* lse, void* workspace, int64_t workspace_bytes,
                                            int32_t B, int32_t Hq, int32_t T, ra_dtype dtype, ra_stream_t stream);
 
-/* Scratch bytes ra_cache_attention_shared needs (-1 for invalid sizes). */
+/* Scratch bytes ra_cache_attention_shared needs (-1 for invalid sizes): those of
+   ra_cache_attention for sizes of which no batch is shared. */
 RA_API int64_t ra_cache_attention_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T,
                                                          int32_t d);
 

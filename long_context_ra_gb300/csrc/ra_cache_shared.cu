@@ -28,6 +28,7 @@ namespace {
 constexpr int kPlanThreads = 1024;    // at most
 constexpr int kPlanSequences = 2048;  // 32 bytes of shared memory each
 constexpr int kTile = 128;            // a multiple of every kernel's key tile
+constexpr int kMostRows = 256;        // of a lot in any kernel
 // Bytes of repeated prefixes below which they are read again: some 25 us at the
 // rate of the decode kernel, which plan, second launch and join take.  (us shared,
 // not shared, tails of 100.  bf16, 8 heads of 128: 4 sequences of 8192, 102 MB, 36
@@ -464,11 +465,17 @@ Room room(int32_t B, int64_t rows1, int32_t heads, int32_t d) {
   return r;
 }
 
+// Whether any type's units and the plan have room for sequences of such a batch:
+// the plain call's workspace serves for the others.
+bool may_share(int32_t B, int64_t rows1) { return B >= 2 && B <= kPlanSequences && 2 * rows1 <= kMostRows; }
+
 }  // namespace
 
 int64_t cache_attention_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t heads, int32_t T, int32_t d) {
   const int64_t plain = cache_attention_workspace_bytes(B, Hq, heads, T, d);
-  const int64_t shared = room(B, static_cast<int64_t>(Hq / heads) * T, heads, d).end;
+  const int64_t rows1 = static_cast<int64_t>(Hq / heads) * T;
+  if (!may_share(B, rows1)) return plain;
+  const int64_t shared = room(B, rows1, heads, d).end;
   return plain > shared ? plain : shared;
 }
 
@@ -498,7 +505,7 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
   // than the plan and the join take.
   const int64_t element = held == RA_F32 ? 4 : held == RA_BF16 ? 2 : 1;
   const int64_t again = ((static_cast<int64_t>(B - 1) * a.c.width) << a.c.page_shift) * a.c.heads * 2 * a.c.d * element;
-  if (B < 2 || B > kPlanSequences || 2 * rows1 > shape[0].rows || rows1 > shape[1].rows || again < kWorthSharing)
+  if (!may_share(B, rows1) || 2 * rows1 > shape[0].rows || rows1 > shape[1].rows || again < kWorthSharing)
     return launch_cache_attention(a, dense, held, s);
 
   const Room r = room(B, rows1, a.c.heads, a.c.d);

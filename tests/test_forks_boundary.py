@@ -204,3 +204,15 @@ def test_fork_refuses_what_lies_over_its_inputs(L, out, near):
     assert fork(L, **far, **{out: far[near] - 4 * (4 if out != "to" else 19)}) == INV
     assert fork(L, **far, **{out: far[near] + 4 * size}) == ARCH
     assert fork(L, **far, **{out: far[near] - 4 * (5 if out != "to" else 20)}) == ARCH
+
+
+@pytest.mark.parametrize("sizes", [(32, 32, 8, 512, 128), (64, 8, 8, 129, 64), (1, 32, 8, 1, 128), (1, 4, 4, 128, 80),
+                                   (2049, 32, 8, 4, 128), (100000, 8, 1, 1, 64), (0, 8, 1, 1, 64), (9, 2, 1, 200, 256)])
+def test_batches_that_never_share_need_the_plain_workspace(L, sizes):
+    """More than 128 query rows of a key head and sequence, a single sequence, or
+    more than 2048: no state of a prefix is kept for the join."""
+    want = L.ra_cache_attention_workspace_bytes(*sizes)
+    assert L.ra_cache_attention_shared_workspace_bytes(*sizes) == want
+    # one that may share keeps two fp32 states a row
+    rows = 16 * 32 * 8
+    assert L.ra_cache_attention_shared_workspace_bytes(16, 32, 8, 8, 128) >= 2 * rows * 130 * 4
