@@ -593,13 +593,28 @@ RA_API int64_t ra_cache_attention_workspace_bytes(int32_t B, int32_t Hq, int32_t
  *           entries and lengths in common, cut to whole tiles and pages; that
  *           part is read through the table row of its first sequence, whether
  *           the others hold the same pages or equal copies.
- * Result, other arguments, limits and errors as ra_cache_attention, whose
- * rounding differs where states are joined; RA_ERR_INVALID_ARG also for a NULL
- * `shared`.  Nothing is shared (each sequence reads its own pages, and equal
- * contents give an equal result) where a key head has more than 128 (RA_F32: 16)
- * query rows of a sequence, or half as many in a batch too small for the larger
- * units, where B is above 2048, and where the whole table of B - 1 sequences
- * stands for less than 160 MiB of the cache, which are read again as fast.
+ * Result, other arguments, limits and errors as ra_cache_attention;
+ * RA_ERR_INVALID_ARG also for a NULL `shared`.  The rounding differs where states
+ * are joined, and over an RA_E4M3 cache with RA_BF16 inputs: where the batch has
+ * more than 16 query rows a key head, a prefix runs in the kernel for many rows,
+ * whose probabilities are bf16 (8 bits), while ra_cache_attention of up to 32 rows
+ * a head, and a sequence's own part, have f16 (11 bits): where the weight lies on
+ * many keys, an rms error of 2.2e-3, as over an RA_BF16 cache, instead of 1.7e-3
+ * (of which the result's own rounding is all).
+ * Nothing is shared (each sequence reads its own pages, and equal contents give an
+ * equal result)
+ *   where a unit has no room for two sequences' query rows of a key head: above
+ *     128 of a sequence (RA_F32: 16; 8 for d = 256), in small batches above half
+ *     of the rows that the kernel for so many takes (RA_BF16: 16 or 128; RA_F32: 4,
+ *     8 or 16);
+ *   where B is above 2048;
+ *   where the whole table of B - 1 sequences stands for less than 160 MiB of the
+ *     cache.  The table's width counts here, since lengths and entries lie on the
+ *     device: in a table much wider than its sequences are long, short prefixes
+ *     take longer shared than read again (3 sequences of 1100 tokens 27 us, not
+ *     17; 16 of 1100 39, not 24), and ra_cache_attention is the call for them.  The
+ *     two are even at some 25000 repeated tokens of 4 sequences and 60000 of 16
+ *     or 64 (8 key heads).
  */
 RA_API ra_status ra_cache_attention_shared(const void* q, const ra_cache* cache, const int32_t* table,
                                            int32_t width, const int32_t* lens, const int32_t* shared,

@@ -29,14 +29,21 @@ constexpr int kPlanThreads = 1024;    // at most
 constexpr int kPlanSequences = 2048;  // 32 bytes of shared memory each
 constexpr int kTile = 128;            // a multiple of every kernel's key tile
 constexpr int kMostRows = 256;        // of a lot in any kernel
-// Bytes of repeated prefixes below which they are read again: some 25 us at the
-// rate of the decode kernel, which plan, second launch and join take.  (us shared,
-// not shared, tails of 100.  bf16, 8 heads of 128: 4 sequences of 8192, 102 MB, 36
-// 36; 4 of 16384, 203 MB, 42 50; 16 of 4096, 260 MB, 48 42; 64 of 1024, 297 MB, 61
-// 54; 16 of 8192, 511 MB, 49 63; 64 of 16384, 77 341.  Out of 8 bits: 4 of 8192, 51 MB,
-// 38 36; 4 of 16384, 101 MB, 42 48; 16 of 4096, 130 MB, 52 46; 64 of 2048, 281 MB, 66
-// 83.  2 heads of 64: 64 of 8192, 268 MB, 46 44.  f32, 4 heads of 80: 4 of 8192,
-// 64 MB, 50 50; 16 of 2048, 84 MB, 59 46; 16 of 4096, 162 MB, 67 75.)
+// Bytes of the table of all sequences but one below which prefixes are read again,
+// as plan, second launch and join take some 20 us and short units more.  The host
+// sees the table's width alone, so the rule is right for tables about as wide as
+// the sequences are long and shares too much in wider ones.  (us shared, not shared,
+// replayed graphs, tails of 100, 4 queries a head; MB repeated.  bf16, 8 heads of
+// 128: 3 sequences of 1024 27 17; 4 of 4096, 50 MB, 27 25; 4 of 8192, 101 MB, 29 29;
+// 4 of 16384, 201 MB, 31 41; 16 of 1024, 63 MB, 39 24; 16 of 2048, 126 MB, 39 29; 16
+// of 4096, 252 MB, 40 39; 16 of 8192, 503 MB, 43 58; 64 of 1024, 264 MB, 54 51; 64 of
+// 2048, 528 MB, 56 70; 64 of 16384, 70 336.  Out of 8 bits: 4 of 8192, 50 MB, 31 31;
+// 4 of 16384, 101 MB, 33 41; 16 of 2048, 63 MB, 41 31; 16 of 4096, 126 MB, 42 40; 16 of
+// 8192, 252 MB, 46 62; 64 of 1024, 132 MB, 54 53; 64 of 2048, 264 MB, 56 74.  2 heads of
+// 64: 64 of 4096, 132 MB, 38 29; 64 of 8192, 264 MB, 39 41.  f32, 4 heads of 80: 4 of
+// 8192, 63 MB, 40 41; 4 of 16384, 126 MB, 45 60; 16 of 2048, 79 MB, 46 39; 16 of 4096,
+// 157 MB, 56 60.)  Groups are not weighed one by one: in a batch that shares, a pair
+// with a tile in common has a lot of its own.
 constexpr int64_t kWorthSharing = 160ll << 20;
 constexpr int kRuns = 9;              // lengths of a run that are tried
 
@@ -485,7 +492,9 @@ cudaError_t launch_cache_attention_shared(const CacheAttnArgs& a, const int32_t*
   const int64_t rows1 = head_rows(a), stacked = B * rows1;
   const bool k8 = held == RA_E4M3;
   // The kernel for lots, by all rows that there may be, and the one for a
-  // sequence's own.
+  // sequence's own.  (Out of 8 bits the former rounds probabilities to bf16, 8
+  // bits, as its operands are; the decode kernel, with f16's 11, has units of 16
+  // rows and would read a prefix again for every 16 of a group's.)
   SharedKernel kernel[2];
   SharedShape shape[2];
   if (dense == RA_F32) {

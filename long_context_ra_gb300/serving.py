@@ -385,7 +385,11 @@ def ra_cache_attention_shared(q, cache: RaCache, table, lens, shared, count=None
     """ra_cache_attention for sequences that share prefixes, each read once for
     all of them: shared [B] (int32) > 0 are the tokens that sequence b has in
     common with the one before it (the next lower one with lens >= 0), else a
-    group begins at b.  `workspace`: ra_cache_attention_shared_workspace_bytes."""
+    group begins at b.  `workspace`: ra_cache_attention_shared_workspace_bytes.
+    Short prefixes (below some 50000 repeated tokens in all) take longer shared
+    than read again, which a table as wide as they are long shows to the call; in
+    one much wider, ra_cache_attention is the call for them.  Over an 8-bit cache
+    a prefix's probabilities are bf16, not f16, where B x T x Hq / heads > 16."""
     if shared is None:
         raise ValueError("shared must be an int32 tensor [B]")
     return _attend(shared, q, cache, table, lens, count, mask, out, lse, workspace, stream)
