@@ -31,9 +31,10 @@ constexpr int kTile = 128;            // a multiple of every kernel's key tile
 constexpr int kMostRows = 256;        // of a lot in any kernel
 // Bytes of the table of all sequences but one below which prefixes are read again,
 // as plan, second launch and join take some 20 us and short units more.  The host
-// sees the table's width alone, so the rule is right for tables about as wide as
-// the sequences are long and shares too much in wider ones.  (us shared, not shared,
-// replayed graphs, tails of 100, 4 queries a head; MB repeated.  bf16, 8 heads of
+// sees the table's width alone, so the rule fits tables about as wide as the
+// sequences are long (at worst 8 us off below: 4 of 16384 out of 8 bits) and shares
+// too much in wider ones.  (us shared, not shared, replayed graphs, tails of 100, 4
+// queries a head, f32 2; MB repeated.  bf16, 8 heads of
 // 128: 3 sequences of 1024 27 17; 4 of 4096, 50 MB, 27 25; 4 of 8192, 101 MB, 29 29;
 // 4 of 16384, 201 MB, 31 41; 16 of 1024, 63 MB, 39 24; 16 of 2048, 126 MB, 39 29; 16
 // of 4096, 252 MB, 40 39; 16 of 8192, 503 MB, 43 58; 64 of 1024, 264 MB, 54 51; 64 of
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   int64_t own_at = own_before.y - sum.y;
   const int64_t own_all = all.y, total = all.x + (a.one_list ? own_all : 0);
   // ---- the run of a CTA.  Lots of a group read the same keys: where they begin
-  // at runs' starts they do so at the same time, out of L2 (9 lots of 65536 keys,
+  // at runs' starts they do so at the same time, out of L2 (10 lots of 65536 keys,
   // 8 heads: 2.5 GB from memory without).  The smallest run, up to an eighth
   // above the even one, with which every lot can take whole runs.
   const int64_t even = (total + a.ctas[0] - 1) / a.ctas[0];

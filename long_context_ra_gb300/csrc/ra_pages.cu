@@ -7,14 +7,17 @@
 // whatever the order in which threads run, and no state can disagree with
 // another.  Counts change by integer atomics, whose order does not matter.
 //
-// Bound by launches and by chains of loads: a fork reads a row of the table and
-// adds to its pages' counts, a block per row, 5 us; a reservation is one block,
-// 10 us for 4 sequences and 13 for 96 with trees of 32 (who asks; the counts of the
-// pages they hold; a scan over them; the free pages, 16 a thread and round); copies
-// and moves go with 16 bytes a lane, four or eight of them under way (96 forks, of
-// which 64 copy a page of 2 x 128 KB: 9 us; 192 sequences' 64 nodes, 12 MB in
-// scattered rows, 12).  96 beams' release, fork, room and copy by graph replay 23 us,
-// of which 48 MB take 7 at the copy rate.
+// Bound by launches and by chains of loads (times of a call among others of its kind,
+// behind one another): a fork reads a row of the table and adds to its pages' counts,
+// a block per row, 5 us; a reservation is one block, 6 us for 4 sequences and 9 for 96
+// with trees of 32 (who asks; the counts of the pages they hold; a scan over them; the
+// free pages, 16 a thread and round); copies and moves go with 16 bytes a lane, four
+// or eight of them under way (96 forks, of which 64 copy a page of 2 x 128 KB: 8 us; 192
+// sequences' 64 nodes, 12 MB in scattered rows, 8).  96 beams' release, fork, room and
+// copy by graph replay 23 us, of which 48 MB take 7 at the copy rate.
+// Rounds beyond the first are slow: one block looks at 16384 pages in some 4 us, and
+// twice, so a pool whose free pages lie behind 95000 held ones takes 60 us a
+// reservation, behind 950000 540.
 
 #include "ra_paged.cuh"
 

@@ -20,9 +20,9 @@
 // Decisions have to be those of the definition next to a border as well, and a
 // border lies in every 1 / V of the unit interval: sums of fp32 would move 1 %
 // of them.  FP64 adds at 1/64 of the rate of fp32, which would bound the pass;
-// sums are pairs of floats (error-free sums, 2^-47), and 64 bits decide.
+// sums are pairs of floats (error-free sums, 2^-45 and better), and 64 bits decide.
 //
-// Measured (fp32 unless said): 128 sequences of 5 drafts, V = 131072, 41 us, of
+// Measured (fp32 unless said): 128 sequences of 5 drafts, V = 131072, 41 to 42 us, of
 // which 134 MB of rows take 20 at the copy rate and the chain of a single sequence
 // some 11; bf16 35 (22 operations an element for the pairs: issue-bound).  One
 // sequence, V = 32768, 14.5 us.  32 trees of 32 chosen tokens, V = 100003, bf16, 25:

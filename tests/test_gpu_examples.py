@@ -1,5 +1,5 @@
-"""The steps of README's serving examples, run as they stand there: what they
-leave in the counts of the pages."""
+"""The documented serving example of samples of prompts, run as it stands: what
+it leaves in the counts of the pages."""
 import re
 from pathlib import Path
 
@@ -10,11 +10,11 @@ import long_context_ra_gb300 as ra
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-README = (Path(__file__).resolve().parent.parent / "README.md").read_text()
+GUIDE = (Path(__file__).resolve().parent.parent / "README.md").read_text()
 
 
 def block(word):
-    (found,) = [b for b in re.findall(r"```python\n(.*?)```", README, re.S) if word in b]
+    (found,) = [b for b in re.findall(r"```python\n(.*?)```", GUIDE, re.S) if word in b]
     return found
 
 
