@@ -13,6 +13,7 @@ import torch
 import fork_ref as F
 import long_context_ra_gb300 as ra
 import serve_ref as R
+from long_context_ra_gb300._native import RA_ERR_PAGE
 from test_gpu_cache_attention import check, tree
 from test_gpu_shared_attention import make, wide
 
@@ -243,6 +244,39 @@ def test_a_beam_search_step():
         if sum(want[0]) == 0:
             break
     assert not m.bad or ra.ra_last_device_status()
+
+
+@pytest.mark.parametrize("pages", [60, 16, 8, 7])
+def test_beams_say_when_pages_run_out(pages):
+    """The status of every step is that of a model: a page error in the step that
+    finds too few free pages, nothing in the others."""
+    page, width, n = 8, 6, 4
+    m = F.Pages(pages, width, page)
+    rows = [([-1] * width, 0, 0)]
+    m.reserve(rows, 19)
+    rows = [(rows[0][0], rows[0][1], 19)]
+    rows, old = m.fork(rows, [0] * n), rows
+    m.trim(old)
+    ref, lens = i32(m.ref), i32([19] * n)
+    table, held = i32([r[0] for r in rows]), i32([r[1] for r in rows])
+    r, said = random.Random(pages), []
+    assert ra.ra_last_device_status() == 0
+    for _ in range(12):
+        source, m.bad = [r.randrange(n) for _ in range(n)], False
+        new = m.fork(rows, source)
+        m.trim(rows)
+        want = m.reserve(new, 1)
+        t, h, ln = ra.ra_pages_fork(ref, table, held, lens, i32(source), page)
+        ra.ra_pages_trim(ref, table, held, None, page)
+        got = ra.ra_pages_reserve(ref, t, h, ln, page, 1)
+        said.append(ra.ra_last_device_status())
+        assert (said[-1] == RA_ERR_PAGE) == m.bad and said[-1] in (0, RA_ERR_PAGE)
+        assert [x.tolist() for x in got] == [list(x) for x in want]
+        rows = [(a, b, c + g) for (a, b, c), g in zip(new, want[0])]
+        ln += got[0]
+        table, held, lens = t, h, ln
+        assert ref.tolist() == m.ref and table.tolist() == [list(x[0]) for x in rows]
+    assert (RA_ERR_PAGE in said) == (pages <= 8)
 
 
 # --------------------------------------------------------- graphs and streams
